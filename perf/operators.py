@@ -96,7 +96,7 @@ def draw(rng: random.Random):
         rows, mb = _log(rng, 1, 128), rng.randint(4, 64)
         fill = rng.uniform(0.05, 0.95)
         nb = int(rows * mb / fill / 1.5) + rng.randint(4, 99)
-        return dict(op=op, dtype=dtype, layers=rng.randint(1, 8), rows=rows, max_blocks=mb, num_blocks=min(nb, 4095),
+        return dict(op=op, dtype=dtype, layers=rng.randint(1, 5), rows=rows, max_blocks=mb, num_blocks=min(nb, 4095),
                     fill=fill, **_fit(heads))
     group = rng.choice([1, 2, 4, 6, 7, 8])
     hd = rng.choice([64, 128, 128, 256])
