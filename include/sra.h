@@ -461,6 +461,115 @@ SRA_API int sra_uclip(const void* x, const float* alpha, const float* gamma, voi
                       int64_t out_h_stride, int alpha_per_channel, int gamma_per_channel, float clip_min,
                       float clip_max, int dtype, void* stream);
 
+/*
+ * Pages of the paged cache: sharing, copying, growing, freeing and moving them.
+ *
+ * Rows of block_table are requests, beams or samples; a page is one index of the caches'
+ * num_blocks dimension, the same in every layer's cache. The state is three int32 device
+ * arrays of the caller:
+ *   block_table [rows, max_blocks_per_seq]   row r's pages, in token order;
+ *   seq_lens    [rows]                       tokens of row r: its first
+ *                                            pages(seq_lens[r]) entries are in use,
+ *                                            pages(L) = ceil(L / block_size);
+ *   ref_counts  [num_blocks]                 how many rows hold a page. A page whose count is
+ *                                            not positive is free.
+ * The first is what sra_paged_decode_attention and sra_shared_prefix_attention read; a
+ * caller's allocator can own all three and call only what it needs. Every result follows
+ * from the state and the arguments in a fixed order, never from timing.
+ *
+ * kv_caches: HOST array of n_caches device pointers (a model's layers), each a contiguous
+ * [2, num_blocks, block_size, n_kv_head, head_dim] of `dtype`, aligned to the dtype; read
+ * during the call only (the pointers go into the kernels' parameters). The caches must not
+ * overlap one another or any other argument. Any head_dim and block_size.
+ * err_count: NULL, or a device int32 to which each call adds what it found wrong, as said
+ * at each; the caller zeroes it. Nothing is read or written out of range for any contents of
+ * the device arrays.
+ * workspace: device memory of at least the matching _workspace_size bytes, 16-byte aligned,
+ * contents on entry and exit without meaning; calls that share one must not overlap on the GPU.
+ * Errors of all: negative or too large sizes (rows, max_blocks_per_seq and num_blocks up to
+ * 2^31 - 1, n up to 524280, for the copy 2^40) -> SRA_ERR_SHAPE; unknown dtype ->
+ * SRA_ERR_DTYPE; NULL -> SRA_ERR_NULL; a workspace too small or misaligned, a cache not
+ * aligned to its dtype -> SRA_ERR_ARG; outputs that overlap one another or an input ->
+ * SRA_ERR_ALIAS. n == 0 is a no-op.
+ */
+
+/*
+ * sra_kv_copy_pages — page dst[i] <- page src[i], K and V, in every cache, i < n.
+ * src, dst: device int32 [n]. A pair with a negative index is padding (skipped); one with an
+ * index >= num_blocks is skipped and adds 1 to err_count. A source may repeat. A page may be a
+ * destination once, and no destination may be a source of another pair: the contents of pages that break this
+ * are undefined (nothing else is). n_caches == 0 is a no-op.
+ */
+SRA_API int sra_kv_copy_pages(void* const* kv_caches, int64_t n_caches, const int32_t* src, const int32_t* dst,
+                              int64_t n, int64_t num_blocks, int block_size, int n_kv_head, int head_dim,
+                              int32_t* err_count, int dtype, void* stream);
+
+/*
+ * sra_kv_fork_rows — row children[i] becomes another holder of row parents[i]'s pages (samples
+ * of one prompt; the reorder of a beam search). No page is copied: a partly filled last
+ * page is shared too, and sra_kv_resize_rows copies it before a row writes into it.
+ *   - parents are read as they were at entry, also where a parent is a child of another entry
+ *     (or of its own);
+ *   - ref_counts rises by one for each of the parent's pages and falls by one for each page
+ *     that the child held;
+ *   - the child's row becomes the parent's used entries, then -1; seq_lens[child] =
+ *     seq_lens[parent] (0 frees the child's pages).
+ * parents, children: device int32 [n]; a negative index in either is padding. One each is added
+ * to err_count, and the entry does nothing, for: an index >= rows; a child that an earlier entry
+ * names; a seq_len of the two rows outside [0, max_blocks_per_seq * block_size]. One each is
+ * added for every used table entry outside [0, num_blocks) (the parent's is passed on as it is)
+ * and for every holder that a count does not have (it stays at zero).
+ */
+SRA_API int sra_kv_fork_rows(int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, const int32_t* parents,
+                             const int32_t* children, int64_t n, int64_t rows, int64_t max_blocks_per_seq,
+                             int64_t num_blocks, int block_size, void* workspace, int64_t workspace_bytes,
+                             int32_t* err_count, void* stream);
+SRA_API int64_t sra_kv_fork_workspace_size(int64_t n, int64_t max_blocks_per_seq);
+
+/*
+ * sra_kv_resize_rows — row row_idx[i] is given lens[i] tokens: a decode step's or a prompt's
+ * new tokens (growth), rejected draft tokens (truncation), the end of a request (0).
+ *   1. Rows that shrink give up their entries [pages(new), pages(old)): ref_counts falls,
+ *      the entries become -1.
+ *   2. Rows that grow get pages, in the order of i, the lowest free pages first (those of step
+ *      1 among them), each with count 1. A row whose partly filled last page has other
+ *      holders (count > 1 after step 1) first gets a page in its place: that page's
+ *      tokens up to the old length are copied, K and V, in every cache, and the old page's
+ *      count falls by one. Entry i is served if the pages that entries 0 .. i need together
+ *      are there; otherwise its row stays as it was and 1 is added to err_count.
+ *   3. seq_lens[row_idx[i]] = lens[i] where served or shrunk.
+ * pos, slot_mapping: NULL, or device int64 [n]: the position of the row's last token after
+ * the call and its slot in the cache (page * block_size + offset), what sra_rope_kv_store
+ * takes for a decode step's token; -1 for an empty row and an entry that does nothing.
+ * row_idx, lens: device int32 [n]; a negative row is padding. One each is added to err_count, and
+ * the entry does nothing, for: a row >= rows or one that an earlier entry names; a length (new
+ * or present) outside [0, max_blocks_per_seq * block_size]; a partly filled last page outside
+ * [0, num_blocks) in a row that grows. One each is added for bad entries and missing holders among the
+ * pages given up, as in sra_kv_fork_rows. New pages' contents are not cleared.  * n_caches >= 1.
+ */
+SRA_API int sra_kv_resize_rows(int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, const int32_t* row_idx,
+                               const int32_t* lens, int64_t n, int64_t rows, int64_t max_blocks_per_seq,
+                               void* const* kv_caches, int64_t n_caches, int64_t num_blocks, int block_size,
+                               int n_kv_head, int head_dim, int64_t* pos, int64_t* slot_mapping, void* workspace,
+                               int64_t workspace_bytes, int32_t* err_count, int dtype, void* stream);
+SRA_API int64_t sra_kv_resize_workspace_size(int64_t n, int64_t num_blocks);
+
+/*
+ * sra_kv_compact_pages — the live pages (count > 0), N of them, are moved to the front of the
+ * caches: the i-th live page at or past N goes to the i-th free page before N, with its K and V in
+ * every cache and its count; used entries of block_table follow. Pages N and up are free
+ * afterwards (their contents stay as they were). num_live: NULL, or a device int32 that gets N.
+ * One each is added to err_count for a row whose seq_len is outside [0, max_blocks_per_seq *
+ * block_size] (its entries stay) and for a used entry that is not a live page (it stays).
+ * n_caches >= 1; rows == 0 only moves the pages.
+ */
+SRA_API int sra_kv_compact_pages(int32_t* block_table, const int32_t* seq_lens, int32_t* ref_counts, int64_t rows,
+                                 int64_t max_blocks_per_seq, void* const* kv_caches, int64_t n_caches,
+                                 int64_t num_blocks, int block_size, int n_kv_head, int head_dim, int32_t* num_live,
+                                 void* workspace, int64_t workspace_bytes, int32_t* err_count, int dtype,
+                                 void* stream);
+SRA_API int64_t sra_kv_compact_workspace_size(int64_t num_blocks);
+
 /* Static text for a status code (never NULL). */
 SRA_API const char* sra_status_string(int status);
 

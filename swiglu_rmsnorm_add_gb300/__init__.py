@@ -11,17 +11,24 @@ no CPU or PyTorch fallback: without the built library every call raises.
 from ._binding import (  # noqa: F401
     SRAError,
     add_rmsnorm,
+    compact_kv_pages,
+    copy_kv_pages,
     decode_attention_workspace,
     dyht,
     force_variant,
+    fork_kv_rows,
     glu,
     glu_linear,
+    kv_compact_workspace,
+    kv_fork_workspace,
+    kv_resize_workspace,
     lib,
     linear_workspace,
     paged_decode_attention,
     paged_decode_attention_noalloc,
     pick_variant,
     reglu,
+    resize_kv_rows,
     rmsnorm,
     rmsnorm_linear,
     rope_kv_store,
@@ -37,7 +44,9 @@ from ._binding import (  # noqa: F401
 
 __all__ = ["rmsnorm", "add_rmsnorm", "rope_kv_store", "swiglu", "reglu", "glu", "uclip", "dyht", "paged_decode_attention",
            "paged_decode_attention_noalloc", "decode_attention_workspace",
-           "rmsnorm_linear", "glu_linear", "linear_workspace", "lib",
+           "rmsnorm_linear", "glu_linear", "linear_workspace",
+           "copy_kv_pages", "fork_kv_rows", "resize_kv_rows", "compact_kv_pages",
+           "kv_fork_workspace", "kv_resize_workspace", "kv_compact_workspace", "lib",
            "SRAError",
            "force_variant", "set_pdl", "variant_count", "variant_name", "pick_variant", "status_string",
            "wait_timeouts", "wait_selftest"]

@@ -65,6 +65,19 @@ def lib() -> ctypes.CDLL:
                        "sra_rmsnorm_linear", "sra_glu_linear", "sra_paged_decode_attention_ws",
                        "sra_paged_decode_attention_noalloc", "sra_rmsnorm_linear_ws", "sra_glu_linear_ws"):
                 getattr(L, fn).restype = i32
+            L.sra_kv_copy_pages.argtypes = [vp, i64, vp, vp, i64, i64, i32, i32, i32, vp, i32, vp]
+            L.sra_kv_fork_rows.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, i64, vp, vp]
+            L.sra_kv_fork_workspace_size.argtypes = [i64, i64]
+            L.sra_kv_resize_rows.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, i64, i32, i32, i32, vp, vp,
+                                             vp, i64, vp, i32, vp]
+            L.sra_kv_resize_workspace_size.argtypes = [i64, i64]
+            L.sra_kv_compact_pages.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, vp, i64, vp,
+                                               i32, vp]
+            L.sra_kv_compact_workspace_size.argtypes = [i64]
+            for fn in ("sra_kv_copy_pages", "sra_kv_fork_rows", "sra_kv_resize_rows", "sra_kv_compact_pages"):
+                getattr(L, fn).restype = i32
+            for fn in ("sra_kv_fork_workspace_size", "sra_kv_resize_workspace_size", "sra_kv_compact_workspace_size"):
+                getattr(L, fn).restype = i64
             L.sra_status_string.argtypes = [i32]
             L.sra_status_string.restype = ctypes.c_char_p
             L.sra_version.restype = i32
@@ -569,3 +582,203 @@ def glu_linear(gate_up: torch.Tensor, W: torch.Tensor, y: torch.Tensor | None = 
                                          ACT_CODE[act], wp, wb, _dtype(gate_up), _stream(gate_up, stream))
             _check("sra_glu_linear_ws", st)
     return y
+
+
+# ------------------------------------------------------------------- pages of the cache
+def _kv_caches(kv_caches):
+    """(first cache, pointer array, count) of one cache [2, num_blocks, block_size, n_kv_head,
+    head_dim], a [layers, 2, ...] tensor of them, or a sequence of caches of one shape and dtype."""
+    if isinstance(kv_caches, torch.Tensor):
+        caches = [kv_caches] if kv_caches.dim() == 5 else list(kv_caches) if kv_caches.dim() == 6 else None
+        if caches is None:
+            raise ValueError("kv_caches must be [2, num_blocks, block_size, n_kv_head, head_dim], or [layers, ...] of it")
+    else:
+        caches = list(kv_caches)
+    if not caches:
+        raise ValueError("kv_caches is empty")
+    first = caches[0]
+    for c in caches:
+        _cuda(c, "kv_caches")
+        if c.dim() != 5 or c.shape[0] != 2 or not c.is_contiguous():
+            raise ValueError("each cache must be contiguous [2, num_blocks, block_size, n_kv_head, head_dim]")
+        if c.shape != first.shape or c.dtype != first.dtype:
+            raise ValueError("the caches must share one shape and dtype")
+    _same_device(*caches)
+    return first, (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches]), len(caches)
+
+
+def _int32(t, name, dim):
+    _cuda(t, name)
+    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension{'s' if dim > 1 else ''}")
+
+
+def _err_ptr(err_count):
+    if err_count is None:
+        return None
+    _cuda(err_count, "err_count")
+    if err_count.dtype != torch.int32:
+        raise ValueError("err_count must be int32")
+    return err_count.data_ptr()
+
+
+def _page_state(block_table, seq_lens, ref_counts):
+    _int32(block_table, "block_table", 2)
+    _int32(seq_lens, "seq_lens", 1)
+    _int32(ref_counts, "ref_counts", 1)
+    _same_device(block_table, seq_lens, ref_counts)
+    if seq_lens.shape[0] != block_table.shape[0]:
+        raise ValueError("block_table and seq_lens must have one row per request")
+    return block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr()
+
+
+def _byte_workspace(fn: str, n: int, device) -> torch.Tensor:
+    if n < 0:
+        _check(fn, int(n))
+    return torch.empty(max(16, int(n)), dtype=torch.uint8, device=device)
+
+
+def _workspace_args(workspace, make, like, stream):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one made for this call. One made
+    here is allocated on the stream that the call runs on, so its memory is not used again before
+    the call's kernels are done with it."""
+    if workspace is None:
+        if stream is None:
+            workspace = make()
+        else:
+            s = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+            with torch.cuda.stream(s):
+                workspace = make()
+    _cuda(workspace, "workspace")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _same_device(like, workspace)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def copy_kv_pages(kv_caches, src: torch.Tensor, dst: torch.Tensor, err_count: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """Page dst[i] <- page src[i] of every cache, K and V.
+
+    kv_caches: a cache as rope_kv_store writes it, a [layers, 2, ...] tensor of caches or a
+    sequence of them. src, dst: int32 [n], negative entries skipped. Destinations must be distinct
+    and no source (their contents are undefined otherwise); an index past the cache is skipped
+    and counted in err_count."""
+    cache, ptrs, count = _kv_caches(kv_caches)
+    _int32(src, "src", 1)
+    _int32(dst, "dst", 1)
+    _same_device(cache, src, dst, err_count)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    _, nb, bs, n_kv, hd = cache.shape
+    with torch.cuda.device(cache.device):
+        st = lib().sra_kv_copy_pages(ptrs, count, src.data_ptr(), dst.data_ptr(), src.numel(), nb, bs, n_kv, hd,
+                                     _err_ptr(err_count), _dtype(cache), _stream(cache, stream))
+    _check("sra_kv_copy_pages", st)
+
+
+def kv_fork_workspace(n: int, max_blocks: int, device) -> torch.Tensor:
+    """A workspace for fork_kv_rows with n entries over a table of max_blocks columns."""
+    return _byte_workspace("sra_kv_fork_workspace_size", lib().sra_kv_fork_workspace_size(n, max_blocks), device)
+
+
+def fork_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, parents: torch.Tensor,
+                 children: torch.Tensor, block_size: int, workspace: torch.Tensor | None = None,
+                 err_count: torch.Tensor | None = None, stream=None) -> None:
+    """Row children[i] becomes another holder of row parents[i]'s pages, and gives up its own.
+
+    block_table int32 [rows, max_blocks], seq_lens int32 [rows] and ref_counts int32
+    [num_blocks] change in place; parents are read as they were at entry. No page is copied:
+    resize_kv_rows copies a shared, partly filled page before a row writes into it."""
+    tp, sp, rp = _page_state(block_table, seq_lens, ref_counts)
+    _int32(parents, "parents", 1)
+    _int32(children, "children", 1)
+    _same_device(block_table, parents, children, err_count)
+    if parents.shape != children.shape:
+        raise ValueError("parents and children must have the same length")
+    n, (rows, mb) = parents.numel(), block_table.shape
+    with torch.cuda.device(block_table.device):
+        workspace, wp, wb = _workspace_args(workspace, lambda: kv_fork_workspace(n, mb, block_table.device),
+                                            block_table, stream)
+        st = lib().sra_kv_fork_rows(tp, sp, rp, parents.data_ptr(), children.data_ptr(), n, rows, mb,
+                                    ref_counts.numel(), int(block_size), wp, wb, _err_ptr(err_count),
+                                    _stream(block_table, stream))
+    _check("sra_kv_fork_rows", st)
+
+
+def kv_resize_workspace(n: int, num_blocks: int, device) -> torch.Tensor:
+    """A workspace for resize_kv_rows with n entries over a cache of num_blocks pages."""
+    return _byte_workspace("sra_kv_resize_workspace_size", lib().sra_kv_resize_workspace_size(n, num_blocks), device)
+
+
+def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
+                   lens: torch.Tensor, kv_caches, pos: torch.Tensor | None = None,
+                   slot_mapping: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   err_count: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Row rows[i] is given lens[i] tokens: grown (the lowest free pages first, a shared last
+    page copied before it is written), truncated, or freed (0). State and caches as in
+    fork_kv_rows and copy_kv_pages, changed in place.
+
+    Returns (pos, slot_mapping), int64 [n]: position and cache slot of each row's last token, what
+    rope_kv_store takes for a decode step; -1 for an empty row or a refused entry. A row whose pages are
+    not there stays as it was and is counted in err_count."""
+    tp, sp, rp = _page_state(block_table, seq_lens, ref_counts)
+    cache, ptrs, count = _kv_caches(kv_caches)
+    _int32(rows, "rows", 1)
+    _int32(lens, "lens", 1)
+    if rows.shape != lens.shape:
+        raise ValueError("rows and lens must have the same length")
+    n = rows.numel()
+    if pos is None:
+        pos = torch.empty(n, dtype=torch.int64, device=block_table.device)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(n, dtype=torch.int64, device=block_table.device)
+    for t, name in ((pos, "pos"), (slot_mapping, "slot_mapping")):
+        _cuda(t, name)
+        if t.dtype != torch.int64 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int64 [{n}]")
+    _same_device(block_table, cache, rows, lens, pos, slot_mapping, err_count)
+    _, nb, bs, n_kv, hd = cache.shape
+    if ref_counts.numel() != nb:
+        raise ValueError("ref_counts must have one entry per page of the caches")
+    with torch.cuda.device(block_table.device):
+        workspace, wp, wb = _workspace_args(workspace, lambda: kv_resize_workspace(n, nb, block_table.device),
+                                            block_table, stream)
+        st = lib().sra_kv_resize_rows(tp, sp, rp, rows.data_ptr(), lens.data_ptr(), n, block_table.shape[0],
+                                      block_table.shape[1], ptrs, count, nb, bs, n_kv, hd, pos.data_ptr(),
+                                      slot_mapping.data_ptr(), wp, wb, _err_ptr(err_count), _dtype(cache),
+                                      _stream(block_table, stream))
+    _check("sra_kv_resize_rows", st)
+    return pos, slot_mapping
+
+
+def kv_compact_workspace(num_blocks: int, device) -> torch.Tensor:
+    """A workspace for compact_kv_pages over a cache of num_blocks pages."""
+    return _byte_workspace("sra_kv_compact_workspace_size", lib().sra_kv_compact_workspace_size(num_blocks), device)
+
+
+def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, kv_caches,
+                     num_live: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     err_count: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Move the live pages (count > 0) to the front of the caches; tables and counts follow.
+    Returns num_live, int32 [1]: the pages from there on are free."""
+    tp, sp, rp = _page_state(block_table, seq_lens, ref_counts)
+    cache, ptrs, count = _kv_caches(kv_caches)
+    if num_live is None:
+        num_live = torch.empty(1, dtype=torch.int32, device=block_table.device)
+    _int32(num_live, "num_live", 1)
+    if num_live.numel() != 1:
+        raise ValueError("num_live must hold one entry")
+    _same_device(block_table, cache, num_live, err_count)
+    _, nb, bs, n_kv, hd = cache.shape
+    if ref_counts.numel() != nb:
+        raise ValueError("ref_counts must have one entry per page of the caches")
+    with torch.cuda.device(block_table.device):
+        workspace, wp, wb = _workspace_args(workspace, lambda: kv_compact_workspace(nb, block_table.device),
+                                            block_table, stream)
+        st = lib().sra_kv_compact_pages(tp, sp, rp, block_table.shape[0], block_table.shape[1], ptrs, count, nb, bs,
+                                        n_kv, hd, num_live.data_ptr(), wp, wb, _err_ptr(err_count), _dtype(cache),
+                                        _stream(block_table, stream))
+    _check("sra_kv_compact_pages", st)
+    return num_live

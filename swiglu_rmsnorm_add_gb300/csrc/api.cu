@@ -1283,6 +1283,325 @@ int sra_uclip(const void* x, const float* alpha, const float* gamma, void* out, 
     return status_from(launch_uclip(a, plan, dtype, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------- pages of the cache
+namespace {
+
+// Sizes of a call on the caches' pages, and the spans it writes and reads for the overlap checks.
+struct PageCall {
+    int64_t page_bytes = 0, plane_bytes = 0;
+    Span spans[kMaxCacheList + 16];
+    int n = 0, written = 0;  // spans[0 .. written) are written, the others only read
+    void add(const void* p, int64_t bytes) {
+        if (p && bytes > 0 && n < static_cast<int>(sizeof(spans) / sizeof(spans[0]))) spans[n++] = span_of(p, 1, 0, bytes, 1);
+    }
+    // Whether a written span meets any other.
+    bool clash() const {
+        for (int i = 0; i < written; ++i)
+            for (int j = i + 1; j < n; ++j)
+                if (overlap(spans[i], spans[j])) return true;
+        return false;
+    }
+};
+
+constexpr int64_t kMaxEntries = 65535 * 8;  // entries of one fork or resize (the grid's y limit, 8 entries a CTA)
+
+bool int32_size(int64_t v) { return v >= 0 && v <= 0x7fffffff; }
+
+int page_sizes(int64_t num_blocks, int block_size, int n_kv_head, int head_dim, int es, PageCall* c) {
+    if (!int32_size(num_blocks) || block_size <= 0 || n_kv_head <= 0 || head_dim <= 0) return SRA_ERR_SHAPE;
+    int64_t b = block_size;
+    if (__builtin_mul_overflow(b, static_cast<int64_t>(n_kv_head), &b) ||
+        __builtin_mul_overflow(b, static_cast<int64_t>(head_dim), &b) ||
+        __builtin_mul_overflow(b, static_cast<int64_t>(es), &c->page_bytes) ||
+        __builtin_mul_overflow(c->page_bytes, 2 * std::max<int64_t>(1, num_blocks), &b))
+        return SRA_ERR_SHAPE;
+    c->plane_bytes = c->page_bytes * num_blocks;
+    return SRA_OK;
+}
+
+// Bytes per access of page copies: the widest that every cache's address and `unit` (what a copy is a
+// multiple of) allow.
+int page_vec(void* const* caches, int64_t n, int64_t unit) {
+    uintptr_t bits = static_cast<uintptr_t>(unit);
+    for (int64_t i = 0; i < n; ++i) bits |= reinterpret_cast<uintptr_t>(caches[i]);
+    return (bits & 15u) == 0 ? 16 : (bits & 7u) == 0 ? 8 : (bits & 3u) == 0 ? 4 : 2;
+}
+
+// The caches' pointers: none NULL (unless the caches are empty) or misaligned for the dtype, all disjoint.
+int check_caches(void* const* caches, int64_t n, int64_t plane_bytes, int es) {
+    if (plane_bytes == 0) return SRA_OK;
+    if (!caches) return SRA_ERR_NULL;
+    for (int64_t i = 0; i < n; ++i) {
+        if (!caches[i]) return SRA_ERR_NULL;
+        if (reinterpret_cast<uintptr_t>(caches[i]) % es) return SRA_ERR_ARG;
+    }
+    for (int64_t i = 0; i < n; ++i)
+        for (int64_t j = i + 1; j < n; ++j)
+            if (overlap(span_of(caches[i], 1, 0, 2 * plane_bytes, 1), span_of(caches[j], 1, 0, 2 * plane_bytes, 1)))
+                return SRA_ERR_ALIAS;
+    return SRA_OK;
+}
+
+// Whether span [p, p + bytes) meets a cache.
+bool meets_caches(void* const* caches, int64_t n, int64_t plane_bytes, const void* p, int64_t bytes) {
+    if (!p || plane_bytes == 0) return false;
+    for (int64_t i = 0; i < n; ++i)
+        if (overlap(span_of(caches[i], 1, 0, 2 * plane_bytes, 1), span_of(p, 1, 0, bytes, 1))) return true;
+    return false;
+}
+bool any_meets_caches(void* const* caches, int64_t n, int64_t plane_bytes, const PageCall& c) {
+    for (int i = 0; i < c.n; ++i)
+        if (meets_caches(caches, n, plane_bytes, reinterpret_cast<const void*>(c.spans[i].lo),
+                         static_cast<int64_t>(c.spans[i].hi - c.spans[i].lo)))
+            return true;
+    return false;
+}
+
+CacheList cache_list(void* const* caches, int64_t first, int64_t n, const PageCall& c) {
+    CacheList l;
+    l.n = static_cast<int>(std::min<int64_t>(n - first, kMaxCacheList));
+    for (int i = 0; i < kMaxCacheList; ++i) l.p[i] = i < l.n && c.plane_bytes > 0 ? caches[first + i] : nullptr;
+    l.page_bytes = c.page_bytes;
+    l.plane_bytes = c.plane_bytes;
+    return l;
+}
+
+// rows x max_blocks: the table's sizes.
+bool table_sizes_ok(int64_t rows, int64_t max_blocks) {
+    int64_t b;
+    return int32_size(rows) && int32_size(max_blocks) && !__builtin_mul_overflow(rows, max_blocks * 4, &b);
+}
+
+int64_t round_up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+int sra_kv_copy_pages(void* const* kv_caches, int64_t n_caches, const int32_t* src, const int32_t* dst, int64_t n,
+                      int64_t num_blocks, int block_size, int n_kv_head, int head_dim, int32_t* err_count, int dtype,
+                      void* stream) {
+    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
+    const int es = elem_bytes(dtype);
+    PageCall c;
+    if (n_caches < 0 || n < 0 || n > (int64_t(1) << 40)) return SRA_ERR_SHAPE;
+    int st = page_sizes(num_blocks, block_size, n_kv_head, head_dim, es, &c);
+    if (st != SRA_OK) return st;
+    if (n == 0 || n_caches == 0) return SRA_OK;
+    if (!src || !dst) return SRA_ERR_NULL;
+    st = check_caches(kv_caches, n_caches, c.plane_bytes, es);
+    if (st != SRA_OK) return st;
+    c.add(err_count, 4);
+    c.written = c.n;
+    c.add(src, n * 4);
+    c.add(dst, n * 4);
+    if (c.clash() || any_meets_caches(kv_caches, n_caches, c.plane_bytes, c)) return SRA_ERR_ALIAS;
+    int dev = 0;
+    PagePlan plan;
+    plan.num_sms = current_sm_count(&dev);
+    if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
+    plan.vec = c.plane_bytes ? page_vec(kv_caches, n_caches, c.page_bytes) : 2;
+    plan.pdl = g_pdl;
+    PageCopyArgs a;
+    a.src = src;
+    a.dst = dst;
+    a.n = n;
+    a.num_blocks = num_blocks;
+    a.err = err_count;
+    for (int64_t f = 0; f < n_caches; f += kMaxCacheList) {
+        a.count_errors = f == 0;
+        st = status_from(launch_copy_pages(cache_list(kv_caches, f, n_caches, c), a, plan, static_cast<cudaStream_t>(stream)));
+        if (st != SRA_OK) return st;
+    }
+    return SRA_OK;
+}
+
+int64_t sra_kv_fork_workspace_size(int64_t n, int64_t max_blocks_per_seq) {
+    if (n < 0 || n > kMaxEntries || !table_sizes_ok(n, max_blocks_per_seq)) return SRA_ERR_SHAPE;
+    return round_up256(n * 8 + n * max_blocks_per_seq * 4);
+}
+
+int sra_kv_fork_rows(int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, const int32_t* parents,
+                     const int32_t* children, int64_t n, int64_t rows, int64_t max_blocks_per_seq, int64_t num_blocks,
+                     int block_size, void* workspace, int64_t workspace_bytes, int32_t* err_count, void* stream) {
+    if (n < 0 || n > kMaxEntries || !table_sizes_ok(rows, max_blocks_per_seq) ||
+        !table_sizes_ok(n, max_blocks_per_seq) || !int32_size(num_blocks) || block_size <= 0)
+        return SRA_ERR_SHAPE;
+    if (workspace_bytes < 0) return SRA_ERR_ARG;
+    if (n == 0) return SRA_OK;
+    if (!parents || !children || !workspace || (rows > 0 && !seq_lens) || (rows * max_blocks_per_seq > 0 && !block_table) ||
+        (num_blocks > 0 && !ref_counts))
+        return SRA_ERR_NULL;
+    const int64_t need = sra_kv_fork_workspace_size(n, max_blocks_per_seq);
+    if (workspace_bytes < need || !aligned16(workspace)) return SRA_ERR_ARG;
+    PageCall c;
+    c.add(block_table, rows * max_blocks_per_seq * 4);
+    c.add(seq_lens, rows * 4);
+    c.add(ref_counts, num_blocks * 4);
+    c.add(workspace, need);
+    c.add(err_count, 4);
+    c.written = c.n;
+    c.add(parents, n * 4);
+    c.add(children, n * 4);
+    if (c.clash()) return SRA_ERR_ALIAS;
+    int dev = 0;
+    PagePlan plan;
+    plan.num_sms = current_sm_count(&dev);
+    if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
+    plan.vec = 16;
+    plan.pdl = g_pdl;
+    ForkArgs a;
+    a.table = block_table;
+    a.seq_lens = seq_lens;
+    a.ref = ref_counts;
+    a.parents = parents;
+    a.children = children;
+    a.n = n;
+    a.rows = rows;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.cap = max_blocks_per_seq * block_size;
+    a.block_size = block_size;
+    a.err = err_count;
+    a.ws_plen = static_cast<int32_t*>(workspace);
+    a.ws_clen = a.ws_plen + n;
+    a.ws_snap = a.ws_clen + n;
+    return status_from(launch_fork_rows(a, plan, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t sra_kv_resize_workspace_size(int64_t n, int64_t num_blocks) {
+    if (n < 0 || n > kMaxEntries || !int32_size(num_blocks)) return SRA_ERR_SHAPE;
+    return round_up256(8 + n * (8 + 12) + num_blocks * 4);
+}
+
+int sra_kv_resize_rows(int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, const int32_t* row_idx,
+                       const int32_t* lens, int64_t n, int64_t rows, int64_t max_blocks_per_seq,
+                       void* const* kv_caches, int64_t n_caches, int64_t num_blocks, int block_size, int n_kv_head,
+                       int head_dim, int64_t* pos, int64_t* slot_mapping, void* workspace, int64_t workspace_bytes,
+                       int32_t* err_count, int dtype, void* stream) {
+    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
+    const int es = elem_bytes(dtype);
+    PageCall c;
+    if (n < 0 || n > kMaxEntries || n_caches <= 0 || !table_sizes_ok(rows, max_blocks_per_seq)) return SRA_ERR_SHAPE;
+    int st = page_sizes(num_blocks, block_size, n_kv_head, head_dim, es, &c);
+    if (st != SRA_OK) return st;
+    if (workspace_bytes < 0) return SRA_ERR_ARG;
+    if (n == 0) return SRA_OK;
+    if (!row_idx || !lens || !workspace || (rows > 0 && !seq_lens) || (rows * max_blocks_per_seq > 0 && !block_table) ||
+        (num_blocks > 0 && !ref_counts))
+        return SRA_ERR_NULL;
+    st = check_caches(kv_caches, n_caches, c.plane_bytes, es);
+    if (st != SRA_OK) return st;
+    const int64_t need = sra_kv_resize_workspace_size(n, num_blocks);
+    if (workspace_bytes < need || !aligned16(workspace)) return SRA_ERR_ARG;
+    c.add(block_table, rows * max_blocks_per_seq * 4);
+    c.add(seq_lens, rows * 4);
+    c.add(ref_counts, num_blocks * 4);
+    c.add(pos, n * 8);
+    c.add(slot_mapping, n * 8);
+    c.add(workspace, need);
+    c.add(err_count, 4);
+    c.written = c.n;
+    c.add(row_idx, n * 4);
+    c.add(lens, n * 4);
+    if (c.clash() || any_meets_caches(kv_caches, n_caches, c.plane_bytes, c)) return SRA_ERR_ALIAS;
+    int dev = 0;
+    PagePlan plan;
+    plan.num_sms = current_sm_count(&dev);
+    if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
+    plan.vec = c.plane_bytes ? page_vec(kv_caches, n_caches, c.page_bytes / block_size) : 2;  // whole tokens are copied
+    // a page's and a plane's start are multiples of a token's bytes
+    plan.pdl = g_pdl;
+    ResizeArgs a;
+    a.table = block_table;
+    a.seq_lens = seq_lens;
+    a.ref = ref_counts;
+    a.row_idx = row_idx;
+    a.lens = lens;
+    a.n = n;
+    a.rows = rows;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.cap = max_blocks_per_seq * block_size;
+    a.block_size = block_size;
+    a.pos = pos;
+    a.slot = slot_mapping;
+    a.err = err_count;
+    a.ws_found = static_cast<int64_t*>(workspace);
+    a.ws_first = a.ws_found + 1;
+    a.ws_old = reinterpret_cast<int32_t*>(a.ws_first + n);
+    a.ws_need = a.ws_old + n;
+    a.ws_from = a.ws_need + n;
+    a.ws_free = a.ws_from + n;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = status_from(launch_resize_plan(a, plan, s));
+    for (int64_t f = 0; f < n_caches && st == SRA_OK; f += kMaxCacheList) {
+        a.bookkeeping = f == 0;
+        st = status_from(launch_resize_assign(cache_list(kv_caches, f, n_caches, c), a, plan, s));
+    }
+    return st;
+}
+
+int64_t sra_kv_compact_workspace_size(int64_t num_blocks) {
+    if (!int32_size(num_blocks)) return SRA_ERR_SHAPE;
+    return round_up256(8 + num_blocks * 12);
+}
+
+int sra_kv_compact_pages(int32_t* block_table, const int32_t* seq_lens, int32_t* ref_counts, int64_t rows,
+                         int64_t max_blocks_per_seq, void* const* kv_caches, int64_t n_caches, int64_t num_blocks,
+                         int block_size, int n_kv_head, int head_dim, int32_t* num_live, void* workspace,
+                         int64_t workspace_bytes, int32_t* err_count, int dtype, void* stream) {
+    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
+    const int es = elem_bytes(dtype);
+    PageCall c;
+    if (n_caches <= 0 || !table_sizes_ok(rows, max_blocks_per_seq)) return SRA_ERR_SHAPE;
+    int st = page_sizes(num_blocks, block_size, n_kv_head, head_dim, es, &c);
+    if (st != SRA_OK) return st;
+    if (workspace_bytes < 0) return SRA_ERR_ARG;
+    if (!workspace || (rows > 0 && !seq_lens) || (rows * max_blocks_per_seq > 0 && !block_table) ||
+        (num_blocks > 0 && !ref_counts))
+        return SRA_ERR_NULL;
+    st = check_caches(kv_caches, n_caches, c.plane_bytes, es);
+    if (st != SRA_OK) return st;
+    const int64_t need = sra_kv_compact_workspace_size(num_blocks);
+    if (workspace_bytes < need || !aligned16(workspace)) return SRA_ERR_ARG;
+    c.add(block_table, rows * max_blocks_per_seq * 4);
+    c.add(ref_counts, num_blocks * 4);
+    c.add(num_live, 4);
+    c.add(workspace, need);
+    c.add(err_count, 4);
+    c.written = c.n;
+    c.add(seq_lens, rows * 4);
+    if (c.clash() || any_meets_caches(kv_caches, n_caches, c.plane_bytes, c)) return SRA_ERR_ALIAS;
+    int dev = 0;
+    PagePlan plan;
+    plan.num_sms = current_sm_count(&dev);
+    if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
+    plan.vec = c.plane_bytes ? page_vec(kv_caches, n_caches, c.page_bytes) : 2;
+    plan.pdl = g_pdl;
+    CompactArgs a;
+    a.table = block_table;
+    a.seq_lens = seq_lens;
+    a.ref = ref_counts;
+    a.rows = rows;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.cap = max_blocks_per_seq * block_size;
+    a.block_size = block_size;
+    a.num_live = num_live;
+    a.err = err_count;
+    a.ws_live = static_cast<int32_t*>(workspace);
+    a.ws_moved = a.ws_live + 1;
+    a.ws_rank = a.ws_moved + 1;
+    a.ws_src = a.ws_rank + num_blocks;
+    a.ws_dst = a.ws_src + num_blocks;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = status_from(launch_compact_plan(a, plan, s));
+    for (int64_t f = 0; f < n_caches && st == SRA_OK; f += kMaxCacheList) {
+        a.bookkeeping = f == 0;
+        st = status_from(launch_compact_move(cache_list(kv_caches, f, n_caches, c), a, plan, s));
+    }
+    return st;
+}
+
 int sra_force_variant(const char* op, int variant) {
     std::atomic<int>* slot = force_slot(op);
     if (!slot) return SRA_ERR_ARG;

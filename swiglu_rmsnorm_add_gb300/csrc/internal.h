@@ -236,4 +236,93 @@ struct UclipPlan {
 
 cudaError_t launch_uclip(const UclipArgs& a, const UclipPlan& p, int dtype, cudaStream_t s);
 
+// ------------------------------------------------------------------- pages of the cache
+// The caches of a model's layers that share one page numbering, by value in the kernel's
+// parameters (kMaxCacheList of them per launch).
+constexpr int kMaxCacheList = 128;
+struct CacheList {
+    void* p[kMaxCacheList];  // [2, num_blocks, block_size, n_kv, head_dim] each
+    int n;
+    int64_t page_bytes;   // one page of one plane
+    int64_t plane_bytes;  // num_blocks pages
+};
+
+struct PagePlan {
+    int vec;  // bytes per access of the page copies: 16, 8, 4 or 2
+    bool pdl;
+    int num_sms;
+};
+
+struct PageCopyArgs {
+    const int32_t* src;
+    const int32_t* dst;
+    int64_t n, num_blocks;
+    int32_t* err;
+    bool count_errors;  // one launch of a call counts
+};
+cudaError_t launch_copy_pages(const CacheList& c, const PageCopyArgs& a, const PagePlan& p, cudaStream_t s);
+
+struct ForkArgs {
+    int32_t* table;     // [rows, max_blocks]
+    int32_t* seq_lens;  // [rows]
+    int32_t* ref;       // [num_blocks]
+    const int32_t* parents;
+    const int32_t* children;
+    int64_t n, rows, max_blocks, num_blocks, cap;  // cap = max_blocks * block_size
+    int block_size;
+    int32_t* err;
+    // workspace: each entry's parent length (-1: does nothing) and child length at entry, and the
+    // parents' table entries
+    int32_t* ws_plen;  // [n]
+    int32_t* ws_clen;  // [n]
+    int32_t* ws_snap;  // [n, max_blocks]
+};
+cudaError_t launch_fork_rows(const ForkArgs& a, const PagePlan& p, cudaStream_t s);
+
+struct ResizeArgs {
+    int32_t* table;
+    int32_t* seq_lens;
+    int32_t* ref;
+    const int32_t* row_idx;
+    const int32_t* lens;
+    int64_t n, rows, max_blocks, num_blocks, cap;
+    int block_size;
+    int64_t* pos;   // nullable
+    int64_t* slot;  // nullable
+    int32_t* err;
+    // workspace
+    int64_t* ws_first;  // [n] where the entry's pages start in ws_free
+    int64_t* ws_found;  // free pages listed
+    int32_t* ws_old;    // [n] length at entry, -1: the entry does nothing
+    int32_t* ws_need;   // [n] pages needed
+    int32_t* ws_from;   // [n] page to copy before it is written, -1: none
+    int32_t* ws_free;   // [num_blocks]
+    // of one launch
+    int64_t copy_from = 0;
+    bool bookkeeping = true;
+};
+cudaError_t launch_resize_plan(const ResizeArgs& a, const PagePlan& p, cudaStream_t s);
+cudaError_t launch_resize_assign(const CacheList& c, const ResizeArgs& a, const PagePlan& p, cudaStream_t s);
+
+struct CompactArgs {
+    int32_t* table;
+    const int32_t* seq_lens;
+    int32_t* ref;
+    int64_t rows, max_blocks, num_blocks, cap;
+    int block_size;
+    int32_t* num_live;  // nullable
+    int32_t* err;
+    // workspace
+    int32_t* ws_live;   // 1
+    int32_t* ws_moved;  // 1
+    int32_t* ws_rank;   // [num_blocks]
+    int32_t* ws_src;    // [num_blocks]
+    int32_t* ws_dst;    // [num_blocks]
+    // of one launch
+    int64_t copy_from = 0;
+    bool bookkeeping = true;
+};
+cudaError_t launch_compact_plan(const CompactArgs& a, const PagePlan& p, cudaStream_t s);
+cudaError_t launch_compact_move(const CacheList& c, const CompactArgs& a, const PagePlan& p, cudaStream_t s);
+
 }  // namespace sra
