@@ -570,6 +570,54 @@ SRA_API int sra_kv_compact_pages(int32_t* block_table, const int32_t* seq_lens, 
                                  void* stream);
 SRA_API int64_t sra_kv_compact_workspace_size(int64_t num_blocks);
 
+/*
+ * sra_shared_prefix_attention — sra_paged_decode_attention for a batch whose requests share their
+ * first tokens (samples of one prompt, requests behind one system prompt): the prefix's K and V are
+ * read once for the batch, not once per request.
+ *
+ *   out[b, h, :] = sum_{t < seq_lens[b]} softmax_t(scale * q[b, h, :] . K_t) V_t
+ *
+ * with token t's page prefix_table[t / block_size] for t < *prefix_len and
+ * block_table[b, t / block_size] behind it. seq_lens count all of a request's tokens, and
+ * block_table's rows are those of sra_paged_decode_attention: the entries that lie wholly below the
+ * prefix's length are not read (they may hold the same pages, as sra_kv_fork_rows leaves them, or
+ * anything). The prefix may end inside a page. A request shorter than the prefix attends to the
+ * tokens that it has; one without tokens gets zeros.
+ *
+ * The tensor-core path takes the queries of all requests that share a KV head as the rows of one
+ * product with the prefix's whole pages, splits it over the GPU along the prefix, takes each
+ * request's own tokens as sra_paged_decode_attention does, and merges the parts through their
+ * maxima and sums of exponentials (fp32). In that path the prefix's probabilities are
+ * rounded once to the dtype before they multiply V (fp32 sums); the request's own tokens and the
+ * path without a workspace keep them to 16 bits or more.
+ *
+ * q, kv_cache, out, scale: as in sra_paged_decode_attention. prefix_table: int32 [prefix_blocks];
+ * prefix_len: device int32, one entry; block_table: int32 [B, max_blocks_per_seq]; seq_lens: int32 [B].
+ * workspace: NULL, or device memory of at least sra_shared_prefix_workspace_size bytes (same sizes,
+ * current device), 16-byte aligned, contents without meaning; calls that share one must not
+ * overlap on the GPU. Without one (or where that size is 0) every request is a decode call of its
+ * own that reads the prefix itself: the form for few requests.
+ * err_count: nullable device int32, incremented once for a prefix_len outside [0, prefix_blocks *
+ * block_size] and once per request whose seq_len lies outside [0, max_blocks_per_seq * block_size]
+ * (both clamped), once per call for each of the prefix's entries outside [0, num_blocks), and
+ * once per request for each such entry of its own that holds a token of it; such entries' tokens
+ * are skipped.
+ * Supported shapes: head_dim 64, 128 or 256; block_size 8, 16 or 32; n_head / n_kv_head <= 8.
+ * Errors: as sra_paged_decode_attention; a workspace too small or misaligned -> SRA_ERR_ARG, one
+ * that overlaps another argument -> SRA_ERR_ALIAS. B == 0 is a no-op.
+ */
+SRA_API int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32_t* prefix_table,
+                                        const int32_t* prefix_len, const int32_t* block_table,
+                                        const int32_t* seq_lens, void* out, int64_t B, int n_head, int n_kv_head,
+                                        int head_dim, int64_t q_tok_stride, int64_t out_tok_stride,
+                                        int64_t num_blocks, int block_size, int64_t prefix_blocks,
+                                        int64_t max_blocks_per_seq, float scale, void* workspace,
+                                        int64_t workspace_bytes, int32_t* err_count, int dtype, void* stream);
+/* Workspace bytes that call uses on the current device (0: none); a negative sra_status for bad sizes. */
+SRA_API int64_t sra_shared_prefix_workspace_size(int64_t B, int n_head, int n_kv_head, int head_dim,
+                                                 int64_t prefix_blocks, int64_t max_blocks_per_seq, int block_size,
+                                                 int dtype);
+
 /* Static text for a status code (never NULL). */
 SRA_API const char* sra_status_string(int status);
 

@@ -33,6 +33,8 @@ from ._binding import (  # noqa: F401
     rmsnorm_linear,
     rope_kv_store,
     set_pdl,
+    shared_prefix_attention,
+    shared_prefix_workspace,
     status_string,
     swiglu,
     uclip,
@@ -46,7 +48,8 @@ __all__ = ["rmsnorm", "add_rmsnorm", "rope_kv_store", "swiglu", "reglu", "glu", 
            "paged_decode_attention_noalloc", "decode_attention_workspace",
            "rmsnorm_linear", "glu_linear", "linear_workspace",
            "copy_kv_pages", "fork_kv_rows", "resize_kv_rows", "compact_kv_pages",
-           "kv_fork_workspace", "kv_resize_workspace", "kv_compact_workspace", "lib",
+           "kv_fork_workspace", "kv_resize_workspace", "kv_compact_workspace",
+           "shared_prefix_attention", "shared_prefix_workspace", "lib",
            "SRAError",
            "force_variant", "set_pdl", "variant_count", "variant_name", "pick_variant", "status_string",
            "wait_timeouts", "wait_selftest"]

@@ -78,6 +78,11 @@ def lib() -> ctypes.CDLL:
                 getattr(L, fn).restype = i32
             for fn in ("sra_kv_fork_workspace_size", "sra_kv_resize_workspace_size", "sra_kv_compact_workspace_size"):
                 getattr(L, fn).restype = i64
+            L.sra_shared_prefix_attention.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, i64, i64,
+                                                      i32, i64, i64, f32, vp, i64, vp, i32, vp]
+            L.sra_shared_prefix_attention.restype = i32
+            L.sra_shared_prefix_workspace_size.argtypes = [i64, i32, i32, i32, i64, i64, i32, i32]
+            L.sra_shared_prefix_workspace_size.restype = i64
             L.sra_status_string.argtypes = [i32]
             L.sra_status_string.restype = ctypes.c_char_p
             L.sra_version.restype = i32
@@ -782,3 +787,54 @@ def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_coun
                                         _stream(block_table, stream))
     _check("sra_kv_compact_pages", st)
     return num_live
+
+
+# ------------------------------------------------------------------- shared prefix
+def shared_prefix_workspace(B: int, n_head: int, n_kv_head: int, head_dim: int, prefix_blocks: int, max_blocks: int,
+                            block_size: int, dtype=torch.bfloat16, device="cuda") -> torch.Tensor | None:
+    """A workspace for shared_prefix_attention, or None where these sizes use none. Reuse it across
+    calls (each call writes what it reads)."""
+    with torch.cuda.device(device):
+        n = lib().sra_shared_prefix_workspace_size(B, n_head, n_kv_head, head_dim, prefix_blocks, max_blocks,
+                                                   block_size, DTYPE_CODE[dtype])
+    if n < 0:
+        _check("sra_shared_prefix_workspace_size", int(n))
+    return torch.empty(int(n), dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def shared_prefix_attention(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.Tensor,
+                            prefix_len: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                            out: torch.Tensor | None = None, scale: float | None = None,
+                            err_count: torch.Tensor | None = None, stream=None,
+                            workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """paged_decode_attention for a batch whose requests share their first prefix_len tokens, whose
+    K and V are read once for the batch.
+
+    q: [B, n_head, head_dim]; kv_cache, block_table [B, max_blocks] and seq_lens [B] (all of a
+    request's tokens) as in paged_decode_attention; prefix_table: int32 [prefix_blocks], the pages of
+    the prefix (a row of block_table that reaches past it will do); prefix_len: int32 [1] on the
+    device. workspace: from shared_prefix_workspace; one is made for the call where none is given."""
+    _int32(prefix_table, "prefix_table", 1)
+    _int32(prefix_len, "prefix_len", 1)
+    if prefix_len.numel() != 1:
+        raise ValueError("prefix_len must hold one entry")
+    out, args, err = _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count)
+    _same_device(q, prefix_table, prefix_len)
+    B, n_head, hd = q.shape
+    _, nb, bs, n_kv, _ = kv_cache.shape
+    mb, pb = block_table.shape[1], prefix_table.shape[0]
+    with torch.cuda.device(q.device):
+        wp, wb = None, 0
+        if workspace is None:
+            n = lib().sra_shared_prefix_workspace_size(B, n_head, n_kv, hd, pb, mb, bs, _dtype(q))
+            if n > 0:
+                workspace, wp, wb = _workspace_args(
+                    None, lambda: torch.empty(int(n), dtype=torch.uint8, device=q.device), q, stream)
+        else:
+            workspace, wp, wb = _workspace_args(workspace, None, q, stream)
+        st = lib().sra_shared_prefix_attention(
+            q.data_ptr(), kv_cache.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), out.data_ptr(), B, n_head, n_kv, hd, args[9], args[10], nb, bs, pb, mb, args[14],
+            wp, wb, err, _dtype(q), _stream(q, stream))
+    _check("sra_shared_prefix_attention", st)
+    return out

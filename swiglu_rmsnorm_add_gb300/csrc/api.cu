@@ -1602,6 +1602,109 @@ int sra_kv_compact_pages(int32_t* block_table, const int32_t* seq_lens, int32_t*
     return st;
 }
 
+// ------------------------------------------------------------------- shared prefix
+namespace {
+
+int prefix_sizes(int64_t B, int n_head, int n_kv_head, int head_dim, int64_t prefix_blocks, int64_t max_blocks,
+                 int block_size, int dtype) {
+    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
+    if (B < 0 || n_head <= 0 || n_kv_head <= 0 || n_head % n_kv_head != 0 || n_head / n_kv_head > 8 ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        (block_size != 8 && block_size != 16 && block_size != 32) || !int32_size(prefix_blocks) ||
+        !table_sizes_ok(B, max_blocks))
+        return SRA_ERR_SHAPE;
+    return SRA_OK;
+}
+
+}  // namespace
+
+int64_t sra_shared_prefix_workspace_size(int64_t B, int n_head, int n_kv_head, int head_dim, int64_t prefix_blocks,
+                                         int64_t max_blocks_per_seq, int block_size, int dtype) {
+    const int st = prefix_sizes(B, n_head, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size, dtype);
+    if (st != SRA_OK) return st;
+    return 0;
+}
+
+int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32_t* prefix_table,
+                                const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens,
+                                void* out, int64_t B, int n_head, int n_kv_head, int head_dim, int64_t q_tok_stride,
+                                int64_t out_tok_stride, int64_t num_blocks, int block_size, int64_t prefix_blocks,
+                                int64_t max_blocks_per_seq, float scale, void* workspace, int64_t workspace_bytes,
+                                int32_t* err_count, int dtype, void* stream) {
+    const int st = prefix_sizes(B, n_head, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size, dtype);
+    if (st != SRA_OK) return st;
+    if (!int32_size(num_blocks)) return SRA_ERR_SHAPE;
+    const int64_t w = static_cast<int64_t>(n_head) * head_dim;
+    if (q_tok_stride < w || out_tok_stride < w) return SRA_ERR_STRIDE;
+    if (!std::isfinite(scale) || workspace_bytes < 0) return SRA_ERR_ARG;
+    if (B == 0) return SRA_OK;
+    if (!q || (num_blocks > 0 && !kv_cache) || (prefix_blocks > 0 && !prefix_table) || !prefix_len ||
+        (max_blocks_per_seq > 0 && !block_table) || !seq_lens || !out)
+        return SRA_ERR_NULL;
+    if (!aligned16(kv_cache)) return SRA_ERR_ARG;
+    const int es = elem_bytes(dtype);
+    const int64_t cache_bytes = 2 * num_blocks * block_size * static_cast<int64_t>(n_kv_head) * head_dim * es;
+    const Span so = span_of(out, B, out_tok_stride, w, es), sq = span_of(q, B, q_tok_stride, w, es);
+    const Span reads[] = {span_of(kv_cache, 1, 0, cache_bytes, 1), span_of(prefix_table, 1, 0, prefix_blocks, 4),
+                          span_of(prefix_len, 1, 0, 1, 4), span_of(block_table, 1, 0, B * max_blocks_per_seq, 4),
+                          span_of(seq_lens, 1, 0, B, 4)};
+    const Span serr = err_count ? span_of(err_count, 1, 0, 1, 4) : Span{0, 0};
+    if (rows_overlap(out, B, out_tok_stride, w, q, B, q_tok_stride, w, es) || overlap(serr, so) || overlap(serr, sq))
+        return SRA_ERR_ALIAS;
+    for (const Span& r : reads)
+        if (overlap(so, r) || overlap(serr, r)) return SRA_ERR_ALIAS;
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
+    if (sms <= 0) return SRA_ERR_DEVICE;
+    const int group = n_head / n_kv_head;
+    const int64_t limit = smem_optin(dev) - 1024;
+    AttnPlan plan;
+    plan.head_dim = head_dim;
+    plan.threads = 128;
+    plan.pdl = g_pdl;
+    plan.num_sms = sms;
+    plan.tensor_cores = dtype != DT_F32 && (head_dim == 64 || head_dim == 128) &&
+                        (reinterpret_cast<uintptr_t>(q) & 3u) == 0 && q_tok_stride % 2 == 0 &&
+                        num_blocks * block_size < (int64_t(1) << 31) &&
+                        static_cast<int64_t>(decode_attention_mma_smem(head_dim, 8)) <= limit;
+    // splits of a (request, kv head) pair over a cluster, as sra_paged_decode_attention's
+    const int64_t groups = B * n_kv_head;
+    int splits = 1;
+    if (plan.tensor_cores) {
+        while (splits < 16 && groups * splits * 2 <= sms && max_blocks_per_seq * block_size >= 256 * splits * 2)
+            splits *= 2;
+    } else {
+        while (splits < 8 && groups * splits < 2 * static_cast<int64_t>(sms) && max_blocks_per_seq >= 4 * splits)
+            splits *= 2;
+    }
+    plan.splits = splits;
+    plan.stages = 2;
+    plan.smem = plan.tensor_cores ? decode_attention_mma_smem(head_dim, 8)
+                                  : decode_attention_smem(group, head_dim, block_size, 2, es);
+    if (static_cast<int64_t>(plan.smem) > limit) return SRA_ERR_SHAPE;
+    AttnArgs a;
+    a.q = q;
+    a.cache = kv_cache;
+    a.table = block_table;
+    a.seq_lens = seq_lens;
+    a.out = out;
+    a.err = err_count;
+    a.B = B;
+    a.qs = q_tok_stride;
+    a.os = out_tok_stride;
+    a.num_blocks = num_blocks;
+    a.max_blocks = max_blocks_per_seq;
+    a.n_head = n_head;
+    a.n_kv = n_kv_head;
+    a.group = group;
+    a.block_size = block_size;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.ptable = prefix_table;
+    a.plen = prefix_len;
+    a.pblocks = prefix_blocks;
+    return status_from(launch_prefix_tail(a, plan, dtype, static_cast<cudaStream_t>(stream)));
+}
+
 int sra_force_variant(const char* op, int variant) {
     std::atomic<int>* slot = force_slot(op);
     if (!slot) return SRA_ERR_ARG;

@@ -90,15 +90,41 @@ __device__ __forceinline__ T from_f32(float v) {
     }
 }
 
-template <typename T, int HD, int STAGES>
+// The shared prefix of a PREFIX launch: tokens below P come through the prefix's table. A
+// request's part of the work is [lo, len): all of its tokens, or, when another kernel takes the
+// prefix's whole pages (a.tail_only) for the requests that reach past them, those behind them.
+struct PrefixRange {
+    int64_t P, lo;
+};
+__device__ __forceinline__ PrefixRange prefix_range(const AttnArgs& a, int64_t len) {
+    int64_t P = *a.plen;
+    const int64_t cap = a.pblocks * a.block_size;
+    P = P < 0 ? 0 : (P > cap ? cap : P);
+    const int64_t whole = P / a.block_size * a.block_size;
+    return {P, a.tail_only && len >= whole ? whole : 0};
+}
+// One CTA of a call: a prefix length out of range and bad entries of the prefix's table, counted once.
+__device__ __forceinline__ void count_prefix_errors(const AttnArgs& a, int64_t P) {
+    if (!a.err) return;
+    int n = threadIdx.x == 0 && *a.plen != P ? 1 : 0;
+    for (int64_t j = threadIdx.x; j * a.block_size < P; j += blockDim.x) {
+        const int32_t e = a.ptable[j];
+        n += e < 0 || e >= a.num_blocks ? 1 : 0;
+    }
+    if (n) atomicAdd(a.err, n);
+}
+
+template <typename T, int HD, int STAGES, bool PREFIX>
 __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
     constexpr int IPT = HD / 64;                                  // (head, 4-dim) slices per thread, G <= 8
     constexpr int EPC = 16 / static_cast<int>(sizeof(T));         // elements per 16-byte copy
     constexpr int CPR = HD / EPC;                                 // copies per row
     extern __shared__ __align__(16) unsigned char smem[];
     cg::cluster_group cluster = cg::this_cluster();
-    const int S = static_cast<int>(cluster.num_blocks());
-    const int rank = static_cast<int>(cluster.block_rank());
+    // PREFIX with a workspace: the splits are independent CTAs whose partials another kernel merges
+    const bool records = PREFIX && a.ws_part != nullptr;
+    const int S = records ? a.gsplits : static_cast<int>(cluster.num_blocks());
+    const int rank = records ? static_cast<int>(blockIdx.x % a.gsplits) : static_cast<int>(cluster.block_rank());
     const int64_t grp = blockIdx.x / S;
     const int64_t b = grp / a.n_kv;
     const int kvh = static_cast<int>(grp - b * a.n_kv);
@@ -118,8 +144,14 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
     if ((len < 0 || len > cap) && kvh == 0 && rank == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
     len = len < 0 ? 0 : (len > cap ? cap : len);
     const int64_t nblk = (len + BS - 1) / BS;
-    const int64_t per = (nblk + S - 1) / S;
-    const int64_t j0 = rank * per < nblk ? rank * per : nblk;
+    int64_t P = 0, jlo = 0;
+    if constexpr (PREFIX) {
+        const PrefixRange r = prefix_range(a, len);
+        P = r.P, jlo = r.lo / BS;
+        if (blockIdx.x == 0) count_prefix_errors(a, P);
+    }
+    const int64_t per = (nblk - jlo + S - 1) / S;
+    const int64_t j0 = jlo + rank * per < nblk ? jlo + rank * per : nblk;
     const int64_t j1 = j0 + per < nblk ? j0 + per : nblk;
 
     for (int i = threadIdx.x; i < G * HD; i += kThreads) {
@@ -135,7 +167,31 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
     const int64_t tok_stride = static_cast<int64_t>(a.n_kv) * HD;          // elements between tokens
     const int64_t v_plane = a.num_blocks * BS * tok_stride;
     auto block_ok = [&](int32_t blk) { return blk >= 0 && blk < a.num_blocks; };
+    // PREFIX: the rows of block j that count, as a mask: those below P through the prefix's entry, the
+    // others (below len) through the request's own
+    auto row_mask = [&](int64_t j) -> unsigned {
+        const int64_t left = len - j * BS, pre = P - j * BS;
+        const int nl = left < BS ? static_cast<int>(left) : BS;
+        const int np = pre <= 0 ? 0 : (pre < nl ? static_cast<int>(pre) : nl);
+        const unsigned all = static_cast<unsigned>((1ull << nl) - 1), first = static_cast<unsigned>((1ull << np) - 1);
+        return (np > 0 && block_ok(a.ptable[j]) ? first : 0u) | (np < nl && block_ok(table[j]) ? all & ~first : 0u);
+    };
     auto issue = [&](int64_t j) {
+        if constexpr (PREFIX) {
+            const unsigned vm = row_mask(j);
+            T* pd = kv + static_cast<size_t>((j - j0) % STAGES) * 2 * BS * HD;
+            for (int c = threadIdx.x; c < 2 * BS * CPR; c += kThreads) {
+                const int plane = c / (BS * CPR);
+                const int r = c - plane * BS * CPR;
+                const int t = r / CPR, col = r - t * CPR;
+                if (!((vm >> t) & 1u)) continue;
+                const int64_t page = j * BS + t < P ? a.ptable[j] : table[j];
+                cp_async16(pd + plane * BS * HD + t * HD + col * EPC,
+                           static_cast<const T*>(a.cache) + (plane ? v_plane : 0) +
+                               ((page * BS + t) * a.n_kv + kvh) * HD + col * EPC);
+            }
+            return;
+        }
         const int32_t blk = table[j];
         if (!block_ok(blk)) return;  // its tokens are skipped, the tile is never read
         T* dst = kv + static_cast<size_t>((j - j0) % STAGES) * 2 * BS * HD;
@@ -163,11 +219,21 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
         __syncthreads();  // tile j landed for every thread's copies; previous tile fully consumed
         if (j + STAGES - 1 < j1) issue(j + STAGES - 1);
         cp_async_commit();
-        const int32_t blk = table[j];
-        const bool ok = block_ok(blk);
-        if (!ok && kvh == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
-        const int64_t left = len - j * BS;
-        const int nvalid = ok ? static_cast<int>(left < BS ? left : BS) : 0;
+        int nvalid;
+        unsigned vm = 0;
+        if constexpr (PREFIX) {
+            vm = row_mask(j);
+            nvalid = BS;
+            // the request's own entry, where the block holds tokens behind the prefix
+            const int64_t end = (j + 1) * BS < len ? (j + 1) * BS : len;
+            if (end > P && !block_ok(table[j]) && kvh == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
+        } else {
+            const int32_t blk = table[j];
+            const bool ok = block_ok(blk);
+            if (!ok && kvh == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
+            const int64_t left = len - j * BS;
+            nvalid = ok ? static_cast<int>(left < BS ? left : BS) : 0;
+        }
         const T* Ks = kv + static_cast<size_t>((j - j0) % STAGES) * 2 * BS * HD;
         const T* Vs = Ks + BS * HD;
 
@@ -176,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
             const int i = i0 + threadIdx.x;
             const bool item = i < G * BS;
             const int g = item ? i / BS : 0, t = i - (i / BS) * BS;
-            const bool valid = item && t < nvalid;
+            const bool valid = item && (PREFIX ? ((vm >> t) & 1u) != 0 : t < nvalid);
             const float m_old = item ? m_run[g] : -INFINITY;
             float sc = -INFINITY;
             if (valid) {
@@ -224,6 +290,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
                 float x0 = acc[k][0] * c, x1 = acc[k][1] * c, x2 = acc[k][2] * c, x3 = acc[k][3] * c;
                 const float* pg = ps + g * BS;
                 for (int t = 0; t < nvalid; ++t) {
+                    if (PREFIX && !((vm >> t) & 1u)) continue;  // never read: what its row holds is not this call's
                     const float pt = pg[t];
                     float vf[4];
                     Vec<T, 4>::unpack(Vec<T, 4>::load(Vs + t * HD + d), vf);
@@ -247,6 +314,14 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
             float* pa = pacc + g * HD + d;
             pa[0] = acc[k][0], pa[1] = acc[k][1], pa[2] = acc[k][2], pa[3] = acc[k][3];
         }
+    }
+    if (records) {
+        // this split's [8 max][8 sum][8 x HD output], as the tensor-core kernel's workspace splits
+        __syncthreads();
+        float* slot = a.ws_part + (static_cast<int64_t>(grp) * S + rank) * (16 + 8 * HD);
+        for (int i = threadIdx.x; i < G * HD; i += kThreads) slot[16 + i] = pacc[i];
+        if (threadIdx.x < G) slot[threadIdx.x] = m_run[threadIdx.x], slot[8 + threadIdx.x] = l_run[threadIdx.x];
+        return;
     }
     cluster.sync();
     T* out = static_cast<T*>(a.out) + b * a.os + static_cast<int64_t>(kvh * G) * HD;
@@ -575,7 +650,9 @@ __device__ __forceinline__ void finish_mma(const AttnArgs& a, unsigned char* sme
 // decode_merge_kernel, launched after them, combines the records.
 // NW warps per CTA: 8 (one CTA per SM) or 4 (two CTAs per SM, so a CTA of the next launch can
 // start beside one of this launch).
-template <typename T, int HD, bool GMERGE, int NW>
+// PREFIX: tokens below the shared prefix's length come through the prefix's table; the splits
+// divide the request's own range of tokens (prefix_range), which is known after the wait only.
+template <typename T, int HD, bool GMERGE, int NW, bool PREFIX>
 __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(AttnArgs a) {
     constexpr int CPR = HD * 2 / 16;      // 16-byte chunks per row
     constexpr int KS = HD / 16;           // k-steps of Q K^T
@@ -593,7 +670,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(At
     const int fg = lane >> 2, ft = lane & 3;  // fragment row group and thread-in-group
     T* ring = reinterpret_cast<T*>(smem) + static_cast<size_t>(warp) * kMmaStages * 2 * TE;
 
-    {
+    if constexpr (!PREFIX) {
         // Before the dependency wait: warm what the first tiles need. First the loads that
         // depend on nothing: this request's seq_len and this split's whole slice of the block
         // table (so the later tiles' table reads hit the L2 and each tile costs one DRAM round
@@ -631,15 +708,24 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(At
     const int64_t cap = a.max_blocks * BS;
     // static split of the table's capacity (not of seq_len), so the block-table reads of the
     // first tiles need not wait for seq_len; tokens at or past seq_len are masked
-    const int64_t per = ((cap + S - 1) / S + kMmaTile - 1) / kMmaTile * kMmaTile;
-    const int64_t t_begin = rank * per < cap ? rank * per : cap;
-    const int64_t t_lim = t_begin + per < cap ? t_begin + per : cap;
+    int64_t P = 0, lo = 0, hi = cap;
+    if constexpr (PREFIX) {
+        hi = a.seq_lens[b];
+        hi = hi < 0 ? 0 : (hi > cap ? cap : hi);
+        const PrefixRange r = prefix_range(a, hi);
+        P = r.P, lo = r.lo;
+        if (blockIdx.x == 0) count_prefix_errors(a, P);
+    }
+    const int64_t per = ((hi - lo + S - 1) / S + kMmaTile - 1) / kMmaTile * kMmaTile;
+    const int64_t t_begin = lo + rank * per < hi ? lo + rank * per : hi;
+    const int64_t t_lim = t_begin + per < hi ? t_begin + per : hi;
     const int32_t* table = a.table + b * a.max_blocks;
     const int bs_log2 = __ffs(BS) - 1;  // block_size is a power of two
     // Block-table entry of token `lane` of tile u (lanes < 16; 0 past the static range). It is
     // read one tile ahead of its use, so the copy issue never waits on the table's latency.
     auto load_blk = [&](int64_t u) -> int32_t {
         const int64_t tok = t_begin + u * kMmaTile + lane;
+        if constexpr (PREFIX) return lane < kMmaTile && tok < t_lim ? (tok < P ? a.ptable : table)[tok >> bs_log2] : 0;
         return lane < kMmaTile && tok < t_lim ? table[tok >> bs_log2] : 0;
     };
     // the first tiles' block ids and seq_len are requested together: one round trip, not two
@@ -684,7 +770,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(At
             if (tok < t_end) {
                 if (block_ok(blk)) {
                     off = ((static_cast<int64_t>(blk) << bs_log2) + (tok & (BS - 1))) * tok_stride + kvh_off;
-                } else if (kvh == 0 && (tok & (BS - 1)) == 0 && a.err) {
+                } else if (kvh == 0 && ((tok & (BS - 1)) == 0 || (PREFIX && tok == P)) && tok >= P && a.err) {
                     atomicAdd(a.err, 1);  // a bad block entry, counted once (kv head 0, its first token)
                 }
             }
@@ -831,11 +917,18 @@ cudaError_t launch_merge(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     return launch_kernel(decode_merge_kernel<T, HD>, grid, dim3(256), 0, s, p.pdl, 1, a);
 }
 
-template <typename T, int HD, int NW>
+template <typename T, int HD, int NW, bool PREFIX = false>
 cudaError_t launch_mma(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     const size_t smem = mma_smem(HD, NW);
-    if (a.gsplits > 0) {
-        auto kg = decode_mma_kernel<T, HD, true, NW>;
+    if (PREFIX && a.ws_part) {
+        auto kp = decode_mma_kernel<T, HD, true, NW, true>;
+        const cudaError_t ep =
+            cudaFuncSetAttribute(kp, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (ep != cudaSuccess) return ep;
+        return launch_kernel(kp, dim3(static_cast<unsigned>(a.B * a.n_kv * a.gsplits)), dim3(NW * 32), smem, s, p.pdl, 1, a);
+    }
+    if (!PREFIX && a.gsplits > 0) {
+        auto kg = decode_mma_kernel<T, HD, true, NW, false>;
         const cudaError_t eg =
             cudaFuncSetAttribute(kg, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (eg != cudaSuccess) return eg;
@@ -843,7 +936,7 @@ cudaError_t launch_mma(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
         const cudaError_t el = launch_kernel(kg, grid, block, smem, s, p.pdl, 1, a);
         return el != cudaSuccess ? el : launch_merge<T, HD>(a, p, s);
     }
-    auto kernel = decode_mma_kernel<T, HD, false, NW>;
+    auto kernel = decode_mma_kernel<T, HD, false, NW, PREFIX>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     int splits = p.splits;
@@ -1112,17 +1205,19 @@ cudaError_t launch_tma(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
                          a, tm);
 }
 
-template <typename T, int HD, int STAGES>
+template <typename T, int HD, int STAGES, bool PREFIX = false>
 cudaError_t launch_hd(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-    auto kernel = decode_kernel<T, HD, STAGES>;
+    auto kernel = decode_kernel<T, HD, STAGES, PREFIX>;
     const size_t smem = layout(a.group, HD, a.block_size, STAGES, sizeof(T)).total;
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid(static_cast<unsigned>(a.B * a.n_kv * p.splits)), block(kThreads);
-    return launch_kernel(kernel, grid, block, smem, s, p.pdl, p.splits, a);
+    const bool records = PREFIX && a.ws_part != nullptr;
+    const int splits = records ? a.gsplits : p.splits;
+    const dim3 grid(static_cast<unsigned>(a.B * a.n_kv * splits)), block(kThreads);
+    return launch_kernel(kernel, grid, block, smem, s, p.pdl, records ? 1 : splits, a);
 }
 
 template <typename T, int STAGES>
@@ -1131,6 +1226,20 @@ cudaError_t launch_stages(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) 
         case 64: return launch_hd<T, 64, STAGES>(a, p, s);
         case 128: return launch_hd<T, 128, STAGES>(a, p, s);
         case 256: return launch_hd<T, 256, STAGES>(a, p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <typename T>
+cudaError_t launch_prefix_typed(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        if (p.tensor_cores)
+            return p.head_dim == 64 ? launch_mma<T, 64, 8, true>(a, p, s) : launch_mma<T, 128, 8, true>(a, p, s);
+    }
+    switch (p.head_dim) {
+        case 64: return launch_hd<T, 64, 2, true>(a, p, s);
+        case 128: return launch_hd<T, 128, 2, true>(a, p, s);
+        case 256: return launch_hd<T, 256, 2, true>(a, p, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -1161,6 +1270,15 @@ cudaError_t launch_decode_attention(const AttnArgs& a, const AttnPlan& p, int dt
         case DT_F32: return attn::launch_typed<float>(a, p, s);
         case DT_F16: return attn::launch_typed<__half>(a, p, s);
         case DT_BF16: return attn::launch_typed<__nv_bfloat16>(a, p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_prefix_tail(const AttnArgs& a, const AttnPlan& p, int dtype, cudaStream_t s) {
+    switch (dtype) {
+        case DT_F32: return attn::launch_prefix_typed<float>(a, p, s);
+        case DT_F16: return attn::launch_prefix_typed<__half>(a, p, s);
+        case DT_BF16: return attn::launch_prefix_typed<__nv_bfloat16>(a, p, s);
         default: return cudaErrorInvalidValue;
     }
 }

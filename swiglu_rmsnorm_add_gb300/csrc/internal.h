@@ -148,6 +148,11 @@ struct AttnArgs {
     // in the workspace, combined by the merge kernel launched after them
     int gsplits = 0;
     float* ws_part = nullptr;  // [B * n_kv][gsplits][16 + 8 * head_dim]
+    // shared prefix (launch_prefix_tail): tokens below *plen come through ptable
+    const int32_t* ptable = nullptr;  // [pblocks]
+    const int32_t* plen = nullptr;
+    int64_t pblocks = 0;
+    bool tail_only = false;  // requests that reach past the prefix's whole pages start behind them
 };
 
 struct AttnPlan {
@@ -164,6 +169,9 @@ struct AttnPlan {
 };
 
 cudaError_t launch_decode_attention(const AttnArgs& a, const AttnPlan& p, int dtype, cudaStream_t s);
+// The same kernels over a request's tokens with a shared prefix in front: the whole attention (no
+// ws_part), or the splits' records [16 + 8 * head_dim] in ws_part (a.gsplits of them per pair).
+cudaError_t launch_prefix_tail(const AttnArgs& a, const AttnPlan& p, int dtype, cudaStream_t s);
 size_t decode_attention_smem(int group, int head_dim, int block_size, int stages, int es);
 size_t decode_attention_mma_smem(int head_dim, int warps);
 size_t decode_attention_tma_smem(int head_dim);

@@ -99,3 +99,32 @@ def test_workspace_sizes(L):
     assert L.sra_kv_resize_workspace_size(10, 1000) >= 8 + 200 + 4000
     assert L.sra_kv_resize_workspace_size(10, -1) == SHAPE
     assert L.sra_kv_compact_workspace_size(1000) >= 12008 and L.sra_kv_compact_workspace_size(1 << 31) == SHAPE
+
+
+def attend(L, q=P, c=CACHE, pt=T, pl=S, bt=R, sl=A, out=B, batch=4, nh=8, kv=2, hd=64, qs=512, os_=512, nb=8, bs=16,
+           pb=4, mb=4, scale=1.0, ws=None, wb=0, err=None, dt=BF16):
+    return L.sra_shared_prefix_attention(q, c, pt, pl, bt, sl, out, batch, nh, kv, hd, qs, os_, nb, bs, pb, mb, scale,
+                                         ws, wb, err, dt, None)
+
+
+def test_shared_prefix(L):
+    assert attend(L, dt=5) == DTYPE
+    for bad in (dict(batch=-1), dict(nh=9), dict(nh=18), dict(hd=96), dict(bs=24), dict(nb=-1), dict(pb=-1),
+                dict(mb=-1), dict(kv=0), dict(nb=1 << 31)):
+        assert attend(L, **bad) == SHAPE, bad
+    assert attend(L, qs=511) == -3 and attend(L, os_=100) == -3
+    assert attend(L, scale=float("nan")) == ARG and attend(L, wb=-1) == ARG and attend(L, c=CACHE + 8) == ARG
+    assert attend(L, batch=0, q=None) == OK
+    for bad in (dict(q=None), dict(c=None), dict(pt=None), dict(pl=None), dict(bt=None), dict(sl=None), dict(out=None)):
+        assert attend(L, **bad) == NULL, bad
+    for bad in (dict(out=P), dict(out=CACHE + 64), dict(out=T), dict(out=S - 16), dict(out=R), dict(out=A),
+                dict(err=B), dict(err=A), dict(err=P)):
+        assert attend(L, **bad) == ALIAS, bad
+
+
+def test_shared_prefix_workspace_size(L):
+    f = L.sra_shared_prefix_workspace_size
+    assert f(4, 8, 2, 64, 4, 4, 16, 7) == DTYPE
+    for bad in ((-1, 8, 2, 64, 4, 4, 16), (4, 9, 2, 64, 4, 4, 16), (4, 8, 2, 60, 4, 4, 16), (4, 8, 2, 64, -1, 4, 16),
+                (4, 8, 2, 64, 4, 4, 17)):
+        assert f(*bad, BF16) == SHAPE
