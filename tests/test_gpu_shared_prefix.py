@@ -85,7 +85,8 @@ class Case:
         u = torch.finfo(self.dtype).eps / 2
         up = 0.0 if self.dtype == torch.float32 else u
         tol = u * o.abs() + (up + 6e-5) * A + 1e-30
-        bad = ~((got.double() - o).abs() <= tol)
+        # a request that is clamped to its row's capacity attends to NaN tokens: NaN is the formula's value
+        bad = ~(((got.double() - o).abs() <= tol) | (o.isnan() & got.isnan()))
         assert not bool(bad.any()), (what, int(bad.sum()), float((got.double() - o).abs().max()),
                                      [int(x) for x in bad.nonzero()[0]])
 
