@@ -582,7 +582,8 @@ SRA_API int64_t sra_kv_compact_workspace_size(int64_t num_blocks);
  * block_table's rows are those of sra_paged_decode_attention: the entries that lie wholly below the
  * prefix's length are not read (they may hold the same pages, as sra_kv_fork_rows leaves them, or
  * anything). The prefix may end inside a page. A request shorter than the prefix attends to the
- * tokens that it has; one without tokens gets zeros.
+ * tokens that it has; one without tokens (or none whose score is above -inf) gets zeros; NaN in what
+ * a request attends to gives NaN.
  *
  * The tensor-core path takes the queries of all requests that share a KV head as the rows of one
  * product with the prefix's whole pages, splits it over the GPU along the prefix, takes each

@@ -103,6 +103,11 @@ __device__ __forceinline__ PrefixRange prefix_range(const AttnArgs& a, int64_t l
     const int64_t whole = P / a.block_size * a.block_size;
     return {P, a.tail_only && len >= whole ? whole : 0};
 }
+// An output: 0 where no token counted (den 0). PREFIX: a NaN among the scores stays NaN.
+template <bool PREFIX>
+__device__ __forceinline__ float quotient(float num, float den) {
+    return (PREFIX ? den != 0.0f : den > 0.0f) ? num / den : 0.0f;
+}
 // One CTA of a call: a prefix length out of range and bad entries of the prefix's table, counted once.
 __device__ __forceinline__ void count_prefix_errors(const AttnArgs& a, int64_t P) {
     if (!a.err) return;
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
                 den = fmaf(w, cluster.map_shared_rank(l_run, r)[g], den);
             }
         }
-        out[idx] = from_f32<T>(den > 0.0f ? num / den : 0.0f);
+        out[idx] = from_f32<T>(quotient<PREFIX>(num, den));
     }
     cluster.sync();  // keep every CTA's shared memory alive until the merge has read it
 }
@@ -531,7 +536,7 @@ __host__ __device__ inline size_t mma_smem(int HD, int NW) { return mma_inbox_of
 // merged in shared memory (over the drained rings), then the splits merged through distributed
 // shared memory (a cluster) or, with GMERGE, through the workspace by the CTA that finishes
 // last. NW warps hold partials; warps past them (a copy-issuing warp) only join the barriers.
-template <typename T, int HD, bool GMERGE, int NW>
+template <typename T, int HD, bool GMERGE, int NW, bool PREFIX = false>
 __device__ __forceinline__ void finish_mma(const AttnArgs& a, unsigned char* smem, float* inbox, float m, float l,
                                            float (&o)[HD / 8][2], int lane, int warp, int64_t grp, int64_t b,
                                            int kvh, int S, int rank, int G, cg::cluster_group& cluster) {
@@ -600,7 +605,7 @@ __device__ __forceinline__ void finish_mma(const AttnArgs& a, unsigned char* sme
         for (int w = 0; w < NW; ++w) num = fmaf(sw[w * 8 + gg], wo[(w * 8 + gg) * WS + d], num);
         if (alone) {
             const float den = pl[gg];
-            out[idx] = from_f32<T>(den > 0.0f ? num / den : 0.0f);
+            out[idx] = from_f32<T>(quotient<PREFIX>(num, den));
         } else if (GMERGE) {
             pacc[idx] = num;
         } else {
@@ -641,7 +646,7 @@ __device__ __forceinline__ void finish_mma(const AttnArgs& a, unsigned char* sme
         float num = 0.0f;
         for (int r = 0; r < S; ++r) num = fmaf(cw[r * 8 + gg], inbox[256 + r * C + (idx - c0)], num);
         const float den = cden[gg];
-        out[idx] = from_f32<T>(den > 0.0f ? num / den : 0.0f);
+        out[idx] = from_f32<T>(quotient<PREFIX>(num, den));
     }
 }
 
@@ -829,7 +834,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(At
                          [](int tok, int chunk) { return tok * HD + ((chunk ^ (tok & 7)) * 8); });
     }
     cp_async_wait<0>();
-    finish_mma<T, HD, GMERGE, NW>(a, smem, reinterpret_cast<float*>(smem + mma_inbox_offset(HD, NW)), m, l, o, lane,
+    finish_mma<T, HD, GMERGE, NW, PREFIX>(a, smem, reinterpret_cast<float*>(smem + mma_inbox_offset(HD, NW)), m, l, o, lane,
                                   warp, grp, b, kvh, S, rank, G, cluster);
 }
 
