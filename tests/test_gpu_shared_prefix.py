@@ -289,10 +289,11 @@ def test_a_prompt_and_its_samples():
     """The operators together, as a sampling loop uses them: a prompt is stored, forked into samples,
     each step grows the rows (the shared last page copied once), stores the new token's K and V by
     rope_kv_store's own slots and attends; then some samples end, the cache is compacted, and the
-    attention of the others is what it was."""
+    attention of the others is what it was. Row 0 keeps the prompt (it does not grow), so the page in
+    which the prompt ends stays held while the prefix's table names it."""
     torch.manual_seed(3)
     n_head, n_kv, hd, bs, nb, L = 12, 2, 128, 16, 120, 2
-    rows, M, prompt, n = 20, 24, 197, 17
+    rows, M, prompt, n = 20, 24, 197, 18
     caches = [torch.full((2, nb, bs, n_kv, hd), float("nan"), device=DEV, dtype=torch.bfloat16) for _ in range(L)]
     i = lambda a: torch.as_tensor(np.asarray(a), dtype=torch.int32).to(DEV)
     table, seq, ref = i(np.full((rows, M), -1)), i([0] * rows), i([0] * nb)
@@ -317,7 +318,8 @@ def test_a_prompt_and_its_samples():
             history[layer][r] = kv
     sra.fork_kv_rows(table, seq, ref, i([0] * (n - 1)), i(range(1, n)), bs, err_count=err)
     ptable, plen = table[0].clone(), i([prompt])
-    live = i(range(n))
+    samples = list(range(1, n))
+    live = i(samples)
 
     def attend(layer, r):
         q = torch.randn(len(r), n_head, hd, device=DEV, generator=torch.Generator(DEV).manual_seed(layer)).to(torch.bfloat16)
@@ -334,21 +336,22 @@ def test_a_prompt_and_its_samples():
         return got
 
     for step in range(1, 14):
-        pos, slot = sra.resize_kv_rows(table, seq, ref, live, i([prompt + step] * n), caches, err_count=err)
+        pos, slot = sra.resize_kv_rows(table, seq, ref, live, i([prompt + step] * (n - 1)), caches,
+                                       err_count=err)
         for layer in range(L):
-            kv = draw(n)
+            kv = draw(n - 1)
             store(layer, kv, pos, slot)
-            for r in range(n):
-                history[layer][r] = torch.cat([history[layer][r], kv[:, r:r + 1]], 1)
+            for k, r in enumerate(samples):
+                history[layer][r] = torch.cat([history[layer][r], kv[:, k:k + 1]], 1)
         if step in (1, 2, 11, 12, 13):
-            attend(step % L, list(range(n)))
+            attend(step % L, samples)
     left = [2, 3, 5, 7, 11, 13]
     before = [attend(layer, left) for layer in range(L)]
-    gone = [r for r in range(n) if r not in left]
+    gone = [r for r in samples if r not in left]
     sra.resize_kv_rows(table, seq, ref, i(gone), i([0] * len(gone)), caches, err_count=err)
     alive = sra.compact_kv_pages(table, seq, ref, caches, err_count=err)
-    assert int(alive.item()) == 12 + len(left) * 2 and bool((ref[int(alive.item()):] == 0).all())
-    ptable = table[left[0]].clone()
+    assert int(alive.item()) == 13 + len(left) * 2 and bool((ref[int(alive.item()):] == 0).all())
+    ptable = table[0].clone()
     after = [attend(layer, left) for layer in range(L)]
     for x, y in zip(before, after):
         assert torch.equal(x, y)
