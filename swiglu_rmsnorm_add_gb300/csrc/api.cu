@@ -710,7 +710,7 @@ int sra_version(void) { return SRA_VERSION; }
 
 int sra_last_cuda_error(void) { return g_last_cuda_error; }
 
-unsigned int sra_wait_timeouts(void) { return linear_wait_timeouts() + attn_wait_timeouts(); }
+unsigned int sra_wait_timeouts(void) { return linear_wait_timeouts() + attn_wait_timeouts() + prefix_wait_timeouts(); }
 
 int sra_wait_selftest(int32_t* result, void* stream) {
     if (!result) return SRA_ERR_NULL;
@@ -1616,13 +1616,54 @@ int prefix_sizes(int64_t B, int n_head, int n_kv_head, int head_dim, int64_t pre
     return SRA_OK;
 }
 
+// How a call is cut for the tensor-core path (use: whether it is taken), and its workspace.
+struct PrefixPlan {
+    bool use = false;
+    int rows = 0, pair_blocks = 0, pair_splits = 0, single_splits = 0, ctas_per_kv = 0, records = 0, tail_splits = 0;
+    int64_t ml_bytes = 0, o_bytes = 0, tail_bytes = 0;
+    int64_t bytes() const { return ml_bytes + o_bytes + tail_bytes; }
+};
+PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t prefix_blocks, int64_t max_blocks,
+                       int block_size, int dtype, int sms) {
+    PrefixPlan p;
+    const int64_t rows = B * group;
+    if (dtype == DT_F32 || head_dim > 128 || rows < 8 || rows > (1 << 24) || prefix_blocks < 1) return p;
+    p.use = true;
+    p.rows = static_cast<int>(rows);
+    // row tiles of 128, two to a CTA; the SMs of a KV head are dealt to its blocks by their tiles, and a
+    // split gets one K / V tile at least
+    const int64_t tiles = ceil_div(prefix_blocks * block_size, 128);
+    const int mt = static_cast<int>(ceil_div(rows, 128)), per_kv = std::max(1, sms / n_kv);
+    p.pair_blocks = mt / 2;
+    if (p.pair_blocks) p.pair_splits = static_cast<int>(std::min<int64_t>(std::max(1, 2 * per_kv / mt), tiles));
+    if (mt & 1)
+        p.single_splits = static_cast<int>(
+            std::min<int64_t>(std::max(1, per_kv - p.pair_blocks * p.pair_splits), ceil_div(tiles, 2)));
+    p.ctas_per_kv = p.pair_blocks * p.pair_splits + p.single_splits;
+    p.records = std::max(p.pair_splits, 2 * p.single_splits);
+    // the requests' own tokens
+    const int64_t groups = B * n_kv, own = std::max<int64_t>(0, max_blocks - prefix_blocks) * block_size;
+    p.tail_splits = 1;
+    while (p.tail_splits < 32 && groups * p.tail_splits * 2 <= sms && own >= 512 * p.tail_splits) p.tail_splits *= 2;
+    const int64_t recs = n_kv * rows * p.records;
+    p.ml_bytes = round_up256(recs * 8);
+    p.o_bytes = round_up256(recs * head_dim * 4);
+    p.tail_bytes = round_up256(groups * p.tail_splits * (16 + 8 * static_cast<int64_t>(head_dim)) * 4);
+    return p;
+}
+
 }  // namespace
 
 int64_t sra_shared_prefix_workspace_size(int64_t B, int n_head, int n_kv_head, int head_dim, int64_t prefix_blocks,
                                          int64_t max_blocks_per_seq, int block_size, int dtype) {
     const int st = prefix_sizes(B, n_head, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size, dtype);
     if (st != SRA_OK) return st;
-    return 0;
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
+    if (sms <= 0) return SRA_ERR_DEVICE;
+    return plan_prefix(B, n_head / n_kv_head, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size, dtype,
+                       sms)
+        .bytes();
 }
 
 int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32_t* prefix_table,
@@ -1702,7 +1743,54 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     a.ptable = prefix_table;
     a.plen = prefix_len;
     a.pblocks = prefix_blocks;
-    return status_from(launch_prefix_tail(a, plan, dtype, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const PrefixPlan pp = plan_prefix(B, group, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size,
+                                      dtype, sms);
+    if (!workspace || !pp.use || !plan.tensor_cores || static_cast<int64_t>(prefix_tc_smem(head_dim)) > limit + 1024 - 256 ||
+        num_blocks * block_size >= (int64_t(1) << 31) - 64)
+        return status_from(launch_prefix_tail(a, plan, dtype, s));
+    if (workspace_bytes < pp.bytes() || !aligned16(workspace)) return SRA_ERR_ARG;
+    const Span sws = span_of(workspace, 1, 0, pp.bytes(), 1);
+    if (overlap(sws, so) || overlap(sws, sq) || overlap(sws, serr)) return SRA_ERR_ALIAS;
+    for (const Span& r : reads)
+        if (overlap(sws, r)) return SRA_ERR_ALIAS;
+    PrefixArgs f;
+    f.q = q;
+    f.ptable = prefix_table;
+    f.plen = prefix_len;
+    f.seq_lens = seq_lens;
+    f.out = out;
+    f.B = B;
+    f.qs = q_tok_stride;
+    f.os = out_tok_stride;
+    f.num_blocks = num_blocks;
+    f.pblocks = prefix_blocks;
+    f.cap = max_blocks_per_seq * block_size;
+    f.n_kv = n_kv_head;
+    f.group = group;
+    f.block_size = block_size;
+    f.scale_log2 = std::fabs(a.scale_log2);
+    f.negate = scale < 0.0f;
+    f.q16 = aligned16(q) && stride_aligned16(q_tok_stride, es);
+    f.rows = pp.rows;
+    f.pair_blocks = pp.pair_blocks;
+    f.pair_splits = pp.pair_splits;
+    f.single_splits = pp.single_splits;
+    f.ctas_per_kv = pp.ctas_per_kv;
+    f.records = pp.records;
+    f.part_ml = static_cast<float2*>(workspace);
+    f.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp.ml_bytes);
+    float* tail = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp.ml_bytes + pp.o_bytes);
+    f.tail = tail;
+    f.tail_splits = pp.tail_splits;
+    a.tail_only = true;
+    a.ws_part = tail;
+    a.gsplits = pp.tail_splits;
+    int rs = status_from(launch_prefix_tc(f, kv_cache, head_dim, dtype, plan.pdl, s));
+    if (rs != SRA_OK) return rs;
+    plan.pdl = true;  // the kernels of this call follow one another
+    rs = status_from(launch_prefix_tail(a, plan, dtype, s));
+    return rs != SRA_OK ? rs : status_from(launch_prefix_merge(f, head_dim, dtype, s));
 }
 
 int sra_force_variant(const char* op, int variant) {

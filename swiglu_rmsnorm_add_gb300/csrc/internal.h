@@ -182,6 +182,34 @@ constexpr int kMaxGsplits = 256;
 int decode_attention_gsplits(int64_t B, int n_kv, int64_t max_blocks, int block_size, int num_sms);
 int64_t decode_attention_ws_bytes(int64_t B, int n_kv, int head_dim, int gsplits);
 
+// ------------------------------------------------------------------- shared prefix
+// The prefix's whole pages against the queries of all requests (tcgen05 path), and the merge of its
+// partial results with the requests' own tokens'.
+struct PrefixArgs {
+    const void* q;            // [B, n_head, head_dim], token stride qs
+    const int32_t* ptable;    // [pblocks]
+    const int32_t* plen;      // 1
+    const int32_t* seq_lens;  // [B]
+    void* out;
+    int64_t B, qs, os, num_blocks, pblocks, cap;  // cap: the most tokens a request's row holds
+    int n_kv, group, block_size;
+    float scale_log2;  // |softmax scale| * log2(e); a negative scale flips the queries' sign
+    bool negate, q16;  // q16: 16-byte aligned query rows
+    // work: rows = B * group query rows of a KV head in tiles of 128. Two tiles share a CTA's K / V
+    // tiles (a pair block); an odd last tile is a block of its own whose CTAs work on two K / V tiles
+    // at a time. A block's K / V range is dealt to its splits, each split (each half of a single block's)
+    // leaves one record per row.
+    int rows, pair_blocks, pair_splits, single_splits, ctas_per_kv, records;
+    float* part_o;   // [n_kv * rows][records][head_dim]
+    float2* part_ml;  // [n_kv * rows][records] maximum (base 2, scaled) and sum
+    const float* tail;  // [B * n_kv][tail_splits][16 + 8 * head_dim]
+    int tail_splits;
+};
+cudaError_t launch_prefix_tc(const PrefixArgs& a, const void* cache, int head_dim, int dtype, bool pdl, cudaStream_t s);
+cudaError_t launch_prefix_merge(const PrefixArgs& a, int head_dim, int dtype, cudaStream_t s);
+size_t prefix_tc_smem(int head_dim);
+unsigned int prefix_wait_timeouts();
+
 // ------------------------------------------------------------------- fused linear
 struct LinArgs {
     const void* x;     // [B, K] (RMSNorm prologue, or h itself) or gate_up [B, 2K] (GLU prologue), row stride xs
