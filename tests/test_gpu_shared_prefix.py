@@ -212,7 +212,7 @@ def test_equals_decode_attention_on_forked_rows():
     c.check(a)
     c.check(b)
     d["prefix_table"] = d["block_table"][3].contiguous()   # a row of the table as the prefix's table
-    assert torch.equal(sra.shared_prefix_attention(**d), a)
+    c.check(sra.shared_prefix_attention(**d))   # (its length sets the splits, so the sums' order may differ)
 
 
 @pytest.mark.parametrize("pdl", [False, True])
