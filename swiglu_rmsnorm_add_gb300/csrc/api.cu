@@ -1632,7 +1632,7 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
     p.rows = static_cast<int>(rows);
     // row tiles of 128, two to a CTA; the SMs of a KV head are dealt to its blocks by their tiles, and a
     // split gets one K / V tile at least
-    const int64_t tiles = ceil_div(prefix_blocks * block_size, 128);
+    const int64_t tiles = ceil_div(prefix_blocks * block_size, 64);
     const int mt = static_cast<int>(ceil_div(rows, 128)), per_kv = std::max(1, sms / n_kv);
     p.pair_blocks = mt / 2;
     if (p.pair_blocks) p.pair_splits = static_cast<int>(std::min<int64_t>(std::max(1, 2 * per_kv / mt), tiles));
@@ -1640,7 +1640,7 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
         p.single_splits = static_cast<int>(
             std::min<int64_t>(std::max(1, per_kv - p.pair_blocks * p.pair_splits), ceil_div(tiles, 2)));
     p.ctas_per_kv = p.pair_blocks * p.pair_splits + p.single_splits;
-    p.records = std::max(p.pair_splits, 2 * p.single_splits);
+    p.records = std::max(p.pair_splits, p.single_splits);
     // the requests' own tokens
     const int64_t groups = B * n_kv, own = std::max<int64_t>(0, max_blocks - prefix_blocks) * block_size;
     p.tail_splits = 1;
@@ -1746,7 +1746,7 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const PrefixPlan pp = plan_prefix(B, group, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size,
                                       dtype, sms);
-    if (!workspace || !pp.use || !plan.tensor_cores || static_cast<int64_t>(prefix_tc_smem(head_dim)) > limit + 1024 - 256 ||
+    if (!workspace || !pp.use || !plan.tensor_cores || static_cast<int64_t>(prefix_tc_smem(head_dim)) > limit - 512 ||
         num_blocks * block_size >= (int64_t(1) << 31) - 64)
         return status_from(launch_prefix_tail(a, plan, dtype, s));
     if (workspace_bytes < pp.bytes() || !aligned16(workspace)) return SRA_ERR_ARG;

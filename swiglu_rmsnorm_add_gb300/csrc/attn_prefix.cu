@@ -18,19 +18,20 @@
 namespace sra {
 namespace prefix {
 
-constexpr int kTok = 128;           // tokens of a K / V tile
+constexpr int kTok = 64;            // tokens of a K / V tile
 constexpr int kRows = 128;          // query rows of a tile (the MMA's M)
-constexpr int kThreads = 384;       // producer, MMA, two spare warps; two softmax warpgroups
+constexpr int kThreads = 384;       // producer, MMA issuer, two warps that help to set up; two softmax warpgroups
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;    // base-2 headroom of the running maximum, see softmax below
 
 template <int HD>
 struct Smem {
     static constexpr int kHalves = HD / 64;
-    static constexpr int kHalfBytes = kTok * 128;              // 64 dims of a tile's 128 rows
-    static constexpr int kTileBytes = kHalves * kHalfBytes;    // a K, V or Q tile
-    static constexpr int kStages = HD == 128 ? 5 : 10;         // K or V tiles in flight
-    static constexpr size_t kTotal = 1024 + (2 + kStages) * static_cast<size_t>(kTileBytes);
+    static constexpr int kHalfBytes = kTok * 128;              // 64 dims of a K or V tile's rows
+    static constexpr int kTileBytes = kHalves * kHalfBytes;    // a K or V tile
+    static constexpr int kQHalf = kRows * 128, kQBytes = kHalves * kQHalf;
+    static constexpr int kStages = 10;                         // K or V tiles in flight
+    static constexpr size_t kTotal = 1024 + 2 * static_cast<size_t>(kQBytes) + kStages * static_cast<size_t>(kTileBytes);
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -39,12 +40,32 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Pairs of fp32 in a 64-bit register: one instruction per pair, each half rounded as the plain operation.
+__device__ __forceinline__ uint64_t f32x2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // What CTA `c` of a KV head's works on.
 struct Work {
     int row0;      // first query row
     bool pair;     // two row tiles on the same K / V tiles, or one row tile on two K / V tiles at a time
     int t0, n;     // K / V tiles
-    int rec;       // record of stream 0 (stream 1: the same in a pair, the next otherwise)
+    int rec;       // its record of each row
 };
 __device__ __forceinline__ Work work_of(const PrefixArgs& a, int c, int64_t tiles) {
     Work w;
@@ -59,7 +80,7 @@ __device__ __forceinline__ Work work_of(const PrefixArgs& a, int c, int64_t tile
         split = c - a.pair_blocks * a.pair_splits, splits = a.single_splits;
         w.pair = false;
         w.row0 = a.pair_blocks * 2 * kRows;
-        w.rec = 2 * split;
+        w.rec = split;
     }
     const int64_t b = tiles * split / splits, e = tiles * (split + 1) / splits;
     w.t0 = static_cast<int>(b);
@@ -72,23 +93,11 @@ __device__ __forceinline__ int64_t whole_pages(const PrefixArgs& a) {
     return (P < 0 ? 0 : (P > cap ? cap : P)) / a.block_size;
 }
 
-// The order in which K and V tiles go through the ring (both sides follow it): entry s of 2 n is V or K
-// of tile t. A pair uses K0 V0 K1 V1 ...; a single block, whose streams take even and odd tiles, needs
-// K0 K1 V0 K2 V1 K3 ... V(n-1).
-__device__ __forceinline__ void ring_entry(bool pair, int n, int s, bool* is_v, int* t) {
-    if (pair) {
-        *is_v = s & 1, *t = s >> 1;
-    } else if (s == 2 * n - 1) {
-        *is_v = true, *t = n - 1;
-    } else {
-        *is_v = s != 0 && (s & 1) == 0;
-        *t = s == 0 ? 0 : *is_v ? (s - 2) / 2 : (s + 1) / 2;
-    }
-}
-__device__ __forceinline__ int ring_k(bool pair, int t) { return pair ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
-__device__ __forceinline__ int ring_v(bool pair, int n, int t) {
-    return pair ? 2 * t + 1 : 2 + 2 * t < 2 * n - 1 ? 2 + 2 * t : 2 * n - 1;
-}
+// The order in which K and V tiles go through the ring (both sides follow it). A round is the tile of
+// a pair, or the two tiles that a single block's streams take at a time (w = 1 or 2 tiles); the ring
+// carries K of round 0, then K of round r + 1 and V of round r for r = 0, 1, ...
+__device__ __forceinline__ int ring_k(int w, int t) { return t + (t >= w ? (t / w - 1) * w : 0); }
+__device__ __forceinline__ int ring_v(int w, int n, int t) { return min(n, (t / w + 2) * w) + t; }
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -96,65 +105,56 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
     return Elem<T>::pack_word(f);
 }
 
+// A CTA takes 256 query rows (two row tiles, one per softmax warpgroup: "streams") through its split's
+// K / V tiles of 64 tokens, or 128 rows with the streams on alternate tiles. Per stream and tile:
+// S = Q K^T (fp32, tensor memory), the softmax warpgroup reads it (a thread is a row), frees it, and
+// writes P (16-bit) back to tensor memory, and O += P V takes P from there.
+// Tensor memory, 512 columns: S 64 per stream, P 32 per stream and buffer (two), O head_dim per stream.
+// S, P and O never share columns, so the next tile's S needs only that this one's has been read: the
+// product S runs under the softmax, and the tensor cores have work of one stream while the other's
+// softmax is under way. (With P over S in 128-token tiles the chain S -> softmax -> P V -> next S has no
+// such overlap: measured 4700 clocks per 128 tokens of both streams, against 2070 of tensor-core work.
+// The price is that S in tiles of 64 tokens reads Q from shared memory twice as often: 48 clocks per
+// K step of 16 instead of 2 x 32, shared-memory bandwidth, so a tile cannot run above 81 % of the peak.)
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC) {
     using L = Smem<HD>;
     constexpr int ST = L::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    // tensor memory: S of the two streams, then O; P (16-bit, 64 columns) over S's first columns
-    constexpr uint32_t kS = 0, kO = 256;
+    constexpr uint32_t kS = 0, kP = 128, kO = 256;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char* qs = smem;                          // two Q tiles
-    unsigned char* ring = smem + 2 * L::kTileBytes;    // ST K / V tiles
-    __shared__ uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2];
+    unsigned char* qs = smem;                       // two Q tiles
+    unsigned char* ring = smem + 2 * L::kQBytes;    // ST K / V tiles
+    __shared__ uint64_t full[ST], empty[ST], s_full[2], s_free[2], p_full[2][2], pv_done[2][2];
     __shared__ uint32_t tmem_base;
+    __shared__ int s_ragged;
+    __shared__ float2 s_ml[kRows];  // a single block's stream 1: maxima and sums
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-        for (int x = 0; x < 2; ++x) mbar_init(&s_full[x], 1), mbar_init(&p_full[x], 4), mbar_init(&pv_done[x], 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&s_full[x], 1), mbar_init(&s_free[x], 4);
+            for (int b = 0; b < 2; ++b) mbar_init(&p_full[x][b], 4), mbar_init(&pv_done[x][b], 1);
+        }
         mbar_init_fence();
+        s_ragged = 0;
     }
     if (warp == 1) {
         tc::alloc(&tmem_base, kTmemCols);
         tc::relinquish();
     }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_base;
     pdl_enter();
     const int kvh = blockIdx.x / a.ctas_per_kv;
     const int64_t pages = whole_pages(a);
     const int ppt = kTok / a.block_size;  // pages of a tile
     const Work w = work_of(a, blockIdx.x - kvh * a.ctas_per_kv, (pages + ppt - 1) / ppt);
+    const int tpr = w.pair ? 1 : 2;  // tiles per round
     const int n0 = w.pair ? w.n : (w.n + 1) / 2, n1 = w.pair ? w.n : w.n / 2;  // tiles of the streams
-
-    // the query rows, swizzled as a TMA copy would leave them; rows past the last are zero
-    {
-        constexpr int kChunks = HD / 8;
-        const int tiles = w.pair ? 2 : 1;
-        for (int i = threadIdx.x; i < tiles * kRows * kChunks && w.n > 0; i += kThreads) {
-            const int r = i / kChunks, c = i - r * kChunks, row = w.row0 + r;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (row < a.rows) {
-                const int b = row / a.group, g = row - b * a.group;
-                const T* src = static_cast<const T*>(a.q) + b * a.qs + (kvh * a.group + g) * HD + c * 8;
-                if (a.q16) {
-                    v = *reinterpret_cast<const uint4*>(src);
-                } else {
-                    const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
-                    v.x = e[0] | static_cast<uint32_t>(e[1]) << 16, v.y = e[2] | static_cast<uint32_t>(e[3]) << 16;
-                    v.z = e[4] | static_cast<uint32_t>(e[5]) << 16, v.w = e[6] | static_cast<uint32_t>(e[7]) << 16;
-                }
-                if (a.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
-            }
-            const int rr = r % kRows;
-            *reinterpret_cast<uint4*>(qs + (r / kRows) * L::kTileBytes + (c / 8) * L::kHalfBytes + rr * 128 +
-                                      (((c & 7) ^ (rr & 7)) * 16)) = v;
-        }
-        fence_proxy_async();  // before the tensor core reads them
-    }
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
-    const uint32_t tmem = tmem_base;
     bool dead = false;  // a bounded wait ran out (counted): this thread waits no more
     auto wait = [&](uint64_t* bar, int phase) {
         if (!dead) dead = !mbar_wait(bar, static_cast<uint32_t>(phase & 1));
@@ -163,75 +163,146 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
     if (warp == 0) {
         // producer: a tile is a box of 64 dims x block_size tokens per page and half. A page past the
         // prefix, or an entry that is no page, is copied from past the cache's end: zeros.
+        // The page entries are read 32 at a time (lane k: entry k of the group), a group ahead of their
+        // use and apart for K and V, so no copy waits for the table.
         const int boxes = ppt * L::kHalves;
-        for (int s = 0; s < 2 * w.n; ++s) {
-            bool is_v;
-            int t;
-            ring_entry(w.pair, w.n, s, &is_v, &t);
-            const int stage = s % ST;
+        const int half = lane / ppt, p = lane - half * ppt;
+        int s = 0, group[2] = {-1, -1};
+        int32_t cur[2] = {-1, -1}, next[2] = {-1, -1};
+        auto entries = [&](int g) -> int32_t {
+            const int64_t j = static_cast<int64_t>(w.t0) * ppt + static_cast<int64_t>(g) * 32 + lane;
+            return j < pages ? a.ptable[j] : -1;
+        };
+        auto load = [&](int t, int plane, int32_t& c, int32_t& nx, int& g) {
+            const int stage = s % ST, first = t * ppt;
+            if (first / 32 != g) {
+                c = g < 0 ? entries(0) : nx;
+                ++g;
+                nx = entries(g + 1);
+            }
+            int64_t blk = __shfl_sync(0xffffffffu, c, (first + p) & 31);
+            if (blk < 0 || blk >= a.num_blocks) blk = a.num_blocks;
             if (s >= ST) wait(&empty[stage], s / ST - 1);
             if (lane == 0) mbar_arrive_expect_tx(&full[stage], L::kTileBytes);
             __syncwarp();
-            for (int i = lane; i < boxes; i += 32) {
-                const int half = i / ppt, p = i - half * ppt;
-                const int64_t j = static_cast<int64_t>(w.t0 + t) * ppt + p;
-                int64_t blk = j < pages ? a.ptable[j] : -1;
-                if (blk < 0 || blk >= a.num_blocks) blk = a.num_blocks;
+            if (lane < boxes)
                 tma_load_4d(ring + stage * L::kTileBytes + half * L::kHalfBytes + p * a.block_size * 128, &tmC,
-                            half * 64, kvh, static_cast<int>(blk * a.block_size), is_v ? 1 : 0, &full[stage]);
+                            half * 64, kvh, static_cast<int>(blk * a.block_size), plane, &full[stage]);
+            ++s;
+        };
+        auto load_k = [&](int t) { load(t, 0, cur[0], next[0], group[0]); };
+        auto load_v = [&](int t) { load(t, 1, cur[1], next[1], group[1]); };
+        for (int t = 0; t < tpr && t < w.n; ++t) load_k(t);
+        for (int r = 0; r < n0; ++r) {
+            for (int t = (r + 1) * tpr; t < (r + 2) * tpr && t < w.n; ++t) load_k(t);
+            for (int t = r * tpr; t < (r + 1) * tpr && t < w.n; ++t) load_v(t);
+        }
+    } else {
+        // the query rows, swizzled as a TMA copy would leave them (rows past the last are zero), and
+        // whether every page of this CTA's tiles counts
+        constexpr int kSetup = kThreads - 32, kChunks = HD / 8;
+        constexpr int kEach = (2 * kRows * kChunks + kSetup - 1) / kSetup;  // 16-byte chunks a thread moves
+        const int tid = threadIdx.x - 32, count = w.n > 0 ? (w.pair ? 2 : 1) * kRows * kChunks : 0;
+        uint4 v[kEach];
+        auto source = [&](int i) -> const T* {  // chunk i's elements, or null past the last row
+            const int r = i / kChunks, row = w.row0 + r;
+            if (i >= count || row >= a.rows) return nullptr;
+            const int b = row / a.group, g = row - b * a.group;
+            return static_cast<const T*>(a.q) + b * a.qs + (kvh * a.group + g) * HD + (i % kChunks) * 8;
+        };
+        if (a.q16) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {  // all loads in flight before the first store
+                const T* src = source(tid + e * kSetup);
+                v[e] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        } else {
+#pragma unroll 1
+            for (int e = 0; e < kEach; ++e) {
+                const unsigned short* h = reinterpret_cast<const unsigned short*>(source(tid + e * kSetup));
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (h) {
+                    u.x = h[0] | static_cast<uint32_t>(h[1]) << 16, u.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
+                    u.z = h[4] | static_cast<uint32_t>(h[5]) << 16, u.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
+                }
+#pragma unroll
+                for (int k = 0; k < kEach; ++k)
+                    if (k == e) v[k] = u;
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = tc::idesc_f16(kBf16, kRows, kTok);
-            constexpr uint32_t kIdescO = tc::idesc_f16(kBf16, kRows, HD) | tc::kTransposeB;
-            auto qk = [&](int x, int t) {
-                const unsigned char* k = ring + (ring_k(w.pair, t) % ST) * L::kTileBytes;
-                const unsigned char* q = qs + (w.pair ? x : 0) * L::kTileBytes;
+        bool bad = false;
+        for (int64_t k = tid; k < static_cast<int64_t>(w.n) * ppt; k += kSetup) {
+            const int64_t j = static_cast<int64_t>(w.t0) * ppt + k;
+            const int32_t e = j < pages ? a.ptable[j] : -1;
+            bad |= e < 0 || e >= a.num_blocks;
+        }
+        if (bad) s_ragged = 1;
+        const uint32_t flip = a.negate ? 0x80008000u : 0u;
 #pragma unroll
-                for (int s = 0; s < HD / 16; ++s) {
-                    const int off = (s / 4) * L::kHalfBytes;
-                    tc::mma_f16(tmem + kS + x * kTok, tc::sdesc_sw128(q + off, (s % 4) * 32),
-                                tc::sdesc_sw128(k + off, (s % 4) * 32), kIdescS, s > 0);
-                }
-                tc::commit(&s_full[x]);
-            };
-            auto pv = [&](int x, int t, bool acc) {
-                const unsigned char* v = ring + (ring_v(w.pair, w.n, t) % ST) * L::kTileBytes;
+        for (int e = 0; e < kEach; ++e) {
+            const int i = tid + e * kSetup, r = i / kChunks, c = i % kChunks, rr = r % kRows;
+            if (i < count)
+                *reinterpret_cast<uint4*>(qs + (r / kRows) * L::kQBytes + (c / 8) * L::kQHalf + rr * 128 +
+                                          (((c & 7) ^ (rr & 7)) * 16)) =
+                    make_uint4(v[e].x ^ flip, v[e].y ^ flip, v[e].z ^ flip, v[e].w ^ flip);
+        }
+        fence_proxy_async();  // before the tensor core reads them
+        asm volatile("bar.sync 1, %0;" ::"r"(kSetup) : "memory");
+    }
+
+    if (warp == 1) {
+        // MMA issuer: the whole warp runs the loop, one lane issues. (Issued from a branch of one lane, whose
+        // descriptors the compiler must move to uniform registers one by one, an instruction took 75
+        // clocks, more than the product itself.)
+        constexpr uint32_t kIdescS = tc::idesc_f16(kBf16, kRows, kTok);
+        constexpr uint32_t kIdescO = tc::idesc_f16(kBf16, kRows, HD) | tc::kTransposeB;
+        const uint32_t elected = tc::elect();
+        const uint32_t q_lo = tc::sdesc_lo(qs, 16), k_lo = tc::sdesc_lo(ring, 16), v_lo = tc::sdesc_lo(ring, L::kHalfBytes);
+        auto ready = [&](int s) {
+            wait(&full[s % ST], s / ST);
+            tc::fence_after();
+        };
+        auto tile = [&](int x, int i) { return w.pair ? i : 2 * i + x; };
+        // a pair's streams share the ring's entries: stream 0 waits for them, stream 1 releases them
+        auto qk = [&](int x, int i) {
+            const int s = ring_k(tpr, tile(x, i)), stage = s % ST;
+            if (!w.pair || x == 0) ready(s);
+            const uint32_t k = k_lo + stage * (L::kTileBytes / 16), q = q_lo + (w.pair ? x : 0) * (L::kQBytes / 16);
 #pragma unroll
-                for (int s = 0; s < kTok / 16; ++s)
-                    tc::mma_f16_ts(tmem + kO + x * HD, tmem + kS + x * kTok + 8 * s,
-                                   tc::sdesc_sw128_mn(v, L::kHalfBytes, s), kIdescO, acc || s > 0);
-                tc::commit(&pv_done[x]);
-            };
-            auto ready = [&](int s) {
-                wait(&full[s % ST], s / ST);
-                tc::fence_after();
-            };
-            auto release = [&](int s) { tc::commit(&empty[s % ST]); };
-            const int nx[2] = {n0, n1};
-            auto tile = [&](int x, int i) { return w.pair ? i : 2 * i + x; };
-            auto load_k = [&](int x, int i) {  // S of stream x's tile i
-                const int s = ring_k(w.pair, tile(x, i));
-                if (!w.pair || x == 0) ready(s);
-                qk(x, tile(x, i));
-                if (!w.pair || x == 1) release(s);
-            };
+            for (int e = 0; e < HD / 16; ++e)
+                tc::mma_f16_ss(elected, tmem + kS + x * kTok, q + (e / 4) * (L::kQHalf / 16) + (e % 4) * 2,
+                               k + (e / 4) * (L::kHalfBytes / 16) + (e % 4) * 2, kIdescS, e > 0);
+            tc::commit(elected, &s_full[x]);
+            if (!w.pair || x == 1) tc::commit(elected, &empty[stage]);
+        };
+        auto pv = [&](int x, int i) {
+            const int s = ring_v(tpr, w.n, tile(x, i)), stage = s % ST;
+            if (!w.pair || x == 0) ready(s);
+            const uint32_t v = v_lo + stage * (L::kTileBytes / 16);
+#pragma unroll
+            for (int e = 0; e < kTok / 16; ++e)
+                tc::mma_f16_ts(elected, tmem + kO + x * HD, tmem + kP + x * 64 + (i & 1) * 32 + 8 * e, v + e * 128,
+                               kIdescO, i > 0 || e > 0);
+            tc::commit(elected, &pv_done[x][i & 1]);
+            if (!w.pair || x == 1) tc::commit(elected, &empty[stage]);
+        };
+        const int nx[2] = {n0, n1};
+        for (int x = 0; x < 2; ++x)
+            if (nx[x] > 0) qk(x, 0);
+        for (int i = 0; i < n0; ++i) {
+#pragma unroll
             for (int x = 0; x < 2; ++x)
-                if (nx[x] > 0) load_k(x, 0);
-            for (int i = 0; i < n0; ++i)
-                for (int x = 0; x < 2; ++x) {
-                    if (i >= nx[x]) continue;
-                    const int s = ring_v(w.pair, w.n, tile(x, i));
-                    if (!w.pair || x == 0) ready(s);
-                    wait(&p_full[x], i);
+                if (i + 1 < nx[x]) {
+                    wait(&s_free[x], i);
                     tc::fence_after();
-                    pv(x, tile(x, i), i > 0);
-                    if (!w.pair || x == 1) release(s);
-                    if (i + 1 < nx[x]) {
-                        wait(&pv_done[x], i);  // P has been read: S may go over it
-                        load_k(x, i + 1);
-                    }
+                    qk(x, i + 1);
+                }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (i < nx[x]) {
+                    wait(&p_full[x][i & 1], i / 2);
+                    tc::fence_after();
+                    pv(x, i);
                 }
         }
         __syncwarp();
@@ -242,48 +313,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
         // and O in tensor memory is scaled seldom.
         const int x = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t tS = tmem + lanes + kS + x * kTok, tO = tmem + lanes + kO + x * HD;
+        const uint32_t tS = tmem + lanes + kS + x * kTok, tP = tmem + lanes + kP + x * 64, tO = tmem + lanes + kO + x * HD;
         const int n = x == 0 ? n0 : n1;
+        const bool ragged = s_ragged != 0;
+        const int bs_log2 = __ffs(a.block_size) - 1;
         const float c = a.scale_log2;
         float m = -INFINITY, l = 0.0f;
-        // the tile's pages that count, asked for a tile ahead
-        auto ask = [&](int i) -> int32_t {
-            const int64_t j = static_cast<int64_t>(w.t0 + (w.pair ? i : 2 * i + x)) * ppt + lane;
-            return i < n && lane < ppt && j < pages ? a.ptable[j] : -1;
-        };
-        int32_t entry = ask(0);
-        const unsigned all_pages = static_cast<unsigned>((1ull << ppt) - 1);
-        const int bs_log2 = __ffs(a.block_size) - 1;
         for (int i = 0; i < n; ++i) {
-            const unsigned valid = __ballot_sync(0xffffffffu, entry >= 0 && entry < a.num_blocks);
-            entry = ask(i + 1);
             wait(&s_full[x], i);
             tc::fence_after();
-            uint32_t lo[2][32], hi[32];
-            tc::ld32(tS, lo[0]);
-            tc::ld32(tS + 32, lo[1]);
+            uint32_t v[2][32];
+            tc::ld32(tS, v[0]);
+            tc::ld32(tS + 32, v[1]);
             tc::wait_ld();
-            auto mask = [&](uint32_t(&v)[32], int c0) {
-                if (valid == all_pages) return;
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[x]);  // this warp has read its rows of S
+            if (ragged) {
+                // some page of the CTA's range does not count: its tokens' scores become -inf
+                const int64_t j = static_cast<int64_t>(w.t0 + (w.pair ? i : 2 * i + x)) * ppt + lane;
+                const int32_t e = lane < ppt && j < pages ? a.ptable[j] : -1;
+                const unsigned valid = __ballot_sync(0xffffffffu, e >= 0 && e < a.num_blocks);
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (!((valid >> ((c0 + k) >> bs_log2)) & 1u)) v[k] = __float_as_uint(-INFINITY);
-            };
-            float mx = -INFINITY;
-            auto top = [&](const uint32_t(&v)[32]) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
-            };
-            mask(lo[0], 0), mask(lo[1], 32);
-            top(lo[0]), top(lo[1]);
-#pragma unroll
-            for (int h = 2; h < 4; ++h) {
-                tc::ld32(tS + 32 * h, hi);
-                tc::wait_ld();
-                mask(hi, 32 * h);
-                top(hi);
+                for (int k = 0; k < 64; ++k)
+                    if (!((valid >> (k >> bs_log2)) & 1u)) v[k / 32][k % 32] = __float_as_uint(-INFINITY);
             }
-            mx *= c;
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 64; k += 8)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    top[u] = fmaxf(fmaxf(top[u], __uint_as_float(v[k / 32][k % 32 + u])),
+                                   __uint_as_float(v[k / 32][k % 32 + 4 + u]));
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
             if (i == 0) {
                 m = mx;
             } else {
@@ -291,64 +353,120 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
                 if (__any_sync(0xffffffffu, move)) {
                     const float f = move ? ex2(m - mx) : 1.0f;
                     if (move) l *= f, m = mx;
-                    wait(&pv_done[x], i - 1);
+                    wait(&pv_done[x][(i - 1) & 1], (i - 1) / 2);
                     tc::fence_after();
 #pragma unroll 1
-                    for (int d = 0; d < HD; d += 32) {
-                        tc::ld32(tO + d, hi);
+                    for (int d = 0; d < HD; d += 16) {
+                        uint32_t o[16];
+                        tc::ld16(tO + d, o);
                         tc::wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) hi[k] = __float_as_uint(__uint_as_float(hi[k]) * f);
-                        tc::st32(tO + d, hi);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tc::st16(tO + d, o);
                     }
                     tc::wait_st();
                 }
             }
-            const float base = m == -INFINITY ? 0.0f : m;
             // p = 2^(c s - m), summed in fp32, rounded once to T: a relative error of half a step of T
-            // per probability, which the product with V averages over the tokens
-            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            auto expo = [&](uint32_t(&v)[32], uint32_t* packed) {
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    const float p0 = ex2(fmaf(__uint_as_float(v[k]), c, -base));
-                    const float p1 = ex2(fmaf(__uint_as_float(v[k + 1]), c, -base));
-                    part[k & 2] += p0, part[(k & 2) + 1] += p1;
-                    packed[k / 2] = pack2<T>(p0, p1);
-                }
-            };
+            // per probability, which the product with V averages over the tokens. Pairs of fp32 go
+            // through the packed multiply-add and add.
+            const float base = m == -INFINITY ? 0.0f : m;
+            const uint64_t c2 = f32x2(c, c), b2 = f32x2(-base, -base);
+            uint64_t part[2] = {0, 0};  // (+0, +0)
             uint32_t pk[32];
-            expo(lo[0], pk), expo(lo[1], pk + 16);
-            tc::st32(tS, pk);  // over columns 0-31 of S, which this thread has read
-            tc::ld32(tS + 64, lo[0]);
-            tc::ld32(tS + 96, lo[1]);
-            tc::wait_ld();
-            mask(lo[0], 64), mask(lo[1], 96);
-            expo(lo[0], pk), expo(lo[1], pk + 16);
-            tc::st32(tS + 32, pk);
-            l += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+                float p0, p1;
+                split2(fma2(f32x2(__uint_as_float(v[k / 32][k % 32]), __uint_as_float(v[k / 32][k % 32 + 1])), c2, b2), p0, p1);
+                p0 = ex2(p0), p1 = ex2(p1);
+                part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], f32x2(p0, p1));
+                pk[k / 2] = pack2<T>(p0, p1);
+            }
+            if (i >= 2) {  // the product that read this buffer of P is done
+                wait(&pv_done[x][i & 1], i / 2 - 1);
+                tc::fence_after();
+            }
+            tc::st32(tP + (i & 1) * 32, pk);
+            float s0, s1, s2, s3;
+            split2(part[0], s0, s1);
+            split2(part[1], s2, s3);
+            l += (s0 + s1) + (s2 + s3);
             tc::wait_st();
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[x]);
+            if (lane == 0) mbar_arrive(&p_full[x][i & 1]);
         }
-        // this stream's record: maximum, sum, O (no tile: a maximum of -inf, and O is not read)
-        const int r = w.row0 + (w.pair ? x * kRows : 0) + quarter * 32 + lane;
-        const int64_t at = (static_cast<int64_t>(kvh) * a.rows + r) * a.records + w.rec + (w.pair ? 0 : x);
-        if (r < a.rows) a.part_ml[at] = make_float2(m, l);
+        // The record of this CTA's rows: maximum, sum, O; no tile, or no token that counts, leaves a maximum of
+        // -inf. The streams of a single block, two parts of the same rows, are merged first. O goes out by
+        // one bulk copy per row from shared memory (a thread's row, padded by 16 bytes: rows apart by a
+        // multiple of 128 bytes would meet in the same banks), over the tiles, which are done with.
+        // (Stored from the threads' registers, 16 bytes per row and instruction, it took 8 us of the call.)
+        constexpr int kRowBytes = HD * 4 + 16;
+        const int rr = quarter * 32 + lane;
+        unsigned char* mine = smem + (x * kRows + rr) * kRowBytes;
         if (n > 0) {
-            wait(&pv_done[x], n - 1);
+            wait(&pv_done[x][(n - 1) & 1], (n - 1) / 2);
             tc::fence_after();
+        }
+        asm volatile("bar.sync 2, 256;" ::: "memory");  // both streams' products are done: the tiles may go
+        float wa = 1.0f, wb = 0.0f;
+        const unsigned char* other = smem + (kRows + rr) * kRowBytes;
+        if (!w.pair) {
+            if (x == 1) s_ml[rr] = make_float2(m, l);
+        }
+        if (w.pair || x == 1) {
+            if (n > 0) {
 #pragma unroll 1
-            for (int d = 0; d < HD; d += 32) {
-                uint32_t v[32];
-                tc::ld32(tO + d, v);
-                tc::wait_ld();
-                if (r < a.rows) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + at * HD + d);
+                for (int d = 0; d < HD; d += 32) {
+                    uint32_t v[32];
+                    tc::ld32(tO + d, v);
+                    tc::wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(mine + (d + 4 * k) * 4) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
+            }
+        }
+        if (!w.pair) {
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            if (x == 0 && n > 0) {
+                const float2 o = s_ml[rr];
+                const bool some = n1 > 0 && !(o.x == -INFINITY && o.y == 0.0f);
+                const float M = some ? fmaxf(m, o.x) : m;
+                wa = m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(m - M);
+                wb = some ? (o.x == -INFINITY ? 1.0f : ex2(o.x - M)) : 0.0f;
+                l = wa * l + (some ? wb * o.y : 0.0f);
+                const bool keep = wa != 0.0f;  // a part without weight is not read: it may hold anything
+                m = M;
+#pragma unroll 1
+                for (int d = 0; d < HD; d += 32) {
+                    uint32_t v[32];
+                    tc::ld32(tO + d, v);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (some) q = *reinterpret_cast<const float4*>(other + (d + k) * 4);
+                        float f[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            f[u] = (keep ? wa * __uint_as_float(v[k + u]) : 0.0f) + (some ? wb * f[u] : 0.0f);
+                        *reinterpret_cast<float4*>(mine + (d + k) * 4) = make_float4(f[0], f[1], f[2], f[3]);
+                    }
+                }
+            }
+        }
+        const int r = w.row0 + (w.pair ? x * kRows : 0) + rr;
+        if ((w.pair || x == 0) && r < a.rows) {
+            const int64_t at = (static_cast<int64_t>(kvh) * a.records + w.rec) * a.rows + r;
+            a.part_ml[at] = make_float2(m, l);
+            if (n > 0) {
+                fence_proxy_async();
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a.part_o + at * HD),
+                             "r"(smem_u32(mine)), "r"(HD * 4)
+                             : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
             }
         }
     }
@@ -399,13 +517,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     len = len < 0 ? 0 : (len > a.cap ? a.cap : len);
     const int64_t row = b * a.group + g;
     const int tile = static_cast<int>(row / kRows);
-    int recs = tile < 2 * a.pair_blocks ? a.pair_splits : 2 * a.single_splits;
+    int recs = tile < 2 * a.pair_blocks ? a.pair_splits : a.single_splits;
     if (len < whole_pages(a) * a.block_size) recs = 0;
-    const int64_t first = (static_cast<int64_t>(kvh) * a.rows + row) * a.records;
+    const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows + row;  // record i: i * rows further
     const float* tail = a.tail + (b * a.n_kv + kvh) * a.tail_splits * (16 + 8 * HD);
     const int all = recs + a.tail_splits;
     auto stat = [&](int i) -> float2 {
-        if (i < recs) return a.part_ml[first + i];
+        if (i < recs) return a.part_ml[first + static_cast<int64_t>(i) * a.rows];
         const float* t = tail + (i - recs) * (16 + 8 * HD);
         return make_float2(t[g], t[8 + g]);
     };
@@ -427,7 +545,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
         if (ml.x == -INFINITY && ml.y == 0.0f) continue;
         const float e = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
         den = fmaf(e, ml.y, den);
-        const float* o = i < recs ? a.part_o + (first + i) * HD : tail + (i - recs) * (16 + 8 * HD) + 16 + g * HD;
+        const float* o = i < recs ? a.part_o + (first + static_cast<int64_t>(i) * a.rows) * HD : tail + (i - recs) * (16 + 8 * HD) + 16 + g * HD;
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = fmaf(e, o[lane + 32 * k], acc[k]);
     }

@@ -197,11 +197,10 @@ struct PrefixArgs {
     bool negate, q16;  // q16: 16-byte aligned query rows
     // work: rows = B * group query rows of a KV head in tiles of 128. Two tiles share a CTA's K / V
     // tiles (a pair block); an odd last tile is a block of its own whose CTAs work on two K / V tiles
-    // at a time. A block's K / V range is dealt to its splits, each split (each half of a single block's)
-    // leaves one record per row.
+    // at a time. A block's K / V range is dealt to its splits, each split leaves one record per row.
     int rows, pair_blocks, pair_splits, single_splits, ctas_per_kv, records;
-    float* part_o;   // [n_kv * rows][records][head_dim]
-    float2* part_ml;  // [n_kv * rows][records] maximum (base 2, scaled) and sum
+    float* part_o;   // [n_kv][records][rows][head_dim]
+    float2* part_ml;  // [n_kv][records][rows] maximum (base 2, scaled) and sum
     const float* tail;  // [B * n_kv][tail_splits][16 + 8 * head_dim]
     int tail_splits;
 };

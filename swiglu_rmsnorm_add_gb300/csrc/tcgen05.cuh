@@ -59,18 +59,9 @@ __device__ __forceinline__ uint64_t sdesc_sw128(const void* tile, int k_bytes) {
 }
 
 // The same tile as a B operand whose N runs along the rows' 64 elements and whose K runs over the
-// rows (MN-major): 64-element blocks of N lie `n_block_bytes` apart (leading-dimension offset), 8-row
-// groups of K 1024 bytes apart (stride-dimension offset); the k-th 16 rows start 2048 k bytes further.
-// The instruction descriptor says that B is transposed (kTransposeB).
-__device__ __forceinline__ uint64_t sdesc_sw128_mn(const void* tile, int n_block_bytes, int k16) {
-    const uint32_t a = smem_u32(tile) + static_cast<uint32_t>(k16) * 2048u;
-    uint64_t d = static_cast<uint64_t>((a >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((static_cast<uint32_t>(n_block_bytes) >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>((1024u >> 4) & 0x3FFFu) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
-}
+// rows (MN-major): the leading-dimension offset is the distance of 64-element blocks of N, the
+// stride-dimension offset (1024) that of 8-row groups of K; the k-th 16 rows start 2048 k bytes
+// further. The instruction descriptor says that B is transposed.
 constexpr uint32_t kTransposeB = 1u << 16;
 
 // Instruction descriptor of kind::f16: D fp32, A and B both bf16 (or both fp16),
@@ -99,14 +90,45 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
         : "memory");
 }
 
-// The same with A in tensor memory (16-bit elements, two per 32-bit column: K = 16 is 8 columns).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// The same two with the descriptors in halves, for a warp that runs its issue loop as a whole and lets one
+// lane (`elected` != 0, see elect()) issue: with no divergent branch around them the operands stay in
+// uniform registers. hi is constant for a layout, lo is the start address >> 4 plus the
+// leading-dimension offset << 16, so tiles and K steps are plain additions to lo.
+// The second form has A in tensor memory (16-bit elements, two per 32-bit column: K = 16 is 8 columns).
+constexpr uint32_t kSdescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 128-byte swizzle, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint32_t sdesc_lo(const void* tile, uint32_t lead_bytes) {
+    return (smem_u32(tile) >> 4) | ((lead_bytes >> 4) << 16);
+}
+__device__ __forceinline__ uint32_t elect() {  // one lane of a converged warp
+    uint32_t e;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t elected, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "mov.b64 da, {%2, %6};\n\t"
+        "mov.b64 db, {%3, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %4, p;\n\t}" ::"r"(elected),
+        "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kSdescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "mov.b64 db, {%3, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], db, %4, p;\n\t}" ::"r"(elected),
+        "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kSdescHi)
         : "memory");
 }
 
@@ -115,6 +137,15 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t elected, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(elected),
+        "r"(smem_u32(bar))
+        : "memory");
 }
 
 // ------------------------------------------------------------------ accumulator loads
@@ -143,6 +174,12 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
