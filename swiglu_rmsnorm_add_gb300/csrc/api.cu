@@ -1620,8 +1620,8 @@ int prefix_sizes(int64_t B, int n_head, int n_kv_head, int head_dim, int64_t pre
 struct PrefixPlan {
     bool use = false;
     int rows = 0, pair_blocks = 0, pair_splits = 0, single_splits = 0, ctas_per_kv = 0, records = 0, tail_splits = 0;
-    int64_t ml_bytes = 0, o_bytes = 0, tail_bytes = 0;
-    int64_t bytes() const { return ml_bytes + o_bytes + tail_bytes; }
+    int64_t ml_bytes = 0, o_bytes = 0, at_bytes = 0, tail_bytes = 0;
+    int64_t bytes() const { return ml_bytes + o_bytes + at_bytes + tail_bytes; }
 };
 PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t prefix_blocks, int64_t max_blocks,
                        int block_size, int dtype, int sms) {
@@ -1641,13 +1641,18 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
             std::min<int64_t>(std::max(1, per_kv - p.pair_blocks * p.pair_splits), ceil_div(tiles, 2)));
     p.ctas_per_kv = p.pair_blocks * p.pair_splits + p.single_splits;
     p.records = std::max(p.pair_splits, p.single_splits);
-    // the requests' own tokens
-    const int64_t groups = B * n_kv, own = std::max<int64_t>(0, max_blocks - prefix_blocks) * block_size;
-    p.tail_splits = 1;
-    while (p.tail_splits < 32 && groups * p.tail_splits * 2 <= sms && own >= 512 * p.tail_splits) p.tail_splits *= 2;
+    // the requests' own tokens: records for parts of 128 tokens of what their part of the table may hold, 16 at
+    // least (a part grows where a request has more)
+    const int64_t groups = B * n_kv, own = std::max<int64_t>(0, max_blocks - prefix_blocks + 1) * block_size;
+    p.tail_splits = static_cast<int>(std::min<int64_t>(std::max<int64_t>(16, ceil_div(own, 128) + 1), 256));
+    if (groups * p.tail_splits >= (int64_t(1) << 30)) {
+        p.use = false;
+        return p;
+    }
     const int64_t recs = n_kv * rows * p.records;
     p.ml_bytes = round_up256(recs * 8);
     p.o_bytes = round_up256(recs * head_dim * 4);
+    p.at_bytes = round_up256((B + 1) * 8);
     p.tail_bytes = round_up256(groups * p.tail_splits * (16 + 8 * static_cast<int64_t>(head_dim)) * 4);
     return p;
 }
@@ -1780,7 +1785,10 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     f.records = pp.records;
     f.part_ml = static_cast<float2*>(workspace);
     f.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp.ml_bytes);
-    float* tail = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp.ml_bytes + pp.o_bytes);
+    int64_t* tail_at = reinterpret_cast<int64_t*>(static_cast<char*>(workspace) + pp.ml_bytes + pp.o_bytes);
+    float* tail = reinterpret_cast<float*>(reinterpret_cast<char*>(tail_at) + pp.at_bytes);
+    f.tail_at = tail_at;
+    a.ws_tail_at = tail_at;
     f.tail = tail;
     f.tail_splits = pp.tail_splits;
     a.tail_only = true;
@@ -1788,7 +1796,14 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     a.gsplits = pp.tail_splits;
     int rs = status_from(launch_prefix_tc(f, kv_cache, head_dim, dtype, plan.pdl, s));
     if (rs != SRA_OK) return rs;
-    plan.pdl = true;  // the kernels of this call follow one another
+    // The tail has room for one CTA per SM beside the prefix's kernel, for three once that is done: three where
+    // its work is the longer one. Both from the table sizes, as tokens' cost: the prefix takes about 1.4 us per
+    // 64 tokens and 256 rows of an SM (batch 256 x 32768: 45 us), the tail, a CTA per SM, 1.2 us per tile of
+    // 16 tokens in each of four warps (requests half as long as their tables allow).
+    const double prefix_us = 1.4 * ceil_div(prefix_blocks * block_size, 64) * ceil_div(pp.rows, 256) * n_kv_head / sms;
+    const double tail_us = 1.2 / 4 / 16 * 0.5 * std::max<int64_t>(0, max_blocks_per_seq - prefix_blocks) * block_size *
+                           static_cast<double>(B * n_kv_head) / sms;
+    plan.tail_ctas = tail_us > prefix_us ? 3 : 1;
     rs = status_from(launch_prefix_tail(a, plan, dtype, s));
     return rs != SRA_OK ? rs : status_from(launch_prefix_merge(f, head_dim, dtype, s));
 }

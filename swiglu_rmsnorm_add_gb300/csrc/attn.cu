@@ -97,7 +97,7 @@ struct PrefixRange {
     int64_t P, lo;
 };
 __device__ __forceinline__ PrefixRange prefix_range(const AttnArgs& a, int64_t len) {
-    int64_t P = *a.plen;
+    int64_t P = __ldcg(a.plen);
     const int64_t cap = a.pblocks * a.block_size;
     P = P < 0 ? 0 : (P > cap ? cap : P);
     const int64_t whole = P / a.block_size * a.block_size;
@@ -111,9 +111,9 @@ __device__ __forceinline__ float quotient(float num, float den) {
 // One CTA of a call: a prefix length out of range and bad entries of the prefix's table, counted once.
 __device__ __forceinline__ void count_prefix_errors(const AttnArgs& a, int64_t P) {
     if (!a.err) return;
-    int n = threadIdx.x == 0 && *a.plen != P ? 1 : 0;
+    int n = threadIdx.x == 0 && __ldcg(a.plen) != P ? 1 : 0;
     for (int64_t j = threadIdx.x; j * a.block_size < P; j += blockDim.x) {
-        const int32_t e = a.ptable[j];
+        const int32_t e = __ldcg(a.ptable + j);
         n += e < 0 || e >= a.num_blocks ? 1 : 0;
     }
     if (n) atomicAdd(a.err, n);
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(At
     // first tiles need not wait for seq_len; tokens at or past seq_len are masked
     int64_t P = 0, lo = 0, hi = cap;
     if constexpr (PREFIX) {
-        hi = a.seq_lens[b];
+        hi = __ldcg(a.seq_lens + b);
         hi = hi < 0 ? 0 : (hi > cap ? cap : hi);
         const PrefixRange r = prefix_range(a, hi);
         P = r.P, lo = r.lo;
@@ -730,14 +730,15 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(At
     // read one tile ahead of its use, so the copy issue never waits on the table's latency.
     auto load_blk = [&](int64_t u) -> int32_t {
         const int64_t tok = t_begin + u * kMmaTile + lane;
-        if constexpr (PREFIX) return lane < kMmaTile && tok < t_lim ? (tok < P ? a.ptable : table)[tok >> bs_log2] : 0;
+        if constexpr (PREFIX)
+            return lane < kMmaTile && tok < t_lim ? __ldcg((tok < P ? a.ptable : table) + (tok >> bs_log2)) : 0;
         return lane < kMmaTile && tok < t_lim ? table[tok >> bs_log2] : 0;
     };
     // the first tiles' block ids and seq_len are requested together: one round trip, not two
     int32_t blk0[kMmaStages];
 #pragma unroll
     for (int k = 0; k < kMmaStages; ++k) blk0[k] = load_blk(warp + static_cast<int64_t>(k) * NW);
-    int64_t len = a.seq_lens[b];
+    int64_t len = PREFIX ? __ldcg(a.seq_lens + b) : a.seq_lens[b];
     if ((len < 0 || len > cap) && kvh == 0 && rank == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
     len = len < 0 ? 0 : (len > cap ? cap : len);
     const int64_t t_end = len < t_begin ? t_begin : (len < t_lim ? len : t_lim);
@@ -922,16 +923,420 @@ cudaError_t launch_merge(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     return launch_kernel(decode_merge_kernel<T, HD>, grid, dim3(256), 0, s, p.pdl, 1, a);
 }
 
+// ------------------------------------------------------------------------------------------
+// The requests' own tokens beside the kernel that takes their shared prefix (attn_prefix.cu).
+//
+// The tiles of 32 tokens of all (request, kv head) pairs, in that order, are one stream, which is cut into
+// equal parts, one per warp (requests differ in length: dealt as whole chunks, the slowest warp had 1.65
+// times the mean's work). Every CTA sums the requests' tiles to find its warps' parts. What a warp finds of a
+// pair is one record [8 max][8 sum][8 x HD]; the merge kernel finds them again from the sums, which CTA 0
+// leaves in the workspace.
+//
+// The kernel is launched while the prefix's runs (programmatic dependent launch) and does not wait for it;
+// only its last CTA does, at its end, so that whatever waits for this grid finds that one complete
+// too. What precedes the prefix's kernel is complete when this one starts (all CTAs of that one have waited
+// for it before they let this one start), and everything is read through the L2, which those grids'
+// writes have reached. Four warps with a tile each, at most 128 registers: a CTA fits beside one of the
+// prefix's on an SM, whose tensor cores and this one's memory traffic then overlap.
+// K's part of a warp's tile is copied again as soon as S is known, V's as soon as it has been used.
+// The products have the tokens (S) or the dims (O) as the rows of the MMA and the up to eight query heads
+// as its eight columns, so no row is empty: S^T = K Q^T and O^T = V^T P^T, 24 MMAs per tile at head_dim
+// 128 where the heads as rows take 48.
+constexpr int kTailWarps = 4;
+template <typename T>
+struct MmaFull;
+template <>
+struct MmaFull<__nv_bfloat16> {
+    __device__ __forceinline__ static void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+template <>
+struct MmaFull<__half> {
+    __device__ __forceinline__ static void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+// An 8 x 8 matrix of 16-bit values, a row's pairs over four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// S^T of 32 tokens and 8 heads: lane (fg, ft) gets tokens fg + 8 k (k < 4) of heads 2 ft + {0, 1} in
+// s[k / 2][2 (k & 1) + head]. qb: Q as B fragments. ks: shared-memory address of the K tile, rows of HD
+// elements, 16-byte chunks XOR-swizzled by row.
+template <typename T, int HD>
+__device__ __forceinline__ void tail_scores(uint32_t ks, const uint32_t (&qb)[HD / 16][2], float (&s)[2][4], int lane) {
+    const int mi = lane >> 3, rr = lane & 7;
+    // K as A: matrices (rows 0-7, dims 0-7), (rows 8-15, dims 0-7), (rows 0-7, dims 8-15), (rows 8-15, dims 8-15)
+    const uint32_t krow = ks + (8 * (mi & 1) + rr) * HD * 2;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < HD / 16; ++e)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t ka[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(ka[0]), "=r"(ka[1]), "=r"(ka[2]), "=r"(ka[3])
+                         : "r"(krow + u * 16 * HD * 2 + (((2 * e + (mi >> 1)) ^ rr) << 4)));
+            MmaFull<T>::run(s[u], ka, qb[e][0], qb[e][1]);
+        }
+}
+// The running softmax over those scores (valid: a bit per token): maxima m of the lane's two heads, this
+// lane's tokens' part l of their sums, corr = 2^(old m - new m); the probabilities as B fragments of the
+// next product, a T-rounded part and its T-rounded residual (about 16 significant bits).
+template <typename T>
+__device__ __forceinline__ void tail_softmax(const float (&s)[2][4], unsigned valid, float (&m)[2], float (&l)[2],
+                                             float (&corr)[2], uint32_t (&hi)[2][2], uint32_t (&lo)[2][2],
+                                             float scale_log2, int lane) {
+    const unsigned FULL = 0xffffffffu;
+    const int fg = lane >> 2;
+    float p[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            p[u][k] = (valid >> (16 * u + 8 * (k >> 1) + fg)) & 1u ? s[u][k] * scale_log2 : -INFINITY;
+    float mx[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) mx[h] = fmaxf(fmaxf(p[0][h], p[0][h + 2]), fmaxf(p[1][h], p[1][h + 2]));
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+        const float a = __shfl_xor_sync(FULL, mx[0], x), b = __shfl_xor_sync(FULL, mx[1], x);
+        mx[0] = fmaxf(mx[0], a), mx[1] = fmaxf(mx[1], b);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float now = fmaxf(m[h], mx[h]);
+        corr[h] = now == -INFINITY ? 1.0f : ex2(m[h] - now);
+        m[h] = now;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[u][k] = p[u][k] == -INFINITY ? 0.0f : ex2(p[u][k] - m[k & 1]);
+        const uint32_t h0 = pack2<T>(p[u][0], p[u][1]), h1 = pack2<T>(p[u][2], p[u][3]);
+        const float2 f0 = unpack2<T>(h0), f1 = unpack2<T>(h1);
+        hi[u][0] = transpose8(h0), hi[u][1] = transpose8(h1);
+        lo[u][0] = transpose8(pack2<T>(p[u][0] - f0.x, p[u][1] - f0.y));
+        lo[u][1] = transpose8(pack2<T>(p[u][2] - f1.x, p[u][3] - f1.y));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) l[h] = fmaf(l[h], corr[h], (p[0][h] + p[0][h + 2]) + (p[1][h] + p[1][h + 2]));
+}
+// O^T = O^T corr + V^T P^T: o[d] holds dims 16 d + fg + {0, 8} of heads 2 ft + {0, 1} (an MMA accumulator).
+template <typename T, int HD>
+__device__ __forceinline__ void tail_values(uint32_t vs, const uint32_t (&hi)[2][2], const uint32_t (&lo)[2][2],
+                                            const float (&corr)[2], float (&o)[HD / 16][4], int lane) {
+    const int mi = lane >> 3, rr = lane & 7;
+    if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) o[d][0] *= corr[0], o[d][1] *= corr[1], o[d][2] *= corr[0], o[d][3] *= corr[1];
+    }
+    // V^T as A: matrices (dims 0-7, tokens 0-7), (dims 8-15, tokens 0-7), (dims 0-7, tokens 8-15), (dims 8-15, tokens 8-15),
+    // each the transpose of a block of V's rows
+    const uint32_t vrow = vs + (8 * (mi >> 1) + rr) * HD * 2;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) {
+            uint32_t va[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(va[0]), "=r"(va[1]), "=r"(va[2]), "=r"(va[3])
+                         : "r"(vrow + u * 16 * HD * 2 + (((2 * d + (mi & 1)) ^ rr) << 4)));
+            MmaFull<T>::run(o[d], va, hi[u][0], hi[u][1]);
+            MmaFull<T>::run(o[d], va, lo[u][0], lo[u][1]);
+        }
+}
+constexpr int kTailThreads = kTailWarps * 32;
+__host__ __device__ constexpr size_t tail_smem(int HD) {
+    return static_cast<size_t>(kTailWarps) * 2 * kTailTok * HD * 2;
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
+    constexpr int CPR = HD * 2 / 16, KS = HD / 16, TE = kTailTok * HD;
+    constexpr int RPI = 32 / CPR;  // rows per copy instruction (CPR lanes per row)
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ int64_t sums[kTailThreads + 1];
+    __shared__ int s_long;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int fg = lane >> 2, ft = lane & 3;
+    const int G = a.group, BS = a.block_size, bs_log2 = __ffs(BS) - 1, B = static_cast<int>(a.B);
+    const T* cache = static_cast<const T*>(a.cache);
+    const int64_t tok_stride = static_cast<int64_t>(a.n_kv) * HD, v_plane = a.num_blocks * BS * tok_stride;
+    const int64_t cap = a.max_blocks * BS;
+    const int P = static_cast<int>(prefix_range(a, 0).P);
+    if (blockIdx.x == 0) count_prefix_errors(a, P);
+    // request b's own part [lo, len)
+    auto range = [&](int b, int* lo, int* len) {
+        int64_t n = b < B ? __ldcg(a.seq_lens + b) : 0;
+        n = n < 0 ? 0 : (n > cap ? cap : n);
+        *lo = static_cast<int>(prefix_range(a, n).lo);
+        *len = static_cast<int>(n);
+    };
+    auto tiles_of = [&](int lo, int len) { return (len - lo + kTailTok - 1) / kTailTok; };
+
+    // Thread t sums requests [t * per, (t + 1) * per): sums[t] = tiles (of one kv head) before them.
+    const int per = (B + kTailThreads - 1) / kTailThreads;
+    int64_t mine = 0;
+    int longest = 0;
+    if (threadIdx.x == 0) s_long = 0;
+    for (int k = 0; k < per; ++k) {
+        const int b = threadIdx.x * per + k;
+        int lo, len;
+        range(b, &lo, &len);
+        const int n = tiles_of(lo, len);
+        mine += n;
+        longest = max(longest, n);
+        if (blockIdx.x == 0 && b < B && a.err) {
+            const int64_t given = __ldcg(a.seq_lens + b);
+            if (given < 0 || given > cap) atomicAdd(a.err, 1);
+        }
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t t = __shfl_up_sync(FULL, inc, x);
+        if (lane >= x) inc += t;
+    }
+    __shared__ int64_t warp_sum[kTailWarps];
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    atomicMax(&s_long, longest);
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kTailWarps; ++w) {
+        before += w < warp ? warp_sum[w] : 0;
+        total += warp_sum[w];
+    }
+    sums[threadIdx.x] = before + inc - mine;
+    if (threadIdx.x == 0) sums[kTailThreads] = total;
+    __syncthreads();
+    const int workers = static_cast<int>(gridDim.x) * kTailWarps;
+    const TailPlan plan = tail_plan(total * a.n_kv, s_long, workers, a.gsplits);
+    if (blockIdx.x == 0) {
+        // for the merge: the tiles before every request, and a part's size
+        int64_t at = sums[threadIdx.x];
+        for (int k = 0; k < per; ++k) {
+            const int b = threadIdx.x * per + k;
+            int lo, len;
+            range(b, &lo, &len);
+            if (b < B) a.ws_tail_at[b] = at;
+            at += tiles_of(lo, len);
+        }
+        if (threadIdx.x == 0) a.ws_tail_at[B] = plan.part;
+    }
+
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * kTailWarps + warp;
+    const int64_t g0 = me * plan.part, all = total * a.n_kv;
+    int64_t todo = g0 < all ? (all - g0 < plan.part ? all - g0 : plan.part) : 0;  // tiles not looked at yet
+    if (todo > 0) {
+        // The request that tile g0 belongs to: the thread that summed it, then along its requests, 32 at a time.
+        // Lane k of the group holds request base + k.
+        int owner = 0;
+        for (int t = lane; t < kTailThreads; t += 32) {
+            const bool here = sums[t] * a.n_kv <= g0 && sums[t + 1] * a.n_kv > g0;
+            const unsigned hit = __ballot_sync(FULL, here);
+            if (hit) owner = t - lane + __ffs(hit) - 1;
+        }
+        int base = owner * per, lo, len, b = 0, kvh = 0, n = 0, t = 0;
+        int64_t at_pair = sums[owner] * a.n_kv;  // tiles before request base's
+        for (;;) {
+            range(base + lane, &lo, &len);
+            const int64_t w = static_cast<int64_t>(tiles_of(lo, len)) * a.n_kv;
+            int64_t upto = w;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const int64_t y = __shfl_up_sync(FULL, upto, x);
+                if (lane >= x) upto += y;
+            }
+            const unsigned hit = __ballot_sync(FULL, at_pair + upto > g0);
+            if (hit) {
+                const int k = __ffs(hit) - 1;
+                b = base + k;
+                n = tiles_of(__shfl_sync(FULL, lo, k), __shfl_sync(FULL, len, k));
+                const int64_t in = g0 - at_pair - __shfl_sync(FULL, upto - w, k);
+                kvh = static_cast<int>(in / n);
+                t = static_cast<int>(in - static_cast<int64_t>(kvh) * n);
+                at_pair = g0 - t;  // the pair's first tile in the stream
+                break;
+            }
+            at_pair += __shfl_sync(FULL, upto, 31);
+            base += 32;
+        }
+        int rec = static_cast<int>(me - at_pair / plan.part);  // parts of the pair before this one
+        // The tile looked at: its pair (b, kvh), first token, end of the pair, page entries asked for
+        int at = 0, end = 0;
+        int32_t blk = 0;
+        bool have = false;
+        auto ask = [&]() {
+            const int k = b - base;
+            at = __shfl_sync(FULL, lo, k) + t * kTailTok;
+            end = __shfl_sync(FULL, len, k);
+            blk = lane < end - at ? __ldcg((at + lane < P ? a.ptable : a.table + static_cast<int64_t>(b) * a.max_blocks) +
+                                           ((at + lane) >> bs_log2))
+                                  : 0;
+            have = true;
+            --todo;
+        };
+        auto look = [&]() {  // to the next tile
+            have = false;
+            if (todo == 0) return;
+            if (++t == n) {
+                t = 0, rec = 0;
+                if (++kvh == a.n_kv) {
+                    kvh = 0;
+                    do {  // the next request that has tiles (there is one: todo > 0)
+                        if (++b == base + 32) {
+                            base = b;
+                            range(base + lane, &lo, &len);
+                        }
+                        n = tiles_of(__shfl_sync(FULL, lo, b - base), __shfl_sync(FULL, len, b - base));
+                    } while (n == 0);
+                }
+            }
+            ask();
+        };
+        const uint32_t ks = smem_u32(smem) + warp * 2 * TE * 2, vs = ks + TE * 2;
+        const int col = lane % CPR, rr0 = lane / CPR;
+        // Copies a plane (0 K, 1 V) of the tile looked at. A group of eight rows lies in one page, unless the
+        // prefix ends inside it; rows that do not count are zero-filled, not read.
+        unsigned valid = 0;
+        auto copy = [&](uint32_t dst, int plane) {
+            const T* from = cache + (plane ? v_plane : 0) + kvh * HD + col * 8;
+            const bool by_row = at < P && P - at < kTailTok;
+#pragma unroll
+            for (int g = 0; g < kTailTok / 8; ++g) {
+                if (!by_row) {
+                    const int64_t row = (static_cast<int64_t>(__shfl_sync(FULL, blk, 8 * g)) << bs_log2) + ((at + 8 * g) & (BS - 1));
+                    const T* src = from + (row + rr0) * tok_stride;
+#pragma unroll
+                    for (int i = 0; i < 8 / RPI; ++i) {
+                        const int r = 8 * g + rr0 + RPI * i;
+                        const bool v = (valid >> r) & 1u;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         dst + r * HD * 2 + ((col ^ (r & 7)) << 4)),
+                                     "l"(v ? src + i * RPI * tok_stride : cache), "r"(v ? 16 : 0)
+                                     : "memory");
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < 8 / RPI; ++i) {
+                        const int r = 8 * g + rr0 + RPI * i;
+                        const int64_t row = (static_cast<int64_t>(__shfl_sync(FULL, blk, r)) << bs_log2) + ((at + r) & (BS - 1));
+                        const bool v = (valid >> r) & 1u;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         dst + r * HD * 2 + ((col ^ (r & 7)) << 4)),
+                                     "l"(v ? from + row * tok_stride : cache), "r"(v ? 16 : 0)
+                                     : "memory");
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+        auto check = [&]() {  // which of its tokens count; a bad entry of the request's own is counted once
+            bool ok = false;
+            if (lane < end - at) {
+                const int tok = at + lane;
+                if (blk >= 0 && blk < a.num_blocks)
+                    ok = true;
+                else if (kvh == 0 && ((tok & (BS - 1)) == 0 || tok == P) && tok >= P && a.err)
+                    atomicAdd(a.err, 1);
+            }
+            valid = __ballot_sync(FULL, ok);
+        };
+        ask();
+        check();
+        copy(ks, 0);
+        copy(vs, 1);
+        uint32_t qb[KS][2];
+        float o[KS][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        auto load_q = [&]() {  // of the pair at hand, column fg = query head fg (zero past G); an empty record
+            const T* qrow = static_cast<const T*>(a.q) + static_cast<int64_t>(b) * a.qs + (kvh * G + fg) * HD;
+#pragma unroll
+            for (int e = 0; e < KS; ++e) {
+                qb[e][0] = fg < G ? __ldcg(reinterpret_cast<const uint32_t*>(qrow + 16 * e + 2 * ft)) : 0u;
+                qb[e][1] = fg < G ? __ldcg(reinterpret_cast<const uint32_t*>(qrow + 16 * e + 8 + 2 * ft)) : 0u;
+                o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
+            }
+            m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.0f;
+        };
+        load_q();
+        while (have) {
+            // the tile in shared memory: its mask and record; then the next one is looked at
+            const unsigned mask = valid;
+            float* out = a.ws_part + ((static_cast<int64_t>(b) * a.n_kv + kvh) * a.gsplits + rec) * (16 + 8 * HD);
+            const bool last_of_pair = t + 1 == n;
+            look();
+            const bool last = last_of_pair || !have;
+            cp_async_wait<1>();  // K has landed
+            __syncwarp();
+            float sc[2][4], corr[2];
+            tail_scores<T, HD>(ks, qb, sc, lane);
+            __syncwarp();  // every lane is done with K
+            if (have) {
+                check();
+                copy(ks, 0);
+            } else {
+                cp_async_commit();
+            }
+            uint32_t hi[2][2], rest[2][2];
+            tail_softmax<T>(sc, mask, m, l, corr, hi, rest, a.scale_log2, lane);
+            cp_async_wait<1>();  // V has landed (the next K is behind it)
+            __syncwarp();
+            tail_values<T, HD>(vs, hi, rest, corr, o, lane);
+            __syncwarp();  // every lane is done with V
+            if (have) copy(vs, 1);
+            if (last) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    l[0] += __shfl_xor_sync(FULL, l[0], x);
+                    l[1] += __shfl_xor_sync(FULL, l[1], x);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (2 * ft + h >= G) continue;
+                    if (fg == 0) out[2 * ft + h] = m[h], out[8 + 2 * ft + h] = l[h];
+                    float* out_row = out + 16 + (2 * ft + h) * HD + fg;  // eight lanes store 32 bytes in a row
+#pragma unroll
+                    for (int d = 0; d < KS; ++d) out_row[16 * d] = o[d][h], out_row[16 * d + 8] = o[d][2 + h];
+                }
+                if (have) load_q();
+            }
+        }
+        cp_async_wait<0>();
+    }
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename T, int HD>
+cudaError_t launch_tail(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+    auto kernel = tail_kernel<T, HD>;
+    constexpr size_t smem = tail_smem(HD);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    const int64_t need = (a.B * a.n_kv * a.gsplits + kTailWarps - 1) / kTailWarps;
+    const int64_t most = p.tail_ctas * static_cast<int64_t>(p.num_sms);
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(kTailThreads), smem, s, true,
+                         1, a);
+}
+
 template <typename T, int HD, int NW, bool PREFIX = false>
 cudaError_t launch_mma(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     const size_t smem = mma_smem(HD, NW);
-    if (PREFIX && a.ws_part) {
-        auto kp = decode_mma_kernel<T, HD, true, NW, true>;
-        const cudaError_t ep =
-            cudaFuncSetAttribute(kp, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (ep != cudaSuccess) return ep;
-        return launch_kernel(kp, dim3(static_cast<unsigned>(a.B * a.n_kv * a.gsplits)), dim3(NW * 32), smem, s, p.pdl, 1, a);
-    }
     if (!PREFIX && a.gsplits > 0) {
         auto kg = decode_mma_kernel<T, HD, true, NW, false>;
         const cudaError_t eg =
@@ -1238,6 +1643,8 @@ cudaError_t launch_stages(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) 
 template <typename T>
 cudaError_t launch_prefix_typed(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     if constexpr (sizeof(T) == 2) {
+        if (p.tensor_cores && a.tail_only)
+            return p.head_dim == 64 ? launch_tail<T, 64>(a, p, s) : launch_tail<T, 128>(a, p, s);
         if (p.tensor_cores)
             return p.head_dim == 64 ? launch_mma<T, 64, 8, true>(a, p, s) : launch_mma<T, 128, 8, true>(a, p, s);
     }

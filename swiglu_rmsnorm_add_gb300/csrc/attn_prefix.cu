@@ -30,7 +30,8 @@ struct Smem {
     static constexpr int kHalfBytes = kTok * 128;              // 64 dims of a K or V tile's rows
     static constexpr int kTileBytes = kHalves * kHalfBytes;    // a K or V tile
     static constexpr int kQHalf = kRows * 128, kQBytes = kHalves * kQHalf;
-    static constexpr int kStages = 10;                         // K or V tiles in flight
+    // K or V tiles in flight; what is left of an SM's shared memory takes a CTA of the tail kernel (attn.cu)
+    static constexpr int kStages = HD == 128 ? 5 : 10;
     static constexpr size_t kTotal = 1024 + 2 * static_cast<size_t>(kQBytes) + kStages * static_cast<size_t>(kTileBytes);
 };
 
@@ -93,11 +94,18 @@ __device__ __forceinline__ int64_t whole_pages(const PrefixArgs& a) {
     return (P < 0 ? 0 : (P > cap ? cap : P)) / a.block_size;
 }
 
-// The order in which K and V tiles go through the ring (both sides follow it). A round is the tile of
-// a pair, or the two tiles that a single block's streams take at a time (w = 1 or 2 tiles); the ring
-// carries K of round 0, then K of round r + 1 and V of round r for r = 0, 1, ...
-__device__ __forceinline__ int ring_k(int w, int t) { return t + (t >= w ? (t / w - 1) * w : 0); }
-__device__ __forceinline__ int ring_v(int w, int n, int t) { return min(n, (t / w + 2) * w) + t; }
+// A place in the ring of tiles: its stage, and the parity of the phase in which that is filled.
+// Both sides walk the ring in one order. A round is the tile of a pair, or the two tiles that a single
+// block's streams take at a time; the ring carries K of round 0, then K of round r + 1 and V of round r
+// for r = 0, 1, ...
+template <int ST>
+struct Place {
+    int stage = 0, phase = 0;
+    __device__ __forceinline__ void next(int k = 1) {
+        stage += k;
+        if (stage >= ST) stage -= ST, phase ^= 1;
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -117,7 +125,7 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 // The price is that S in tiles of 64 tokens reads Q from shared memory twice as often: 48 clocks per
 // K step of 16 instead of 2 x 32, shared-memory bandwidth, so a tile cannot run above 81 % of the peak.)
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC) {
+__global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC) {
     using L = Smem<HD>;
     constexpr int ST = L::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -132,7 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
     __shared__ float2 s_ml[kRows];  // a single block's stream 1: maxima and sums
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        // a pair's streams both release a tile
+        const bool pair = static_cast<int>(blockIdx.x) % a.ctas_per_kv < a.pair_blocks * a.pair_splits;
+        for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], pair ? 2 : 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1), mbar_init(&s_free[x], 4);
             for (int b = 0; b < 2; ++b) mbar_init(&p_full[x][b], 4), mbar_init(&pv_done[x][b], 1);
@@ -140,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
         mbar_init_fence();
         s_ragged = 0;
     }
-    if (warp == 1) {
+    if (warp == 0) {
         tc::alloc(&tmem_base, kTmemCols);
         tc::relinquish();
     }
@@ -151,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
     pdl_enter();
     const int kvh = blockIdx.x / a.ctas_per_kv;
     const int64_t pages = whole_pages(a);
-    const int ppt = kTok / a.block_size;  // pages of a tile
+    const int ppt = kTok >> (__ffs(a.block_size) - 1);  // pages of a tile
     const Work w = work_of(a, blockIdx.x - kvh * a.ctas_per_kv, (pages + ppt - 1) / ppt);
     const int tpr = w.pair ? 1 : 2;  // tiles per round
     const int n0 = w.pair ? w.n : (w.n + 1) / 2, n1 = w.pair ? w.n : w.n / 2;  // tiles of the streams
@@ -160,35 +170,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
         if (!dead) dead = !mbar_wait(bar, static_cast<uint32_t>(phase & 1));
     };
 
-    if (warp == 0) {
-        // producer: a tile is a box of 64 dims x block_size tokens per page and half. A page past the
-        // prefix, or an entry that is no page, is copied from past the cache's end: zeros.
-        // The page entries are read 32 at a time (lane k: entry k of the group), a group ahead of their
-        // use and apart for K and V, so no copy waits for the table.
-        const int boxes = ppt * L::kHalves;
-        const int half = lane / ppt, p = lane - half * ppt;
-        int s = 0, group[2] = {-1, -1};
+    if (warp == 0 || warp == 3) {
+        // producers: a tile is a box of 64 dims x block_size tokens per page and half, dealt to two warps
+        // (a warp issues a box in about 80 clocks). A page past the prefix, or an entry that is no page, is
+        // copied from past the cache's end: zeros. The page entries are read 32 at a time (lane k: entry k
+        // of the group), a group ahead of their use and apart for K and V, so no copy waits for the table.
+        const int ppt_log2 = __ffs(ppt) - 1, boxes = ppt * L::kHalves;
+        const int box = lane * 2 + (warp == 0 ? 0 : 1), half = box >> ppt_log2, p = box & (ppt - 1);
+        unsigned char* dst = ring + half * L::kHalfBytes + p * a.block_size * 128;
+        Place<ST> at;
+        int filled = 0, group[2] = {-1, -1};
         int32_t cur[2] = {-1, -1}, next[2] = {-1, -1};
         auto entries = [&](int g) -> int32_t {
             const int64_t j = static_cast<int64_t>(w.t0) * ppt + static_cast<int64_t>(g) * 32 + lane;
             return j < pages ? a.ptable[j] : -1;
         };
         auto load = [&](int t, int plane, int32_t& c, int32_t& nx, int& g) {
-            const int stage = s % ST, first = t * ppt;
-            if (first / 32 != g) {
+            const int first = t << ppt_log2;
+            if (first >> 5 != g) {
                 c = g < 0 ? entries(0) : nx;
                 ++g;
                 nx = entries(g + 1);
             }
             int64_t blk = __shfl_sync(0xffffffffu, c, (first + p) & 31);
             if (blk < 0 || blk >= a.num_blocks) blk = a.num_blocks;
-            if (s >= ST) wait(&empty[stage], s / ST - 1);
-            if (lane == 0) mbar_arrive_expect_tx(&full[stage], L::kTileBytes);
+            if (filled == ST) wait(&empty[at.stage], at.phase ^ 1);
+            if (filled < ST) ++filled;
+            if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&full[at.stage], L::kTileBytes);
+            if (box < boxes)
+                tma_load_4d(dst + at.stage * L::kTileBytes, &tmC, half * 64, kvh, static_cast<int>(blk * a.block_size),
+                            plane, &full[at.stage]);
             __syncwarp();
-            if (lane < boxes)
-                tma_load_4d(ring + stage * L::kTileBytes + half * L::kHalfBytes + p * a.block_size * 128, &tmC,
-                            half * 64, kvh, static_cast<int>(blk * a.block_size), plane, &full[stage]);
-            ++s;
+            at.next();
         };
         auto load_k = [&](int t) { load(t, 0, cur[0], next[0], group[0]); };
         auto load_v = [&](int t) { load(t, 1, cur[1], next[1], group[1]); };
@@ -200,31 +213,40 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
     } else {
         // the query rows, swizzled as a TMA copy would leave them (rows past the last are zero), and
         // whether every page of this CTA's tiles counts
-        constexpr int kSetup = kThreads - 32, kChunks = HD / 8;
+        constexpr int kSetup = kThreads - 64, kChunks = HD / 8;
         constexpr int kEach = (2 * kRows * kChunks + kSetup - 1) / kSetup;  // 16-byte chunks a thread moves
-        const int tid = threadIdx.x - 32, count = w.n > 0 ? (w.pair ? 2 : 1) * kRows * kChunks : 0;
+        const int tid = threadIdx.x - (warp < 3 ? 32 : 64), count = w.n > 0 ? (w.pair ? 2 : 1) * kRows * kChunks : 0;
         uint4 v[kEach];
-        auto source = [&](int i) -> const T* {  // chunk i's elements, or null past the last row
-            const int r = i / kChunks, row = w.row0 + r;
-            if (i >= count || row >= a.rows) return nullptr;
-            const int b = row / a.group, g = row - b * a.group;
-            return static_cast<const T*>(a.q) + b * a.qs + (kvh * a.group + g) * HD + (i % kChunks) * 8;
+        // a thread's chunks share their place in the row and lie kStep rows apart: one division, then steps
+        constexpr int kStep = kSetup / kChunks;
+        static_assert(kSetup % kChunks == 0, "a thread's chunks share a column");
+        const int c = tid % kChunks, r0 = tid / kChunks, dg = kStep % a.group;
+        int g = (w.row0 + r0) % a.group;
+        const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>((w.row0 + r0) / a.group) * a.qs +
+                       (kvh * a.group + g) * HD + c * 8;
+        const int64_t step = static_cast<int64_t>(kStep / a.group) * a.qs + dg * HD, wrap = a.qs - a.group * HD;
+        const int rows = count / kChunks < a.rows - w.row0 ? count / kChunks : a.rows - w.row0;
+        auto advance = [&]() {
+            src += step;
+            if ((g += dg) >= a.group) g -= a.group, src += wrap;
         };
         if (a.q16) {
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {  // all loads in flight before the first store
-                const T* src = source(tid + e * kSetup);
-                v[e] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+                v[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (r0 + e * kStep < rows) v[e] = *reinterpret_cast<const uint4*>(src);
+                advance();
             }
         } else {
 #pragma unroll 1
             for (int e = 0; e < kEach; ++e) {
-                const unsigned short* h = reinterpret_cast<const unsigned short*>(source(tid + e * kSetup));
                 uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (h) {
+                if (r0 + e * kStep < rows) {
+                    const unsigned short* h = reinterpret_cast<const unsigned short*>(src);
                     u.x = h[0] | static_cast<uint32_t>(h[1]) << 16, u.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
                     u.z = h[4] | static_cast<uint32_t>(h[5]) << 16, u.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
                 }
+                advance();
 #pragma unroll
                 for (int k = 0; k < kEach; ++k)
                     if (k == e) v[k] = u;
@@ -240,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
         const uint32_t flip = a.negate ? 0x80008000u : 0u;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            const int i = tid + e * kSetup, r = i / kChunks, c = i % kChunks, rr = r % kRows;
-            if (i < count)
+            const int r = r0 + e * kStep, rr = r % kRows;
+            if (r < count / kChunks)
                 *reinterpret_cast<uint4*>(qs + (r / kRows) * L::kQBytes + (c / 8) * L::kQHalf + rr * 128 +
                                           (((c & 7) ^ (rr & 7)) * 16)) =
                     make_uint4(v[e].x ^ flip, v[e].y ^ flip, v[e].z ^ flip, v[e].w ^ flip);
@@ -250,60 +272,56 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
         asm volatile("bar.sync 1, %0;" ::"r"(kSetup) : "memory");
     }
 
-    if (warp == 1) {
-        // MMA issuer: the whole warp runs the loop, one lane issues. (Issued from a branch of one lane, whose
-        // descriptors the compiler must move to uniform registers one by one, an instruction took 75
-        // clocks, more than the product itself.)
+    if (warp == 1 || warp == 2) {
+        // MMA issuers, one warp per stream: the whole warp runs the loop, one lane issues. (Issued from a branch
+        // of one lane, whose descriptors the compiler must move to uniform registers one by one, an
+        // instruction took 75 clocks, more than the product itself. A wait or a commit costs about
+        // 120 clocks, so one warp for both streams was busy for 2300 clocks per tile of both, against
+        // 1290 of tensor-core work.)
+        const int x = warp - 1, n = x == 0 ? n0 : n1;
         constexpr uint32_t kIdescS = tc::idesc_f16(kBf16, kRows, kTok);
         constexpr uint32_t kIdescO = tc::idesc_f16(kBf16, kRows, HD) | tc::kTransposeB;
         const uint32_t elected = tc::elect();
-        const uint32_t q_lo = tc::sdesc_lo(qs, 16), k_lo = tc::sdesc_lo(ring, 16), v_lo = tc::sdesc_lo(ring, L::kHalfBytes);
-        auto ready = [&](int s) {
-            wait(&full[s % ST], s / ST);
+        const uint32_t q = tc::sdesc_lo(qs, 16) + (w.pair ? x : 0) * (L::kQBytes / 16);
+        const uint32_t k_lo = tc::sdesc_lo(ring, 16), v_lo = tc::sdesc_lo(ring, L::kHalfBytes);
+        const uint32_t tS = tmem + kS + x * kTok, tP = tmem + kP + x * 64, tO = tmem + kO + x * HD;
+        Place<ST> at;  // of the round's tiles; a single block's stream 1 takes the second of them
+        auto take = [&]() -> int {
+            Place<ST> mine = at;
+            if (!w.pair && x == 1) mine.next();
+            wait(&full[mine.stage], mine.phase);
             tc::fence_after();
+            return mine.stage;
         };
-        auto tile = [&](int x, int i) { return w.pair ? i : 2 * i + x; };
-        // a pair's streams share the ring's entries: stream 0 waits for them, stream 1 releases them
-        auto qk = [&](int x, int i) {
-            const int s = ring_k(tpr, tile(x, i)), stage = s % ST;
-            if (!w.pair || x == 0) ready(s);
-            const uint32_t k = k_lo + stage * (L::kTileBytes / 16), q = q_lo + (w.pair ? x : 0) * (L::kQBytes / 16);
+        auto tiles_of = [&](int r) { return min(tpr, w.n - r * tpr); };
+        auto qk = [&](int i) {
+            const int stage = take();
+            const uint32_t k = k_lo + stage * (L::kTileBytes / 16);
 #pragma unroll
             for (int e = 0; e < HD / 16; ++e)
-                tc::mma_f16_ss(elected, tmem + kS + x * kTok, q + (e / 4) * (L::kQHalf / 16) + (e % 4) * 2,
+                tc::mma_f16_ss(elected, tS, q + (e / 4) * (L::kQHalf / 16) + (e % 4) * 2,
                                k + (e / 4) * (L::kHalfBytes / 16) + (e % 4) * 2, kIdescS, e > 0);
             tc::commit(elected, &s_full[x]);
-            if (!w.pair || x == 1) tc::commit(elected, &empty[stage]);
+            tc::commit(elected, &empty[stage]);
+            at.next(tiles_of(i));
         };
-        auto pv = [&](int x, int i) {
-            const int s = ring_v(tpr, w.n, tile(x, i)), stage = s % ST;
-            if (!w.pair || x == 0) ready(s);
-            const uint32_t v = v_lo + stage * (L::kTileBytes / 16);
+        if (n > 0) qk(0);
+        for (int i = 0; i < n; ++i) {
+            if (i + 1 < n) {
+                wait(&s_free[x], i);
+                qk(i + 1);
+            } else if (i + 1 < n0) {
+                at.next(tiles_of(i + 1));  // the other stream's last tile
+            }
+            wait(&p_full[x][i & 1], i >> 1);
+            const int stage = take();
+            const uint32_t v = v_lo + stage * (L::kTileBytes / 16), p = tP + (i & 1) * 32;
 #pragma unroll
             for (int e = 0; e < kTok / 16; ++e)
-                tc::mma_f16_ts(elected, tmem + kO + x * HD, tmem + kP + x * 64 + (i & 1) * 32 + 8 * e, v + e * 128,
-                               kIdescO, i > 0 || e > 0);
+                tc::mma_f16_ts(elected, tO, p + 8 * e, v + e * 128, kIdescO, i > 0 || e > 0);
             tc::commit(elected, &pv_done[x][i & 1]);
-            if (!w.pair || x == 1) tc::commit(elected, &empty[stage]);
-        };
-        const int nx[2] = {n0, n1};
-        for (int x = 0; x < 2; ++x)
-            if (nx[x] > 0) qk(x, 0);
-        for (int i = 0; i < n0; ++i) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (i + 1 < nx[x]) {
-                    wait(&s_free[x], i);
-                    tc::fence_after();
-                    qk(x, i + 1);
-                }
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (i < nx[x]) {
-                    wait(&p_full[x][i & 1], i / 2);
-                    tc::fence_after();
-                    pv(x, i);
-                }
+            tc::commit(elected, &empty[stage]);
+            at.next(tiles_of(i));
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -472,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a, co
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 0) {
         tc::fence_after();
         tc::dealloc(tmem, kTmemCols);
     }
@@ -491,7 +509,9 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
         return cudaErrorNotSupported;
     auto kernel = prefix_tc_kernel<T, HD>;
     constexpr size_t smem = Smem<HD>::kTotal;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // all of the SM's shared memory, so that a CTA of the tail kernel finds room beside this one's
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(a.ctas_per_kv * a.n_kv)), dim3(kThreads), smem, s, pdl, 1,
                          a, tm);
@@ -518,10 +538,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     const int64_t row = b * a.group + g;
     const int tile = static_cast<int>(row / kRows);
     int recs = tile < 2 * a.pair_blocks ? a.pair_splits : a.single_splits;
-    if (len < whole_pages(a) * a.block_size) recs = 0;
+    const int64_t behind = whole_pages(a) * a.block_size, lo = len >= behind ? behind : 0;
+    if (len < behind) recs = 0;
     const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows + row;  // record i: i * rows further
     const float* tail = a.tail + (b * a.n_kv + kvh) * a.tail_splits * (16 + 8 * HD);
-    const int all = recs + a.tail_splits;
+    // its own tokens' records: the parts of the tail's stream that its tiles touch
+    const int64_t tiles = (len - lo + kTailTok - 1) / kTailTok, part = a.tail_at[a.B];
+    const int64_t t0 = a.tail_at[b] * a.n_kv + tiles * kvh;
+    const int all = recs + (tiles > 0 ? static_cast<int>((t0 + tiles - 1) / part - t0 / part + 1) : 0);
     auto stat = [&](int i) -> float2 {
         if (i < recs) return a.part_ml[first + static_cast<int64_t>(i) * a.rows];
         const float* t = tail + (i - recs) * (16 + 8 * HD);

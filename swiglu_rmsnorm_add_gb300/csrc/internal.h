@@ -153,6 +153,7 @@ struct AttnArgs {
     const int32_t* plen = nullptr;
     int64_t pblocks = 0;
     bool tail_only = false;  // requests that reach past the prefix's whole pages start behind them
+    int64_t* ws_tail_at = nullptr;  // [B + 1], see PrefixArgs::tail_at
 };
 
 struct AttnPlan {
@@ -162,6 +163,7 @@ struct AttnPlan {
     int stages;    // K/V tiles in flight per CTA (CUDA-core path)
     bool tensor_cores;  // bf16 / fp16, head_dim 64 or 128: the mma.sync path
     bool tma = false;   // ... with the K / V tiles moved by TMA (decode_tma_kernel)
+    int tail_ctas = 1;  // launch_prefix_tail with tail_only: CTAs per SM
     int mma_warps = 8;  // warps per CTA of the mma.sync kernel: 8 (one CTA per SM) or 4 (two)
     size_t smem;
     bool pdl;
@@ -169,8 +171,8 @@ struct AttnPlan {
 };
 
 cudaError_t launch_decode_attention(const AttnArgs& a, const AttnPlan& p, int dtype, cudaStream_t s);
-// The same kernels over a request's tokens with a shared prefix in front: the whole attention (no
-// ws_part), or the splits' records [16 + 8 * head_dim] in ws_part (a.gsplits of them per pair).
+// The same kernels over a request's tokens with a shared prefix in front: the whole attention or, with
+// a.tail_only, the records [16 + 8 * head_dim] of its own tokens in ws_part (up to a.gsplits per pair).
 cudaError_t launch_prefix_tail(const AttnArgs& a, const AttnPlan& p, int dtype, cudaStream_t s);
 size_t decode_attention_smem(int group, int head_dim, int block_size, int stages, int es);
 size_t decode_attention_mma_smem(int head_dim, int warps);
@@ -183,6 +185,19 @@ int decode_attention_gsplits(int64_t B, int n_kv, int64_t max_blocks, int block_
 int64_t decode_attention_ws_bytes(int64_t B, int n_kv, int head_dim, int gsplits);
 
 // ------------------------------------------------------------------- shared prefix
+// The requests' own tokens: tiles of kTailTok tokens of all (request, kv head) pairs in a row, cut into
+// parts for the workers; a part is as large as every worker needs it (at least two tiles), and no pair
+// has more than `records` parts' shares (its longest has `longest` tiles).
+constexpr int kTailTok = 32;
+struct TailPlan {
+    int64_t part;  // tiles
+};
+inline SRA_HD TailPlan tail_plan(int64_t tiles, int longest, int64_t workers, int records) {
+    int64_t part = (tiles + workers - 1) / workers;
+    const int64_t least = (longest + records - 2) / (records - 1);
+    if (part < least) part = least;
+    return {part < 2 ? 2 : part};
+}
 // The prefix's whole pages against the queries of all requests (tcgen05 path), and the merge of its
 // partial results with the requests' own tokens'.
 struct PrefixArgs {
@@ -202,7 +217,8 @@ struct PrefixArgs {
     float* part_o;   // [n_kv][records][rows][head_dim]
     float2* part_ml;  // [n_kv][records][rows] maximum (base 2, scaled) and sum
     const float* tail;  // [B * n_kv][tail_splits][16 + 8 * head_dim]
-    int tail_splits;
+    int tail_splits;    // records of a pair's own tokens at most (tail_plan)
+    const int64_t* tail_at;  // [B + 1] tiles before each request (of one kv head); a part's tiles
 };
 cudaError_t launch_prefix_tc(const PrefixArgs& a, const void* cache, int head_dim, int dtype, bool pdl, cudaStream_t s);
 cudaError_t launch_prefix_merge(const PrefixArgs& a, int head_dim, int dtype, cudaStream_t s);
