@@ -19,7 +19,7 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
 std::atomic<int> g_smem_optin[kMaxDevices];
 std::atomic<int> g_force_norm{-1}, g_force_rope{-1}, g_force_glu{-1}, g_force_attn{-1}, g_force_lin{-1},
-    g_force_narrow{-1};
+    g_force_narrow{-1}, g_force_prefix{-1};
 thread_local bool g_pdl = false;  // programmatic dependent launch for this thread's calls
 thread_local int g_force_nv = 0;  // accesses per thread forced for A/B measurement (0 = planner's)
 thread_local int g_force_g = 0;   // warps per row forced for warps_row A/B measurement (0 = planner's)
@@ -545,6 +545,7 @@ std::atomic<int>* force_slot(const char* op) {
     if (std::strcmp(op, "rope_kv_store") == 0) return &g_force_rope;
     if (std::strcmp(op, "glu") == 0) return &g_force_glu;
     if (std::strcmp(op, "decode_attention") == 0) return &g_force_attn;
+    if (std::strcmp(op, "shared_prefix") == 0) return &g_force_prefix;
     if (std::strcmp(op, "linear") == 0) return &g_force_lin;
     if (std::strcmp(op, "linear_narrow") == 0) return &g_force_narrow;
     return nullptr;
@@ -555,6 +556,7 @@ int variant_count(const char* op) {
     if (std::strcmp(op, "rmsnorm") == 0) return NORM_NUM_VARIANTS;
     if (std::strcmp(op, "rope_kv_store") == 0) return ROPE_NUM_VARIANTS;
     if (std::strcmp(op, "glu") == 0) return GLU_NUM_VARIANTS;
+    if (std::strcmp(op, "shared_prefix") == 0) return 2;
     if (std::strcmp(op, "decode_attention") == 0) return 3;  // CUDA cores, mma.sync, mma.sync fed by TMA
     if (std::strcmp(op, "linear") == 0) return 2;            // mma.sync, tcgen05 (projection over h)
     if (std::strcmp(op, "linear_narrow") == 0) return 1;     // the decode-batch kernel (K split forced)
@@ -1627,7 +1629,14 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
                        int block_size, int dtype, int sms) {
     PrefixPlan p;
     const int64_t rows = B * group;
-    if (dtype == DT_F32 || head_dim > 128 || rows < 8 || rows > (1 << 24) || prefix_blocks < 1) return p;
+    if (dtype == DT_F32 || head_dim > 128 || rows < 1 || rows > (1 << 24) || prefix_blocks < 1) return p;
+    // What every request reading the prefix for itself would move (L2 to SM) decides: up to 70 MB that is as
+    // fast as the two or three kernels of the other path, whose fixed part is 14 to 16 us (measured at
+    // 67 MB: 32 requests x 2048 tokens of 12 / 2 heads of 128 16.4 against 18.5 us, 64 x 1024 of 32 / 4 heads of
+    // 64 20.5 against 18.5; at 134 MB 24.6 and 26.7 against 19.6 and 21.6; at 34 MB 12.3 against 16.4).
+    const int forced = g_force_prefix.load(std::memory_order_relaxed);
+    const double moved = static_cast<double>(B) * prefix_blocks * block_size * n_kv * head_dim * 4.0;
+    if (forced == 0 || (forced < 0 && moved <= 70e6)) return p;
     p.use = true;
     p.rows = static_cast<int>(rows);
     // row tiles of 128, two to a CTA; the SMs of a KV head are dealt to its blocks by their tiles, and a
@@ -1751,6 +1760,8 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const PrefixPlan pp = plan_prefix(B, group, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size,
                                       dtype, sms);
+    if (g_force_prefix.load(std::memory_order_relaxed) == 1 && (!workspace || !pp.use || !plan.tensor_cores))
+        return SRA_ERR_VARIANT;
     if (!workspace || !pp.use || !plan.tensor_cores || static_cast<int64_t>(prefix_tc_smem(head_dim)) > limit - 512 ||
         num_blocks * block_size >= (int64_t(1) << 31) - 64)
         return status_from(launch_prefix_tail(a, plan, dtype, s));
@@ -1774,7 +1785,9 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     f.n_kv = n_kv_head;
     f.group = group;
     f.block_size = block_size;
-    f.scale_log2 = std::fabs(a.scale_log2);
+    // not 0: the kernel scales masked scores of -inf too (1e-37 times any score that is not itself near 1e37 is 0
+    // next to 1, the weight that a scale of 0 gives every token)
+    f.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-37f);
     f.negate = scale < 0.0f;
     f.q16 = aligned16(q) && stride_aligned16(q_tok_stride, es);
     f.rows = pp.rows;
@@ -1826,12 +1839,14 @@ const char* sra_variant_name(const char* op, int variant) {
     static const char* const glu_names[] = {"cols_rows", "cols_rows_regs"};
     static const char* const attn_names[] = {"cuda_cores", "mma_sync", "mma_sync_tma"};
     static const char* const lin_names[] = {"mma_sync", "tcgen05"};
+    static const char* const prefix_names[] = {"decode", "tcgen05"};
     static const char* const narrow_names[] = {"cluster_k_split"};
     const int n = variant_count(op);
     if (n < 0 || variant < 0 || variant >= n) return nullptr;
     if (std::strcmp(op, "rmsnorm") == 0) return norm_names[variant];
     if (std::strcmp(op, "rope_kv_store") == 0) return rope_names[variant];
     if (std::strcmp(op, "decode_attention") == 0) return attn_names[variant];
+    if (std::strcmp(op, "shared_prefix") == 0) return prefix_names[variant];
     if (std::strcmp(op, "linear") == 0) return lin_names[variant];
     if (std::strcmp(op, "linear_narrow") == 0) return narrow_names[variant];
     return glu_names[variant];

@@ -926,9 +926,10 @@ cudaError_t launch_merge(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
 // ------------------------------------------------------------------------------------------
 // The requests' own tokens beside the kernel that takes their shared prefix (attn_prefix.cu).
 //
-// The tiles of 32 tokens of all (request, kv head) pairs, in that order, are one stream, which is cut into
-// equal parts, one per warp (requests differ in length: dealt as whole chunks, the slowest warp had 1.65
-// times the mean's work). Every CTA sums the requests' tiles to find its warps' parts. What a warp finds of a
+// The tiles of 32 tokens of all requests, in order, are one stream, which is cut into equal parts; a warp
+// takes a part for one kv head, neighbouring warps the same part for the other heads, whose rows lie beside
+// its own (requests differ in length: dealt as whole chunks, the slowest warp had 1.65 times the mean's work).
+// Every CTA sums the requests' tiles to find its warps' parts. What a warp finds of a (request, kv head)
 // pair is one record [8 max][8 sum][8 x HD]; the merge kernel finds them again from the sums, which CTA 0
 // leaves in the workspace.
 //
@@ -1125,7 +1126,7 @@ __global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
     if (threadIdx.x == 0) sums[kTailThreads] = total;
     __syncthreads();
     const int workers = static_cast<int>(gridDim.x) * kTailWarps;
-    const TailPlan plan = tail_plan(total * a.n_kv, s_long, workers, a.gsplits);
+    const TailPlan plan = tail_plan(total, s_long, workers / a.n_kv, a.gsplits);
     if (blockIdx.x == 0) {
         // for the merge: the tiles before every request, and a part's size
         int64_t at = sums[threadIdx.x];
@@ -1139,55 +1140,65 @@ __global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
         if (threadIdx.x == 0) a.ws_tail_at[B] = plan.part;
     }
 
-    const int64_t me = static_cast<int64_t>(blockIdx.x) * kTailWarps + warp;
-    const int64_t g0 = me * plan.part, all = total * a.n_kv;
-    int64_t todo = g0 < all ? (all - g0 < plan.part ? all - g0 : plan.part) : 0;  // tiles not looked at yet
-    if (todo > 0) {
+    const int64_t parts = (total + plan.part - 1) / plan.part;
+    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kTailWarps + warp; unit < parts * a.n_kv; unit += workers) {
+        const int64_t mine_part = unit / a.n_kv, g0 = mine_part * plan.part;
+        const int kvh = static_cast<int>(unit - mine_part * a.n_kv);
+        int64_t todo = total - g0 < plan.part ? total - g0 : plan.part;  // tiles not looked at yet
         // The request that tile g0 belongs to: the thread that summed it, then along its requests, 32 at a time.
         // Lane k of the group holds request base + k.
         int owner = 0;
         for (int t = lane; t < kTailThreads; t += 32) {
-            const bool here = sums[t] * a.n_kv <= g0 && sums[t + 1] * a.n_kv > g0;
-            const unsigned hit = __ballot_sync(FULL, here);
+            const unsigned hit = __ballot_sync(FULL, sums[t] <= g0 && sums[t + 1] > g0);
             if (hit) owner = t - lane + __ffs(hit) - 1;
         }
-        int base = owner * per, lo, len, b = 0, kvh = 0, n = 0, t = 0;
-        int64_t at_pair = sums[owner] * a.n_kv;  // tiles before request base's
+        int base = owner * per, lo, len, b = 0, n = 0, t = 0;
+        int64_t at_row = sums[owner];  // tiles before request base's
         for (;;) {
             range(base + lane, &lo, &len);
-            const int64_t w = static_cast<int64_t>(tiles_of(lo, len)) * a.n_kv;
+            const int64_t w = tiles_of(lo, len);
             int64_t upto = w;
 #pragma unroll
             for (int x = 1; x < 32; x <<= 1) {
                 const int64_t y = __shfl_up_sync(FULL, upto, x);
                 if (lane >= x) upto += y;
             }
-            const unsigned hit = __ballot_sync(FULL, at_pair + upto > g0);
+            const unsigned hit = __ballot_sync(FULL, at_row + upto > g0);
             if (hit) {
                 const int k = __ffs(hit) - 1;
                 b = base + k;
-                n = tiles_of(__shfl_sync(FULL, lo, k), __shfl_sync(FULL, len, k));
-                const int64_t in = g0 - at_pair - __shfl_sync(FULL, upto - w, k);
-                kvh = static_cast<int>(in / n);
-                t = static_cast<int>(in - static_cast<int64_t>(kvh) * n);
-                at_pair = g0 - t;  // the pair's first tile in the stream
+                n = static_cast<int>(__shfl_sync(FULL, w, k));
+                at_row += __shfl_sync(FULL, upto - w, k);  // the request's first tile in the stream
+                t = static_cast<int>(g0 - at_row);
                 break;
             }
-            at_pair += __shfl_sync(FULL, upto, 31);
+            at_row += __shfl_sync(FULL, upto, 31);
             base += 32;
         }
-        int rec = static_cast<int>(me - at_pair / plan.part);  // parts of the pair before this one
-        // The tile looked at: its pair (b, kvh), first token, end of the pair, page entries asked for
+        int rec = static_cast<int>(mine_part - at_row / plan.part);  // parts of the request before this one
+        // The tile looked at: first token, the request's end, its page entries
         int at = 0, end = 0;
-        int32_t blk = 0;
+        int32_t blk = 0, entries = 0;
+        int win = 0, win_id = -2;
         bool have = false;
         auto ask = [&]() {
             const int k = b - base;
             at = __shfl_sync(FULL, lo, k) + t * kTailTok;
             end = __shfl_sync(FULL, len, k);
-            blk = lane < end - at ? __ldcg((at + lane < P ? a.ptable : a.table + static_cast<int64_t>(b) * a.max_blocks) +
-                                           ((at + lane) >> bs_log2))
-                                  : 0;
+            const int32_t* own = a.table + static_cast<int64_t>(b) * a.max_blocks;
+            const bool pre = at < P;
+            if (pre && P - at < kTailTok) {  // the prefix ends inside the tile
+                blk = lane < end - at ? __ldcg((at + lane < P ? a.ptable : own) + ((at + lane) >> bs_log2)) : 0;
+            } else {
+                // a tile's pages (up to four) come from a window of 32 entries, lane k's win + k
+                const int first = at >> bs_log2, id = pre ? -1 : b;
+                if (id != win_id || first < win || first + kTailTok / 8 > win + 32) {
+                    win = first, win_id = id;
+                    const int64_t most = pre ? a.pblocks : a.max_blocks;
+                    entries = first + lane < most ? __ldcg((pre ? a.ptable : own) + first + lane) : -1;
+                }
+                blk = __shfl_sync(FULL, entries, (((at + lane) >> bs_log2) - win) & 31);
+            }
             have = true;
             --todo;
         };
@@ -1196,16 +1207,13 @@ __global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
             if (todo == 0) return;
             if (++t == n) {
                 t = 0, rec = 0;
-                if (++kvh == a.n_kv) {
-                    kvh = 0;
-                    do {  // the next request that has tiles (there is one: todo > 0)
-                        if (++b == base + 32) {
-                            base = b;
-                            range(base + lane, &lo, &len);
-                        }
-                        n = tiles_of(__shfl_sync(FULL, lo, b - base), __shfl_sync(FULL, len, b - base));
-                    } while (n == 0);
-                }
+                do {  // the next request that has tiles (there is one: todo > 0)
+                    if (++b == base + 32) {
+                        base = b;
+                        range(base + lane, &lo, &len);
+                    }
+                    n = tiles_of(__shfl_sync(FULL, lo, b - base), __shfl_sync(FULL, len, b - base));
+                } while (n == 0);
             }
             ask();
         };

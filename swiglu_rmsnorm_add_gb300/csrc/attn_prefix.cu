@@ -520,9 +520,10 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
 // ------------------------------------------------------------------ merge
 // CTA = one output row (request, query head). Its parts are the prefix's records, unless the request
 // does not reach past the prefix's whole pages (then its own part holds all of its tokens), and its own
-// splits' records. Warp w takes records w, w + warps, ... and the warps' sums meet in shared memory, in a
+// records. Warp w takes parts w, w + warps, ..., kBatch of them loaded at a time (statistics and values
+// together, one round trip), with a running maximum of its own; the warps' sums meet in shared memory, in a
 // fixed order.
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 4, kBatch = 4;
 template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     constexpr int V = HD / 32;  // outputs per lane
@@ -534,57 +535,76 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     const int kvh = h / a.group, g = h - kvh * a.group;
     pdl_enter();
     int64_t len = a.seq_lens[b];
+    const int64_t part = a.tail_at[a.B], before = a.tail_at[b], behind = whole_pages(a) * a.block_size;
     len = len < 0 ? 0 : (len > a.cap ? a.cap : len);
     const int64_t row = b * a.group + g;
     const int tile = static_cast<int>(row / kRows);
     int recs = tile < 2 * a.pair_blocks ? a.pair_splits : a.single_splits;
-    const int64_t behind = whole_pages(a) * a.block_size, lo = len >= behind ? behind : 0;
+    const int64_t lo = len >= behind ? behind : 0;
     if (len < behind) recs = 0;
     const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows + row;  // record i: i * rows further
     const float* tail = a.tail + (b * a.n_kv + kvh) * a.tail_splits * (16 + 8 * HD);
     // its own tokens' records: the parts of the tail's stream that its tiles touch
-    const int64_t tiles = (len - lo + kTailTok - 1) / kTailTok, part = a.tail_at[a.B];
-    const int64_t t0 = a.tail_at[b] * a.n_kv + tiles * kvh;
-    const int all = recs + (tiles > 0 ? static_cast<int>((t0 + tiles - 1) / part - t0 / part + 1) : 0);
-    auto stat = [&](int i) -> float2 {
-        if (i < recs) return a.part_ml[first + static_cast<int64_t>(i) * a.rows];
-        const float* t = tail + (i - recs) * (16 + 8 * HD);
-        return make_float2(t[g], t[8 + g]);
-    };
-    float M = -INFINITY;
-    for (int i = threadIdx.x; i < all; i += blockDim.x) M = fmaxf(M, stat(i).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) s_m[warp] = M;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kMergeWarps; ++k) M = fmaxf(M, s_m[k]);
-    float den = 0.0f, acc[V];
+    const int64_t tiles = (len - lo + kTailTok - 1) / kTailTok;
+    const int all = recs + (tiles > 0 ? static_cast<int>((before + tiles - 1) / part - before / part + 1) : 0);
+    float m = -INFINITY, l = 0.0f, acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-#pragma unroll 4
-    for (int i = warp; i < all; i += kMergeWarps) {
-        const float2 ml = stat(i);
-        // a part without a token that counts has no sum (NaN among its scores leaves one that is NaN)
-        if (ml.x == -INFINITY && ml.y == 0.0f) continue;
-        const float e = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
-        den = fmaf(e, ml.y, den);
-        const float* o = i < recs ? a.part_o + (first + static_cast<int64_t>(i) * a.rows) * HD : tail + (i - recs) * (16 + 8 * HD) + 16 + g * HD;
+    for (int i0 = warp; i0 < all; i0 += kMergeWarps * kBatch) {
+        float pm[kBatch], pl[kBatch], po[kBatch][V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(e, o[lane + 32 * k], acc[k]);
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kMergeWarps;
+            pm[u] = -INFINITY, pl[u] = 0.0f;
+            const float* o = tail;
+            if (i < recs) {
+                const float2 ml = a.part_ml[first + static_cast<int64_t>(i) * a.rows];
+                pm[u] = ml.x, pl[u] = ml.y;
+                o = a.part_o + (first + static_cast<int64_t>(i) * a.rows) * HD;
+            } else if (i < all) {
+                const float* t = tail + (i - recs) * (16 + 8 * HD);
+                pm[u] = t[g], pl[u] = t[8 + g];
+                o = t + 16 + g * HD;
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k) po[u][k] = i < all ? o[lane + 32 * k] : 0.0f;
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) top = fmaxf(top, pm[u]);
+        const float keep = m == top ? 1.0f : ex2(m - top);  // (the first time m is -inf: 0, and l and acc are 0)
+        l *= keep;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] *= keep;
+        m = top;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            // a part without a token that counts has no sum, and its values are not its own (NaN among a part's
+            // scores leaves a sum that is NaN)
+            if (pm[u] == -INFINITY && pl[u] == 0.0f) continue;
+            const float e = pm[u] == m ? 1.0f : ex2(pm[u] - m);
+            l = fmaf(e, pl[u], l);
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = fmaf(e, po[u][k], acc[k]);
+        }
     }
-    if (lane == 0) s_l[warp] = den;
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
     for (int k = 0; k < V; ++k) s_o[warp][lane + 32 * k] = acc[k];
     __syncthreads();
-    den = 0.0f;
+    float M = -INFINITY, w[kMergeWarps], den = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kMergeWarps; ++k) den += s_l[k];
+    for (int k = 0; k < kMergeWarps; ++k) M = fmaxf(M, s_m[k]);
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) {
+        w[k] = s_m[k] == M ? 1.0f : ex2(s_m[k] - M);
+        den = fmaf(w[k], s_l[k], den);
+    }
     T* out = static_cast<T*>(a.out) + b * a.os + static_cast<int64_t>(h) * HD;
     for (int d = threadIdx.x; d < HD; d += blockDim.x) {
         float num = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kMergeWarps; ++k) num += s_o[k][d];
+        for (int k = 0; k < kMergeWarps; ++k) num = fmaf(w[k], s_o[k][d], num);
         out[d] = from_f32<T>(den != 0.0f ? num / den : 0.0f);
     }
 }

@@ -185,14 +185,15 @@ int decode_attention_gsplits(int64_t B, int n_kv, int64_t max_blocks, int block_
 int64_t decode_attention_ws_bytes(int64_t B, int n_kv, int head_dim, int gsplits);
 
 // ------------------------------------------------------------------- shared prefix
-// The requests' own tokens: tiles of kTailTok tokens of all (request, kv head) pairs in a row, cut into
-// parts for the workers; a part is as large as every worker needs it (at least two tiles), and no pair
-// has more than `records` parts' shares (its longest has `longest` tiles).
+// The requests' own tokens: tiles of kTailTok tokens of all requests in a row, cut into parts for the
+// workers of a kv head; a part is as large as every worker needs it (at least two tiles), and no request
+// touches more than `records` parts (the longest has `longest` tiles).
 constexpr int kTailTok = 32;
 struct TailPlan {
     int64_t part;  // tiles
 };
 inline SRA_HD TailPlan tail_plan(int64_t tiles, int longest, int64_t workers, int records) {
+    if (workers < 1) workers = 1;
     int64_t part = (tiles + workers - 1) / workers;
     const int64_t least = (longest + records - 2) / (records - 1);
     if (part < least) part = least;

@@ -103,6 +103,18 @@ def run(c, what="", expect_errors=0, **kw):
     return got
 
 
+@pytest.fixture(params=["auto", "decode", "tcgen05"])
+def path(request):
+    """The automatic choice, and each of the two paths forced."""
+    sra.force_variant("shared_prefix", {"auto": -1, "decode": 0, "tcgen05": 1}[request.param])
+    yield request.param
+    sra.force_variant("shared_prefix", -1)
+
+
+def serves(path, dtype, hd, prefix_pages=1):
+    return path != "tcgen05" or (dtype != torch.float32 and hd <= 128 and prefix_pages > 0)
+
+
 def ragged(B, prefix, own, seed):
     r = np.random.default_rng(seed)
     lens = prefix + r.integers(0, own + 1, B)
@@ -116,7 +128,9 @@ def ragged(B, prefix, own, seed):
 @pytest.mark.parametrize("hd", [64, 128, 256])
 @pytest.mark.parametrize("n_head,n_kv", [(8, 8), (12, 2), (21, 3), (8, 1)])
 @pytest.mark.parametrize("bs", [8, 16, 32])
-def test_shapes_dtypes(dtype, hd, n_head, n_kv, bs):
+def test_shapes_dtypes(dtype, hd, n_head, n_kv, bs, path):
+    if not serves(path, dtype, hd):
+        pytest.skip("the tensor-core path serves 16-bit data with head_dim 64 or 128")
     B = {8: 5, 16: 19, 32: 40}[bs]
     prefix = {64: 200, 128: 391, 256: 128}[hd]
     run(Case(B, n_head, n_kv, hd, bs, prefix, ragged(B, prefix, 70, hd + bs), dtype, hd + bs + n_head))
@@ -125,7 +139,9 @@ def test_shapes_dtypes(dtype, hd, n_head, n_kv, bs):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("prefix", [0, 1, 15, 16, 17, 127, 128, 129, 256, 511, 640])
 @pytest.mark.parametrize("B", [1, 2, 23, 65])
-def test_prefix_lengths(dtype, prefix, B):
+def test_prefix_lengths(dtype, prefix, B, path):
+    if not serves(path, dtype, 128):
+        pytest.skip("the tensor-core path serves 16-bit data with head_dim 64 or 128")
     run(Case(B, 12, 2, 128, 16, prefix, ragged(B, prefix, 40, prefix + B), dtype, prefix + B))
 
 
@@ -136,7 +152,9 @@ def test_long_prefixes(hd, n_head, n_kv, B):
 
 
 @pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float32, 64), (torch.float16, 256)])
-def test_no_own_tokens_no_prefix_nothing(dtype, hd):
+def test_no_own_tokens_no_prefix_nothing(dtype, hd, path):
+    if not serves(path, dtype, hd):
+        pytest.skip("the tensor-core path serves 16-bit data with head_dim 64 or 128")
     run(Case(30, 8, 2, hd, 16, 300, [300] * 30, dtype, 1), "only the prefix")
     run(Case(30, 8, 2, hd, 16, 300, [0] * 30, dtype, 2), "no tokens at all")
     run(Case(30, 8, 2, hd, 16, 300, list(range(30)), dtype, 3), "all shorter than the prefix")
@@ -146,14 +164,18 @@ def test_no_own_tokens_no_prefix_nothing(dtype, hd):
 
 
 @pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float16, 64), (torch.float32, 128)])
-def test_peaked_scores(dtype, hd):
+def test_peaked_scores(dtype, hd, path):
     """Scores of some hundreds: the running maximum moves many times and most weights vanish."""
+    if not serves(path, dtype, hd):
+        pytest.skip("the tensor-core path serves 16-bit data with head_dim 64 or 128")
     run(Case(40, 12, 2, hd, 16, 1000, ragged(40, 1000, 90, 7), dtype, 7, scale=1.0, spread=2.0))
 
 
 @pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float16, 64), (torch.float32, 64),
                                       (torch.bfloat16, 256)])
-def test_bad_entries_are_skipped_and_counted(dtype, hd):
+def test_bad_entries_are_skipped_and_counted(dtype, hd, path):
+    if not serves(path, dtype, hd):
+        pytest.skip("the tensor-core path serves 16-bit data with head_dim 64 or 128")
     c = Case(33, 8, 2, hd, 16, 417, [600] * 33, dtype, 11)
     c.ptable[3], c.ptable[9] = -1, c.nb
     c.table[4, 30] = 2 ** 31 - 1
@@ -165,7 +187,7 @@ def test_bad_entries_are_skipped_and_counted(dtype, hd):
     run(c, expect_errors=2 + 1 + 1 + 1 + 1 + bad_of_7)
 
 
-def test_prefix_length_is_clamped():
+def test_prefix_length_is_clamped(path):
     c = Case(20, 8, 2, 128, 16, 64, [64] * 20, torch.bfloat16, 12)
     d = c.dev()
     d["prefix_table"] = d["prefix_table"][:4].contiguous()
@@ -180,8 +202,10 @@ def test_prefix_length_is_clamped():
 
 
 @pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float32, 64)])
-def test_strided_queries_and_outputs(dtype, hd):
+def test_strided_queries_and_outputs(dtype, hd, path):
     """q as a view of a fused QKV buffer, out as a view of a wider one whose other columns stay."""
+    if not serves(path, dtype, hd):
+        pytest.skip("the tensor-core path serves 16-bit data with head_dim 64 or 128")
     c = Case(50, 8, 2, hd, 16, 500, ragged(50, 500, 50, 3), dtype, 3)
     d = c.dev()
     qkv = torch.randn(50, 12, hd, device=DEV).to(dtype)
@@ -193,16 +217,35 @@ def test_strided_queries_and_outputs(dtype, hd):
     assert bool((wide[:, :2] == 7).all()) and bool((wide[:, 10:] == 7).all())
 
 
-def test_queries_at_an_odd_element():
+def test_queries_at_an_odd_element(path):
     c = Case(50, 8, 2, 128, 16, 500, ragged(50, 500, 50, 4), torch.bfloat16, 4)
     d = c.dev()
     flat = torch.empty(c.q.numel() + 1, device=DEV, dtype=torch.bfloat16)[1:]
     d["q"] = flat.copy_(d["q"].reshape(-1)).view(c.q.shape)
     out = torch.empty(c.q.numel() + 1, device=DEV, dtype=torch.bfloat16)[1:].view(c.q.shape)
+    if path == "tcgen05":   # wants query rows aligned to 4 bytes
+        with pytest.raises(sra.SRAError) as e:
+            sra.shared_prefix_attention(**d, scale=c.scale, out=out)
+        assert e.value.status == -7
+        return
     c.check(sra.shared_prefix_attention(**d, scale=c.scale, out=out))
 
 
-def test_equals_decode_attention_on_forked_rows():
+@pytest.mark.parametrize("off", [2, 4])
+def test_queries_at_4_and_8_bytes(off, path):
+    c = Case(50, 8, 2, 128, 16, 500, ragged(50, 500, 50, 4), torch.bfloat16, 4)
+    d = c.dev()
+    flat = torch.empty(c.q.numel() + off, device=DEV, dtype=torch.bfloat16)[off:]
+    d["q"] = flat.copy_(d["q"].reshape(-1)).view(c.q.shape)
+    c.check(sra.shared_prefix_attention(**d, scale=c.scale))
+
+
+def test_negative_and_zero_scale(path):
+    for scale in (-0.09, 0.0):
+        run(Case(30, 8, 2, 64, 16, 300, ragged(30, 300, 50, 8), torch.float16, 8, scale=scale))
+
+
+def test_equals_decode_attention_on_forked_rows(path):
     """Rows that hold the prefix's pages themselves: the same call, the same answer within both tolerances."""
     c = Case(24, 12, 2, 128, 16, 1024, 1024 + np.arange(24) * 5, torch.bfloat16, 6)
     c.table[:, :64] = c.ptable[:64]
@@ -216,7 +259,7 @@ def test_equals_decode_attention_on_forked_rows():
 
 
 @pytest.mark.parametrize("pdl", [False, True])
-def test_graph_replay_with_new_lengths(pdl):
+def test_graph_replay_with_new_lengths(pdl, path):
     """One captured call: prefix, lengths, tables and queries change between replays; two graphs with a
     workspace each do not disturb one another."""
     a = Case(70, 12, 2, 128, 16, 800, ragged(70, 800, 100, 1), torch.bfloat16, 1, extra_cols=40)
@@ -255,7 +298,7 @@ def test_graph_replay_with_new_lengths(pdl):
         a.check(out)
 
 
-def test_same_result_every_time_and_on_another_stream():
+def test_same_result_every_time_and_on_another_stream(path):
     c = Case(64, 12, 2, 128, 16, 3000, ragged(64, 3000, 200, 5), torch.bfloat16, 5)
     d = c.dev()
     first = sra.shared_prefix_attention(**d, scale=c.scale)
@@ -285,7 +328,7 @@ def test_refusals():
     assert e.value.status == -6
 
 
-def test_a_prompt_and_its_samples():
+def test_a_prompt_and_its_samples(path):
     """The operators together, as a sampling loop uses them: a prompt is stored, forked into samples,
     each step grows the rows (the shared last page copied once), stores the new token's K and V by
     rope_kv_store's own slots and attends; then some samples end, the cache is compacted, and the
