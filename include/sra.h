@@ -589,9 +589,9 @@ SRA_API int64_t sra_kv_compact_workspace_size(int64_t num_blocks);
  * The tensor-core path takes the queries of all requests that share a KV head as the rows of one
  * product with the prefix's whole pages, splits it over the GPU along the prefix, takes each
  * request's own tokens as sra_paged_decode_attention does, and merges the parts through their
- * maxima and sums of exponentials (fp32). In that path the prefix's probabilities are
- * rounded once to the dtype before they multiply V (fp32 sums); the request's own tokens and the
- * path without a workspace keep them to 16 bits or more.
+ * maxima and sums of exponentials (fp32). In that path the probabilities are rounded once to
+ * the dtype before they multiply V (fp32 sums); the path without a workspace keeps them to 16 bits or
+ * more.
  *
  * q, kv_cache, out, scale: as in sra_paged_decode_attention. prefix_table: int32 [prefix_blocks];
  * prefix_len: device int32, one entry; block_table: int32 [B, max_blocks_per_seq]; seq_lens: int32 [B].

@@ -941,16 +941,27 @@ cudaError_t launch_merge(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
 // prefix's on an SM, whose tensor cores and this one's memory traffic then overlap.
 // K's part of a warp's tile is copied again as soon as S is known, V's as soon as it has been used.
 // The products have the tokens (S) or the dims (O) as the rows of the MMA and the up to eight query heads
-// as its eight columns, so no row is empty: S^T = K Q^T and O^T = V^T P^T, 24 MMAs per tile at head_dim
-// 128 where the heads as rows take 48.
+// as its eight columns, so no row is empty: S^T = K Q^T and O^T = V^T P^T, 32 MMAs per 32 tokens at
+// head_dim 128 where the heads as rows take 64.
 constexpr int kTailWarps = 4;
+// These loads and products are not volatile, so that the compiler may have many of them under way (in program
+// order, each product behind its own load, a tile took twice as long): they hang on the tile's address, which
+// `after` makes depend on the wait for the copies, and `pin` keeps their results ahead of the next copies.
+__device__ __forceinline__ uint32_t after(uint32_t address) {
+    asm volatile("" : "+r"(address)::"memory");
+    return address;
+}
+template <int N>
+__device__ __forceinline__ void pin(float (&v)[N][4]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i][0]), "+f"(v[i][1]), "+f"(v[i][2]), "+f"(v[i][3])::"memory");
+}
 template <typename T>
 struct MmaFull;
 template <>
 struct MmaFull<__nv_bfloat16> {
     __device__ __forceinline__ static void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
@@ -958,8 +969,7 @@ struct MmaFull<__nv_bfloat16> {
 template <>
 struct MmaFull<__half> {
     __device__ __forceinline__ static void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
@@ -967,7 +977,7 @@ struct MmaFull<__half> {
 // An 8 x 8 matrix of 16-bit values, a row's pairs over four lanes, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 
@@ -986,27 +996,31 @@ __device__ __forceinline__ void tail_scores(uint32_t ks, const uint32_t (&qb)[HD
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             uint32_t ka[4];
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+            asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                          : "=r"(ka[0]), "=r"(ka[1]), "=r"(ka[2]), "=r"(ka[3])
                          : "r"(krow + u * 16 * HD * 2 + (((2 * e + (mi >> 1)) ^ rr) << 4)));
             MmaFull<T>::run(s[u], ka, qb[e][0], qb[e][1]);
         }
 }
 // The running softmax over those scores (valid: a bit per token): maxima m of the lane's two heads, this
-// lane's tokens' part l of their sums, corr = 2^(old m - new m); the probabilities as B fragments of the
-// next product, a T-rounded part and its T-rounded residual (about 16 significant bits).
+// lane's tokens' part l of their sums, corr = 2^(old m - new m); the probabilities, rounded once to T (half a
+// step of T each, as the prefix's), as B fragments of the next product.
 template <typename T>
-__device__ __forceinline__ void tail_softmax(const float (&s)[2][4], unsigned valid, float (&m)[2], float (&l)[2],
-                                             float (&corr)[2], uint32_t (&hi)[2][2], uint32_t (&lo)[2][2],
-                                             float scale_log2, int lane) {
+__device__ __forceinline__ void tail_softmax(float (&p)[2][4], unsigned valid, float (&m)[2], float (&l)[2],
+                                             float (&corr)[2], uint32_t (&pb)[2][2], float scale_log2, int lane) {
     const unsigned FULL = 0xffffffffu;
     const int fg = lane >> 2;
-    float p[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            p[u][k] = (valid >> (16 * u + 8 * (k >> 1) + fg)) & 1u ? s[u][k] * scale_log2 : -INFINITY;
+        for (int k = 0; k < 4; ++k) p[u][k] *= scale_log2;
+    if (valid != FULL) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (!((valid >> (16 * u + 8 * (k >> 1) + fg)) & 1u)) p[u][k] = -INFINITY;
+    }
     float mx[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) mx[h] = fmaxf(fmaxf(p[0][h], p[0][h + 2]), fmaxf(p[1][h], p[1][h + 2]));
@@ -1015,29 +1029,28 @@ __device__ __forceinline__ void tail_softmax(const float (&s)[2][4], unsigned va
         const float a = __shfl_xor_sync(FULL, mx[0], x), b = __shfl_xor_sync(FULL, mx[1], x);
         mx[0] = fmaxf(mx[0], a), mx[1] = fmaxf(mx[1], b);
     }
+    float base[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float now = fmaxf(m[h], mx[h]);
+        base[h] = now == -INFINITY ? 0.0f : now;  // (then every p is 2^-inf = 0)
         corr[h] = now == -INFINITY ? 1.0f : ex2(m[h] - now);
         m[h] = now;
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p[u][k] = p[u][k] == -INFINITY ? 0.0f : ex2(p[u][k] - m[k & 1]);
-        const uint32_t h0 = pack2<T>(p[u][0], p[u][1]), h1 = pack2<T>(p[u][2], p[u][3]);
-        const float2 f0 = unpack2<T>(h0), f1 = unpack2<T>(h1);
-        hi[u][0] = transpose8(h0), hi[u][1] = transpose8(h1);
-        lo[u][0] = transpose8(pack2<T>(p[u][0] - f0.x, p[u][1] - f0.y));
-        lo[u][1] = transpose8(pack2<T>(p[u][2] - f1.x, p[u][3] - f1.y));
+        for (int k = 0; k < 4; ++k) p[u][k] = ex2(p[u][k] - base[k & 1]);
+        pb[u][0] = transpose8(pack2<T>(p[u][0], p[u][1]));
+        pb[u][1] = transpose8(pack2<T>(p[u][2], p[u][3]));
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) l[h] = fmaf(l[h], corr[h], (p[0][h] + p[0][h + 2]) + (p[1][h] + p[1][h + 2]));
 }
 // O^T = O^T corr + V^T P^T: o[d] holds dims 16 d + fg + {0, 8} of heads 2 ft + {0, 1} (an MMA accumulator).
 template <typename T, int HD>
-__device__ __forceinline__ void tail_values(uint32_t vs, const uint32_t (&hi)[2][2], const uint32_t (&lo)[2][2],
-                                            const float (&corr)[2], float (&o)[HD / 16][4], int lane) {
+__device__ __forceinline__ void tail_values(uint32_t vs, const uint32_t (&pb)[2][2], const float (&corr)[2],
+                                            float (&o)[HD / 16][4], int lane) {
     const int mi = lane >> 3, rr = lane & 7;
     if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
 #pragma unroll
@@ -1051,11 +1064,10 @@ __device__ __forceinline__ void tail_values(uint32_t vs, const uint32_t (&hi)[2]
 #pragma unroll
         for (int d = 0; d < HD / 16; ++d) {
             uint32_t va[4];
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+            asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                          : "=r"(va[0]), "=r"(va[1]), "=r"(va[2]), "=r"(va[3])
                          : "r"(vrow + u * 16 * HD * 2 + (((2 * d + (mi & 1)) ^ rr) << 4)));
-            MmaFull<T>::run(o[d], va, hi[u][0], hi[u][1]);
-            MmaFull<T>::run(o[d], va, lo[u][0], lo[u][1]);
+            MmaFull<T>::run(o[d], va, pb[u][0], pb[u][1]);
         }
 }
 constexpr int kTailThreads = kTailWarps * 32;
@@ -1219,37 +1231,39 @@ __global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
         };
         const uint32_t ks = smem_u32(smem) + warp * 2 * TE * 2, vs = ks + TE * 2;
         const int col = lane % CPR, rr0 = lane / CPR;
-        // Copies a plane (0 K, 1 V) of the tile looked at. A group of eight rows lies in one page, unless the
-        // prefix ends inside it; rows that do not count are zero-filled, not read.
+        // Copies a plane (0 K, 1 V) of the tile looked at. Usually all of its rows count and eight rows in a row
+        // lie in one page: a lane's place in them is fixed. Otherwise (the end of a request, a bad entry, the
+        // prefix's end inside) row by row; rows that do not count are zero-filled, not read.
         unsigned valid = 0;
-        auto copy = [&](uint32_t dst, int plane) {
-            const T* from = cache + (plane ? v_plane : 0) + kvh * HD + col * 8;
-            const bool by_row = at < P && P - at < kTailTok;
+        uint32_t dst_at[8 / RPI];
 #pragma unroll
-            for (int g = 0; g < kTailTok / 8; ++g) {
-                if (!by_row) {
-                    const int64_t row = (static_cast<int64_t>(__shfl_sync(FULL, blk, 8 * g)) << bs_log2) + ((at + 8 * g) & (BS - 1));
-                    const T* src = from + (row + rr0) * tok_stride;
+        for (int i = 0; i < 8 / RPI; ++i) {
+            const int r = rr0 + RPI * i;
+            dst_at[i] = r * HD * 2 + ((col ^ r) << 4);
+        }
+        const T* lane_from = cache + rr0 * tok_stride + kvh * HD + col * 8;
+        const int64_t step = RPI * tok_stride;
+        auto copy = [&](uint32_t dst, int64_t plane) {
+            if (valid == FULL && (at >= P || P - at >= kTailTok)) {
+#pragma unroll
+                for (int g = 0; g < kTailTok / 8; ++g) {
+                    const int32_t page = __shfl_sync(FULL, blk, 8 * g);
+                    const T* src = lane_from + plane + ((static_cast<int64_t>(page) << bs_log2) + ((at + 8 * g) & (BS - 1))) * tok_stride;
 #pragma unroll
                     for (int i = 0; i < 8 / RPI; ++i) {
-                        const int r = 8 * g + rr0 + RPI * i;
-                        const bool v = (valid >> r) & 1u;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                         dst + r * HD * 2 + ((col ^ (r & 7)) << 4)),
-                                     "l"(v ? src + i * RPI * tok_stride : cache), "r"(v ? 16 : 0)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + dst_at[i] + g * 8 * HD * 2), "l"(src)
                                      : "memory");
+                        src += step;
                     }
-                } else {
+                }
+            } else {
 #pragma unroll 1
-                    for (int i = 0; i < 8 / RPI; ++i) {
-                        const int r = 8 * g + rr0 + RPI * i;
-                        const int64_t row = (static_cast<int64_t>(__shfl_sync(FULL, blk, r)) << bs_log2) + ((at + r) & (BS - 1));
-                        const bool v = (valid >> r) & 1u;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                         dst + r * HD * 2 + ((col ^ (r & 7)) << 4)),
-                                     "l"(v ? from + row * tok_stride : cache), "r"(v ? 16 : 0)
-                                     : "memory");
-                    }
+                for (int r = rr0; r < kTailTok; r += RPI) {
+                    const int64_t row = (static_cast<int64_t>(__shfl_sync(FULL, blk, r)) << bs_log2) + ((at + r) & (BS - 1));
+                    const bool v = (valid >> r) & 1u;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * HD * 2 + ((col ^ (r & 7)) << 4)),
+                                 "l"(v ? cache + plane + kvh * HD + col * 8 + row * tok_stride : cache), "r"(v ? 16 : 0)
+                                 : "memory");
                 }
             }
             cp_async_commit();
@@ -1268,7 +1282,7 @@ __global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
         ask();
         check();
         copy(ks, 0);
-        copy(vs, 1);
+        copy(vs, v_plane);
         uint32_t qb[KS][2];
         float o[KS][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         auto load_q = [&]() {  // of the pair at hand, column fg = query head fg (zero past G); an empty record
@@ -1292,7 +1306,8 @@ __global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
             cp_async_wait<1>();  // K has landed
             __syncwarp();
             float sc[2][4], corr[2];
-            tail_scores<T, HD>(ks, qb, sc, lane);
+            tail_scores<T, HD>(after(ks), qb, sc, lane);
+            pin(sc);
             __syncwarp();  // every lane is done with K
             if (have) {
                 check();
@@ -1300,13 +1315,14 @@ __global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
             } else {
                 cp_async_commit();
             }
-            uint32_t hi[2][2], rest[2][2];
-            tail_softmax<T>(sc, mask, m, l, corr, hi, rest, a.scale_log2, lane);
+            uint32_t pb[2][2];
+            tail_softmax<T>(sc, mask, m, l, corr, pb, a.scale_log2, lane);
             cp_async_wait<1>();  // V has landed (the next K is behind it)
             __syncwarp();
-            tail_values<T, HD>(vs, hi, rest, corr, o, lane);
+            tail_values<T, HD>(after(vs), pb, corr, o, lane);
+            pin(o);
             __syncwarp();  // every lane is done with V
-            if (have) copy(vs, 1);
+            if (have) copy(vs, v_plane);
             if (last) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) {
