@@ -1,6 +1,8 @@
 """ctypes binding of include/sra.h (argument marshalling only)."""
 from __future__ import annotations
 
+import array
+import contextlib
 import ctypes
 import os
 import threading
@@ -187,8 +189,20 @@ def _as_rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
     return rows, width, stride
 
 
+# torch's current stream of a device as an integer, without a Stream object (0.1 us instead of 2)
+_raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_HERE = contextlib.nullcontext()
+
+
+def _on(index: int):
+    """A guard for the CUDA device of that index; none where it is the current one."""
+    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
 def _stream(t: torch.Tensor, stream) -> int:
     if stream is None:
+        if _raw_current_stream is not None:
+            return _raw_current_stream(t.get_device())
         stream = torch.cuda.current_stream(t.device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -590,10 +604,24 @@ def glu_linear(gate_up: torch.Tensor, W: torch.Tensor, y: torch.Tensor | None = 
 
 
 # ------------------------------------------------------------------- pages of the cache
+# A call's checks come twice: once as a cheap test that everything is as it should be (these calls are
+# short, and so is the time that a decode loop has for them), and, where that fails, one by one to say
+# what is not.
+def _kv_cache_ok(c: torch.Tensor) -> bool:
+    return c.dim() == 5 and c.shape[0] == 2 and c.is_contiguous() and c.is_cuda
+
+
 def _kv_caches(kv_caches):
-    """(first cache, pointer array, count) of one cache [2, num_blocks, block_size, n_kv_head,
-    head_dim], a [layers, 2, ...] tensor of them, or a sequence of caches of one shape and dtype."""
+    """(shape, dtype, device index, pointers, count) of one cache [2, num_blocks, block_size, n_kv_head,
+    head_dim], a [layers, 2, ...] tensor of them, or a sequence of caches of one shape and dtype. The
+    pointers are an array that has to live until the call returns."""
     if isinstance(kv_caches, torch.Tensor):
+        if kv_caches.dim() == 6 and kv_caches.is_cuda and kv_caches.shape[0] > 0 and kv_caches.shape[1] == 2 \
+                and kv_caches.is_contiguous():
+            n, first = kv_caches.shape[0], kv_caches.data_ptr()
+            step = kv_caches.stride(0) * kv_caches.element_size()
+            ptrs = array.array("Q", range(first, first + n * step, step) if step else [first] * n)
+            return kv_caches.shape[1:], kv_caches.dtype, kv_caches.get_device(), ptrs, n
         caches = [kv_caches] if kv_caches.dim() == 5 else list(kv_caches) if kv_caches.dim() == 6 else None
         if caches is None:
             raise ValueError("kv_caches must be [2, num_blocks, block_size, n_kv_head, head_dim], or [layers, ...] of it")
@@ -601,40 +629,52 @@ def _kv_caches(kv_caches):
         caches = list(kv_caches)
     if not caches:
         raise ValueError("kv_caches is empty")
-    first = caches[0]
     for c in caches:
         _cuda(c, "kv_caches")
-        if c.dim() != 5 or c.shape[0] != 2 or not c.is_contiguous():
+        if not _kv_cache_ok(c):
             raise ValueError("each cache must be contiguous [2, num_blocks, block_size, n_kv_head, head_dim]")
-        if c.shape != first.shape or c.dtype != first.dtype:
+    first = caches[0]
+    shape, dtype, dev = first.shape, first.dtype, first.get_device()
+    for c in caches:
+        if c.shape != shape or c.dtype != dtype:
             raise ValueError("the caches must share one shape and dtype")
-    _same_device(*caches)
-    return first, (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches]), len(caches)
+        if c.get_device() != dev:
+            raise ValueError("all tensors must be on the same CUDA device")
+    return shape, dtype, dev, array.array("Q", [c.data_ptr() for c in caches]), len(caches)
 
 
-def _int32(t, name, dim):
+def _int32(t, name, dim, dev=None):
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == dim and t.is_contiguous() \
+            and t.get_device() == dev:
+        return
     _cuda(t, name)
     if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension{'s' if dim > 1 else ''}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
 
 
-def _err_ptr(err_count):
+def _err_ptr(err_count, dev):
     if err_count is None:
         return None
     _cuda(err_count, "err_count")
     if err_count.dtype != torch.int32:
         raise ValueError("err_count must be int32")
+    if err_count.get_device() != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
     return err_count.data_ptr()
 
 
 def _page_state(block_table, seq_lens, ref_counts):
-    _int32(block_table, "block_table", 2)
-    _int32(seq_lens, "seq_lens", 1)
-    _int32(ref_counts, "ref_counts", 1)
-    _same_device(block_table, seq_lens, ref_counts)
+    """The device index of the state; its tensors checked."""
+    _cuda(block_table, "block_table")
+    dev = block_table.get_device()
+    _int32(block_table, "block_table", 2, dev)
+    _int32(seq_lens, "seq_lens", 1, dev)
+    _int32(ref_counts, "ref_counts", 1, dev)
     if seq_lens.shape[0] != block_table.shape[0]:
         raise ValueError("block_table and seq_lens must have one row per request")
-    return block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr()
+    return dev
 
 
 def _byte_workspace(fn: str, n: int, device) -> torch.Tensor:
@@ -643,7 +683,7 @@ def _byte_workspace(fn: str, n: int, device) -> torch.Tensor:
     return torch.empty(max(16, int(n)), dtype=torch.uint8, device=device)
 
 
-def _workspace_args(workspace, make, like, stream):
+def _workspace_args(workspace, make, dev, stream):
     """(tensor, pointer, bytes) of the caller's workspace, or of one made for this call. One made
     here is allocated on the stream that the call runs on, so its memory is not used again before
     the call's kernels are done with it."""
@@ -652,14 +692,15 @@ def _workspace_args(workspace, make, like, stream):
             workspace = make()
         else:
             s = stream if isinstance(stream, torch.cuda.Stream) else \
-                torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+                torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=torch.device("cuda", dev))
             with torch.cuda.stream(s):
                 workspace = make()
     _cuda(workspace, "workspace")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _same_device(like, workspace)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def copy_kv_pages(kv_caches, src: torch.Tensor, dst: torch.Tensor, err_count: torch.Tensor | None = None,
@@ -670,16 +711,17 @@ def copy_kv_pages(kv_caches, src: torch.Tensor, dst: torch.Tensor, err_count: to
     sequence of them. src, dst: int32 [n], negative entries skipped. Destinations must be distinct
     and no source (their contents are undefined otherwise); an index past the cache is skipped
     and counted in err_count."""
-    cache, ptrs, count = _kv_caches(kv_caches)
-    _int32(src, "src", 1)
-    _int32(dst, "dst", 1)
-    _same_device(cache, src, dst, err_count)
-    if src.shape != dst.shape:
+    (_, nb, bs, n_kv, hd), dtype, dev, ptrs, count = _kv_caches(kv_caches)
+    _int32(src, "src", 1, dev)
+    _int32(dst, "dst", 1, dev)
+    n = src.shape[0]
+    if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
-    _, nb, bs, n_kv, hd = cache.shape
-    with torch.cuda.device(cache.device):
-        st = lib().sra_kv_copy_pages(ptrs, count, src.data_ptr(), dst.data_ptr(), src.numel(), nb, bs, n_kv, hd,
-                                     _err_ptr(err_count), _dtype(cache), _stream(cache, stream))
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    with _on(dev):
+        st = lib().sra_kv_copy_pages(ptrs.buffer_info()[0], count, src.data_ptr(), dst.data_ptr(), n, nb, bs, n_kv, hd,
+                                     _err_ptr(err_count, dev), DTYPE_CODE[dtype], _stream(src, stream))
     _check("sra_kv_copy_pages", st)
 
 
@@ -696,25 +738,31 @@ def fork_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: 
     block_table int32 [rows, max_blocks], seq_lens int32 [rows] and ref_counts int32
     [num_blocks] change in place; parents are read as they were at entry. No page is copied:
     resize_kv_rows copies a shared, partly filled page before a row writes into it."""
-    tp, sp, rp = _page_state(block_table, seq_lens, ref_counts)
-    _int32(parents, "parents", 1)
-    _int32(children, "children", 1)
-    _same_device(block_table, parents, children, err_count)
-    if parents.shape != children.shape:
+    dev = _page_state(block_table, seq_lens, ref_counts)
+    _int32(parents, "parents", 1, dev)
+    _int32(children, "children", 1, dev)
+    n, (rows, mb) = parents.shape[0], block_table.shape
+    if children.shape[0] != n:
         raise ValueError("parents and children must have the same length")
-    n, (rows, mb) = parents.numel(), block_table.shape
-    with torch.cuda.device(block_table.device):
-        workspace, wp, wb = _workspace_args(workspace, lambda: kv_fork_workspace(n, mb, block_table.device),
-                                            block_table, stream)
-        st = lib().sra_kv_fork_rows(tp, sp, rp, parents.data_ptr(), children.data_ptr(), n, rows, mb,
-                                    ref_counts.numel(), int(block_size), wp, wb, _err_ptr(err_count),
-                                    _stream(block_table, stream))
+    with _on(dev):
+        workspace, wp, wb = _workspace_args(workspace, lambda: kv_fork_workspace(n, mb, block_table.device), dev, stream)
+        st = lib().sra_kv_fork_rows(block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
+                                    parents.data_ptr(), children.data_ptr(), n, rows, mb, ref_counts.shape[0],
+                                    int(block_size), wp, wb, _err_ptr(err_count, dev), _stream(block_table, stream))
     _check("sra_kv_fork_rows", st)
 
 
 def kv_resize_workspace(n: int, num_blocks: int, device) -> torch.Tensor:
     """A workspace for resize_kv_rows with n entries over a cache of num_blocks pages."""
     return _byte_workspace("sra_kv_resize_workspace_size", lib().sra_kv_resize_workspace_size(n, num_blocks), device)
+
+
+def _int64_out(t, name, n, dev):
+    _cuda(t, name)
+    if t.dtype != torch.int64 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int64 [{n}]")
+    if t.get_device() != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
 
 
 def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
@@ -728,31 +776,35 @@ def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts
     Returns (pos, slot_mapping), int64 [n]: position and cache slot of each row's last token, what
     rope_kv_store takes for a decode step; -1 for an empty row or a refused entry. A row whose pages are
     not there stays as it was and is counted in err_count."""
-    tp, sp, rp = _page_state(block_table, seq_lens, ref_counts)
-    cache, ptrs, count = _kv_caches(kv_caches)
-    _int32(rows, "rows", 1)
-    _int32(lens, "lens", 1)
-    if rows.shape != lens.shape:
+    dev = _page_state(block_table, seq_lens, ref_counts)
+    (_, nb, bs, n_kv, hd), dtype, cache_dev, ptrs, count = _kv_caches(kv_caches)
+    _int32(rows, "rows", 1, dev)
+    _int32(lens, "lens", 1, dev)
+    n = rows.shape[0]
+    if lens.shape[0] != n:
         raise ValueError("rows and lens must have the same length")
-    n = rows.numel()
-    if pos is None:
-        pos = torch.empty(n, dtype=torch.int64, device=block_table.device)
-    if slot_mapping is None:
-        slot_mapping = torch.empty(n, dtype=torch.int64, device=block_table.device)
-    for t, name in ((pos, "pos"), (slot_mapping, "slot_mapping")):
-        _cuda(t, name)
-        if t.dtype != torch.int64 or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous int64 [{n}]")
-    _same_device(block_table, cache, rows, lens, pos, slot_mapping, err_count)
-    _, nb, bs, n_kv, hd = cache.shape
-    if ref_counts.numel() != nb:
+    if cache_dev != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if pos is None and slot_mapping is None:
+        pos, slot_mapping = torch.empty(2, n, dtype=torch.int64, device=block_table.device).unbind(0)
+    else:
+        if pos is None:
+            pos = torch.empty(n, dtype=torch.int64, device=block_table.device)
+        if slot_mapping is None:
+            slot_mapping = torch.empty(n, dtype=torch.int64, device=block_table.device)
+        _int64_out(pos, "pos", n, dev)
+        _int64_out(slot_mapping, "slot_mapping", n, dev)
+    if ref_counts.shape[0] != nb:
         raise ValueError("ref_counts must have one entry per page of the caches")
-    with torch.cuda.device(block_table.device):
-        workspace, wp, wb = _workspace_args(workspace, lambda: kv_resize_workspace(n, nb, block_table.device),
-                                            block_table, stream)
-        st = lib().sra_kv_resize_rows(tp, sp, rp, rows.data_ptr(), lens.data_ptr(), n, block_table.shape[0],
-                                      block_table.shape[1], ptrs, count, nb, bs, n_kv, hd, pos.data_ptr(),
-                                      slot_mapping.data_ptr(), wp, wb, _err_ptr(err_count), _dtype(cache),
+    with _on(dev):
+        workspace, wp, wb = _workspace_args(workspace, lambda: kv_resize_workspace(n, nb, block_table.device), dev,
+                                            stream)
+        st = lib().sra_kv_resize_rows(block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
+                                      rows.data_ptr(), lens.data_ptr(), n, block_table.shape[0], block_table.shape[1],
+                                      ptrs.buffer_info()[0], count, nb, bs, n_kv, hd, pos.data_ptr(),
+                                      slot_mapping.data_ptr(), wp, wb, _err_ptr(err_count, dev), DTYPE_CODE[dtype],
                                       _stream(block_table, stream))
     _check("sra_kv_resize_rows", st)
     return pos, slot_mapping
@@ -768,23 +820,25 @@ def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_coun
                      err_count: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Move the live pages (count > 0) to the front of the caches; tables and counts follow.
     Returns num_live, int32 [1]: the pages from there on are free."""
-    tp, sp, rp = _page_state(block_table, seq_lens, ref_counts)
-    cache, ptrs, count = _kv_caches(kv_caches)
+    dev = _page_state(block_table, seq_lens, ref_counts)
+    (_, nb, bs, n_kv, hd), dtype, cache_dev, ptrs, count = _kv_caches(kv_caches)
     if num_live is None:
         num_live = torch.empty(1, dtype=torch.int32, device=block_table.device)
-    _int32(num_live, "num_live", 1)
+    _int32(num_live, "num_live", 1, dev)
     if num_live.numel() != 1:
         raise ValueError("num_live must hold one entry")
-    _same_device(block_table, cache, num_live, err_count)
-    _, nb, bs, n_kv, hd = cache.shape
-    if ref_counts.numel() != nb:
+    if cache_dev != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if ref_counts.shape[0] != nb:
         raise ValueError("ref_counts must have one entry per page of the caches")
-    with torch.cuda.device(block_table.device):
-        workspace, wp, wb = _workspace_args(workspace, lambda: kv_compact_workspace(nb, block_table.device),
-                                            block_table, stream)
-        st = lib().sra_kv_compact_pages(tp, sp, rp, block_table.shape[0], block_table.shape[1], ptrs, count, nb, bs,
-                                        n_kv, hd, num_live.data_ptr(), wp, wb, _err_ptr(err_count), _dtype(cache),
-                                        _stream(block_table, stream))
+    with _on(dev):
+        workspace, wp, wb = _workspace_args(workspace, lambda: kv_compact_workspace(nb, block_table.device), dev, stream)
+        st = lib().sra_kv_compact_pages(block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
+                                        block_table.shape[0], block_table.shape[1], ptrs.buffer_info()[0], count, nb, bs,
+                                        n_kv, hd, num_live.data_ptr(), wp, wb, _err_ptr(err_count, dev),
+                                        DTYPE_CODE[dtype], _stream(block_table, stream))
     _check("sra_kv_compact_pages", st)
     return num_live
 
@@ -814,27 +868,39 @@ def shared_prefix_attention(q: torch.Tensor, kv_cache: torch.Tensor, prefix_tabl
     request's tokens) as in paged_decode_attention; prefix_table: int32 [prefix_blocks], the pages of
     the prefix (a row of block_table that reaches past it will do); prefix_len: int32 [1] on the
     device. workspace: from shared_prefix_workspace; one is made for the call where none is given."""
-    _int32(prefix_table, "prefix_table", 1)
-    _int32(prefix_len, "prefix_len", 1)
+    _cuda(q, "q")
+    dev, dtype = q.get_device(), q.dtype
+    _int32(prefix_table, "prefix_table", 1, dev)
+    _int32(prefix_len, "prefix_len", 1, dev)
     if prefix_len.numel() != 1:
         raise ValueError("prefix_len must hold one entry")
-    out, args, err = _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count)
-    _same_device(q, prefix_table, prefix_len)
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    if not (isinstance(kv_cache, torch.Tensor) and q.dim() == 3 and dtype in DTYPE_CODE and kv_cache.dtype is dtype
+            and out.dtype is dtype and _kv_cache_ok(kv_cache) and kv_cache.get_device() == dev
+            and out.get_device() == dev and out.shape == q.shape and kv_cache.shape[4] == q.shape[2]
+            and block_table.dim() == 2 and block_table.shape[0] == q.shape[0] and seq_lens.numel() == q.shape[0]):
+        _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count)
+    _int32(block_table, "block_table", 2, dev)
+    if seq_lens.dtype is not torch.int32 or not seq_lens.is_contiguous() or seq_lens.get_device() != dev:
+        raise ValueError("seq_lens must be contiguous int32 on the queries' device")
     B, n_head, hd = q.shape
     _, nb, bs, n_kv, _ = kv_cache.shape
     mb, pb = block_table.shape[1], prefix_table.shape[0]
-    with torch.cuda.device(q.device):
+    code = DTYPE_CODE[dtype]
+    with _on(dev):
         wp, wb = None, 0
-        if workspace is None:
-            n = lib().sra_shared_prefix_workspace_size(B, n_head, n_kv, hd, pb, mb, bs, _dtype(q))
+        if workspace is not None:
+            workspace, wp, wb = _workspace_args(workspace, None, dev, stream)
+        else:
+            n = lib().sra_shared_prefix_workspace_size(B, n_head, n_kv, hd, pb, mb, bs, code)
             if n > 0:
                 workspace, wp, wb = _workspace_args(
-                    None, lambda: torch.empty(int(n), dtype=torch.uint8, device=q.device), q, stream)
-        else:
-            workspace, wp, wb = _workspace_args(workspace, None, q, stream)
+                    None, lambda: torch.empty(int(n), dtype=torch.uint8, device=q.device), dev, stream)
         st = lib().sra_shared_prefix_attention(
             q.data_ptr(), kv_cache.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(), block_table.data_ptr(),
-            seq_lens.data_ptr(), out.data_ptr(), B, n_head, n_kv, hd, args[9], args[10], nb, bs, pb, mb, args[14],
-            wp, wb, err, _dtype(q), _stream(q, stream))
+            seq_lens.data_ptr(), out.data_ptr(), B, n_head, n_kv, hd, _tok_stride(q, "q"), _tok_stride(out, "out"), nb,
+            bs, pb, mb, float(scale) if scale is not None else 1.0 / float(hd) ** 0.5, wp, wb, _err_ptr(err_count, dev),
+            code, _stream(q, stream))
     _check("sra_shared_prefix_attention", st)
     return out

@@ -1349,8 +1349,8 @@ template <typename T, int HD>
 cudaError_t launch_tail(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     auto kernel = tail_kernel<T, HD>;
     constexpr size_t smem = tail_smem(HD);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = set_smem_once(kernel, smem, true, &done);
     if (e != cudaSuccess) return e;
     const int64_t need = (a.B * a.n_kv * a.gsplits + kTailWarps - 1) / kTailWarps;
     const int64_t most = p.tail_ctas * static_cast<int64_t>(p.num_sms);

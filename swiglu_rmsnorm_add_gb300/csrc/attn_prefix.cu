@@ -509,9 +509,9 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
         return cudaErrorNotSupported;
     auto kernel = prefix_tc_kernel<T, HD>;
     constexpr size_t smem = Smem<HD>::kTotal;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     // all of the SM's shared memory, so that a CTA of the tail kernel finds room beside this one's
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = set_smem_once(kernel, smem, true, &done);
     if (e != cudaSuccess) return e;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(a.ctas_per_kv * a.n_kv)), dim3(kThreads), smem, s, pdl, 1,
                          a, tm);

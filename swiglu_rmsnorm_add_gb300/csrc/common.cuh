@@ -8,6 +8,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
 #include <mutex>
 #include <unordered_map>
 #include <utility>
@@ -38,6 +39,21 @@ inline int resident_ctas_per_sm(void (*kernel)(KArgs...), int threads, size_t sm
     std::lock_guard<std::mutex> g(mu);
     cache[key] = n;
     return n;
+}
+
+// Gives `kernel` its dynamic shared memory (and, asked for, all of the SM's shared memory as its
+// preference), once per device: `done` is a static of the caller's, a bit per device.
+template <typename... KArgs>
+inline cudaError_t set_smem_once(void (*kernel)(KArgs...), size_t smem, bool whole_sm, std::atomic<uint64_t>* done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess && whole_sm) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // A persistent grid: `needed` CTAs, capped at what is resident at once.
