@@ -685,7 +685,7 @@ SRA_API int sra_set_pdl(int enable);
  * decode-batch projection kernel of the fused entry points, up to 16 rows: variant 0,
  * OR-ed with (s << 8), s in 1..8, forces the CTAs of its cluster along K),
  * "shared_prefix" (0 = a decode call per request, 1 = the prefix on the tensor cores for all
- * requests, for bf16 / fp16 with head_dim 64 or 128 and a workspace; it also sets what
+ * requests, for bf16 / fp16 and a workspace; it also sets what
  * sra_shared_prefix_workspace_size answers).
  * variant: -1 = automatic per-shape choice (the default); otherwise an index
  * < sra_variant_count(op), optionally OR-ed with (nv << 8) to also force the

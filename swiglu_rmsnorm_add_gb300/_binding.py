@@ -262,6 +262,8 @@ def add_rmsnorm(x: torch.Tensor, res: torch.Tensor, w: torch.Tensor, out: torch.
 def _tok_stride(t: torch.Tensor, name: str) -> int:
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
+    if t.is_contiguous():
+        return t.shape[1] * t.shape[2]
     if t.numel() == 0:
         return t.shape[1] * t.shape[2]
     if t.stride(-1) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
@@ -787,14 +789,13 @@ def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts
         raise ValueError("all tensors must be on the same CUDA device")
     if dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
-    if pos is None and slot_mapping is None:
-        pos, slot_mapping = torch.empty(2, n, dtype=torch.int64, device=block_table.device).unbind(0)
+    if pos is None:
+        pos = torch.empty(n, dtype=torch.int64, device=block_table.device)
     else:
-        if pos is None:
-            pos = torch.empty(n, dtype=torch.int64, device=block_table.device)
-        if slot_mapping is None:
-            slot_mapping = torch.empty(n, dtype=torch.int64, device=block_table.device)
         _int64_out(pos, "pos", n, dev)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(n, dtype=torch.int64, device=block_table.device)
+    else:
         _int64_out(slot_mapping, "slot_mapping", n, dev)
     if ref_counts.shape[0] != nb:
         raise ValueError("ref_counts must have one entry per page of the caches")

@@ -1629,23 +1629,25 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
                        int block_size, int dtype, int sms) {
     PrefixPlan p;
     const int64_t rows = B * group;
-    if (dtype == DT_F32 || head_dim > 128 || rows < 1 || rows > (1 << 24) || prefix_blocks < 1) return p;
+    if (dtype == DT_F32 || rows < 1 || rows > (1 << 24) || prefix_blocks < 1) return p;
     // What every request reading the prefix for itself would move (L2 to SM) decides: up to 70 MB that is as
     // fast as the two or three kernels of the other path, whose fixed part is 14 to 16 us (measured at
     // 67 MB: 32 requests x 2048 tokens of 12 / 2 heads of 128 16.4 against 18.5 us, 64 x 1024 of 32 / 4 heads of
-    // 64 20.5 against 18.5; at 134 MB 24.6 and 26.7 against 19.6 and 21.6; at 34 MB 12.3 against 16.4).
+    // 64 20.5 against 18.5; at 134 MB 24.6 and 26.7 against 19.6 and 21.6; at 34 MB 12.3 against 16.4). With
+    // head_dim 256 the other form runs on the CUDA cores, at 0.9 TB/s of those reads.
     const int forced = g_force_prefix.load(std::memory_order_relaxed);
     const double moved = static_cast<double>(B) * prefix_blocks * block_size * n_kv * head_dim * 4.0;
-    if (forced == 0 || (forced < 0 && moved <= 70e6)) return p;
+    if (forced == 0 || (forced < 0 && moved <= (head_dim > 128 ? 12e6 : 70e6))) return p;
     p.use = true;
     p.rows = static_cast<int>(rows);
     // row tiles of 128, two to a CTA; the SMs of a KV head are dealt to its blocks by their tiles, and a
     // split gets one K / V tile at least
     const int64_t tiles = ceil_div(prefix_blocks * block_size, 64);
     const int mt = static_cast<int>(ceil_div(rows, 128)), per_kv = std::max(1, sms / n_kv);
-    p.pair_blocks = mt / 2;
-    if (p.pair_blocks) p.pair_splits = static_cast<int>(std::min<int64_t>(std::max(1, 2 * per_kv / mt), tiles));
-    if (mt & 1)
+    p.pair_blocks = head_dim > 128 ? mt : mt / 2;  // (head_dim 256: a row tile to a CTA)
+    const int share = head_dim > 128 ? 1 : 2;  // row tiles of a pair block
+    if (p.pair_blocks) p.pair_splits = static_cast<int>(std::min<int64_t>(std::max(1, share * per_kv / mt), tiles));
+    if (head_dim <= 128 && (mt & 1))
         p.single_splits = static_cast<int>(
             std::min<int64_t>(std::max(1, per_kv - p.pair_blocks * p.pair_splits), ceil_div(tiles, 2)));
     p.ctas_per_kv = p.pair_blocks * p.pair_splits + p.single_splits;
@@ -1760,11 +1762,14 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const PrefixPlan pp = plan_prefix(B, group, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size,
                                       dtype, sms);
-    if (g_force_prefix.load(std::memory_order_relaxed) == 1 && (!workspace || !pp.use || !plan.tensor_cores))
-        return SRA_ERR_VARIANT;
-    if (!workspace || !pp.use || !plan.tensor_cores || static_cast<int64_t>(prefix_tc_smem(head_dim)) > limit - 512 ||
-        num_blocks * block_size >= (int64_t(1) << 31) - 64)
+    // the tensor-core path reads queries four bytes at a time
+    const bool together = workspace && pp.use && (reinterpret_cast<uintptr_t>(q) & 3u) == 0 && q_tok_stride % 2 == 0 &&
+                          static_cast<int64_t>(prefix_tc_smem(head_dim)) <= limit - 512 &&
+                          num_blocks * block_size < (int64_t(1) << 31) - 64;
+    if (!together) {
+        if (g_force_prefix.load(std::memory_order_relaxed) == 1) return SRA_ERR_VARIANT;
         return status_from(launch_prefix_tail(a, plan, dtype, s));
+    }
     if (workspace_bytes < pp.bytes() || !aligned16(workspace)) return SRA_ERR_ARG;
     const Span sws = span_of(workspace, 1, 0, pp.bytes(), 1);
     if (overlap(sws, so) || overlap(sws, sq) || overlap(sws, serr)) return SRA_ERR_ALIAS;
@@ -1816,7 +1821,7 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     const double prefix_us = 1.4 * ceil_div(prefix_blocks * block_size, 64) * ceil_div(pp.rows, 256) * n_kv_head / sms;
     const double tail_us = 1.2 / 4 / 16 * 0.5 * std::max<int64_t>(0, max_blocks_per_seq - prefix_blocks) * block_size *
                            static_cast<double>(B * n_kv_head) / sms;
-    plan.tail_ctas = tail_us > prefix_us ? 3 : 1;
+    plan.tail_ctas = head_dim > 128 ? 1 : tail_us > prefix_us ? 3 : 1;
     rs = status_from(launch_prefix_tail(a, plan, dtype, s));
     return rs != SRA_OK ? rs : status_from(launch_prefix_merge(f, head_dim, dtype, s));
 }

@@ -937,8 +937,8 @@ cudaError_t launch_merge(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
 // only its last CTA does, at its end, so that whatever waits for this grid finds that one complete
 // too. What precedes the prefix's kernel is complete when this one starts (all CTAs of that one have waited
 // for it before they let this one start), and everything is read through the L2, which those grids'
-// writes have reached. Four warps with a tile each, at most 128 registers: a CTA fits beside one of the
-// prefix's on an SM, whose tensor cores and this one's memory traffic then overlap.
+// writes have reached. Four warps with a tile each, at most 128 registers (up to head_dim 128): a CTA fits
+// beside one of the prefix's on an SM, whose tensor cores and this one's memory traffic then overlap.
 // K's part of a warp's tile is copied again as soon as S is known, V's as soon as it has been used.
 // The products have the tokens (S) or the dims (O) as the rows of the MMA and the up to eight query heads
 // as its eight columns, so no row is empty: S^T = K Q^T and O^T = V^T P^T, 32 MMAs per 32 tokens at
@@ -1076,7 +1076,7 @@ __host__ __device__ constexpr size_t tail_smem(int HD) {
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kTailThreads, 4) tail_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(AttnArgs a) {
     constexpr int CPR = HD * 2 / 16, KS = HD / 16, TE = kTailTok * HD;
     constexpr int RPI = 32 / CPR;  // rows per copy instruction (CPR lanes per row)
     extern __shared__ __align__(16) unsigned char smem[];
@@ -1667,8 +1667,10 @@ cudaError_t launch_stages(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) 
 template <typename T>
 cudaError_t launch_prefix_typed(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        if (p.tensor_cores && a.tail_only)
-            return p.head_dim == 64 ? launch_tail<T, 64>(a, p, s) : launch_tail<T, 128>(a, p, s);
+        if (a.tail_only)
+            return p.head_dim == 64    ? launch_tail<T, 64>(a, p, s)
+                   : p.head_dim == 128 ? launch_tail<T, 128>(a, p, s)
+                                       : launch_tail<T, 256>(a, p, s);
         if (p.tensor_cores)
             return p.head_dim == 64 ? launch_mma<T, 64, 8, true>(a, p, s) : launch_mma<T, 128, 8, true>(a, p, s);
     }

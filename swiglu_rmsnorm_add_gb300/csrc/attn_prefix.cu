@@ -30,9 +30,15 @@ struct Smem {
     static constexpr int kHalfBytes = kTok * 128;              // 64 dims of a K or V tile's rows
     static constexpr int kTileBytes = kHalves * kHalfBytes;    // a K or V tile
     static constexpr int kQHalf = kRows * 128, kQBytes = kHalves * kQHalf;
+    // head_dim 256: one row tile, its streams take a half of V's dims each (and compute the same S and P)
+    static constexpr bool kSplitV = HD > 128;
+    static constexpr int kDims = kSplitV ? 128 : HD;           // of a stream's O
+    static constexpr int kQTiles = kSplitV ? 1 : 2;
     // K or V tiles in flight; what is left of an SM's shared memory takes a CTA of the tail kernel (attn.cu)
-    static constexpr int kStages = HD == 128 ? 5 : 10;
-    static constexpr size_t kTotal = 1024 + 2 * static_cast<size_t>(kQBytes) + kStages * static_cast<size_t>(kTileBytes);
+    // for head_dim 64 and 128
+    static constexpr int kStages = HD == 64 ? 10 : 5;
+    static constexpr size_t kTotal =
+        1024 + kQTiles * static_cast<size_t>(kQBytes) + kStages * static_cast<size_t>(kTileBytes);
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -61,13 +67,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// What CTA `c` of a KV head's works on.
+// What CTA `c` of a KV head's works on (RPB: query rows of a pair block).
 struct Work {
     int row0;      // first query row
     bool pair;     // two row tiles on the same K / V tiles, or one row tile on two K / V tiles at a time
     int t0, n;     // K / V tiles
     int rec;       // its record of each row
 };
+template <int RPB>
 __device__ __forceinline__ Work work_of(const PrefixArgs& a, int c, int64_t tiles) {
     Work w;
     int split, splits;
@@ -75,12 +82,12 @@ __device__ __forceinline__ Work work_of(const PrefixArgs& a, int c, int64_t tile
         const int blk = c / a.pair_splits;
         split = c - blk * a.pair_splits, splits = a.pair_splits;
         w.pair = true;
-        w.row0 = blk * 2 * kRows;
+        w.row0 = blk * RPB;
         w.rec = split;
     } else {
         split = c - a.pair_blocks * a.pair_splits, splits = a.single_splits;
         w.pair = false;
-        w.row0 = a.pair_blocks * 2 * kRows;
+        w.row0 = a.pair_blocks * RPB;
         w.rec = split;
     }
     const int64_t b = tiles * split / splits, e = tiles * (split + 1) / splits;
@@ -124,6 +131,8 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 // such overlap: measured 4700 clocks per 128 tokens of both streams, against 2070 of tensor-core work.
 // The price is that S in tiles of 64 tokens reads Q from shared memory twice as often: 48 clocks per
 // K step of 16 instead of 2 x 32, shared-memory bandwidth, so a tile cannot run above 81 % of the peak.)
+// With head_dim 256 O alone would fill tensor memory for two row tiles, so the streams share a row tile and a
+// CTA's S and take half of V's dims each; S is computed twice (62 % of the work is needed work).
 template <typename T, int HD>
 __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC) {
     using L = Smem<HD>;
@@ -132,8 +141,8 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
     constexpr uint32_t kS = 0, kP = 128, kO = 256;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char* qs = smem;                       // two Q tiles
-    unsigned char* ring = smem + 2 * L::kQBytes;    // ST K / V tiles
+    unsigned char* qs = smem;                              // two Q tiles (head_dim 256: one)
+    unsigned char* ring = smem + L::kQTiles * L::kQBytes;  // ST K / V tiles
     __shared__ uint64_t full[ST], empty[ST], s_full[2], s_free[2], p_full[2][2], pv_done[2][2];
     __shared__ uint32_t tmem_base;
     __shared__ int s_ragged;
@@ -162,7 +171,7 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
     const int kvh = blockIdx.x / a.ctas_per_kv;
     const int64_t pages = whole_pages(a);
     const int ppt = kTok >> (__ffs(a.block_size) - 1);  // pages of a tile
-    const Work w = work_of(a, blockIdx.x - kvh * a.ctas_per_kv, (pages + ppt - 1) / ppt);
+    const Work w = work_of<L::kQTiles * kRows>(a, blockIdx.x - kvh * a.ctas_per_kv, (pages + ppt - 1) / ppt);
     const int tpr = w.pair ? 1 : 2;  // tiles per round
     const int n0 = w.pair ? w.n : (w.n + 1) / 2, n1 = w.pair ? w.n : w.n / 2;  // tiles of the streams
     bool dead = false;  // a bounded wait ran out (counted): this thread waits no more
@@ -214,8 +223,8 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         // the query rows, swizzled as a TMA copy would leave them (rows past the last are zero), and
         // whether every page of this CTA's tiles counts
         constexpr int kSetup = kThreads - 64, kChunks = HD / 8;
-        constexpr int kEach = (2 * kRows * kChunks + kSetup - 1) / kSetup;  // 16-byte chunks a thread moves
-        const int tid = threadIdx.x - (warp < 3 ? 32 : 64), count = w.n > 0 ? (w.pair ? 2 : 1) * kRows * kChunks : 0;
+        constexpr int kEach = (L::kQTiles * kRows * kChunks + kSetup - 1) / kSetup;  // 16-byte chunks a thread moves
+        const int tid = threadIdx.x - (warp < 3 ? 32 : 64), count = w.n > 0 ? (w.pair ? L::kQTiles : 1) * kRows * kChunks : 0;
         uint4 v[kEach];
         // a thread's chunks share their place in the row and lie kStep rows apart: one division, then steps
         constexpr int kStep = kSetup / kChunks;
@@ -280,11 +289,11 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         // 1290 of tensor-core work.)
         const int x = warp - 1, n = x == 0 ? n0 : n1;
         constexpr uint32_t kIdescS = tc::idesc_f16(kBf16, kRows, kTok);
-        constexpr uint32_t kIdescO = tc::idesc_f16(kBf16, kRows, HD) | tc::kTransposeB;
+        constexpr uint32_t kIdescO = tc::idesc_f16(kBf16, kRows, L::kDims) | tc::kTransposeB;
         const uint32_t elected = tc::elect();
-        const uint32_t q = tc::sdesc_lo(qs, 16) + (w.pair ? x : 0) * (L::kQBytes / 16);
-        const uint32_t k_lo = tc::sdesc_lo(ring, 16), v_lo = tc::sdesc_lo(ring, L::kHalfBytes);
-        const uint32_t tS = tmem + kS + x * kTok, tP = tmem + kP + x * 64, tO = tmem + kO + x * HD;
+        const uint32_t q = tc::sdesc_lo(qs, 16) + (w.pair && !L::kSplitV ? x : 0) * (L::kQBytes / 16);
+        const uint32_t k_lo = tc::sdesc_lo(ring, 16), v_lo = tc::sdesc_lo(ring + (L::kSplitV ? 2 * x * L::kHalfBytes : 0), L::kHalfBytes);
+        const uint32_t tS = tmem + kS + x * kTok, tP = tmem + kP + x * 64, tO = tmem + kO + x * L::kDims;
         Place<ST> at;  // of the round's tiles; a single block's stream 1 takes the second of them
         auto take = [&]() -> int {
             Place<ST> mine = at;
@@ -331,7 +340,8 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         // and O in tensor memory is scaled seldom.
         const int x = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t tS = tmem + lanes + kS + x * kTok, tP = tmem + lanes + kP + x * 64, tO = tmem + lanes + kO + x * HD;
+        const uint32_t tS = tmem + lanes + kS + x * kTok, tP = tmem + lanes + kP + x * 64,
+                       tO = tmem + lanes + kO + x * L::kDims;
         const int n = x == 0 ? n0 : n1;
         const bool ragged = s_ragged != 0;
         const int bs_log2 = __ffs(a.block_size) - 1;
@@ -374,7 +384,7 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
                     wait(&pv_done[x][(i - 1) & 1], (i - 1) / 2);
                     tc::fence_after();
 #pragma unroll 1
-                    for (int d = 0; d < HD; d += 16) {
+                    for (int d = 0; d < L::kDims; d += 16) {
                         uint32_t o[16];
                         tc::ld16(tO + d, o);
                         tc::wait_ld();
@@ -419,7 +429,7 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         // one bulk copy per row from shared memory (a thread's row, padded by 16 bytes: rows apart by a
         // multiple of 128 bytes would meet in the same banks), over the tiles, which are done with.
         // (Stored from the threads' registers, 16 bytes per row and instruction, it took 8 us of the call.)
-        constexpr int kRowBytes = HD * 4 + 16;
+        constexpr int kRowBytes = L::kDims * 4 + 16;
         const int rr = quarter * 32 + lane;
         unsigned char* mine = smem + (x * kRows + rr) * kRowBytes;
         if (n > 0) {
@@ -435,7 +445,7 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         if (w.pair || x == 1) {
             if (n > 0) {
 #pragma unroll 1
-                for (int d = 0; d < HD; d += 32) {
+                for (int d = 0; d < L::kDims; d += 32) {
                     uint32_t v[32];
                     tc::ld32(tO + d, v);
                     tc::wait_ld();
@@ -457,7 +467,7 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
                 const bool keep = wa != 0.0f;  // a part without weight is not read: it may hold anything
                 m = M;
 #pragma unroll 1
-                for (int d = 0; d < HD; d += 32) {
+                for (int d = 0; d < L::kDims; d += 32) {
                     uint32_t v[32];
                     tc::ld32(tO + d, v);
                     tc::wait_ld();
@@ -474,14 +484,15 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
                 }
             }
         }
-        const int r = w.row0 + (w.pair ? x * kRows : 0) + rr;
+        const int r = w.row0 + (w.pair && !L::kSplitV ? x * kRows : 0) + rr;
         if ((w.pair || x == 0) && r < a.rows) {
             const int64_t at = (static_cast<int64_t>(kvh) * a.records + w.rec) * a.rows + r;
-            a.part_ml[at] = make_float2(m, l);
+            if (!L::kSplitV || x == 0) a.part_ml[at] = make_float2(m, l);
             if (n > 0) {
                 fence_proxy_async();
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a.part_o + at * HD),
-                             "r"(smem_u32(mine)), "r"(HD * 4)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                 a.part_o + at * HD + (L::kSplitV ? x * L::kDims : 0)),
+                             "r"(smem_u32(mine)), "r"(L::kDims * 4)
                              : "memory");
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -539,7 +550,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     len = len < 0 ? 0 : (len > a.cap ? a.cap : len);
     const int64_t row = b * a.group + g;
     const int tile = static_cast<int>(row / kRows);
-    int recs = tile < 2 * a.pair_blocks ? a.pair_splits : a.single_splits;
+    int recs = tile < (HD > 128 ? 1 : 2) * a.pair_blocks ? a.pair_splits : a.single_splits;
     const int64_t lo = len >= behind ? behind : 0;
     if (len < behind) recs = 0;
     const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows + row;  // record i: i * rows further
@@ -615,20 +626,30 @@ cudaError_t merge_typed(const PrefixArgs& a, int head_dim, cudaStream_t s) {
     switch (head_dim) {
         case 64: return launch_kernel(merge_kernel<T, 64>, grid, block, 0, s, true, 1, a);
         case 128: return launch_kernel(merge_kernel<T, 128>, grid, block, 0, s, true, 1, a);
+        case 256: return launch_kernel(merge_kernel<T, 256>, grid, block, 0, s, true, 1, a);
         default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace prefix
 
-size_t prefix_tc_smem(int head_dim) { return head_dim == 64 ? prefix::Smem<64>::kTotal : prefix::Smem<128>::kTotal; }
+size_t prefix_tc_smem(int head_dim) {
+    return head_dim == 64 ? prefix::Smem<64>::kTotal : head_dim == 128 ? prefix::Smem<128>::kTotal : prefix::Smem<256>::kTotal;
+}
+
+template <typename T>
+static cudaError_t launch_prefix_tc_typed(const PrefixArgs& a, const void* cache, int head_dim, bool pdl, cudaStream_t s) {
+    switch (head_dim) {
+        case 64: return prefix::launch_tc<T, 64>(a, cache, pdl, s);
+        case 128: return prefix::launch_tc<T, 128>(a, cache, pdl, s);
+        case 256: return prefix::launch_tc<T, 256>(a, cache, pdl, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
 
 cudaError_t launch_prefix_tc(const PrefixArgs& a, const void* cache, int head_dim, int dtype, bool pdl, cudaStream_t s) {
-    if (dtype == DT_BF16)
-        return head_dim == 64 ? prefix::launch_tc<__nv_bfloat16, 64>(a, cache, pdl, s)
-                              : prefix::launch_tc<__nv_bfloat16, 128>(a, cache, pdl, s);
-    return head_dim == 64 ? prefix::launch_tc<__half, 64>(a, cache, pdl, s)
-                          : prefix::launch_tc<__half, 128>(a, cache, pdl, s);
+    return dtype == DT_BF16 ? launch_prefix_tc_typed<__nv_bfloat16>(a, cache, head_dim, pdl, s)
+                            : launch_prefix_tc_typed<__half>(a, cache, head_dim, pdl, s);
 }
 
 cudaError_t launch_prefix_merge(const PrefixArgs& a, int head_dim, int dtype, cudaStream_t s) {
