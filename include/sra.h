@@ -586,12 +586,12 @@ SRA_API int64_t sra_kv_compact_workspace_size(int64_t num_blocks);
  * tokens that it has; one without tokens (or none whose score is above -inf) gets zeros; NaN in what
  * a request attends to gives NaN.
  *
- * The tensor-core path takes the queries of all requests that share a KV head as the rows of one
- * product with the prefix's whole pages, splits it over the GPU along the prefix, takes each
- * request's own tokens as sra_paged_decode_attention does, and merges the parts through their
- * maxima and sums of exponentials (fp32). In that path the probabilities are rounded once to
- * the dtype before they multiply V (fp32 sums); the path without a workspace keeps them to 16 bits or
- * more.
+ * With a workspace the queries of all requests that share a KV head are the rows of one product with
+ * the prefix's whole pages, split over the GPU along the prefix (bf16 and fp16 on the fifth-generation
+ * tensor cores, fp32 on the CUDA cores); each request's own tokens follow as in
+ * sra_paged_decode_attention, and the parts are merged through their maxima and sums of
+ * exponentials (fp32). In bf16 and fp16 the probabilities are then rounded once to the dtype before
+ * they multiply V (fp32 sums); the path without a workspace keeps them to 16 bits or more.
  *
  * q, kv_cache, out, scale: as in sra_paged_decode_attention. prefix_table: int32 [prefix_blocks];
  * prefix_len: device int32, one entry; block_table: int32 [B, max_blocks_per_seq]; seq_lens: int32 [B].
@@ -684,9 +684,8 @@ SRA_API int sra_set_pdl(int enable);
  * of the projection over h), "linear_narrow" (the
  * decode-batch projection kernel of the fused entry points, up to 16 rows: variant 0,
  * OR-ed with (s << 8), s in 1..8, forces the CTAs of its cluster along K),
- * "shared_prefix" (0 = a decode call per request, 1 = the prefix on the tensor cores for all
- * requests, for bf16 / fp16 and a workspace; it also sets what
- * sra_shared_prefix_workspace_size answers).
+ * "shared_prefix" (0 = a decode call per request, 1 = the prefix for all requests at once, given a
+ * workspace; it also sets what sra_shared_prefix_workspace_size answers).
  * variant: -1 = automatic per-shape choice (the default); otherwise an index
  * < sra_variant_count(op), optionally OR-ed with (nv << 8) to also force the
  * number of 16-byte accesses each thread holds in the register variants of

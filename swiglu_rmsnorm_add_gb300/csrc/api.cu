@@ -1629,25 +1629,28 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
                        int block_size, int dtype, int sms) {
     PrefixPlan p;
     const int64_t rows = B * group;
-    if (dtype == DT_F32 || rows < 1 || rows > (1 << 24) || prefix_blocks < 1) return p;
+    if (rows < 1 || rows > (1 << 24) || prefix_blocks < 1) return p;
     // What every request reading the prefix for itself would move (L2 to SM) decides: up to 70 MB that is as
     // fast as the two or three kernels of the other path, whose fixed part is 14 to 16 us (measured at
     // 67 MB: 32 requests x 2048 tokens of 12 / 2 heads of 128 16.4 against 18.5 us, 64 x 1024 of 32 / 4 heads of
     // 64 20.5 against 18.5; at 134 MB 24.6 and 26.7 against 19.6 and 21.6; at 34 MB 12.3 against 16.4). With
-    // head_dim 256 the other form runs on the CUDA cores, at 0.9 TB/s of those reads.
+    // head_dim 256 or fp32 the other form runs on the CUDA cores, at 0.9 to 1.5 TB/s of those reads.
     const int forced = g_force_prefix.load(std::memory_order_relaxed);
-    const double moved = static_cast<double>(B) * prefix_blocks * block_size * n_kv * head_dim * 4.0;
-    if (forced == 0 || (forced < 0 && moved <= (head_dim > 128 ? 12e6 : 70e6))) return p;
+    const double moved = static_cast<double>(B) * prefix_blocks * block_size * n_kv * head_dim * 2.0 * elem_bytes(dtype);
+    const bool cores = head_dim > 128 || dtype == DT_F32;
+    if (forced == 0 || (forced < 0 && moved <= (cores ? 12e6 : 70e6))) return p;
     p.use = true;
     p.rows = static_cast<int>(rows);
     // row tiles of 128, two to a CTA; the SMs of a KV head are dealt to its blocks by their tiles, and a
-    // split gets one K / V tile at least
+    // split gets one K / V tile at least. (head_dim 256: one row tile to a CTA; fp32: 64 rows, and three, one
+    // and one CTAs an SM for head_dim 64, 128 and 256.)
+    const bool f32 = dtype == DT_F32, lone = f32 || head_dim > 128;
     const int64_t tiles = ceil_div(prefix_blocks * block_size, 64);
-    const int mt = static_cast<int>(ceil_div(rows, 128)), per_kv = std::max(1, sms / n_kv);
-    p.pair_blocks = head_dim > 128 ? mt : mt / 2;  // (head_dim 256: a row tile to a CTA)
-    const int share = head_dim > 128 ? 1 : 2;  // row tiles of a pair block
+    const int mt = static_cast<int>(ceil_div(rows, f32 ? 64 : 128)), share = lone ? 1 : 2;
+    const int per_kv = std::max(1, (f32 && head_dim == 64 ? 3 * sms : sms) / n_kv);
+    p.pair_blocks = lone ? mt : mt / 2;
     if (p.pair_blocks) p.pair_splits = static_cast<int>(std::min<int64_t>(std::max(1, share * per_kv / mt), tiles));
-    if (head_dim <= 128 && (mt & 1))
+    if (!lone && (mt & 1))
         p.single_splits = static_cast<int>(
             std::min<int64_t>(std::max(1, per_kv - p.pair_blocks * p.pair_splits), ceil_div(tiles, 2)));
     p.ctas_per_kv = p.pair_blocks * p.pair_splits + p.single_splits;
@@ -1656,6 +1659,11 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
     // least (a part grows where a request has more)
     const int64_t groups = B * n_kv, own = std::max<int64_t>(0, max_blocks - prefix_blocks + 1) * block_size;
     p.tail_splits = static_cast<int>(std::min<int64_t>(std::max<int64_t>(16, ceil_div(own, 128) + 1), 256));
+    if (f32) {  // the decode kernel's splits of 64 tokens or more, two CTAs an SM
+        p.tail_splits = 1;
+        while (p.tail_splits < 16 && groups * p.tail_splits < 2 * static_cast<int64_t>(sms) && own >= 128 * p.tail_splits)
+            p.tail_splits *= 2;
+    }
     if (groups * p.tail_splits >= (int64_t(1) << 30)) {
         p.use = false;
         return p;
@@ -1763,8 +1771,9 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     const PrefixPlan pp = plan_prefix(B, group, n_kv_head, head_dim, prefix_blocks, max_blocks_per_seq, block_size,
                                       dtype, sms);
     // the tensor-core path reads queries four bytes at a time
-    const bool together = workspace && pp.use && (reinterpret_cast<uintptr_t>(q) & 3u) == 0 && q_tok_stride % 2 == 0 &&
-                          static_cast<int64_t>(prefix_tc_smem(head_dim)) <= limit - 512 &&
+    const bool together = workspace && pp.use && (reinterpret_cast<uintptr_t>(q) & 3u) == 0 &&
+                          (dtype == DT_F32 || q_tok_stride % 2 == 0) &&
+                          static_cast<int64_t>(prefix_smem(head_dim, dtype)) <= limit - 512 &&
                           num_blocks * block_size < (int64_t(1) << 31) - 64;
     if (!together) {
         if (g_force_prefix.load(std::memory_order_relaxed) == 1) return SRA_ERR_VARIANT;
@@ -1805,14 +1814,14 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     f.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp.ml_bytes);
     int64_t* tail_at = reinterpret_cast<int64_t*>(static_cast<char*>(workspace) + pp.ml_bytes + pp.o_bytes);
     float* tail = reinterpret_cast<float*>(reinterpret_cast<char*>(tail_at) + pp.at_bytes);
-    f.tail_at = tail_at;
+    f.tail_at = dtype == DT_F32 ? nullptr : tail_at;
     a.ws_tail_at = tail_at;
     f.tail = tail;
     f.tail_splits = pp.tail_splits;
     a.tail_only = true;
     a.ws_part = tail;
     a.gsplits = pp.tail_splits;
-    int rs = status_from(launch_prefix_tc(f, kv_cache, head_dim, dtype, plan.pdl, s));
+    int rs = status_from(launch_prefix_whole(f, kv_cache, head_dim, dtype, plan.pdl, s));
     if (rs != SRA_OK) return rs;
     // The tail has room for one CTA per SM beside the prefix's kernel, for three once that is done: three where
     // its work is the longer one. Both from the table sizes, as tokens' cost: the prefix takes about 1.4 us per
@@ -1844,7 +1853,7 @@ const char* sra_variant_name(const char* op, int variant) {
     static const char* const glu_names[] = {"cols_rows", "cols_rows_regs"};
     static const char* const attn_names[] = {"cuda_cores", "mma_sync", "mma_sync_tma"};
     static const char* const lin_names[] = {"mma_sync", "tcgen05"};
-    static const char* const prefix_names[] = {"decode", "tcgen05"};
+    static const char* const prefix_names[] = {"decode", "batched"};
     static const char* const narrow_names[] = {"cluster_k_split"};
     const int n = variant_count(op);
     if (n < 0 || variant < 0 || variant >= n) return nullptr;

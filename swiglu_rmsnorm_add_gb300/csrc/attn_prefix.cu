@@ -528,6 +528,172 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
                          a, tm);
 }
 
+// ------------------------------------------------------------------ fp32
+// The same cut for fp32, on the CUDA cores (the tensor cores have no fp32 products, and parts of fewer bits
+// would have to be paid for six times): a CTA takes 64 query rows through its split's K / V tiles of 64
+// tokens. A thread holds 4 rows x 4 tokens of S and 4 rows x head_dim / 16 dims of O, so that a load of 16
+// bytes from shared memory feeds 5 (S) to 6 (O) FMAs a lane; the rows of its operands are padded by 16 bytes, so
+// that the lanes of a load meet different banks. K of the next tile is copied under P V, V under Q K^T.
+constexpr int kF32Rows = 64, kF32Tok = 64, kF32Threads = 256;
+template <int HD>
+struct SmemF32 {
+    static constexpr int kRow = HD + 4;        // floats of a Q, K or V row
+    static constexpr int kPRow = kF32Tok + 4;  // floats of a P row
+    static constexpr size_t kTotal = (static_cast<size_t>(kF32Rows + 2 * kF32Tok) * kRow + kF32Rows * kPRow) * 4;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kF32Threads) prefix_f32_kernel(PrefixArgs a, const float* cache) {
+    using L = SmemF32<HD>;
+    constexpr int RS = L::kRow, PS = L::kPRow, J = HD / 64, CPR = HD / 4;
+    extern __shared__ __align__(16) float sm[];
+    float *qs = sm, *ks = qs + kF32Rows * RS, *vs = ks + kF32Tok * RS, *ps = vs + kF32Tok * RS;
+    __shared__ int page[2][kF32Tok / 8];
+    const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16;  // rows 4 tr + i; tokens tc + 16 j, dims 4 tc + 64 j
+    pdl_enter();
+    const int kvh = blockIdx.x / a.ctas_per_kv;
+    const int64_t pages = whole_pages(a);
+    const int bs_log2 = __ffs(a.block_size) - 1, ppt = kF32Tok >> bs_log2;
+    const Work w = work_of<kF32Rows>(a, blockIdx.x - kvh * a.ctas_per_kv, (pages + ppt - 1) / ppt);
+    const int64_t tok_stride = static_cast<int64_t>(a.n_kv) * HD, v_plane = a.num_blocks * a.block_size * tok_stride;
+    // the pages of tile t (-1: does not count), then its rows of a plane, zero where they do not count
+    auto find = [&](int t) {
+        if (tid < ppt) {
+            const int64_t j = static_cast<int64_t>(w.t0 + t) * ppt + tid;
+            const int32_t e = j < pages ? a.ptable[j] : -1;
+            page[t & 1][tid] = e >= 0 && e < a.num_blocks ? e : -1;
+        }
+    };
+    auto copy = [&](float* dst, int t, int64_t plane) {
+        for (int i = tid; i < kF32Tok * CPR; i += kF32Threads) {
+            const int r = i / CPR, c = i % CPR, e = page[t & 1][r >> bs_log2];
+            const float* src = cache + plane +
+                               ((static_cast<int64_t>(e) << bs_log2) + (r & (a.block_size - 1))) * tok_stride + kvh * HD + c * 4;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * RS + c * 4)),
+                         "l"(e >= 0 ? src : cache), "r"(e >= 0 ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (w.n > 0) {
+        find(0);
+        for (int i = tid; i < kF32Rows * HD; i += kF32Threads) {
+            const int r = i / HD, d = i % HD, row = w.row0 + r;
+            float v = 0.0f;
+            if (row < a.rows) {
+                const int b = row / a.group, g = row - b * a.group;
+                v = static_cast<const float*>(a.q)[b * a.qs + (kvh * a.group + g) * HD + d];
+            }
+            qs[r * RS + d] = a.negate ? -v : v;
+        }
+        __syncthreads();
+        copy(ks, 0, 0);
+    }
+    float m[4], l[4], o[4][4 * J];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY, l[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4 * J; ++j) o[i][j] = 0.0f;
+    }
+    for (int t = 0; t < w.n; ++t) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // K has landed; everyone is done with V and P of the tile before
+        copy(vs, t, v_plane);
+        if (t + 1 < w.n) find(t + 1);
+        float s[4][4] = {};
+#pragma unroll 4
+        for (int d = 0; d < HD; d += 4) {
+            float4 qv[4], kv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(qs + (4 * tr + i) * RS + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (tc + 16 * j) * RS + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+                    s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+                    s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+                    s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                }
+        }
+        // the running softmax: a row's 64 scores lie in 16 lanes
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = page[t & 1][(tc + 16 * j) >> bs_log2] >= 0 ? s[i][j] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float now = fmaxf(m[i], mx), base = now == -INFINITY ? 0.0f : now;
+            const float f = now == -INFINITY ? 1.0f : exp2f(m[i] - now);
+            m[i] = now;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - base);
+                ps[(4 * tr + i) * PS + tc + 16 * j] = p;
+                sum += p;
+            }
+            l[i] = l[i] * f + sum;  // this lane's tokens' part
+#pragma unroll
+            for (int j = 0; j < 4 * J; ++j) o[i][j] *= f;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // V has landed, P is written, everyone is done with K
+        if (t + 1 < w.n) copy(ks, t + 1, 0);
+#pragma unroll 2
+        for (int k = 0; k < kF32Tok; k += 4) {
+            float4 pv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(ps + (4 * tr + i) * PS + k);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const float4 v = *reinterpret_cast<const float4*>(vs + (k + u) * RS + 4 * tc + 64 * j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p = u == 0 ? pv[i].x : u == 1 ? pv[i].y : u == 2 ? pv[i].z : pv[i].w;
+                        o[i][4 * j] = fmaf(p, v.x, o[i][4 * j]);
+                        o[i][4 * j + 1] = fmaf(p, v.y, o[i][4 * j + 1]);
+                        o[i][4 * j + 2] = fmaf(p, v.z, o[i][4 * j + 2]);
+                        o[i][4 * j + 3] = fmaf(p, v.w, o[i][4 * j + 3]);
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = w.row0 + 4 * tr + i;
+#pragma unroll
+        for (int x = 1; x < 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+        if (row >= a.rows) continue;
+        const int64_t at = (static_cast<int64_t>(kvh) * a.records + w.rec) * a.rows + row;
+        if (tc == 0) a.part_ml[at] = make_float2(m[i], l[i]);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            *reinterpret_cast<float4*>(a.part_o + at * HD + 4 * tc + 64 * j) =
+                make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
+    }
+}
+
+template <int HD>
+cudaError_t launch_f32(const PrefixArgs& a, const void* cache, bool pdl, cudaStream_t s) {
+    auto kernel = prefix_f32_kernel<HD>;
+    constexpr size_t smem = SmemF32<HD>::kTotal;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = set_smem_once(kernel, smem, false, &done);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(a.ctas_per_kv * a.n_kv)), dim3(kF32Threads), smem, s, pdl, 1,
+                         a, static_cast<const float*>(cache));
+}
+
 // ------------------------------------------------------------------ merge
 // CTA = one output row (request, query head). Its parts are the prefix's records, unless the request
 // does not reach past the prefix's whole pages (then its own part holds all of its tokens), and its own
@@ -546,7 +712,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     const int kvh = h / a.group, g = h - kvh * a.group;
     pdl_enter();
     int64_t len = a.seq_lens[b];
-    const int64_t part = a.tail_at[a.B], before = a.tail_at[b], behind = whole_pages(a) * a.block_size;
+    const bool stream = a.tail_at != nullptr;  // fp32: every split of the own tokens leaves a record
+    const int64_t part = stream ? a.tail_at[a.B] : 1, before = stream ? a.tail_at[b] : 0, behind = whole_pages(a) * a.block_size;
     len = len < 0 ? 0 : (len > a.cap ? a.cap : len);
     const int64_t row = b * a.group + g;
     const int tile = static_cast<int>(row / kRows);
@@ -557,7 +724,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     const float* tail = a.tail + (b * a.n_kv + kvh) * a.tail_splits * (16 + 8 * HD);
     // its own tokens' records: the parts of the tail's stream that its tiles touch
     const int64_t tiles = (len - lo + kTailTok - 1) / kTailTok;
-    const int all = recs + (tiles > 0 ? static_cast<int>((before + tiles - 1) / part - before / part + 1) : 0);
+    const int all = recs + (!stream     ? a.tail_splits
+                            : tiles > 0 ? static_cast<int>((before + tiles - 1) / part - before / part + 1)
+                                        : 0);
     float m = -INFINITY, l = 0.0f, acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.0f;
@@ -633,7 +802,11 @@ cudaError_t merge_typed(const PrefixArgs& a, int head_dim, cudaStream_t s) {
 
 }  // namespace prefix
 
-size_t prefix_tc_smem(int head_dim) {
+size_t prefix_smem(int head_dim, int dtype) {
+    if (dtype == DT_F32)
+        return head_dim == 64    ? prefix::SmemF32<64>::kTotal
+               : head_dim == 128 ? prefix::SmemF32<128>::kTotal
+                                 : prefix::SmemF32<256>::kTotal;
     return head_dim == 64 ? prefix::Smem<64>::kTotal : head_dim == 128 ? prefix::Smem<128>::kTotal : prefix::Smem<256>::kTotal;
 }
 
@@ -647,7 +820,15 @@ static cudaError_t launch_prefix_tc_typed(const PrefixArgs& a, const void* cache
     }
 }
 
-cudaError_t launch_prefix_tc(const PrefixArgs& a, const void* cache, int head_dim, int dtype, bool pdl, cudaStream_t s) {
+cudaError_t launch_prefix_whole(const PrefixArgs& a, const void* cache, int head_dim, int dtype, bool pdl, cudaStream_t s) {
+    if (dtype == DT_F32) {
+        switch (head_dim) {
+            case 64: return prefix::launch_f32<64>(a, cache, pdl, s);
+            case 128: return prefix::launch_f32<128>(a, cache, pdl, s);
+            case 256: return prefix::launch_f32<256>(a, cache, pdl, s);
+            default: return cudaErrorInvalidValue;
+        }
+    }
     return dtype == DT_BF16 ? launch_prefix_tc_typed<__nv_bfloat16>(a, cache, head_dim, pdl, s)
                             : launch_prefix_tc_typed<__half>(a, cache, head_dim, pdl, s);
 }

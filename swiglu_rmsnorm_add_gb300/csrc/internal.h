@@ -199,7 +199,7 @@ inline SRA_HD TailPlan tail_plan(int64_t tiles, int longest, int64_t workers, in
     if (part < least) part = least;
     return {part < 2 ? 2 : part};
 }
-// The prefix's whole pages against the queries of all requests (tcgen05 path), and the merge of its
+// The prefix's whole pages against the queries of all requests, and the merge of its
 // partial results with the requests' own tokens'.
 struct PrefixArgs {
     const void* q;            // [B, n_head, head_dim], token stride qs
@@ -219,11 +219,12 @@ struct PrefixArgs {
     float2* part_ml;  // [n_kv][records][rows] maximum (base 2, scaled) and sum
     const float* tail;  // [B * n_kv][tail_splits][16 + 8 * head_dim]
     int tail_splits;    // records of a pair's own tokens at most (tail_plan)
-    const int64_t* tail_at;  // [B + 1] tiles before each request (of one kv head); a part's tiles
+    // [B + 1] tiles before each request (of one kv head); a part's tiles. Null (fp32): tail_splits records each
+    const int64_t* tail_at;
 };
-cudaError_t launch_prefix_tc(const PrefixArgs& a, const void* cache, int head_dim, int dtype, bool pdl, cudaStream_t s);
+cudaError_t launch_prefix_whole(const PrefixArgs& a, const void* cache, int head_dim, int dtype, bool pdl, cudaStream_t s);
 cudaError_t launch_prefix_merge(const PrefixArgs& a, int head_dim, int dtype, cudaStream_t s);
-size_t prefix_tc_smem(int head_dim);
+size_t prefix_smem(int head_dim, int dtype);
 unsigned int prefix_wait_timeouts();
 
 // ------------------------------------------------------------------- fused linear

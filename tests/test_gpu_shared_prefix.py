@@ -103,16 +103,16 @@ def run(c, what="", expect_errors=0, **kw):
     return got
 
 
-@pytest.fixture(params=["auto", "decode", "tcgen05"])
+@pytest.fixture(params=["auto", "decode", "batched"])
 def path(request):
     """The automatic choice, and each of the two paths forced."""
-    sra.force_variant("shared_prefix", {"auto": -1, "decode": 0, "tcgen05": 1}[request.param])
+    sra.force_variant("shared_prefix", {"auto": -1, "decode": 0, "batched": 1}[request.param])
     yield request.param
     sra.force_variant("shared_prefix", -1)
 
 
 def serves(path, dtype, hd, prefix_pages=1):
-    return path != "tcgen05" or (dtype != torch.float32 and prefix_pages > 0)
+    return path != "batched" or prefix_pages > 0
 
 
 def ragged(B, prefix, own, seed):
@@ -130,7 +130,7 @@ def ragged(B, prefix, own, seed):
 @pytest.mark.parametrize("bs", [8, 16, 32])
 def test_shapes_dtypes(dtype, hd, n_head, n_kv, bs, path):
     if not serves(path, dtype, hd):
-        pytest.skip("the tensor-core path serves 16-bit data")
+        pytest.skip("the prefix needs a page")
     B = {8: 5, 16: 19, 32: 40}[bs]
     prefix = {64: 200, 128: 391, 256: 128}[hd]
     run(Case(B, n_head, n_kv, hd, bs, prefix, ragged(B, prefix, 70, hd + bs), dtype, hd + bs + n_head))
@@ -141,7 +141,7 @@ def test_shapes_dtypes(dtype, hd, n_head, n_kv, bs, path):
 @pytest.mark.parametrize("B", [1, 2, 23, 65])
 def test_prefix_lengths(dtype, prefix, B, path):
     if not serves(path, dtype, 128):
-        pytest.skip("the tensor-core path serves 16-bit data")
+        pytest.skip("the prefix needs a page")
     run(Case(B, 12, 2, 128, 16, prefix, ragged(B, prefix, 40, prefix + B), dtype, prefix + B))
 
 
@@ -154,7 +154,7 @@ def test_long_prefixes(hd, n_head, n_kv, B):
 @pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float32, 64), (torch.float16, 256)])
 def test_no_own_tokens_no_prefix_nothing(dtype, hd, path):
     if not serves(path, dtype, hd):
-        pytest.skip("the tensor-core path serves 16-bit data")
+        pytest.skip("the prefix needs a page")
     run(Case(30, 8, 2, hd, 16, 300, [300] * 30, dtype, 1), "only the prefix")
     run(Case(30, 8, 2, hd, 16, 300, [0] * 30, dtype, 2), "no tokens at all")
     run(Case(30, 8, 2, hd, 16, 300, list(range(30)), dtype, 3), "all shorter than the prefix")
@@ -167,7 +167,7 @@ def test_no_own_tokens_no_prefix_nothing(dtype, hd, path):
 def test_peaked_scores(dtype, hd, path):
     """Scores of some hundreds: the running maximum moves many times and most weights vanish."""
     if not serves(path, dtype, hd):
-        pytest.skip("the tensor-core path serves 16-bit data")
+        pytest.skip("the prefix needs a page")
     run(Case(40, 12, 2, hd, 16, 1000, ragged(40, 1000, 90, 7), dtype, 7, scale=1.0, spread=2.0))
 
 
@@ -175,7 +175,7 @@ def test_peaked_scores(dtype, hd, path):
                                       (torch.bfloat16, 256)])
 def test_bad_entries_are_skipped_and_counted(dtype, hd, path):
     if not serves(path, dtype, hd):
-        pytest.skip("the tensor-core path serves 16-bit data")
+        pytest.skip("the prefix needs a page")
     c = Case(33, 8, 2, hd, 16, 417, [600] * 33, dtype, 11)
     c.ptable[3], c.ptable[9] = -1, c.nb
     c.table[4, 30] = 2 ** 31 - 1
@@ -205,7 +205,7 @@ def test_prefix_length_is_clamped(path):
 def test_strided_queries_and_outputs(dtype, hd, path):
     """q as a view of a fused QKV buffer, out as a view of a wider one whose other columns stay."""
     if not serves(path, dtype, hd):
-        pytest.skip("the tensor-core path serves 16-bit data")
+        pytest.skip("the prefix needs a page")
     c = Case(50, 8, 2, hd, 16, 500, ragged(50, 500, 50, 3), dtype, 3)
     d = c.dev()
     qkv = torch.randn(50, 12, hd, device=DEV).to(dtype)
@@ -223,7 +223,7 @@ def test_queries_at_an_odd_element(path):
     flat = torch.empty(c.q.numel() + 1, device=DEV, dtype=torch.bfloat16)[1:]
     d["q"] = flat.copy_(d["q"].reshape(-1)).view(c.q.shape)
     out = torch.empty(c.q.numel() + 1, device=DEV, dtype=torch.bfloat16)[1:].view(c.q.shape)
-    if path == "tcgen05":   # wants query rows aligned to 4 bytes
+    if path == "batched":   # wants query rows aligned to 4 bytes
         with pytest.raises(sra.SRAError) as e:
             sra.shared_prefix_attention(**d, scale=c.scale, out=out)
         assert e.value.status == -7
