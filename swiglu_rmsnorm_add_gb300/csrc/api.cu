@@ -1656,9 +1656,9 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
     p.ctas_per_kv = p.pair_blocks * p.pair_splits + p.single_splits;
     p.records = std::max(p.pair_splits, p.single_splits);
     // the requests' own tokens: records for parts of 128 tokens of what their part of the table may hold, 16 at
-    // least (a part grows where a request has more)
+    // least, and 8192 in all (a part grows where a request has more; one that ends inside the prefix may)
     const int64_t groups = B * n_kv, own = std::max<int64_t>(0, max_blocks - prefix_blocks + 1) * block_size;
-    p.tail_splits = static_cast<int>(std::min<int64_t>(std::max<int64_t>(16, ceil_div(own, 128) + 1), 256));
+    p.tail_splits = static_cast<int>(std::min<int64_t>(std::max<int64_t>({16, ceil_div(own, 128) + 1, 8192 / groups}), 256));
     if (f32) {  // the decode kernel's splits of 64 tokens or more, two CTAs an SM
         p.tail_splits = 1;
         while (p.tail_splits < 16 && groups * p.tail_splits < 2 * static_cast<int64_t>(sms) && own >= 128 * p.tail_splits)

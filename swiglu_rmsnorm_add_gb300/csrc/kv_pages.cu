@@ -105,16 +105,37 @@ __device__ __forceinline__ bool named_before(const int32_t* idx, int64_t i, int 
     return __any_sync(FULL, hit);
 }
 
+// A group of kCols threads takes kRows entries of a call, a thread a column of the table (every
+// `x_groups` x kCols columns). The table kernels run these steps either with a group to a CTA and a launch
+// per step, or, for small calls, with all groups in one CTA and a barrier between the steps: a launch costs
+// about 3 us, a step on 640 entries less than 2.
+struct Group {
+    int tid;            // thread of the group
+    int64_t i0;         // first entry
+    int x, x_groups;    // column slice
+    int barrier;        // named barrier of the group
+    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(kCols) : "memory"); }
+};
+__device__ __forceinline__ Group group_of_cta() {
+    return {static_cast<int>(threadIdx.x), static_cast<int64_t>(blockIdx.y) * kRows, static_cast<int>(blockIdx.x),
+            static_cast<int>(gridDim.x), 1};
+}
+// Group threadIdx.x / kCols of a CTA that holds all of a call's (round: its groups so far).
+__device__ __forceinline__ Group group_of_all(int64_t round) {
+    const int g = static_cast<int>(threadIdx.x) / kCols;
+    return {static_cast<int>(threadIdx.x) % kCols, (round + g) * kRows, 0, 1, 1 + g};
+}
+constexpr int kGroups = 8;              // groups of a CTA that holds all of a call's
+constexpr int64_t kSmallCall = 16384;   // table entries of such a call
+
 // What entry i of a fork does: the parent's and the child's length at entry, or parent_len -1
-// where it does nothing. Written by the first column slice, used by both kernels.
+// where it does nothing. Written by the first column slice, used by both steps.
 // Entries of table row `row` at column j are changed by runs: rows of a group that hold the
 // same page in a column change its count once.
-__global__ void __launch_bounds__(kCols) fork_take_kernel(ForkArgs a) {
-    __shared__ int s_len[kRows], s_row[kRows];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kRows;
-    const bool first = blockIdx.x == 0;
-    pdl_enter();
+__device__ __forceinline__ void fork_take(const ForkArgs& a, const Group& q, int (&s_len)[kRows], int (&s_row)[kRows]) {
+    const int lane = threadIdx.x & 31, warp = q.tid >> 5;
+    const int64_t i0 = q.i0;
+    const bool first = q.x == 0;
     for (int r = warp; r < kRows; r += kCols / 32) {
         const int64_t i = i0 + r;
         int plen = -1, clen = -1, prow = 0;
@@ -141,9 +162,8 @@ __global__ void __launch_bounds__(kCols) fork_take_kernel(ForkArgs a) {
         }
         if (lane == 0) s_len[r] = plen, s_row[r] = prow;
     }
-    __syncthreads();
-    for (int64_t j = static_cast<int64_t>(blockIdx.x) * kCols + threadIdx.x; j < a.max_blocks;
-         j += static_cast<int64_t>(gridDim.x) * kCols) {
+    q.sync();
+    for (int64_t j = static_cast<int64_t>(q.x) * kCols + q.tid; j < a.max_blocks; j += static_cast<int64_t>(q.x_groups) * kCols) {
         int32_t e[kRows];
         unsigned has = 0;
 #pragma unroll
@@ -174,21 +194,19 @@ __global__ void __launch_bounds__(kCols) fork_take_kernel(ForkArgs a) {
     }
 }
 
-__global__ void __launch_bounds__(kCols) fork_give_kernel(ForkArgs a) {
-    __shared__ int s_plen[kRows], s_clen[kRows], s_row[kRows];
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kRows;
-    pdl_enter();
-    if (threadIdx.x < kRows) {
-        const int64_t i = i0 + threadIdx.x;
+__device__ __forceinline__ void fork_give(const ForkArgs& a, const Group& q, int (&s_plen)[kRows], int (&s_clen)[kRows],
+                                          int (&s_row)[kRows]) {
+    const int64_t i0 = q.i0;
+    if (q.tid < kRows) {
+        const int64_t i = i0 + q.tid;
         const int plen = i < a.n ? a.ws_plen[i] : -1;
-        s_plen[threadIdx.x] = plen;
-        s_clen[threadIdx.x] = plen >= 0 ? a.ws_clen[i] : 0;
-        s_row[threadIdx.x] = plen >= 0 ? a.children[i] : 0;
-        if (plen >= 0 && blockIdx.x == 0) a.seq_lens[a.children[i]] = plen;
+        s_plen[q.tid] = plen;
+        s_clen[q.tid] = plen >= 0 ? a.ws_clen[i] : 0;
+        s_row[q.tid] = plen >= 0 ? a.children[i] : 0;
+        if (plen >= 0 && q.x == 0) a.seq_lens[a.children[i]] = plen;
     }
-    __syncthreads();
-    for (int64_t j = static_cast<int64_t>(blockIdx.x) * kCols + threadIdx.x; j < a.max_blocks;
-         j += static_cast<int64_t>(gridDim.x) * kCols) {
+    q.sync();
+    for (int64_t j = static_cast<int64_t>(q.x) * kCols + q.tid; j < a.max_blocks; j += static_cast<int64_t>(q.x_groups) * kCols) {
         int32_t old[kRows], now[kRows];
         unsigned has = 0;
 #pragma unroll
@@ -222,15 +240,38 @@ __global__ void __launch_bounds__(kCols) fork_give_kernel(ForkArgs a) {
     }
 }
 
+__global__ void __launch_bounds__(kCols) fork_take_kernel(ForkArgs a) {
+    __shared__ int len[kRows], row[kRows];
+    pdl_enter();
+    fork_take(a, group_of_cta(), len, row);
+}
+__global__ void __launch_bounds__(kCols) fork_give_kernel(ForkArgs a) {
+    __shared__ int plen[kRows], clen[kRows], row[kRows];
+    pdl_enter();
+    fork_give(a, group_of_cta(), plen, clen, row);
+}
+__global__ void __launch_bounds__(kGroups * kCols) fork_small_kernel(ForkArgs a) {
+    __shared__ int s[3][kGroups][kRows];
+    const int g = threadIdx.x / kCols;
+    pdl_enter();
+    for (int64_t round = 0; round * kRows < a.n; round += kGroups) {
+        fork_take(a, group_of_all(round), s[0][g], s[1][g]);
+        __syncthreads();
+    }
+    for (int64_t round = 0; round * kRows < a.n; round += kGroups) {
+        fork_give(a, group_of_all(round), s[0][g], s[1][g], s[2][g]);
+        __syncthreads();
+    }
+}
+
 // ------------------------------------------------------------------ resize
 // Release: the pages that shrinking rows hold past their new length. Also what each entry
 // will do (ws_old: the row's length at entry, or -1 where the entry does nothing).
-__global__ void __launch_bounds__(kCols) resize_release_kernel(ResizeArgs a) {
-    __shared__ int s_old[kRows], s_new[kRows], s_row[kRows];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kRows;
-    const bool first = blockIdx.x == 0;
-    pdl_enter();
+__device__ __forceinline__ void resize_release(const ResizeArgs& a, const Group& q, int (&s_old)[kRows],
+                                               int (&s_new)[kRows], int (&s_row)[kRows]) {
+    const int lane = threadIdx.x & 31, warp = q.tid >> 5;
+    const int64_t i0 = q.i0;
+    const bool first = q.x == 0;
     for (int r = warp; r < kRows; r += kCols / 32) {
         const int64_t i = i0 + r;
         int old = -1, len = 0, row = 0;
@@ -254,9 +295,8 @@ __global__ void __launch_bounds__(kCols) resize_release_kernel(ResizeArgs a) {
         }
         if (lane == 0) s_old[r] = old, s_new[r] = len, s_row[r] = row;
     }
-    __syncthreads();
-    for (int64_t j = static_cast<int64_t>(blockIdx.x) * kCols + threadIdx.x; j < a.max_blocks;
-         j += static_cast<int64_t>(gridDim.x) * kCols) {
+    q.sync();
+    for (int64_t j = static_cast<int64_t>(q.x) * kCols + q.tid; j < a.max_blocks; j += static_cast<int64_t>(q.x_groups) * kCols) {
         int32_t e[kRows];
         unsigned has = 0;
 #pragma unroll
@@ -287,33 +327,45 @@ __global__ void __launch_bounds__(kCols) resize_release_kernel(ResizeArgs a) {
     }
 }
 
-constexpr int kScanThreads = 1024;
+__global__ void __launch_bounds__(kCols) resize_release_kernel(ResizeArgs a) {
+    __shared__ int old[kRows], len[kRows], row[kRows];
+    pdl_enter();
+    resize_release(a, group_of_cta(), old, len, row);
+}
+
+constexpr int kScanThreads = 1024;  // at most; a CTA has as many as its pages or entries need
 constexpr int kScanPages = 16;  // pages a thread looks at per step: four 16-byte loads in flight
 
-// Exclusive prefix sum of v over the CTA's threads; *total gets the sum. `scratch`: 33 words.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* total) {
+// Exclusive prefix sum of v over the CTA's threads; *total gets the sum. `scratch`: 33 words. (A CTA of one
+// warp meets no barrier.)
+template <typename I>
+__device__ __forceinline__ I block_scan(I v, I* scratch, I* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t inc = v;
+    I inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(FULL, inc, o);
+        const I t = __shfl_up_sync(FULL, inc, o);
         if (lane >= o) inc += t;
+    }
+    if (blockDim.x == 32) {
+        *total = __shfl_sync(FULL, inc, 31);
+        return inc - v;
     }
     if (lane == 31) scratch[warp] = inc;
     __syncthreads();
     if (warp == 0) {
-        int64_t w = lane < static_cast<int>(blockDim.x >> 5) ? scratch[lane] : 0;
-        const int64_t mine = w;
+        I w = lane < static_cast<int>(blockDim.x >> 5) ? scratch[lane] : 0;
+        const I mine = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t t = __shfl_up_sync(FULL, w, o);
+            const I t = __shfl_up_sync(FULL, w, o);
             if (lane >= o) w += t;
         }
         scratch[lane] = w - mine;
         if (lane == 31) scratch[32] = w;
     }
     __syncthreads();
-    const int64_t before = scratch[warp] + inc - v;
+    const I before = scratch[warp] + inc - v;
     *total = scratch[32];
     __syncthreads();
     return before;
@@ -339,11 +391,9 @@ __device__ __forceinline__ unsigned live_mask(const int32_t* ref, int64_t p, int
 
 // One CTA: how many pages each growing entry needs and where its pages start in the list of
 // free pages, then that list, lowest page first, as far as it is needed.
-__global__ void __launch_bounds__(kScanThreads) resize_plan_kernel(ResizeArgs a) {
-    __shared__ int64_t scratch[33];
-    pdl_enter();
+__device__ __forceinline__ void resize_plan(const ResizeArgs& a, int64_t* scratch) {
     int64_t total = 0;
-    for (int64_t base = 0; base < a.n; base += kScanThreads) {
+    for (int64_t base = 0; base < a.n; base += blockDim.x) {
         const int64_t i = base + threadIdx.x;
         int64_t need = 0;
         int32_t from = -1;
@@ -377,17 +427,33 @@ __global__ void __launch_bounds__(kScanThreads) resize_plan_kernel(ResizeArgs a)
     }
     const bool vec = (reinterpret_cast<uintptr_t>(a.ref) & 15u) == 0;
     int64_t found = 0;
-    for (int64_t base = 0; base < a.num_blocks && found < total; base += kScanThreads * kScanPages) {
+    for (int64_t base = 0; base < a.num_blocks && found < total; base += static_cast<int64_t>(blockDim.x) * kScanPages) {
         const int64_t p = base + static_cast<int64_t>(threadIdx.x) * kScanPages;
         const int64_t left = a.num_blocks - p;
         const unsigned in = left >= kScanPages ? (1u << kScanPages) - 1u : left > 0 ? (1u << left) - 1u : 0u;
         unsigned free = ~live_mask(a.ref, p, a.num_blocks, vec) & in;
-        int64_t sum;
-        int64_t at = found + block_scan(__popc(free), scratch, &sum);
+        int sum;
+        int64_t at = found + block_scan(__popc(free), reinterpret_cast<int*>(scratch), &sum);
         for (; free && at < total; free &= free - 1, ++at) a.ws_free[at] = static_cast<int32_t>(p + __ffs(free) - 1);
         found += sum;
     }
     if (threadIdx.x == 0) *a.ws_found = found;
+}
+__global__ void __launch_bounds__(kScanThreads) resize_plan_kernel(ResizeArgs a) {
+    __shared__ int64_t scratch[33];
+    pdl_enter();
+    resize_plan(a, scratch);
+}
+__global__ void __launch_bounds__(kGroups * kCols) resize_small_kernel(ResizeArgs a) {
+    __shared__ int s[3][kGroups][kRows];
+    __shared__ int64_t scratch[33];
+    const int g = threadIdx.x / kCols;
+    pdl_enter();
+    for (int64_t round = 0; round * kRows < a.n; round += kGroups) {
+        resize_release(a, group_of_all(round), s[0][g], s[1][g], s[2][g]);
+        __syncthreads();
+    }
+    resize_plan(a, scratch);
 }
 
 // The CTAs below a.copy_from hand out the pages and finish the rows; the others copy the pages
@@ -459,20 +525,20 @@ __global__ void __launch_bounds__(kCols) resize_assign_kernel(CacheList c, Resiz
 // One CTA: N live pages; the free pages below N in order (ws_dst), and for every page its rank
 // among the live ones, or -1 (ws_rank). Live page p >= N is the (rank - (N - moved))-th to move.
 __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(CompactArgs a) {
-    __shared__ int64_t scratch[33];
+    __shared__ int scratch[33];
     pdl_enter();
     const bool vec = (reinterpret_cast<uintptr_t>(a.ref) & 15u) == 0;
-    constexpr int64_t kStep = static_cast<int64_t>(kScanThreads) * kScanPages;
-    int64_t mine = 0, live = 0;
-    for (int64_t base = 0; base < a.num_blocks; base += kStep)
+    const int64_t step = static_cast<int64_t>(blockDim.x) * kScanPages;
+    int mine = 0, live = 0;  // (fewer than 2^31 pages)
+    for (int64_t base = 0; base < a.num_blocks; base += step)
         mine += __popc(live_mask(a.ref, base + static_cast<int64_t>(threadIdx.x) * kScanPages, a.num_blocks, vec));
     block_scan(mine, scratch, &live);
-    int64_t seen = 0;  // live pages before this step's
-    for (int64_t base = 0; base < a.num_blocks; base += kStep) {
+    int seen = 0;  // live pages before this step's
+    for (int64_t base = 0; base < a.num_blocks; base += step) {
         const int64_t p = base + static_cast<int64_t>(threadIdx.x) * kScanPages;
         const unsigned m = live_mask(a.ref, p, a.num_blocks, vec);
-        int64_t sum;
-        int64_t rank = seen + block_scan(__popc(m), scratch, &sum);
+        int sum;
+        int rank = seen + block_scan(__popc(m), scratch, &sum);
         for (int u = 0; u < kScanPages && p + u < a.num_blocks; ++u) {
             const bool on = (m >> u) & 1u;
             a.ws_rank[p + u] = on ? static_cast<int32_t>(rank) : -1;
@@ -561,18 +627,36 @@ static dim3 table_grid(int64_t n, int64_t max_blocks) {
                 static_cast<unsigned>((n + pages::kRows - 1) / pages::kRows));
 }
 
+// Threads of a CTA that scans `pages` pages and holds `entries` entries a thread each.
+static dim3 scan_block(int64_t pages, int64_t entries) {
+    int64_t t = (pages + pages::kScanPages - 1) / pages::kScanPages;
+    t = ((t > entries ? t : entries) + 31) / 32 * 32;
+    return dim3(static_cast<unsigned>(t < 32 ? 32 : t > pages::kScanThreads ? pages::kScanThreads : t));
+}
+
+// Calls whose groups all go into one CTA, and its threads.
+static bool small_call(int64_t n, int64_t max_blocks) { return n * (max_blocks > 32 ? max_blocks : 32) <= pages::kSmallCall; }
+static dim3 small_block(int64_t n) {
+    const int64_t g = (n + pages::kRows - 1) / pages::kRows;
+    return dim3(static_cast<unsigned>((g < pages::kGroups ? g : pages::kGroups) * pages::kCols));
+}
+
 cudaError_t launch_fork_rows(const ForkArgs& a, const PagePlan& p, cudaStream_t s) {
+    if (small_call(a.n, a.max_blocks))
+        return launch_kernel(pages::fork_small_kernel, dim3(1), small_block(a.n), 0, s, p.pdl, 1, a);
     const dim3 grid = table_grid(a.n, a.max_blocks), block(pages::kCols);
     const cudaError_t e = launch_kernel(pages::fork_take_kernel, grid, block, 0, s, p.pdl, 1, a);
     return e != cudaSuccess ? e : launch_kernel(pages::fork_give_kernel, grid, block, 0, s, true, 1, a);
 }
 
 cudaError_t launch_resize_plan(const ResizeArgs& a, const PagePlan& p, cudaStream_t s) {
+    if (small_call(a.n, a.max_blocks))
+        return launch_kernel(pages::resize_small_kernel, dim3(1), small_block(a.n), 0, s, p.pdl, 1, a);
     const cudaError_t e = launch_kernel(pages::resize_release_kernel, table_grid(a.n, a.max_blocks),
                                         dim3(pages::kCols), 0, s, p.pdl, 1, a);
     return e != cudaSuccess
                ? e
-               : launch_kernel(pages::resize_plan_kernel, dim3(1), dim3(pages::kScanThreads), 0, s, true, 1, a);
+               : launch_kernel(pages::resize_plan_kernel, dim3(1), scan_block(a.num_blocks, a.n), 0, s, true, 1, a);
 }
 
 cudaError_t launch_resize_assign(const CacheList& c, const ResizeArgs& a, const PagePlan& p, cudaStream_t s) {
@@ -587,7 +671,7 @@ cudaError_t launch_resize_assign(const CacheList& c, const ResizeArgs& a, const 
 }
 
 cudaError_t launch_compact_plan(const CompactArgs& a, const PagePlan& p, cudaStream_t s) {
-    return launch_kernel(pages::compact_plan_kernel, dim3(1), dim3(pages::kScanThreads), 0, s, p.pdl, 1, a);
+    return launch_kernel(pages::compact_plan_kernel, dim3(1), scan_block(a.num_blocks, 0), 0, s, p.pdl, 1, a);
 }
 
 cudaError_t launch_compact_move(const CacheList& c, const CompactArgs& a, const PagePlan& p, cudaStream_t s) {
