@@ -1647,7 +1647,12 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
     const bool f32 = dtype == DT_F32, lone = f32 || head_dim > 128;
     const int64_t tiles = ceil_div(prefix_blocks * block_size, 64);
     const int mt = static_cast<int>(ceil_div(rows, f32 ? 64 : 128)), share = lone ? 1 : 2;
-    const int per_kv = std::max(1, (f32 && head_dim == 64 ? 3 * sms : sms) / n_kv);
+    int per_kv = std::max(1, (f32 && head_dim == 64 ? 3 * sms : sms) / n_kv);
+    // Every split costs its rows' Q, its records and their merge whatever it works on: below twelve tiles of 128
+    // rows a split (six of a pair) fewer splits are faster, down to half (batch 64 x 8192 with 512 own tokens 24.3
+    // us with all SMs, 22.4 with three quarters, 20.5 with half, 23.3 with a third; 128 x 8192 24.4, 22.0, 24.3;
+    // 64 x 32768 30.3, 33.5, 41.2).
+    if (!lone) per_kv = std::max<int>(std::max(1, per_kv / 2), static_cast<int>(std::min<int64_t>(per_kv, tiles * mt / 12)));
     p.pair_blocks = lone ? mt : mt / 2;
     if (p.pair_blocks) p.pair_splits = static_cast<int>(std::min<int64_t>(std::max(1, share * per_kv / mt), tiles));
     if (!lone && (mt & 1))
