@@ -1669,14 +1669,16 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
         while (p.tail_splits < 16 && groups * p.tail_splits < 2 * static_cast<int64_t>(sms) && own >= 128 * p.tail_splits)
             p.tail_splits *= 2;
     }
-    if (groups * p.tail_splits >= (int64_t(1) << 30)) {
+    // (the tail's counts of records and of tiles of 32 tokens are 32-bit)
+    if (groups * p.tail_splits >= (int64_t(1) << 30) ||
+        static_cast<double>(B) * max_blocks * block_size / 32 + B >= static_cast<double>(1 << 30)) {
         p.use = false;
         return p;
     }
     const int64_t recs = n_kv * rows * p.records;
     p.ml_bytes = round_up256(recs * 8);
     p.o_bytes = round_up256(recs * head_dim * 4);
-    p.at_bytes = round_up256((B + 1) * 8);
+    p.at_bytes = round_up256((B + 1) * 4);
     p.tail_bytes = round_up256(groups * p.tail_splits * (16 + 8 * static_cast<int64_t>(head_dim)) * 4);
     return p;
 }
@@ -1817,7 +1819,7 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     f.records = pp.records;
     f.part_ml = static_cast<float2*>(workspace);
     f.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp.ml_bytes);
-    int64_t* tail_at = reinterpret_cast<int64_t*>(static_cast<char*>(workspace) + pp.ml_bytes + pp.o_bytes);
+    int32_t* tail_at = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + pp.ml_bytes + pp.o_bytes);
     float* tail = reinterpret_cast<float*>(reinterpret_cast<char*>(tail_at) + pp.at_bytes);
     f.tail_at = dtype == DT_F32 ? nullptr : tail_at;
     a.ws_tail_at = tail_at;

@@ -1080,8 +1080,8 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
     constexpr int CPR = HD * 2 / 16, KS = HD / 16, TE = kTailTok * HD;
     constexpr int RPI = 32 / CPR;  // rows per copy instruction (CPR lanes per row)
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int64_t sums[kTailThreads + 1];
-    __shared__ int s_long;
+    // (32-bit sums: the host keeps the tiles of a batch below 2^31)
+    __shared__ int sums[kTailThreads + 1], s_lo[kTailThreads], s_len[kTailThreads], warp_sum[kTailWarps], s_long;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1090,45 +1090,43 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
     const T* cache = static_cast<const T*>(a.cache);
     const int64_t tok_stride = static_cast<int64_t>(a.n_kv) * HD, v_plane = a.num_blocks * BS * tok_stride;
     const int64_t cap = a.max_blocks * BS;
-    const int P = static_cast<int>(prefix_range(a, 0).P);
+    // Thread t sums requests [t * per, (t + 1) * per); its first one's length is asked for with the prefix's.
+    const int per = (B + kTailThreads - 1) / kTailThreads;
+    const int first_row = threadIdx.x * per;
+    const int32_t given = first_row < B ? __ldcg(a.seq_lens + first_row) : 0;
+    const int P = static_cast<int>(prefix_range(a, 0).P), whole = P >> bs_log2 << bs_log2;
     if (blockIdx.x == 0) count_prefix_errors(a, P);
-    // request b's own part [lo, len)
-    auto range = [&](int b, int* lo, int* len) {
-        int64_t n = b < B ? __ldcg(a.seq_lens + b) : 0;
-        n = n < 0 ? 0 : (n > cap ? cap : n);
-        *lo = static_cast<int>(prefix_range(a, n).lo);
-        *len = static_cast<int>(n);
+    // a request's own part [lo, len), and its tiles
+    auto part_of = [&](int32_t n, int* lo, int* len) {
+        const int64_t l = n < 0 ? 0 : (n > cap ? cap : n);
+        *len = static_cast<int>(l);
+        *lo = *len >= whole ? whole : 0;
     };
     auto tiles_of = [&](int lo, int len) { return (len - lo + kTailTok - 1) / kTailTok; };
-
-    // Thread t sums requests [t * per, (t + 1) * per): sums[t] = tiles (of one kv head) before them.
-    const int per = (B + kTailThreads - 1) / kTailThreads;
-    int64_t mine = 0;
-    int longest = 0;
+    int mine = 0, longest = 0;
     if (threadIdx.x == 0) s_long = 0;
     for (int k = 0; k < per; ++k) {
-        const int b = threadIdx.x * per + k;
+        const int b = first_row + k;
+        const int32_t n = k == 0 ? given : b < B ? __ldcg(a.seq_lens + b) : 0;
         int lo, len;
-        range(b, &lo, &len);
-        const int n = tiles_of(lo, len);
-        mine += n;
-        longest = max(longest, n);
-        if (blockIdx.x == 0 && b < B && a.err) {
-            const int64_t given = __ldcg(a.seq_lens + b);
-            if (given < 0 || given > cap) atomicAdd(a.err, 1);
-        }
+        part_of(n, &lo, &len);
+        if (k == 0) s_lo[threadIdx.x] = lo, s_len[threadIdx.x] = len;
+        const int t = tiles_of(lo, len);
+        mine += t;
+        longest = max(longest, t);
+        if (blockIdx.x == 0 && a.err && (n < 0 || n > cap)) atomicAdd(a.err, 1);
     }
-    int64_t inc = mine;
+    int inc = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-        const int64_t t = __shfl_up_sync(FULL, inc, x);
+        const int t = __shfl_up_sync(FULL, inc, x);
         if (lane >= x) inc += t;
     }
-    __shared__ int64_t warp_sum[kTailWarps];
+    longest = __reduce_max_sync(FULL, longest);
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    atomicMax(&s_long, longest);
-    int64_t before = 0, total = 0;
+    if (lane == 0) atomicMax(&s_long, longest);
+    int before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kTailWarps; ++w) {
         before += w < warp ? warp_sum[w] : 0;
@@ -1138,25 +1136,25 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
     if (threadIdx.x == 0) sums[kTailThreads] = total;
     __syncthreads();
     const int workers = static_cast<int>(gridDim.x) * kTailWarps;
-    const TailPlan plan = tail_plan(total, s_long, workers / a.n_kv, a.gsplits);
+    const int part = tail_part(total, s_long, workers / a.n_kv, a.gsplits);
     if (blockIdx.x == 0) {
         // for the merge: the tiles before every request, and a part's size
-        int64_t at = sums[threadIdx.x];
+        int at = sums[threadIdx.x];
         for (int k = 0; k < per; ++k) {
-            const int b = threadIdx.x * per + k;
+            const int b = first_row + k;
             int lo, len;
-            range(b, &lo, &len);
+            part_of(b < B ? __ldcg(a.seq_lens + b) : 0, &lo, &len);
             if (b < B) a.ws_tail_at[b] = at;
             at += tiles_of(lo, len);
         }
-        if (threadIdx.x == 0) a.ws_tail_at[B] = plan.part;
+        if (threadIdx.x == 0) a.ws_tail_at[B] = part;
     }
 
-    const int64_t parts = (total + plan.part - 1) / plan.part;
-    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kTailWarps + warp; unit < parts * a.n_kv; unit += workers) {
-        const int64_t mine_part = unit / a.n_kv, g0 = mine_part * plan.part;
-        const int kvh = static_cast<int>(unit - mine_part * a.n_kv);
-        int64_t todo = total - g0 < plan.part ? total - g0 : plan.part;  // tiles not looked at yet
+    const int64_t units = static_cast<int64_t>((total + part - 1) / part) * a.n_kv;
+    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kTailWarps + warp; unit < units; unit += workers) {
+        const int mine_part = static_cast<int>(unit / a.n_kv), g0 = mine_part * part;
+        const int kvh = static_cast<int>(unit - static_cast<int64_t>(mine_part) * a.n_kv);
+        int todo = total - g0 < part ? total - g0 : part;  // tiles not looked at yet
         // The request that tile g0 belongs to: the thread that summed it, then along its requests, 32 at a time.
         // Lane k of the group holds request base + k.
         int owner = 0;
@@ -1164,30 +1162,38 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
             const unsigned hit = __ballot_sync(FULL, sums[t] <= g0 && sums[t + 1] > g0);
             if (hit) owner = t - lane + __ffs(hit) - 1;
         }
-        int base = owner * per, lo, len, b = 0, n = 0, t = 0;
-        int64_t at_row = sums[owner];  // tiles before request base's
+        int base = owner * per, lo = 0, len = 0, b = 0, n = 0, t = 0;
+        auto load_group = [&]() {
+            const int r = base + lane;
+            if (per == 1) {
+                lo = r < kTailThreads ? s_lo[r] : 0, len = r < kTailThreads ? s_len[r] : 0;
+            } else {
+                part_of(r < B ? __ldcg(a.seq_lens + r) : 0, &lo, &len);
+            }
+        };
+        int at_row = sums[owner];  // tiles before request base's
         for (;;) {
-            range(base + lane, &lo, &len);
-            const int64_t w = tiles_of(lo, len);
-            int64_t upto = w;
+            load_group();
+            const int w = tiles_of(lo, len);
+            int upto = w;
 #pragma unroll
             for (int x = 1; x < 32; x <<= 1) {
-                const int64_t y = __shfl_up_sync(FULL, upto, x);
+                const int y = __shfl_up_sync(FULL, upto, x);
                 if (lane >= x) upto += y;
             }
             const unsigned hit = __ballot_sync(FULL, at_row + upto > g0);
             if (hit) {
                 const int k = __ffs(hit) - 1;
                 b = base + k;
-                n = static_cast<int>(__shfl_sync(FULL, w, k));
+                n = __shfl_sync(FULL, w, k);
                 at_row += __shfl_sync(FULL, upto - w, k);  // the request's first tile in the stream
-                t = static_cast<int>(g0 - at_row);
+                t = g0 - at_row;
                 break;
             }
             at_row += __shfl_sync(FULL, upto, 31);
             base += 32;
         }
-        int rec = static_cast<int>(mine_part - at_row / plan.part);  // parts of the request before this one
+        int rec = mine_part - at_row / part;  // parts of the request before this one
         // The tile looked at: first token, the request's end, its page entries
         int at = 0, end = 0;
         int32_t blk = 0, entries = 0;
@@ -1222,7 +1228,7 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
                 do {  // the next request that has tiles (there is one: todo > 0)
                     if (++b == base + 32) {
                         base = b;
-                        range(base + lane, &lo, &len);
+                        load_group();
                     }
                     n = tiles_of(__shfl_sync(FULL, lo, b - base), __shfl_sync(FULL, len, b - base));
                 } while (n == 0);

@@ -706,14 +706,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     constexpr int V = HD / 32;  // outputs per lane
     __shared__ float s_m[kMergeWarps], s_l[kMergeWarps], s_o[kMergeWarps][HD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t head = blockIdx.x;
-    const int64_t b = head / (a.n_kv * a.group);
-    const int h = static_cast<int>(head - b * a.n_kv * a.group);
+    const unsigned heads = static_cast<unsigned>(a.n_kv * a.group);
+    const int64_t b = blockIdx.x / heads;
+    const int h = static_cast<int>(blockIdx.x % heads);
     const int kvh = h / a.group, g = h - kvh * a.group;
     pdl_enter();
     int64_t len = a.seq_lens[b];
     const bool stream = a.tail_at != nullptr;  // fp32: every split of the own tokens leaves a record
-    const int64_t part = stream ? a.tail_at[a.B] : 1, before = stream ? a.tail_at[b] : 0, behind = whole_pages(a) * a.block_size;
+    const int part = stream ? a.tail_at[a.B] : 1, before = stream ? a.tail_at[b] : 0;
+    const int64_t behind = whole_pages(a) * a.block_size;
     len = len < 0 ? 0 : (len > a.cap ? a.cap : len);
     const int64_t row = b * a.group + g;
     const int tile = static_cast<int>(row / kRows);
@@ -723,9 +724,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows + row;  // record i: i * rows further
     const float* tail = a.tail + (b * a.n_kv + kvh) * a.tail_splits * (16 + 8 * HD);
     // its own tokens' records: the parts of the tail's stream that its tiles touch
-    const int64_t tiles = (len - lo + kTailTok - 1) / kTailTok;
+    const int tiles = static_cast<int>((len - lo + kTailTok - 1) / kTailTok);
     const int all = recs + (!stream     ? a.tail_splits
-                            : tiles > 0 ? static_cast<int>((before + tiles - 1) / part - before / part + 1)
+                            : tiles > 0 ? (before + tiles - 1) / part - before / part + 1
                                         : 0);
     float m = -INFINITY, l = 0.0f, acc[V];
 #pragma unroll

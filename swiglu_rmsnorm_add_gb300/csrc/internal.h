@@ -153,7 +153,7 @@ struct AttnArgs {
     const int32_t* plen = nullptr;
     int64_t pblocks = 0;
     bool tail_only = false;  // requests that reach past the prefix's whole pages start behind them
-    int64_t* ws_tail_at = nullptr;  // [B + 1], see PrefixArgs::tail_at
+    int32_t* ws_tail_at = nullptr;  // [B + 1], see PrefixArgs::tail_at
 };
 
 struct AttnPlan {
@@ -189,15 +189,12 @@ int64_t decode_attention_ws_bytes(int64_t B, int n_kv, int head_dim, int gsplits
 // workers of a kv head; a part is as large as every worker needs it (at least two tiles), and no request
 // touches more than `records` parts (the longest has `longest` tiles).
 constexpr int kTailTok = 32;
-struct TailPlan {
-    int64_t part;  // tiles
-};
-inline SRA_HD TailPlan tail_plan(int64_t tiles, int longest, int64_t workers, int records) {
+inline SRA_HD int tail_part(int tiles, int longest, int workers, int records) {
     if (workers < 1) workers = 1;
-    int64_t part = (tiles + workers - 1) / workers;
-    const int64_t least = (longest + records - 2) / (records - 1);
+    int part = tiles / workers + (tiles % workers ? 1 : 0);
+    const int least = (longest + records - 2) / (records - 1);
     if (part < least) part = least;
-    return {part < 2 ? 2 : part};
+    return part < 2 ? 2 : part;
 }
 // The prefix's whole pages against the queries of all requests, and the merge of its
 // partial results with the requests' own tokens'.
@@ -218,9 +215,9 @@ struct PrefixArgs {
     float* part_o;   // [n_kv][records][rows][head_dim]
     float2* part_ml;  // [n_kv][records][rows] maximum (base 2, scaled) and sum
     const float* tail;  // [B * n_kv][tail_splits][16 + 8 * head_dim]
-    int tail_splits;    // records of a pair's own tokens at most (tail_plan)
+    int tail_splits;    // records of a pair's own tokens at most (tail_part)
     // [B + 1] tiles before each request (of one kv head); a part's tiles. Null (fp32): tail_splits records each
-    const int64_t* tail_at;
+    const int32_t* tail_at;
 };
 cudaError_t launch_prefix_whole(const PrefixArgs& a, const void* cache, int head_dim, int dtype, bool pdl, cudaStream_t s);
 cudaError_t launch_prefix_merge(const PrefixArgs& a, int head_dim, int dtype, cudaStream_t s);

@@ -38,6 +38,7 @@ __device__ __forceinline__ void drop_refs(int32_t* ref, int32_t page, int k, int
 }
 
 // ------------------------------------------------------------------ copying
+// (Plain loads and stores: streaming hints on them cost a tenth: 1021 pages of 28 layers, 937 MB read and written, 171 us with them, 147 without, 6.4 TB/s.)
 template <typename V>
 __device__ __forceinline__ void copy_span(char* dst, const char* src, int64_t nvec, int tid, int threads) {
     constexpr int kUnroll = 4;
@@ -47,11 +48,11 @@ __device__ __forceinline__ void copy_span(char* dst, const char* src, int64_t nv
     for (; i + (kUnroll - 1) * threads < nvec; i += kUnroll * threads) {
         V v[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u] = __ldcs(s + i + u * threads);
+        for (int u = 0; u < kUnroll; ++u) v[u] = s[i + u * threads];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) __stcs(d + i + u * threads, v[u]);
+        for (int u = 0; u < kUnroll; ++u) d[i + u * threads] = v[u];
     }
-    for (; i < nvec; i += threads) __stcs(d + i, __ldcs(s + i));
+    for (; i < nvec; i += threads) d[i] = s[i];
 }
 
 struct Pair {
