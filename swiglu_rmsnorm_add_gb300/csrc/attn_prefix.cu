@@ -67,32 +67,32 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// What CTA `c` of a KV head's works on (RPB: query rows of a pair block).
+// What CTA `c` of a KV head's works on (RPB: query rows of a pair block): its rows, which follow from
+// `c`, and its tiles, which follow from the prefix's length.
 struct Work {
     int row0;      // first query row
     bool pair;     // two row tiles on the same K / V tiles, or one row tile on two K / V tiles at a time
-    int t0, n;     // K / V tiles
-    int rec;       // its record of each row
+    int split, splits;
+    int t0 = 0, n = 0;  // K / V tiles
+    __device__ __forceinline__ void cut(int64_t tiles) {
+        const int64_t b = tiles * split / splits, e = tiles * (split + 1) / splits;
+        t0 = static_cast<int>(b);
+        n = static_cast<int>(e - b);
+    }
 };
 template <int RPB>
-__device__ __forceinline__ Work work_of(const PrefixArgs& a, int c, int64_t tiles) {
+__device__ __forceinline__ Work rows_of(const PrefixArgs& a, int c) {
     Work w;
-    int split, splits;
     if (c < a.pair_blocks * a.pair_splits) {
         const int blk = c / a.pair_splits;
-        split = c - blk * a.pair_splits, splits = a.pair_splits;
+        w.split = c - blk * a.pair_splits, w.splits = a.pair_splits;
         w.pair = true;
         w.row0 = blk * RPB;
-        w.rec = split;
     } else {
-        split = c - a.pair_blocks * a.pair_splits, splits = a.single_splits;
+        w.split = c - a.pair_blocks * a.pair_splits, w.splits = a.single_splits;
         w.pair = false;
         w.row0 = a.pair_blocks * RPB;
-        w.rec = split;
     }
-    const int64_t b = tiles * split / splits, e = tiles * (split + 1) / splits;
-    w.t0 = static_cast<int>(b);
-    w.n = static_cast<int>(e - b);
     return w;
 }
 // Whole pages of the prefix, and its K / V tiles.
@@ -134,7 +134,8 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 // With head_dim 256 O alone would fill tensor memory for two row tiles, so the streams share a row tile and a
 // CTA's S and take half of V's dims each; S is computed twice (62 % of the work is needed work).
 template <typename T, int HD>
-__global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC) {
+__global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC,
+                                                                  const __grid_constant__ CUtensorMap tmO) {
     using L = Smem<HD>;
     constexpr int ST = L::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -167,11 +168,55 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = tmem_base;
-    pdl_enter();
     const int kvh = blockIdx.x / a.ctas_per_kv;
+    Work w = rows_of<L::kQTiles * kRows>(a, blockIdx.x - kvh * a.ctas_per_kv);
+    // The threads that set up (all but the producers) ask for the query rows first, the prefix's length after. A
+    // thread's 16-byte chunks share their place in the row and lie kStep rows apart: one division, then steps.
+    const bool producer = warp == 0 || warp == 3;
+    constexpr int kSetup = kThreads - 64, kChunks = HD / 8, kStep = kSetup / kChunks;
+    constexpr int kEach = (L::kQTiles * kRows * kChunks + kSetup - 1) / kSetup;
+    static_assert(kSetup % kChunks == 0, "a thread's chunks share a column");
+    const int setup_tid = threadIdx.x - (warp < 3 ? 32 : 64);
+    const int chunk = setup_tid % kChunks, r0 = setup_tid / kChunks, count = (w.pair ? L::kQTiles : 1) * kRows;
+    uint4 qv[kEach];
+    pdl_enter();
+    if (!producer) {
+        const int dg = kStep % a.group;
+        int g = (w.row0 + r0) % a.group;
+        const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>((w.row0 + r0) / a.group) * a.qs +
+                       (kvh * a.group + g) * HD + chunk * 8;
+        const int64_t step = static_cast<int64_t>(kStep / a.group) * a.qs + dg * HD, wrap = a.qs - a.group * HD;
+        const int rows = count < a.rows - w.row0 ? count : a.rows - w.row0;
+        auto advance = [&]() {
+            src += step;
+            if ((g += dg) >= a.group) g -= a.group, src += wrap;
+        };
+        if (a.q16) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {  // all loads in flight before the first store
+                qv[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (r0 + e * kStep < rows) qv[e] = *reinterpret_cast<const uint4*>(src);
+                advance();
+            }
+        } else {
+#pragma unroll 1
+            for (int e = 0; e < kEach; ++e) {
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (r0 + e * kStep < rows) {
+                    const unsigned short* h = reinterpret_cast<const unsigned short*>(src);
+                    u.x = h[0] | static_cast<uint32_t>(h[1]) << 16, u.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
+                    u.z = h[4] | static_cast<uint32_t>(h[5]) << 16, u.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
+                }
+                advance();
+#pragma unroll
+                for (int k = 0; k < kEach; ++k)
+                    if (k == e) qv[k] = u;
+            }
+        }
+    }
     const int64_t pages = whole_pages(a);
     const int ppt = kTok >> (__ffs(a.block_size) - 1);  // pages of a tile
-    const Work w = work_of<L::kQTiles * kRows>(a, blockIdx.x - kvh * a.ctas_per_kv, (pages + ppt - 1) / ppt);
+    w.cut((pages + ppt - 1) / ppt);
     const int tpr = w.pair ? 1 : 2;  // tiles per round
     const int n0 = w.pair ? w.n : (w.n + 1) / 2, n1 = w.pair ? w.n : w.n / 2;  // tiles of the streams
     bool dead = false;  // a bounded wait ran out (counted): this thread waits no more
@@ -179,7 +224,7 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         if (!dead) dead = !mbar_wait(bar, static_cast<uint32_t>(phase & 1));
     };
 
-    if (warp == 0 || warp == 3) {
+    if (producer) {
         // producers: a tile is a box of 64 dims x block_size tokens per page and half, dealt to two warps
         // (a warp issues a box in about 80 clocks). A page past the prefix, or an entry that is no page, is
         // copied from past the cache's end: zeros. The page entries are read 32 at a time (lane k: entry k
@@ -220,49 +265,10 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
             for (int t = r * tpr; t < (r + 1) * tpr && t < w.n; ++t) load_v(t);
         }
     } else {
-        // the query rows, swizzled as a TMA copy would leave them (rows past the last are zero), and
-        // whether every page of this CTA's tiles counts
-        constexpr int kSetup = kThreads - 64, kChunks = HD / 8;
-        constexpr int kEach = (L::kQTiles * kRows * kChunks + kSetup - 1) / kSetup;  // 16-byte chunks a thread moves
-        const int tid = threadIdx.x - (warp < 3 ? 32 : 64), count = w.n > 0 ? (w.pair ? L::kQTiles : 1) * kRows * kChunks : 0;
-        uint4 v[kEach];
-        // a thread's chunks share their place in the row and lie kStep rows apart: one division, then steps
-        constexpr int kStep = kSetup / kChunks;
-        static_assert(kSetup % kChunks == 0, "a thread's chunks share a column");
-        const int c = tid % kChunks, r0 = tid / kChunks, dg = kStep % a.group;
-        int g = (w.row0 + r0) % a.group;
-        const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>((w.row0 + r0) / a.group) * a.qs +
-                       (kvh * a.group + g) * HD + c * 8;
-        const int64_t step = static_cast<int64_t>(kStep / a.group) * a.qs + dg * HD, wrap = a.qs - a.group * HD;
-        const int rows = count / kChunks < a.rows - w.row0 ? count / kChunks : a.rows - w.row0;
-        auto advance = [&]() {
-            src += step;
-            if ((g += dg) >= a.group) g -= a.group, src += wrap;
-        };
-        if (a.q16) {
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {  // all loads in flight before the first store
-                v[e] = make_uint4(0u, 0u, 0u, 0u);
-                if (r0 + e * kStep < rows) v[e] = *reinterpret_cast<const uint4*>(src);
-                advance();
-            }
-        } else {
-#pragma unroll 1
-            for (int e = 0; e < kEach; ++e) {
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (r0 + e * kStep < rows) {
-                    const unsigned short* h = reinterpret_cast<const unsigned short*>(src);
-                    u.x = h[0] | static_cast<uint32_t>(h[1]) << 16, u.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
-                    u.z = h[4] | static_cast<uint32_t>(h[5]) << 16, u.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
-                }
-                advance();
-#pragma unroll
-                for (int k = 0; k < kEach; ++k)
-                    if (k == e) v[k] = u;
-            }
-        }
+        // the query rows into shared memory, swizzled as a TMA copy would leave them (rows past the last are
+        // zero), and whether every page of this CTA's tiles counts
         bool bad = false;
-        for (int64_t k = tid; k < static_cast<int64_t>(w.n) * ppt; k += kSetup) {
+        for (int64_t k = setup_tid; k < static_cast<int64_t>(w.n) * ppt; k += kSetup) {
             const int64_t j = static_cast<int64_t>(w.t0) * ppt + k;
             const int32_t e = j < pages ? a.ptable[j] : -1;
             bad |= e < 0 || e >= a.num_blocks;
@@ -272,10 +278,10 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int r = r0 + e * kStep, rr = r % kRows;
-            if (r < count / kChunks)
-                *reinterpret_cast<uint4*>(qs + (r / kRows) * L::kQBytes + (c / 8) * L::kQHalf + rr * 128 +
-                                          (((c & 7) ^ (rr & 7)) * 16)) =
-                    make_uint4(v[e].x ^ flip, v[e].y ^ flip, v[e].z ^ flip, v[e].w ^ flip);
+            if (r < count)
+                *reinterpret_cast<uint4*>(qs + (r / kRows) * L::kQBytes + (chunk / 8) * L::kQHalf + rr * 128 +
+                                          (((chunk & 7) ^ (rr & 7)) * 16)) =
+                    make_uint4(qv[e].x ^ flip, qv[e].y ^ flip, qv[e].z ^ flip, qv[e].w ^ flip);
         }
         fence_proxy_async();  // before the tensor core reads them
         asm volatile("bar.sync 1, %0;" ::"r"(kSetup) : "memory");
@@ -425,23 +431,19 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
             if (lane == 0) mbar_arrive(&p_full[x][i & 1]);
         }
         // The record of this CTA's rows: maximum, sum, O; no tile, or no token that counts, leaves a maximum of
-        // -inf. The streams of a single block, two parts of the same rows, are merged first. O goes out by
-        // one bulk copy per row from shared memory (a thread's row, padded by 16 bytes: rows apart by a
-        // multiple of 128 bytes would meet in the same banks), over the tiles, which are done with.
-        // (Stored from the threads' registers, 16 bytes per row and instruction, it took 8 us of the call.)
-        constexpr int kRowBytes = L::kDims * 4 + 16;
+        // -inf. The streams of a single block, two parts of the same rows, are merged first. O goes out by TMA
+        // from shared memory, over the tiles, which are done with: blocks of 32 columns x 128 rows, 128-byte
+        // swizzled, so that the threads of a warp, a row each, meet different banks. (Stored from registers, 16
+        // bytes per row and instruction, it took 10900 clocks; by a bulk copy per row 4600.)
+        constexpr int kBlock = kRows * 128, kBlocks = L::kDims / 32;
         const int rr = quarter * 32 + lane;
-        unsigned char* mine = smem + (x * kRows + rr) * kRowBytes;
+        unsigned char* mine = smem + x * kBlocks * kBlock + rr * 128;
+        auto at16 = [&](int c) { return (c >> 3) * kBlock + (((c & 7) ^ (rr & 7)) << 4); };  // 16-byte chunk c of the row
         if (n > 0) {
             wait(&pv_done[x][(n - 1) & 1], (n - 1) / 2);
             tc::fence_after();
         }
         asm volatile("bar.sync 2, 256;" ::: "memory");  // both streams' products are done: the tiles may go
-        float wa = 1.0f, wb = 0.0f;
-        const unsigned char* other = smem + (kRows + rr) * kRowBytes;
-        if (!w.pair) {
-            if (x == 1) s_ml[rr] = make_float2(m, l);
-        }
         if (w.pair || x == 1) {
             if (n > 0) {
 #pragma unroll 1
@@ -451,20 +453,22 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
                     tc::wait_ld();
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4*>(mine + (d + 4 * k) * 4) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        *reinterpret_cast<uint4*>(mine + at16(d / 4 + k)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
             }
         }
         if (!w.pair) {
+            if (x == 1) s_ml[rr] = make_float2(m, l);
             asm volatile("bar.sync 2, 256;" ::: "memory");
             if (x == 0 && n > 0) {
+                const unsigned char* other = mine + kBlocks * kBlock;
                 const float2 o = s_ml[rr];
                 const bool some = n1 > 0 && !(o.x == -INFINITY && o.y == 0.0f);
                 const float M = some ? fmaxf(m, o.x) : m;
-                wa = m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(m - M);
-                wb = some ? (o.x == -INFINITY ? 1.0f : ex2(o.x - M)) : 0.0f;
+                // a part without weight is not read: it may hold anything
+                const float wa = m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(m - M);
+                const float wb = some ? (o.x == -INFINITY ? 1.0f : ex2(o.x - M)) : 0.0f;
                 l = wa * l + (some ? wb * o.y : 0.0f);
-                const bool keep = wa != 0.0f;  // a part without weight is not read: it may hold anything
                 m = M;
 #pragma unroll 1
                 for (int d = 0; d < L::kDims; d += 32) {
@@ -474,28 +478,35 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
                         float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (some) q = *reinterpret_cast<const float4*>(other + (d + k) * 4);
+                        if (some) q = *reinterpret_cast<const float4*>(other + at16((d + k) / 4));
                         float f[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            f[u] = (keep ? wa * __uint_as_float(v[k + u]) : 0.0f) + (some ? wb * f[u] : 0.0f);
-                        *reinterpret_cast<float4*>(mine + (d + k) * 4) = make_float4(f[0], f[1], f[2], f[3]);
+                            f[u] = (wa != 0.0f ? wa * __uint_as_float(v[k + u]) : 0.0f) + (some ? wb * f[u] : 0.0f);
+                        *reinterpret_cast<float4*>(mine + at16((d + k) / 4)) = make_float4(f[0], f[1], f[2], f[3]);
                     }
                 }
             }
         }
-        const int r = w.row0 + (w.pair && !L::kSplitV ? x * kRows : 0) + rr;
-        if ((w.pair || x == 0) && r < a.rows) {
-            const int64_t at = (static_cast<int64_t>(kvh) * a.records + w.rec) * a.rows + r;
-            if (!L::kSplitV || x == 0) a.part_ml[at] = make_float2(m, l);
-            if (n > 0) {
+        if (w.pair || x == 0) {
+            const int first = w.row0 + (w.pair && !L::kSplitV ? x * kRows : 0), r = first + rr;
+            const int64_t rec = static_cast<int64_t>(kvh) * a.records + w.split;
+            if (r < a.rows && (!L::kSplitV || x == 0)) a.part_ml[rec * a.rows_pad + r] = make_float2(m, l);
+            if (n > 0 && first < a.rows) {
                 fence_proxy_async();
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                                 a.part_o + at * HD + (L::kSplitV ? x * L::kDims : 0)),
-                             "r"(smem_u32(mine)), "r"(L::kDims * 4)
-                             : "memory");
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                asm volatile("bar.sync %0, 128;" ::"r"(3 + x) : "memory");
+                if (rr == 0) {
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k)
+                        asm volatile(
+                            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                                reinterpret_cast<uint64_t>(&tmO)),
+                            "r"(((L::kSplitV ? x * L::kDims : 0) + 32 * k) * 2), "r"(static_cast<int>(rec * a.rows_pad + first)),
+                            "r"(smem_u32(smem + (x * kBlocks + k) * kBlock))
+                            : "memory");
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                }
             }
         }
     }
@@ -518,6 +529,11 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
     CUtensorMap tm;
     if (!encode_tmap_16_nd(&tm, cache, 4, dims, strides, box, std::is_same<T, __nv_bfloat16>::value, true))
         return cudaErrorNotSupported;
+    // the records' O, [n_kv * records * rows_pad][HD] fp32, as 16-bit halves: blocks of 32 columns x 128 rows
+    CUtensorMap to;
+    const uint64_t odims[2] = {2 * HD, static_cast<uint64_t>(a.n_kv) * a.records * a.rows_pad}, ostride[1] = {HD * 4};
+    const uint32_t obox[2] = {64, kRows};
+    if (!encode_tmap_16_nd(&to, a.part_o, 2, odims, ostride, obox, true, true)) return cudaErrorNotSupported;
     auto kernel = prefix_tc_kernel<T, HD>;
     constexpr size_t smem = Smem<HD>::kTotal;
     // all of the SM's shared memory, so that a CTA of the tail kernel finds room beside this one's
@@ -525,7 +541,7 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
     const cudaError_t e = set_smem_once(kernel, smem, true, &done);
     if (e != cudaSuccess) return e;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(a.ctas_per_kv * a.n_kv)), dim3(kThreads), smem, s, pdl, 1,
-                         a, tm);
+                         a, tm, to);
 }
 
 // ------------------------------------------------------------------ fp32
@@ -554,7 +570,8 @@ __global__ void __launch_bounds__(kF32Threads) prefix_f32_kernel(PrefixArgs a, c
     const int kvh = blockIdx.x / a.ctas_per_kv;
     const int64_t pages = whole_pages(a);
     const int bs_log2 = __ffs(a.block_size) - 1, ppt = kF32Tok >> bs_log2;
-    const Work w = work_of<kF32Rows>(a, blockIdx.x - kvh * a.ctas_per_kv, (pages + ppt - 1) / ppt);
+    Work w = rows_of<kF32Rows>(a, blockIdx.x - kvh * a.ctas_per_kv);
+    w.cut((pages + ppt - 1) / ppt);
     const int64_t tok_stride = static_cast<int64_t>(a.n_kv) * HD, v_plane = a.num_blocks * a.block_size * tok_stride;
     // the pages of tile t (-1: does not count), then its rows of a plane, zero where they do not count
     auto find = [&](int t) {
@@ -674,7 +691,7 @@ __global__ void __launch_bounds__(kF32Threads) prefix_f32_kernel(PrefixArgs a, c
 #pragma unroll
         for (int x = 1; x < 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
         if (row >= a.rows) continue;
-        const int64_t at = (static_cast<int64_t>(kvh) * a.records + w.rec) * a.rows + row;
+        const int64_t at = (static_cast<int64_t>(kvh) * a.records + w.split) * a.rows_pad + row;
         if (tc == 0) a.part_ml[at] = make_float2(m[i], l[i]);
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -721,7 +738,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     int recs = tile < (HD > 128 ? 1 : 2) * a.pair_blocks ? a.pair_splits : a.single_splits;
     const int64_t lo = len >= behind ? behind : 0;
     if (len < behind) recs = 0;
-    const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows + row;  // record i: i * rows further
+    const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows_pad + row;  // record i: i * rows_pad further
     const float* tail = a.tail + (b * a.n_kv + kvh) * a.tail_splits * (16 + 8 * HD);
     // its own tokens' records: the parts of the tail's stream that its tiles touch
     const int tiles = static_cast<int>((len - lo + kTailTok - 1) / kTailTok);
@@ -739,9 +756,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
             pm[u] = -INFINITY, pl[u] = 0.0f;
             const float* o = tail;
             if (i < recs) {
-                const float2 ml = a.part_ml[first + static_cast<int64_t>(i) * a.rows];
+                const float2 ml = a.part_ml[first + static_cast<int64_t>(i) * a.rows_pad];
                 pm[u] = ml.x, pl[u] = ml.y;
-                o = a.part_o + (first + static_cast<int64_t>(i) * a.rows) * HD;
+                o = a.part_o + (first + static_cast<int64_t>(i) * a.rows_pad) * HD;
             } else if (i < all) {
                 const float* t = tail + (i - recs) * (16 + 8 * HD);
                 pm[u] = t[g], pl[u] = t[8 + g];
