@@ -1621,7 +1621,7 @@ int prefix_sizes(int64_t B, int n_head, int n_kv_head, int head_dim, int64_t pre
 // How a call is cut for the tensor-core path (use: whether it is taken), and its workspace.
 struct PrefixPlan {
     bool use = false;
-    int rows = 0, rows_pad = 0, pair_blocks = 0, pair_splits = 0, single_splits = 0, ctas_per_kv = 0, records = 0, tail_splits = 0;
+    int rows = 0, pair_blocks = 0, pair_splits = 0, single_splits = 0, ctas_per_kv = 0, records = 0, tail_splits = 0;
     int64_t ml_bytes = 0, o_bytes = 0, at_bytes = 0, tail_bytes = 0;
     int64_t bytes() const { return ml_bytes + o_bytes + at_bytes + tail_bytes; }
 };
@@ -1675,12 +1675,7 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
         p.use = false;
         return p;
     }
-    p.rows_pad = static_cast<int>(ceil_div(rows, 128) * 128);
-    const int64_t recs = static_cast<int64_t>(n_kv) * p.rows_pad * p.records;
-    if (recs >= (int64_t(1) << 31)) {
-        p.use = false;
-        return p;
-    }
+    const int64_t recs = static_cast<int64_t>(n_kv) * rows * p.records;
     p.ml_bytes = round_up256(recs * 8);
     p.o_bytes = round_up256(recs * head_dim * 4);
     p.at_bytes = round_up256((B + 1) * 4);
@@ -1817,7 +1812,6 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     f.negate = scale < 0.0f;
     f.q16 = aligned16(q) && stride_aligned16(q_tok_stride, es);
     f.rows = pp.rows;
-    f.rows_pad = pp.rows_pad;
     f.pair_blocks = pp.pair_blocks;
     f.pair_splits = pp.pair_splits;
     f.single_splits = pp.single_splits;

@@ -134,8 +134,7 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 // With head_dim 256 O alone would fill tensor memory for two row tiles, so the streams share a row tile and a
 // CTA's S and take half of V's dims each; S is computed twice (62 % of the work is needed work).
 template <typename T, int HD>
-__global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC,
-                                                                  const __grid_constant__ CUtensorMap tmO) {
+__global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC) {
     using L = Smem<HD>;
     constexpr int ST = L::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -431,10 +430,11 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
             if (lane == 0) mbar_arrive(&p_full[x][i & 1]);
         }
         // The record of this CTA's rows: maximum, sum, O; no tile, or no token that counts, leaves a maximum of
-        // -inf. The streams of a single block, two parts of the same rows, are merged first. O goes out by TMA
-        // from shared memory, over the tiles, which are done with: blocks of 32 columns x 128 rows, 128-byte
-        // swizzled, so that the threads of a warp, a row each, meet different banks. (Stored from registers, 16
-        // bytes per row and instruction, it took 10900 clocks; by a bulk copy per row 4600.)
+        // -inf. The streams of a single block, two parts of the same rows, are merged first. O goes out through
+        // shared memory, over the tiles, which are done with: blocks of 32 columns x 128 rows, their 16-byte
+        // chunks XOR-swizzled by row, so that the threads of a warp, a row each, meet different banks, and so do
+        // those that then write a row together. (128 KB take 4100 clocks, 32 bytes a clock, what an SM stores;
+        // straight from registers, 16 bytes per row and instruction, 10900; by TMA 4500.)
         constexpr int kBlock = kRows * 128, kBlocks = L::kDims / 32;
         const int rr = quarter * 32 + lane;
         unsigned char* mine = smem + x * kBlocks * kBlock + rr * 128;
@@ -491,21 +491,20 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         if (w.pair || x == 0) {
             const int first = w.row0 + (w.pair && !L::kSplitV ? x * kRows : 0), r = first + rr;
             const int64_t rec = static_cast<int64_t>(kvh) * a.records + w.split;
-            if (r < a.rows && (!L::kSplitV || x == 0)) a.part_ml[rec * a.rows_pad + r] = make_float2(m, l);
-            if (n > 0 && first < a.rows) {
-                fence_proxy_async();
-                asm volatile("bar.sync %0, 128;" ::"r"(3 + x) : "memory");
-                if (rr == 0) {
-#pragma unroll
-                    for (int k = 0; k < kBlocks; ++k)
-                        asm volatile(
-                            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                                reinterpret_cast<uint64_t>(&tmO)),
-                            "r"(((L::kSplitV ? x * L::kDims : 0) + 32 * k) * 2), "r"(static_cast<int>(rec * a.rows_pad + first)),
-                            "r"(smem_u32(smem + (x * kBlocks + k) * kBlock))
-                            : "memory");
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (r < a.rows && (!L::kSplitV || x == 0)) a.part_ml[rec * a.rows + r] = make_float2(m, l);
+            if (n > 0) {
+                // a warp writes its own 32 rows, a row per instruction
+                __syncwarp();
+                constexpr int kLanes = L::kDims / 4;  // 16-byte chunks of a row
+                const int row0 = quarter * 32 + lane / kLanes, c = lane % kLanes;
+                const unsigned char* from = smem + x * kBlocks * kBlock + (c >> 3) * kBlock;
+                float* to = a.part_o + (rec * a.rows + first) * HD + (L::kSplitV ? x * L::kDims : 0) + c * 4;
+#pragma unroll 8
+                for (int k = 0; k < 32; k += 32 / kLanes) {
+                    const int row = row0 + k;
+                    if (first + row < a.rows)
+                        *reinterpret_cast<uint4*>(to + static_cast<int64_t>(row) * HD) =
+                            *reinterpret_cast<const uint4*>(from + row * 128 + (((c & 7) ^ (row & 7)) << 4));
                 }
             }
         }
@@ -529,11 +528,6 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
     CUtensorMap tm;
     if (!encode_tmap_16_nd(&tm, cache, 4, dims, strides, box, std::is_same<T, __nv_bfloat16>::value, true))
         return cudaErrorNotSupported;
-    // the records' O, [n_kv * records * rows_pad][HD] fp32, as 16-bit halves: blocks of 32 columns x 128 rows
-    CUtensorMap to;
-    const uint64_t odims[2] = {2 * HD, static_cast<uint64_t>(a.n_kv) * a.records * a.rows_pad}, ostride[1] = {HD * 4};
-    const uint32_t obox[2] = {64, kRows};
-    if (!encode_tmap_16_nd(&to, a.part_o, 2, odims, ostride, obox, true, true)) return cudaErrorNotSupported;
     auto kernel = prefix_tc_kernel<T, HD>;
     constexpr size_t smem = Smem<HD>::kTotal;
     // all of the SM's shared memory, so that a CTA of the tail kernel finds room beside this one's
@@ -541,7 +535,7 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
     const cudaError_t e = set_smem_once(kernel, smem, true, &done);
     if (e != cudaSuccess) return e;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(a.ctas_per_kv * a.n_kv)), dim3(kThreads), smem, s, pdl, 1,
-                         a, tm, to);
+                         a, tm);
 }
 
 // ------------------------------------------------------------------ fp32
@@ -691,7 +685,7 @@ __global__ void __launch_bounds__(kF32Threads) prefix_f32_kernel(PrefixArgs a, c
 #pragma unroll
         for (int x = 1; x < 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
         if (row >= a.rows) continue;
-        const int64_t at = (static_cast<int64_t>(kvh) * a.records + w.split) * a.rows_pad + row;
+        const int64_t at = (static_cast<int64_t>(kvh) * a.records + w.split) * a.rows + row;
         if (tc == 0) a.part_ml[at] = make_float2(m[i], l[i]);
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -738,7 +732,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     int recs = tile < (HD > 128 ? 1 : 2) * a.pair_blocks ? a.pair_splits : a.single_splits;
     const int64_t lo = len >= behind ? behind : 0;
     if (len < behind) recs = 0;
-    const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows_pad + row;  // record i: i * rows_pad further
+    const int64_t first = static_cast<int64_t>(kvh) * a.records * a.rows + row;  // record i: i * rows further
     const float* tail = a.tail + (b * a.n_kv + kvh) * a.tail_splits * (16 + 8 * HD);
     // its own tokens' records: the parts of the tail's stream that its tiles touch
     const int tiles = static_cast<int>((len - lo + kTailTok - 1) / kTailTok);
@@ -756,9 +750,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
             pm[u] = -INFINITY, pl[u] = 0.0f;
             const float* o = tail;
             if (i < recs) {
-                const float2 ml = a.part_ml[first + static_cast<int64_t>(i) * a.rows_pad];
+                const float2 ml = a.part_ml[first + static_cast<int64_t>(i) * a.rows];
                 pm[u] = ml.x, pl[u] = ml.y;
-                o = a.part_o + (first + static_cast<int64_t>(i) * a.rows_pad) * HD;
+                o = a.part_o + (first + static_cast<int64_t>(i) * a.rows) * HD;
             } else if (i < all) {
                 const float* t = tail + (i - recs) * (16 + 8 * HD);
                 pm[u] = t[g], pl[u] = t[8 + g];

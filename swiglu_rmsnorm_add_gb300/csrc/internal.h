@@ -211,9 +211,9 @@ struct PrefixArgs {
     // work: rows = B * group query rows of a KV head in tiles of 128. Two tiles share a CTA's K / V
     // tiles (a pair block); an odd last tile is a block of its own whose CTAs work on two K / V tiles
     // at a time. A block's K / V range is dealt to its splits, each split leaves one record per row.
-    int rows, rows_pad, pair_blocks, pair_splits, single_splits, ctas_per_kv, records;  // rows_pad: to a multiple of 128
-    float* part_o;    // [n_kv][records][rows_pad][head_dim] (rows past the last hold nothing of meaning)
-    float2* part_ml;  // [n_kv][records][rows_pad] maximum (base 2, scaled) and sum
+    int rows, pair_blocks, pair_splits, single_splits, ctas_per_kv, records;
+    float* part_o;    // [n_kv][records][rows][head_dim]
+    float2* part_ml;  // [n_kv][records][rows] maximum (base 2, scaled) and sum
     const float* tail;  // [B * n_kv][tail_splits][16 + 8 * head_dim]
     int tail_splits;    // records of a pair's own tokens at most (tail_part)
     // [B + 1] tiles before each request (of one kv head); a part's tiles. Null (fp32): tail_splits records each
