@@ -1172,7 +1172,7 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
             }
         };
         int at_row = sums[owner];  // tiles before request base's
-        for (;;) {
+        while (base < B) {  // (always finds its request, unless the lengths change while the kernel reads them)
             load_group();
             const int w = tiles_of(lo, len);
             int upto = w;
@@ -1193,7 +1193,9 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
             at_row += __shfl_sync(FULL, upto, 31);
             base += 32;
         }
+        if (n == 0) continue;
         int rec = mine_part - at_row / part;  // parts of the request before this one
+        if (rec < 0 || rec >= a.gsplits) continue;
         // The tile looked at: first token, the request's end, its page entries
         int at = 0, end = 0;
         int32_t blk = 0, entries = 0;
@@ -1231,7 +1233,8 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
                         load_group();
                     }
                     n = tiles_of(__shfl_sync(FULL, lo, b - base), __shfl_sync(FULL, len, b - base));
-                } while (n == 0);
+                } while (n == 0 && b < B);
+                if (n == 0) return;
             }
             ask();
         };

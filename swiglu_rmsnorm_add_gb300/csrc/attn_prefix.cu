@@ -37,6 +37,9 @@ struct Smem {
     // K or V tiles in flight; what is left of an SM's shared memory takes a CTA of the tail kernel (attn.cu)
     // for head_dim 64 and 128
     static constexpr int kStages = HD == 64 ? 10 : 5;
+    // a single block has one Q tile, whose streams have half of the stages each
+    static constexpr int kOwn = kSplitV ? 0 : (kStages + kQBytes / kTileBytes) / 2;
+    static constexpr int kBars = kSplitV ? kStages : 2 * kOwn;
     static constexpr size_t kTotal =
         1024 + kQTiles * static_cast<size_t>(kQBytes) + kStages * static_cast<size_t>(kTileBytes);
 };
@@ -101,16 +104,16 @@ __device__ __forceinline__ int64_t whole_pages(const PrefixArgs& a) {
     return (P < 0 ? 0 : (P > cap ? cap : P)) / a.block_size;
 }
 
-// A place in the ring of tiles: its stage, and the parity of the phase in which that is filled.
-// Both sides walk the ring in one order. A round is the tile of a pair, or the two tiles that a single
-// block's streams take at a time; the ring carries K of round 0, then K of round r + 1 and V of round r
-// for r = 0, 1, ...
-template <int ST>
+// A place in a ring of tiles: its stage, and the parity of the phase in which that is filled. A pair's streams
+// both use every tile of one ring. A single block's streams use every other tile, each in a ring of its
+// own: whoever waits for a stage's phase has waited for the phase before it, as a wait on a parity requires.
+// (In one ring a stage could pass from one stream to the other, which then took a tile that was still on its
+// way for the one after it.) A ring carries K of its tile 0, then K of tile i + 1 and V of tile i for i = 0, 1, ...
 struct Place {
-    int stage = 0, phase = 0;
-    __device__ __forceinline__ void next(int k = 1) {
-        stage += k;
-        if (stage >= ST) stage -= ST, phase ^= 1;
+    int stage, first, end, phase = 0;
+    __device__ __forceinline__ Place(int first, int stages) : stage(first), first(first), end(first + stages) {}
+    __device__ __forceinline__ void next() {
+        if (++stage == end) stage = first, phase ^= 1;
     }
 };
 
@@ -136,14 +139,12 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 template <typename T, int HD>
 __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC) {
     using L = Smem<HD>;
-    constexpr int ST = L::kStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t kS = 0, kP = 128, kO = 256;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char* qs = smem;                              // two Q tiles (head_dim 256: one)
-    unsigned char* ring = smem + L::kQTiles * L::kQBytes;  // ST K / V tiles
-    __shared__ uint64_t full[ST], empty[ST], s_full[2], s_free[2], p_full[2][2], pv_done[2][2];
+    __shared__ uint64_t full[L::kBars], empty[L::kBars], s_full[2], s_free[2], p_full[2][2], pv_done[2][2];
     __shared__ uint32_t tmem_base;
     __shared__ int s_ragged;
     __shared__ float2 s_ml[kRows];  // a single block's stream 1: maxima and sums
@@ -151,7 +152,7 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
     if (threadIdx.x == 0) {
         // a pair's streams both release a tile
         const bool pair = static_cast<int>(blockIdx.x) % a.ctas_per_kv < a.pair_blocks * a.pair_splits;
-        for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], pair ? 2 : 1);
+        for (int i = 0; i < L::kBars; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], pair ? 2 : 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1), mbar_init(&s_free[x], 4);
             for (int b = 0; b < 2; ++b) mbar_init(&p_full[x][b], 4), mbar_init(&pv_done[x][b], 1);
@@ -169,6 +170,8 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
     const uint32_t tmem = tmem_base;
     const int kvh = blockIdx.x / a.ctas_per_kv;
     Work w = rows_of<L::kQTiles * kRows>(a, blockIdx.x - kvh * a.ctas_per_kv);
+    unsigned char* ring = smem + (w.pair ? L::kQTiles : 1) * L::kQBytes;  // K / V tiles
+    auto ring_of = [&](int x) { return w.pair ? Place(0, L::kStages) : Place(x * L::kOwn, L::kOwn); };
     // The threads that set up (all but the producers) ask for the query rows first, the prefix's length after. A
     // thread's 16-byte chunks share their place in the row and lie kStep rows apart: one division, then steps.
     const bool producer = warp == 0 || warp == 3;
@@ -221,6 +224,7 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
     bool dead = false;  // a bounded wait ran out (counted): this thread waits no more
     auto wait = [&](uint64_t* bar, int phase) {
         if (!dead) dead = !mbar_wait(bar, static_cast<uint32_t>(phase & 1));
+        __syncwarp();  // tensor-memory accesses behind it are a whole warp's
     };
 
     if (producer) {
@@ -231,8 +235,8 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         const int ppt_log2 = __ffs(ppt) - 1, boxes = ppt * L::kHalves;
         const int box = lane * 2 + (warp == 0 ? 0 : 1), half = box >> ppt_log2, p = box & (ppt - 1);
         unsigned char* dst = ring + half * L::kHalfBytes + p * a.block_size * 128;
-        Place<ST> at;
-        int filled = 0, group[2] = {-1, -1};
+        Place at0 = ring_of(0), at1 = ring_of(1);  // at1: a single block's odd tiles
+        int group[2] = {-1, -1};
         int32_t cur[2] = {-1, -1}, next[2] = {-1, -1};
         auto entries = [&](int g) -> int32_t {
             const int64_t j = static_cast<int64_t>(w.t0) * ppt + static_cast<int64_t>(g) * 32 + lane;
@@ -247,14 +251,18 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
             }
             int64_t blk = __shfl_sync(0xffffffffu, c, (first + p) & 31);
             if (blk < 0 || blk >= a.num_blocks) blk = a.num_blocks;
-            if (filled == ST) wait(&empty[at.stage], at.phase ^ 1);
-            if (filled < ST) ++filled;
-            if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&full[at.stage], L::kTileBytes);
+            const bool odd = !w.pair && (t & 1);
+            const int stage = odd ? at1.stage : at0.stage;
+            wait(&empty[stage], (odd ? at1.phase : at0.phase) ^ 1);  // (passes at once the first time round)
+            if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&full[stage], L::kTileBytes);
             if (box < boxes)
-                tma_load_4d(dst + at.stage * L::kTileBytes, &tmC, half * 64, kvh, static_cast<int>(blk * a.block_size),
-                            plane, &full[at.stage]);
+                tma_load_4d(dst + stage * L::kTileBytes, &tmC, half * 64, kvh, static_cast<int>(blk * a.block_size), plane,
+                            &full[stage]);
             __syncwarp();
-            at.next();
+            if (odd)
+                at1.next();
+            else
+                at0.next();
         };
         auto load_k = [&](int t) { load(t, 0, cur[0], next[0], group[0]); };
         auto load_v = [&](int t) { load(t, 1, cur[1], next[1], group[1]); };
@@ -299,16 +307,15 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         const uint32_t q = tc::sdesc_lo(qs, 16) + (w.pair && !L::kSplitV ? x : 0) * (L::kQBytes / 16);
         const uint32_t k_lo = tc::sdesc_lo(ring, 16), v_lo = tc::sdesc_lo(ring + (L::kSplitV ? 2 * x * L::kHalfBytes : 0), L::kHalfBytes);
         const uint32_t tS = tmem + kS + x * kTok, tP = tmem + kP + x * 64, tO = tmem + kO + x * L::kDims;
-        Place<ST> at;  // of the round's tiles; a single block's stream 1 takes the second of them
+        Place at = ring_of(x);
         auto take = [&]() -> int {
-            Place<ST> mine = at;
-            if (!w.pair && x == 1) mine.next();
-            wait(&full[mine.stage], mine.phase);
+            const int stage = at.stage;
+            wait(&full[stage], at.phase);
             tc::fence_after();
-            return mine.stage;
+            at.next();
+            return stage;
         };
-        auto tiles_of = [&](int r) { return min(tpr, w.n - r * tpr); };
-        auto qk = [&](int i) {
+        auto qk = [&]() {
             const int stage = take();
             const uint32_t k = k_lo + stage * (L::kTileBytes / 16);
 #pragma unroll
@@ -317,15 +324,12 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
                                k + (e / 4) * (L::kHalfBytes / 16) + (e % 4) * 2, kIdescS, e > 0);
             tc::commit(elected, &s_full[x]);
             tc::commit(elected, &empty[stage]);
-            at.next(tiles_of(i));
         };
-        if (n > 0) qk(0);
+        if (n > 0) qk();
         for (int i = 0; i < n; ++i) {
             if (i + 1 < n) {
                 wait(&s_free[x], i);
-                qk(i + 1);
-            } else if (i + 1 < n0) {
-                at.next(tiles_of(i + 1));  // the other stream's last tile
+                qk();
             }
             wait(&p_full[x][i & 1], i >> 1);
             const int stage = take();
@@ -335,7 +339,6 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
                 tc::mma_f16_ts(elected, tO, p + 8 * e, v + e * 128, kIdescO, i > 0 || e > 0);
             tc::commit(elected, &pv_done[x][i & 1]);
             tc::commit(elected, &empty[stage]);
-            at.next(tiles_of(i));
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -736,9 +739,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(PrefixArgs a) {
     const float* tail = a.tail + (b * a.n_kv + kvh) * a.tail_splits * (16 + 8 * HD);
     // its own tokens' records: the parts of the tail's stream that its tiles touch
     const int tiles = static_cast<int>((len - lo + kTailTok - 1) / kTailTok);
-    const int all = recs + (!stream     ? a.tail_splits
-                            : tiles > 0 ? (before + tiles - 1) / part - before / part + 1
-                                        : 0);
+    const int count = !stream ? a.tail_splits : tiles > 0 ? (before + tiles - 1) / max(part, 1) - before / max(part, 1) + 1 : 0;
+    const int all = recs + min(max(count, 0), a.tail_splits);  // (in range whatever the lengths do meanwhile)
     float m = -INFINITY, l = 0.0f, acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.0f;

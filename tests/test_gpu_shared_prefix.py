@@ -312,6 +312,41 @@ def test_same_result_every_time_and_on_another_stream(path):
         assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("dtype,hd,B", [(torch.bfloat16, 128, 64), (torch.float16, 64, 21), (torch.bfloat16, 128, 43),
+                                        (torch.bfloat16, 256, 21)])
+def test_calls_in_a_row_on_cold_caches(dtype, hd, B):
+    """Calls that nothing waits between, on caches in turn that do not fit the L2 together and on workspaces that
+    hold NaN: copies of K and V arrive late and out of order, whatever is taken too early shows. The rows
+    are an odd number of tiles (the last has both streams on tiles of its own), several laps of the ring long."""
+    cases = [Case(B, 48, 8, hd, 16, 2900 + 16 * k, ragged(B, 2900, 60, k), dtype, k) for k in range(2)]
+    d = [c.dev() for c in cases]
+    far = [torch.empty(2, 6 * c.nb, 16, 8, hd, dtype=dtype, device=DEV) for c in cases for _ in range(3)]
+    for k, f in enumerate(far):     # the same pages, six times as far apart
+        f.fill_(float("nan"))
+        f[:, ::6] = d[k // 3]["kv_cache"]
+    six = lambda t: torch.where((t >= 0) & (t < 1 << 20), t * 6, t)
+    calls = []
+    for k, f in enumerate(far):
+        x = dict(d[k // 3], kv_cache=f)
+        x["prefix_table"], x["block_table"] = six(x["prefix_table"]), six(x["block_table"])
+        calls.append(x)
+    want = [sra.shared_prefix_attention(**d[i], scale=cases[i].scale) for i in range(2)]
+    for c, w in zip(cases, want):
+        c.check(w)
+    ws = [sra.shared_prefix_workspace(B, 48, 8, hd, x["prefix_table"].numel(), x["block_table"].shape[1], 16, dtype, DEV)
+          for x in calls]
+    before = sra.wait_timeouts()
+    for _ in range(20):
+        for w in ws:
+            w.view(torch.uint8).fill_(255)
+        got = [sra.shared_prefix_attention(**x, scale=cases[0].scale, workspace=w) for x, w in zip(calls, ws)]
+        again = [sra.shared_prefix_attention(**x, scale=cases[0].scale, workspace=w) for x, w in zip(calls, ws)]
+        torch.cuda.synchronize()
+        for k in range(len(calls)):
+            assert torch.equal(got[k], want[k // 3]) and torch.equal(again[k], want[k // 3]), k
+    assert sra.wait_timeouts() == before
+
+
 def test_refusals():
     c = Case(8, 8, 2, 128, 16, 100, [120] * 8, torch.bfloat16, 2)
     d = c.dev()
