@@ -14,6 +14,9 @@
  *   sra_paged_decode_attention  softmax decode attention read through the paged cache's block table
  *   sra_rmsnorm_linear / sra_glu_linear  RMSNorm / GLU fused into the projection they feed
  *   sra_rmsnorm_linear_ws / sra_glu_linear_ws  the same, given a workspace for larger batches
+ *   sra_kv_copy_pages / sra_kv_fork_rows / sra_kv_resize_rows / sra_kv_compact_pages  the pages of the
+ *                      cache: copied, shared, grown with copy on write, given back, moved together
+ *   sra_shared_prefix_attention  decode attention of a batch that shares a prefix, read once for it
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -38,10 +41,11 @@
  *    (cudaGetLastError after the launch). A zero-sized call (rows == 0 or
  *    T == 0) validates its arguments, enqueues nothing and returns SRA_OK.
  *  - No call waits for the device to finish, and no kernel traps or asserts. The
- *    device-side waits are the fused projections' and the TMA-fed attention
- *    variant's waits for their own tile copies, each bounded and counted when it
- *    runs out (sra_wait_timeouts), and the cluster kernels' barriers among the
- *    CTAs of one cluster, which the hardware schedules together.
+ *    device-side waits are the fused projections', the TMA-fed attention variant's
+ *    and the shared prefix's waits for their own tile copies and matrix products,
+ *    each bounded and counted when it runs out (sra_wait_timeouts), and the cluster
+ *    kernels' barriers among the CTAs of one cluster, which the hardware schedules
+ *    together.
  *  - Thread safety: calls may be made concurrently from several host threads.
  *    sra_force_variant changes process-wide state and is meant for A/B
  *    measurement only.
@@ -545,7 +549,7 @@ SRA_API int64_t sra_kv_fork_workspace_size(int64_t n, int64_t max_blocks_per_seq
  * the entry does nothing, for: a row >= rows or one that an earlier entry names; a length (new
  * or present) outside [0, max_blocks_per_seq * block_size]; a partly filled last page outside
  * [0, num_blocks) in a row that grows. One each is added for bad entries and missing holders among the
- * pages given up, as in sra_kv_fork_rows. New pages' contents are not cleared.  * n_caches >= 1.
+ * pages given up, as in sra_kv_fork_rows. New pages' contents are not cleared. n_caches >= 1.
  */
 SRA_API int sra_kv_resize_rows(int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, const int32_t* row_idx,
                                const int32_t* lens, int64_t n, int64_t rows, int64_t max_blocks_per_seq,
@@ -636,8 +640,8 @@ SRA_API int sra_last_cuda_error(void);
  * Bounded device waits that gave up, on the current device, since the library was
  * loaded. Kernels that stream tiles with tensor-memory-access copies
  * (sra_rmsnorm_linear, sra_glu_linear and their _ws forms; decode attention's
- * TMA-fed variant) wait on shared-memory barriers for those copies; each wait is bounded (about a second), and a wait that runs out is
- * counted here and the kernel goes on, so a copy that never completes cannot hang
+ * TMA-fed variant; sra_shared_prefix_attention) wait on shared-memory barriers for those
+ * copies; each wait is bounded (about a second), and a wait that runs out is counted here and the kernel goes on, so a copy that never completes cannot hang
  * the GPU (that call's output is then not valid). Reads the counter synchronously
  * (cudaMemcpyFromSymbol); 0 on a device that ran none of those kernels. No paper
  * section defines this; it is the library's own failure report.

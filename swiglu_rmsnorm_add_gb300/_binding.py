@@ -620,10 +620,10 @@ def _kv_caches(kv_caches):
     if isinstance(kv_caches, torch.Tensor):
         if kv_caches.dim() == 6 and kv_caches.is_cuda and kv_caches.shape[0] > 0 and kv_caches.shape[1] == 2 \
                 and kv_caches.is_contiguous():
-            n, first = kv_caches.shape[0], kv_caches.data_ptr()
+            (n, *shape), first = kv_caches.shape, kv_caches.data_ptr()
             step = kv_caches.stride(0) * kv_caches.element_size()
             ptrs = array.array("Q", range(first, first + n * step, step) if step else [first] * n)
-            return kv_caches.shape[1:], kv_caches.dtype, kv_caches.get_device(), ptrs, n
+            return shape, kv_caches.dtype, kv_caches.get_device(), ptrs, n
         caches = [kv_caches] if kv_caches.dim() == 5 else list(kv_caches) if kv_caches.dim() == 6 else None
         if caches is None:
             raise ValueError("kv_caches must be [2, num_blocks, block_size, n_kv_head, head_dim], or [layers, ...] of it")
@@ -645,8 +645,20 @@ def _kv_caches(kv_caches):
     return shape, dtype, dev, array.array("Q", [c.data_ptr() for c in caches]), len(caches)
 
 
+_I32 = torch.int32
+
+
+def _vectors_ok(dev, *ts) -> bool:
+    """Whether all are what _int32 asks of one dimension."""
+    for t in ts:
+        if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.dim() != 1 or t.get_device() != dev \
+                or not t.is_contiguous():
+            return False
+    return True
+
+
 def _int32(t, name, dim, dev=None):
-    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == dim and t.is_contiguous() \
+    if isinstance(t, torch.Tensor) and t.dtype is _I32 and t.dim() == dim and t.is_contiguous() \
             and t.get_device() == dev:
         return
     _cuda(t, name)
@@ -667,16 +679,20 @@ def _err_ptr(err_count, dev):
     return err_count.data_ptr()
 
 
-def _page_state(block_table, seq_lens, ref_counts):
-    """The device index of the state; its tensors checked."""
-    _cuda(block_table, "block_table")
+def _page_state(block_table, seq_lens, ref_counts, **vectors):
+    """(device index, rows, max_blocks, num_blocks) of the state; its tensors and the call's int32 vectors checked."""
+    if not (isinstance(block_table, torch.Tensor) and block_table.is_cuda):
+        _cuda(block_table, "block_table")
     dev = block_table.get_device()
-    _int32(block_table, "block_table", 2, dev)
-    _int32(seq_lens, "seq_lens", 1, dev)
-    _int32(ref_counts, "ref_counts", 1, dev)
-    if seq_lens.shape[0] != block_table.shape[0]:
+    if block_table.dtype is not _I32 or block_table.dim() != 2 or not block_table.is_contiguous() \
+            or not _vectors_ok(dev, seq_lens, ref_counts, *vectors.values()):
+        _int32(block_table, "block_table", 2, dev)
+        for name, t in dict(seq_lens=seq_lens, ref_counts=ref_counts, **vectors).items():
+            _int32(t, name, 1, dev)
+    rows, mb = block_table.shape
+    if seq_lens.numel() != rows:
         raise ValueError("block_table and seq_lens must have one row per request")
-    return dev
+    return dev, rows, mb, ref_counts.numel()
 
 
 def _byte_workspace(fn: str, n: int, device) -> torch.Tensor:
@@ -697,7 +713,8 @@ def _workspace_args(workspace, make, dev, stream):
                 torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=torch.device("cuda", dev))
             with torch.cuda.stream(s):
                 workspace = make()
-    _cuda(workspace, "workspace")
+    if not (isinstance(workspace, torch.Tensor) and workspace.is_cuda):
+        _cuda(workspace, "workspace")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     if workspace.get_device() != dev:
@@ -714,10 +731,11 @@ def copy_kv_pages(kv_caches, src: torch.Tensor, dst: torch.Tensor, err_count: to
     and no source (their contents are undefined otherwise); an index past the cache is skipped
     and counted in err_count."""
     (_, nb, bs, n_kv, hd), dtype, dev, ptrs, count = _kv_caches(kv_caches)
-    _int32(src, "src", 1, dev)
-    _int32(dst, "dst", 1, dev)
-    n = src.shape[0]
-    if dst.shape[0] != n:
+    if not _vectors_ok(dev, src, dst):
+        _int32(src, "src", 1, dev)
+        _int32(dst, "dst", 1, dev)
+    n = src.numel()
+    if dst.numel() != n:
         raise ValueError("src and dst must have the same length")
     if dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
@@ -740,16 +758,14 @@ def fork_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: 
     block_table int32 [rows, max_blocks], seq_lens int32 [rows] and ref_counts int32
     [num_blocks] change in place; parents are read as they were at entry. No page is copied:
     resize_kv_rows copies a shared, partly filled page before a row writes into it."""
-    dev = _page_state(block_table, seq_lens, ref_counts)
-    _int32(parents, "parents", 1, dev)
-    _int32(children, "children", 1, dev)
-    n, (rows, mb) = parents.shape[0], block_table.shape
-    if children.shape[0] != n:
+    dev, rows, mb, nb = _page_state(block_table, seq_lens, ref_counts, parents=parents, children=children)
+    n = parents.numel()
+    if children.numel() != n:
         raise ValueError("parents and children must have the same length")
     with _on(dev):
         workspace, wp, wb = _workspace_args(workspace, lambda: kv_fork_workspace(n, mb, block_table.device), dev, stream)
         st = lib().sra_kv_fork_rows(block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
-                                    parents.data_ptr(), children.data_ptr(), n, rows, mb, ref_counts.shape[0],
+                                    parents.data_ptr(), children.data_ptr(), n, rows, mb, nb,
                                     int(block_size), wp, wb, _err_ptr(err_count, dev), _stream(block_table, stream))
     _check("sra_kv_fork_rows", st)
 
@@ -778,32 +794,30 @@ def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts
     Returns (pos, slot_mapping), int64 [n]: position and cache slot of each row's last token, what
     rope_kv_store takes for a decode step; -1 for an empty row or a refused entry. A row whose pages are
     not there stays as it was and is counted in err_count."""
-    dev = _page_state(block_table, seq_lens, ref_counts)
+    dev, table_rows, mb, counts = _page_state(block_table, seq_lens, ref_counts, rows=rows, lens=lens)
     (_, nb, bs, n_kv, hd), dtype, cache_dev, ptrs, count = _kv_caches(kv_caches)
-    _int32(rows, "rows", 1, dev)
-    _int32(lens, "lens", 1, dev)
-    n = rows.shape[0]
-    if lens.shape[0] != n:
+    n = rows.numel()
+    if lens.numel() != n:
         raise ValueError("rows and lens must have the same length")
     if cache_dev != dev:
         raise ValueError("all tensors must be on the same CUDA device")
     if dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
     if pos is None:
-        pos = torch.empty(n, dtype=torch.int64, device=block_table.device)
+        pos = torch.empty(n, dtype=torch.int64, device=rows.device)
     else:
         _int64_out(pos, "pos", n, dev)
     if slot_mapping is None:
-        slot_mapping = torch.empty(n, dtype=torch.int64, device=block_table.device)
+        slot_mapping = torch.empty(n, dtype=torch.int64, device=rows.device)
     else:
         _int64_out(slot_mapping, "slot_mapping", n, dev)
-    if ref_counts.shape[0] != nb:
+    if counts != nb:
         raise ValueError("ref_counts must have one entry per page of the caches")
     with _on(dev):
         workspace, wp, wb = _workspace_args(workspace, lambda: kv_resize_workspace(n, nb, block_table.device), dev,
                                             stream)
         st = lib().sra_kv_resize_rows(block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
-                                      rows.data_ptr(), lens.data_ptr(), n, block_table.shape[0], block_table.shape[1],
+                                      rows.data_ptr(), lens.data_ptr(), n, table_rows, mb,
                                       ptrs.buffer_info()[0], count, nb, bs, n_kv, hd, pos.data_ptr(),
                                       slot_mapping.data_ptr(), wp, wb, _err_ptr(err_count, dev), DTYPE_CODE[dtype],
                                       _stream(block_table, stream))
@@ -821,10 +835,10 @@ def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_coun
                      err_count: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Move the live pages (count > 0) to the front of the caches; tables and counts follow.
     Returns num_live, int32 [1]: the pages from there on are free."""
-    dev = _page_state(block_table, seq_lens, ref_counts)
+    dev, rows, mb, counts = _page_state(block_table, seq_lens, ref_counts)
     (_, nb, bs, n_kv, hd), dtype, cache_dev, ptrs, count = _kv_caches(kv_caches)
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=block_table.device)
+        num_live = torch.empty(1, dtype=_I32, device=seq_lens.device)
     _int32(num_live, "num_live", 1, dev)
     if num_live.numel() != 1:
         raise ValueError("num_live must hold one entry")
@@ -832,12 +846,12 @@ def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_coun
         raise ValueError("all tensors must be on the same CUDA device")
     if dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
-    if ref_counts.shape[0] != nb:
+    if counts != nb:
         raise ValueError("ref_counts must have one entry per page of the caches")
     with _on(dev):
         workspace, wp, wb = _workspace_args(workspace, lambda: kv_compact_workspace(nb, block_table.device), dev, stream)
         st = lib().sra_kv_compact_pages(block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
-                                        block_table.shape[0], block_table.shape[1], ptrs.buffer_info()[0], count, nb, bs,
+                                        rows, mb, ptrs.buffer_info()[0], count, nb, bs,
                                         n_kv, hd, num_live.data_ptr(), wp, wb, _err_ptr(err_count, dev),
                                         DTYPE_CODE[dtype], _stream(block_table, stream))
     _check("sra_kv_compact_pages", st)
@@ -869,10 +883,12 @@ def shared_prefix_attention(q: torch.Tensor, kv_cache: torch.Tensor, prefix_tabl
     request's tokens) as in paged_decode_attention; prefix_table: int32 [prefix_blocks], the pages of
     the prefix (a row of block_table that reaches past it will do); prefix_len: int32 [1] on the
     device. workspace: from shared_prefix_workspace; one is made for the call where none is given."""
-    _cuda(q, "q")
+    if not (isinstance(q, torch.Tensor) and q.is_cuda):
+        _cuda(q, "q")
     dev, dtype = q.get_device(), q.dtype
-    _int32(prefix_table, "prefix_table", 1, dev)
-    _int32(prefix_len, "prefix_len", 1, dev)
+    if not _vectors_ok(dev, prefix_table, prefix_len):
+        _int32(prefix_table, "prefix_table", 1, dev)
+        _int32(prefix_len, "prefix_len", 1, dev)
     if prefix_len.numel() != 1:
         raise ValueError("prefix_len must hold one entry")
     if out is None:
@@ -887,7 +903,7 @@ def shared_prefix_attention(q: torch.Tensor, kv_cache: torch.Tensor, prefix_tabl
         raise ValueError("seq_lens must be contiguous int32 on the queries' device")
     B, n_head, hd = q.shape
     _, nb, bs, n_kv, _ = kv_cache.shape
-    mb, pb = block_table.shape[1], prefix_table.shape[0]
+    mb, pb = block_table.size(1), prefix_table.numel()
     code = DTYPE_CODE[dtype]
     with _on(dev):
         wp, wb = None, 0
