@@ -586,8 +586,8 @@ SRA_API int64_t sra_kv_compact_workspace_size(int64_t num_blocks);
  * block_table's rows are those of sra_paged_decode_attention: the entries that lie wholly below the
  * prefix's length are not read (they may hold the same pages, as sra_kv_fork_rows leaves them, or
  * anything). The prefix may end inside a page; the caller keeps the prefix's pages held meanwhile (by
- * a row that does not grow, or by giving only the whole pages, which the requests hold). A request shorter than the prefix attends to the
- * tokens that it has; one without tokens (or none whose score is above -inf) gets zeros; NaN in what
+ * a row that does not grow, or by giving only the whole pages, which the requests hold). A request
+ * shorter than the prefix attends to the tokens that it has; one without tokens (or none whose score is above -inf) gets zeros; NaN in what
  * a request attends to gives NaN.
  *
  * With a workspace the queries of all requests that share a KV head are the rows of one product with

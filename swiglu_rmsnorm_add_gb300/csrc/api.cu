@@ -1337,7 +1337,12 @@ int check_caches(void* const* caches, int64_t n, int64_t plane_bytes, int es) {
         if (!caches[i]) return SRA_ERR_NULL;
         if (reinterpret_cast<uintptr_t>(caches[i]) % es) return SRA_ERR_ARG;
     }
-    for (int64_t i = 0; i < n; ++i)
+    // in ascending order neighbours are all that can meet
+    bool apart = true;
+    for (int64_t i = 1; i < n && apart; ++i)
+        apart = reinterpret_cast<uintptr_t>(caches[i - 1]) + static_cast<uintptr_t>(2 * plane_bytes) <=
+                reinterpret_cast<uintptr_t>(caches[i]);
+    for (int64_t i = 0; i < n && !apart; ++i)
         for (int64_t j = i + 1; j < n; ++j)
             if (overlap(span_of(caches[i], 1, 0, 2 * plane_bytes, 1), span_of(caches[j], 1, 0, 2 * plane_bytes, 1)))
                 return SRA_ERR_ALIAS;
@@ -1352,8 +1357,15 @@ bool meets_caches(void* const* caches, int64_t n, int64_t plane_bytes, const voi
     return false;
 }
 bool any_meets_caches(void* const* caches, int64_t n, int64_t plane_bytes, const PageCall& c) {
+    if (plane_bytes == 0) return false;
+    uintptr_t lo = UINTPTR_MAX, hi = 0;  // what lies outside of all the caches' range meets none
+    for (int64_t i = 0; i < n; ++i) {
+        lo = std::min(lo, reinterpret_cast<uintptr_t>(caches[i]));
+        hi = std::max(hi, reinterpret_cast<uintptr_t>(caches[i]) + static_cast<uintptr_t>(2 * plane_bytes));
+    }
     for (int i = 0; i < c.n; ++i)
-        if (meets_caches(caches, n, plane_bytes, reinterpret_cast<const void*>(c.spans[i].lo),
+        if (c.spans[i].lo < hi && c.spans[i].hi > lo &&
+            meets_caches(caches, n, plane_bytes, reinterpret_cast<const void*>(c.spans[i].lo),
                          static_cast<int64_t>(c.spans[i].hi - c.spans[i].lo)))
             return true;
     return false;
@@ -1669,8 +1681,9 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
         while (p.tail_splits < 16 && groups * p.tail_splits < 2 * static_cast<int64_t>(sms) && own >= 128 * p.tail_splits)
             p.tail_splits *= 2;
     }
-    // (the tail's counts of records and of tiles of 32 tokens are 32-bit)
-    if (groups * p.tail_splits >= (int64_t(1) << 30) ||
+    // (tokens, and the tail's counts of records and of tiles of 32 tokens, are 32-bit)
+    if (groups * p.tail_splits >= (int64_t(1) << 30) || prefix_blocks >= ((int64_t(1) << 31) - 64) / block_size ||
+        max_blocks >= ((int64_t(1) << 31) - 64) / block_size ||
         static_cast<double>(B) * max_blocks * block_size / 32 + B >= static_cast<double>(1 << 30)) {
         p.use = false;
         return p;
@@ -1780,7 +1793,7 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     // the tensor-core path reads queries four bytes at a time
     const bool together = workspace && pp.use && (reinterpret_cast<uintptr_t>(q) & 3u) == 0 &&
                           (dtype == DT_F32 || q_tok_stride % 2 == 0) &&
-                          static_cast<int64_t>(prefix_smem(head_dim, dtype)) <= limit - 512 &&
+                          static_cast<int64_t>(prefix_smem(head_dim, dtype)) <= limit - 512 && num_blocks > 0 &&
                           num_blocks * block_size < (int64_t(1) << 31) - 64;
     if (!together) {
         if (g_force_prefix.load(std::memory_order_relaxed) == 1) return SRA_ERR_VARIANT;

@@ -38,7 +38,8 @@ __device__ __forceinline__ void drop_refs(int32_t* ref, int32_t page, int k, int
 }
 
 // ------------------------------------------------------------------ copying
-// (Plain loads and stores: streaming hints on them cost a tenth: 1021 pages of 28 layers, 937 MB read and written, 171 us with them, 147 without, 6.4 TB/s.)
+// (Plain loads and stores: with streaming hints 1021 pages of 28 layers, 937 MB read and written, took 171 us,
+// without 140, 6.7 TB/s.)
 template <typename V>
 __device__ __forceinline__ void copy_span(char* dst, const char* src, int64_t nvec, int tid, int threads) {
     constexpr int kUnroll = 4;

@@ -56,6 +56,17 @@ def test_copy(L):
     assert copy(L, src=CACHE + 128) == ALIAS and copy(L, err=A) == ALIAS and copy(L, err=CACHE) == ALIAS
 
 
+def test_caches_in_any_order(L):
+    # a cache is 65536 bytes
+    step = 1 << 16
+    for bad in ((CACHE + step - 8, CACHE), (CACHE + step, CACHE, CACHE + step - 16), (CACHE, CACHE + 2 * step, CACHE),
+                (CACHE + 3 * step, CACHE + step, CACHE + 2 * step - 2)):
+        assert copy(L, c=caches(*bad), k=len(bad)) == ALIAS, bad
+    apart = caches(CACHE + 6 * step, CACHE, CACHE + 3 * step)
+    for src in (CACHE + 6 * step + 64, CACHE + 7 * step - 4, CACHE - 8, CACHE + 3 * step - 12, CACHE + 4 * step - 4):
+        assert copy(L, c=apart, k=3, src=src) == ALIAS, hex(src)
+
+
 def test_fork(L):
     for bad in (dict(n=-1), dict(rows=-1), dict(M=-1), dict(nb=-1), dict(bs=0), dict(n=524281), dict(rows=1 << 31)):
         assert fork(L, **bad) == SHAPE, bad
