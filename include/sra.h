@@ -595,7 +595,8 @@ SRA_API int64_t sra_kv_compact_workspace_size(int64_t num_blocks);
  * tensor cores, fp32 on the CUDA cores); each request's own tokens follow as in
  * sra_paged_decode_attention, and the parts are merged through their maxima and sums of
  * exponentials (fp32). In bf16 and fp16 the probabilities are then rounded once to the dtype before
- * they multiply V (fp32 sums); the path without a workspace keeps them to 16 bits or more.
+ * they multiply V (fp32 sums; in fp16 one that is subnormal is off by up to 2^-32 of its part's largest);
+ * the path without a workspace keeps them to 16 bits or more.
  *
  * q, kv_cache, out, scale: as in sra_paged_decode_attention. prefix_table: int32 [prefix_blocks];
  * prefix_len: device int32, one entry; block_table: int32 [B, max_blocks_per_seq]; seq_lens: int32 [B].

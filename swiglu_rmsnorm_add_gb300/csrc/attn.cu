@@ -1003,8 +1003,8 @@ __device__ __forceinline__ void tail_scores(uint32_t ks, const uint32_t (&qb)[HD
         }
 }
 // The running softmax over those scores (valid: a bit per token): maxima m of the lane's two heads, this
-// lane's tokens' part l of their sums, corr = 2^(old m - new m); the probabilities, rounded once to T (half a
-// step of T each, as the prefix's), as B fragments of the next product.
+// lane's tokens' part l of their sums, corr = 2^(old m - new m); the probabilities (relative to 2^(m - kUnderMax), as
+// l), rounded once to T (half a step of T each, as the prefix's), as B fragments of the next product.
 template <typename T>
 __device__ __forceinline__ void tail_softmax(float (&p)[2][4], unsigned valid, float (&m)[2], float (&l)[2],
                                              float (&corr)[2], uint32_t (&pb)[2][2], float scale_log2, int lane) {
@@ -1033,7 +1033,7 @@ __device__ __forceinline__ void tail_softmax(float (&p)[2][4], unsigned valid, f
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float now = fmaxf(m[h], mx[h]);
-        base[h] = now == -INFINITY ? 0.0f : now;  // (then every p is 2^-inf = 0)
+        base[h] = now == -INFINITY ? 0.0f : now - kUnderMax<T>;  // (then every p is 2^-inf = 0)
         corr[h] = now == -INFINITY ? 1.0f : ex2(m[h] - now);
         m[h] = now;
     }
@@ -1341,7 +1341,7 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (2 * ft + h >= G) continue;
-                    if (fg == 0) out[2 * ft + h] = m[h], out[8 + 2 * ft + h] = l[h];
+                    if (fg == 0) out[2 * ft + h] = m[h] - kUnderMax<T>, out[8 + 2 * ft + h] = l[h];
                     float* out_row = out + 16 + (2 * ft + h) * HD + fg;  // eight lanes store 32 bytes in a row
 #pragma unroll
                     for (int d = 0; d < KS; ++d) out_row[16 * d] = o[d][h], out_row[16 * d + 8] = o[d][2 + h];

@@ -345,7 +345,10 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         // softmax: thread = query row of stream x. The running maximum m (base 2, scaled) is moved only
         // when a tile's maximum passes it by more than kRescale: o and l are sums of 2^(s - m) for one
         // m, so any m will do as long as nothing overflows (2^8 times a row's sum of values does not),
-        // and O in tensor memory is scaled seldom.
+        // and O in tensor memory is scaled seldom. fp16 has few exponents: there m stays 7 below the maximum
+        // (p up to 2^15), so that probabilities down to 2^-21 of the largest are normal numbers and those to 2^-32
+        // are not lost.
+        constexpr float kUnder = kUnderMax<T>;
         const int x = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + lanes + kS + x * kTok, tP = tmem + lanes + kP + x * 64,
@@ -383,12 +386,12 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
                                    __uint_as_float(v[k / 32][k % 32 + 4 + u]));
             const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
             if (i == 0) {
-                m = mx;
+                m = mx - kUnder;
             } else {
-                const bool move = mx > m + kRescale;
+                const bool move = mx > m + (kUnder + kRescale);
                 if (__any_sync(0xffffffffu, move)) {
-                    const float f = move ? ex2(m - mx) : 1.0f;
-                    if (move) l *= f, m = mx;
+                    const float f = move ? ex2(m - (mx - kUnder)) : 1.0f;
+                    if (move) l *= f, m = mx - kUnder;
                     wait(&pv_done[x][(i - 1) & 1], (i - 1) / 2);
                     tc::fence_after();
 #pragma unroll 1

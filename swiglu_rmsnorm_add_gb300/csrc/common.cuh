@@ -152,6 +152,11 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(v);
 }
 
+// How far below a row's maximum (in powers of two) softmax kernels that round probabilities to T put their
+// exponents' base: fp16's normal numbers end at 2^-14.
+template <typename T> constexpr float kUnderMax = 0.0f;
+template <> inline constexpr float kUnderMax<__half> = 7.0f;
+
 // Round an fp32 value to T and back (the value a T store would hold).
 template <typename T> __device__ __forceinline__ float round_trip(float v) {
     return to_f32(from_f32<T>(v));

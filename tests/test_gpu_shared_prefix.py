@@ -171,6 +171,34 @@ def test_peaked_scores(dtype, hd, path):
     run(Case(40, 12, 2, hd, 16, 1000, ragged(40, 1000, 90, 7), dtype, 7, scale=1.0, spread=2.0))
 
 
+@pytest.mark.parametrize("B,prefix,own", [(3, 9000, 40), (40, 9000, 40), (3, 64, 9000), (40, 64, 3000)])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_many_small_probabilities(hd, B, prefix, own):
+    """One token has nearly all of the weight and V = 0 (the first of the longer part), all the others 2^-25.5 of
+    it each and V = 1. In fp16 the probabilities, at 2^7 relative to the largest, are subnormal here, with a step of 2^-24
+    and an error of half of one: 2^-32 of the largest, per token, beside what every fp16 result is allowed (half a step of
+    its own, 2^-25 or more, and the evaluation in fp32)."""
+    c = Case(B, 12, 2, hd, 16, prefix, [prefix + own] * B, torch.float16, 3, scale=float(np.log(2.0)))
+    c.q.zero_()
+    c.q[..., 0] = 1
+    some = ~c.cache[0].isnan().any(-1)
+    for plane, value in ((0, 0.0), (1, 1.0)):
+        c.cache[plane][some] = value
+    c.cache[0][..., 0][some] = -5.5
+    pages = [(c.ptable[0], 0)] if prefix > own else [(c.table[b, prefix // 16], 0) for b in range(B)]
+    for page, at in pages:
+        c.cache[0, page, at, :, 0], c.cache[1, page, at] = 20, 0
+    sra.force_variant("shared_prefix", 1)
+    try:
+        got = sra.shared_prefix_attention(**c.dev(), scale=c.scale)
+    finally:
+        sra.force_variant("shared_prefix", -1)
+    o, A = c.want()
+    assert float(o.min()) > 3000 * 2.0 ** -26
+    step = torch.maximum(2.0 ** -11 * o, torch.full_like(o, 2.0 ** -25))
+    assert bool(((got.double() - o).abs() <= step + 6e-5 * A + (prefix + own) * 2.0 ** -32).all())
+
+
 @pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float16, 64), (torch.float32, 64),
                                       (torch.bfloat16, 256)])
 def test_bad_entries_are_skipped_and_counted(dtype, hd, path):
