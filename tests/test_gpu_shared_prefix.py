@@ -375,6 +375,51 @@ def test_calls_in_a_row_on_cold_caches(dtype, hd, B):
     assert sra.wait_timeouts() == before
 
 
+@pytest.mark.parametrize("pdl", [False, True])
+def test_calls_at_once_beside_other_tensor_memory_users(pdl):
+    """Calls on two streams, each with a workspace of its own, beside projections on a third: all of them
+    allocate tensor memory on the SMs that they share, and each gives what it gives alone."""
+    cs = [Case(64, 12, 2, 128, 16, 3000, ragged(64, 3000, 200, 5), torch.bfloat16, 5),
+          Case(30, 32, 4, 64, 32, 2500, ragged(30, 2500, 100, 6), torch.float16, 6)]
+    x = torch.randn(64, 1536, device=DEV).to(torch.bfloat16)
+    w, W = torch.ones(1536, device=DEV, dtype=torch.bfloat16), torch.randn(2048, 1536, device=DEV).to(torch.bfloat16)
+    lw = sra.linear_workspace(64, 1536, torch.bfloat16, DEV, N=2048)
+    prev = sra.set_pdl(pdl)
+    try:
+        calls = []
+        for c in cs:
+            d = c.dev()
+            ws = sra.shared_prefix_workspace(c.B, c.q.shape[1], c.n_kv, c.hd, d["prefix_table"].numel(),
+                                             d["block_table"].shape[1], c.bs, c.dtype, DEV)
+            assert ws is not None
+            out = torch.empty_like(d["q"])
+            calls.append((lambda s, d=d, ws=ws, out=out, c=c: sra.shared_prefix_attention(
+                **d, scale=c.scale, workspace=ws, out=out, stream=s), out))
+        y = torch.empty(64, 2048, device=DEV, dtype=torch.bfloat16)
+        calls.append((lambda s: sra.rmsnorm_linear(x, w, W, y, workspace=lw, stream=s), y))
+        want = []
+        for call, out in calls:
+            call(None)
+            torch.cuda.synchronize()
+            want.append(out.clone())
+        for c, v in zip(cs, want):
+            c.check(v)
+        streams = [torch.cuda.Stream() for _ in calls]
+        for _ in range(10):
+            for _, out in calls:
+                out.fill_(float("nan"))
+            torch.cuda.synchronize()
+            for _ in range(20):
+                for (call, _), s in zip(calls, streams):
+                    call(s)
+            torch.cuda.synchronize()
+            for (_, out), v in zip(calls, want):
+                assert torch.equal(out, v)
+        assert sra.wait_timeouts() == 0
+    finally:
+        sra.set_pdl(prev)
+
+
 def test_refusals():
     c = Case(8, 8, 2, 128, 16, 100, [120] * 8, torch.bfloat16, 2)
     d = c.dev()
