@@ -279,3 +279,31 @@ def test_refusals():
         sra.fork_kv_rows(t, s, ref, i32([0]), i32([1]), 4, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
     assert e.value.status == -6
     assert t.tolist() == [[0, 1], [2, 3]]
+
+
+def test_cache_past_32_bit_offsets():
+    """A cache whose planes have more than 2^31 elements: pages copied, copied on write and moved at its far end."""
+    bs, n_kv, hd = 16, 8, 128
+    nb = 2 ** 31 // (bs * n_kv * hd) + 64
+    cache = torch.empty(2, nb, bs, n_kv, hd, dtype=torch.bfloat16, device=DEV)
+    cache[:, -64:] = torch.randn(2, 64, bs, n_kv, hd, device=DEV).to(torch.bfloat16)
+    end = cache[:, -64:].clone()
+    sra.copy_kv_pages(cache, i32([nb - 64, nb - 1]), i32([nb - 2, 5]))
+    assert torch.equal(cache[:, nb - 2], end[:, 0]) and torch.equal(cache[:, 5], end[:, 63])
+    # rows 0 and 1 hold a last page of 3 tokens together; every page but two at the end is taken
+    table, seq = i32([[nb - 60, nb - 50], [nb - 60, nb - 50]]), i32([19, 19])
+    ref = torch.ones(nb, dtype=torch.int32, device=DEV)
+    ref[[nb - 60, nb - 50]] = 2
+    ref[[nb - 40, nb - 30]] = 0
+    pos, slot = sra.resize_kv_rows(table, seq, ref, i32([0, 1]), i32([20, 20]), cache)
+    assert table.cpu().tolist() == [[nb - 60, nb - 40], [nb - 60, nb - 30]]
+    assert slot.cpu().tolist() == [(nb - 40) * bs + 3, (nb - 30) * bs + 3] and pos.cpu().tolist() == [19, 19]
+    for page in (nb - 40, nb - 30):
+        assert torch.equal(cache[:, page, :3], end[:, 14, :3])
+    # all but these rows' pages free: they move to the front
+    ref.zero_()
+    ref[[nb - 60, nb - 40, nb - 30]] = i32([2, 1, 1])
+    kept = cache[:, [nb - 60, nb - 40, nb - 30]].clone()
+    assert int(sra.compact_kv_pages(table, seq, ref, cache).item()) == 3
+    assert table.cpu().tolist() == [[0, 1], [0, 2]] and torch.equal(cache[:, :3], kept)
+    assert ref[:3].cpu().tolist() == [2, 1, 1] and int(ref.sum()) == 4

@@ -420,6 +420,21 @@ def test_calls_at_once_beside_other_tensor_memory_users(pdl):
         sra.set_pdl(prev)
 
 
+@pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float16, 256), (torch.float32, 64)])
+def test_cache_past_32_bit_offsets(dtype, hd, path):
+    """The pages of a small cache at the far end of one whose planes have more than 2^31 elements: the same result."""
+    c = Case(40, 48, 8, hd, 16, 1500, ragged(40, 1500, 60, 7), dtype, 7)
+    d = c.dev()
+    want = sra.shared_prefix_attention(**d, scale=c.scale)
+    c.check(want)
+    nb = 2 ** 31 // (16 * 8 * hd) + c.nb
+    far = torch.empty(2, nb, 16, 8, hd, dtype=dtype, device=DEV)
+    far[:, -c.nb:] = d["kv_cache"]
+    move = lambda t: torch.where((t >= 0) & (t < c.nb), t + (nb - c.nb), t)
+    d["kv_cache"], d["prefix_table"], d["block_table"] = far, move(d["prefix_table"]), move(d["block_table"])
+    assert torch.equal(sra.shared_prefix_attention(**d, scale=c.scale), want)
+
+
 def test_refusals():
     c = Case(8, 8, 2, 128, 16, 100, [120] * 8, torch.bfloat16, 2)
     d = c.dev()
