@@ -370,6 +370,7 @@ struct CompactArgs {
     int32_t* ws_dst;    // [num_blocks]
     // of one launch
     int64_t copy_from = 0;
+    int64_t few = 0;  // CTAs that copy where there are many pages
     bool bookkeeping = true;
 };
 cudaError_t launch_compact_plan(const CompactArgs& a, const PagePlan& p, cudaStream_t s);

@@ -39,7 +39,7 @@ __device__ __forceinline__ void drop_refs(int32_t* ref, int32_t page, int k, int
 
 // ------------------------------------------------------------------ copying
 // (Plain loads and stores: with streaming hints 1021 pages of 28 layers, 937 MB read and written, took 171 us,
-// without 140, 6.7 TB/s.)
+// without 147 at the time.)
 template <typename V>
 __device__ __forceinline__ void copy_span(char* dst, const char* src, int64_t nvec, int tid, int threads) {
     constexpr int kUnroll = 4;
@@ -61,14 +61,15 @@ struct Pair {
     int64_t bytes;  // of the page's start, in each plane (0: nothing)
 };
 
-// The CTAs [first, first + ctas) of a launch copy: item (pair, cache, plane) per step, pairs
-// slowest, so that neighbouring CTAs work on one pair and its indices come from the L2 once.
+// The CTAs [0, ctas) of a launch copy: item (cache, plane, pair) per step, pairs fastest, so that a page that is
+// the source of several copies is read again while the L2 has it (1021 copies, some of one source, 140 us
+// with the pairs slowest, 122 so).
 template <typename V, typename F>
 __device__ __forceinline__ void copy_items(const CacheList& c, int64_t count, int64_t cta, int64_t ctas, F&& pair) {
     const int64_t per = 2 * static_cast<int64_t>(c.n);
     for (int64_t item = cta; item < count * per; item += ctas) {
-        const int64_t i = item / per;
-        const int rest = static_cast<int>(item - i * per);
+        const int rest = static_cast<int>(item / count);
+        const int64_t i = item - rest * count;
         const Pair p = pair(i, rest == 0);
         if (p.bytes <= 0) continue;
         char* base = static_cast<char*>(c.p[rest >> 1]) + (rest & 1) * c.plane_bytes;
@@ -566,8 +567,13 @@ __global__ void __launch_bounds__(kCols) compact_move_kernel(CacheList c, Compac
     pdl_enter();
     const int64_t live = *a.ws_live, moved = *a.ws_moved, below = live - moved;
     if (blockIdx.x >= a.copy_from) {
-        copy_items<V>(c, moved, blockIdx.x - a.copy_from, gridDim.x - a.copy_from,
-                      [&](int64_t i, bool) { return Pair{a.ws_src[below + i], a.ws_dst[i], c.page_bytes}; });
+        // Many pages are copied by five CTAs an SM, 6 MB in flight (974 pages of 28 layers: 143 us; by four 154, by
+        // six 147, by all twelve 151); few by all, whose index reads then overlap (70 MB 15 us, by six an SM 21).
+        const int64_t all = gridDim.x - a.copy_from, cta = blockIdx.x - a.copy_from;
+        const int64_t ctas = moved * 2 * c.n >= 16 * all && a.few < all ? a.few : all;
+        if (cta < ctas)
+            copy_items<V>(c, moved, cta, ctas,
+                          [&](int64_t i, bool) { return Pair{a.ws_src[below + i], a.ws_dst[i], c.page_bytes}; });
         return;
     }
     if (!a.bookkeeping) return;
@@ -607,10 +613,13 @@ cudaError_t by_vec(int vec, F&& f) {
     }
 }
 
-// CTAs that copy `items` (pair, cache, plane) spans: all resident at once at most.
+// CTAs that copy `items` (pair, cache, plane) spans: all resident at once at most, beside `others` CTAs of the
+// launch (a copying CTA that starts when those are done ends late: the copies on write of 121 rows in 28 layers
+// 16.8 us, beside them 15.3).
 template <typename... KArgs>
-int64_t copy_ctas(void (*kernel)(KArgs...), int num_sms, int64_t items) {
-    return persistent_grid(kernel, kCopyThreads, 0, num_sms, items);
+int64_t copy_ctas(void (*kernel)(KArgs...), int num_sms, int64_t items, int64_t others = 0) {
+    const int64_t all = persistent_grid(kernel, kCopyThreads, 0, num_sms, items + others);
+    return all - others > all / 2 ? all - others : all / 2 + 1;
 }
 
 }  // namespace pages
@@ -664,9 +673,9 @@ cudaError_t launch_resize_plan(const ResizeArgs& a, const PagePlan& p, cudaStrea
 cudaError_t launch_resize_assign(const CacheList& c, const ResizeArgs& a, const PagePlan& p, cudaStream_t s) {
     return pages::by_vec(p.vec, [&](auto v) {
         auto kernel = pages::resize_assign_kernel<decltype(v)>;
-        const int64_t copy = pages::copy_ctas(kernel, p.num_sms, a.n * c.n * 2);
         ResizeArgs b = a;
         b.copy_from = a.n < p.num_sms ? a.n : p.num_sms;
+        const int64_t copy = pages::copy_ctas(kernel, p.num_sms, a.n * c.n * 2, b.copy_from);
         return launch_kernel(kernel, dim3(static_cast<unsigned>(b.copy_from + copy)), dim3(pages::kCols), 0, s, true, 1,
                              c, b);
     });
@@ -679,9 +688,10 @@ cudaError_t launch_compact_plan(const CompactArgs& a, const PagePlan& p, cudaStr
 cudaError_t launch_compact_move(const CacheList& c, const CompactArgs& a, const PagePlan& p, cudaStream_t s) {
     return pages::by_vec(p.vec, [&](auto v) {
         auto kernel = pages::compact_move_kernel<decltype(v)>;
-        const int64_t copy = pages::copy_ctas(kernel, p.num_sms, a.num_blocks / 2 * c.n * 2 + 1);
         CompactArgs b = a;
         b.copy_from = a.rows < p.num_sms && a.rows > 0 ? a.rows : p.num_sms;
+        const int64_t copy = pages::copy_ctas(kernel, p.num_sms, a.num_blocks / 2 * c.n * 2 + 1, b.copy_from);
+        b.few = 5 * static_cast<int64_t>(p.num_sms);
         return launch_kernel(kernel, dim3(static_cast<unsigned>(b.copy_from + copy)), dim3(pages::kCols), 0, s, true, 1,
                              c, b);
     });
