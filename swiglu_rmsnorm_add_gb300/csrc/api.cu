@@ -1846,7 +1846,9 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     // The tail has room for one CTA per SM beside the prefix's kernel, for three once that is done: three where
     // its work is the longer one. Both from the table sizes, as tokens' cost: the prefix takes about 1.4 us per
     // 64 tokens and 256 rows of an SM (batch 256 x 32768: 45 us), the tail, a CTA per SM, 1.2 us per tile of
-    // 16 tokens in each of four warps (requests half as long as their tables allow).
+    // 16 tokens in each of four warps (requests half as long as their tables allow). Measured with 1024 own tokens at
+    // batch 256, one, two and three CTAs: 69.4, 72.6, 74.6 us behind 32768 tokens, 51.0, 51.5, 47.0 behind
+    // 4096 and 47.9, 39.5, 40.1 behind 64.
     const double prefix_us = 1.4 * ceil_div(prefix_blocks * block_size, 64) * ceil_div(pp.rows, 256) * n_kv_head / sms;
     const double tail_us = 1.2 / 4 / 16 * 0.5 * std::max<int64_t>(0, max_blocks_per_seq - prefix_blocks) * block_size *
                            static_cast<double>(B * n_kv_head) / sms;
