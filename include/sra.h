@@ -642,8 +642,9 @@ SRA_API int sra_last_cuda_error(void);
  * loaded. Kernels that stream tiles with tensor-memory-access copies
  * (sra_rmsnorm_linear, sra_glu_linear and their _ws forms; decode attention's
  * TMA-fed variant; sra_shared_prefix_attention) wait on shared-memory barriers for those
- * copies; each wait is bounded (about a second), and a wait that runs out is counted here and the kernel goes on, so a copy that never completes cannot hang
- * the GPU (that call's output is then not valid). Reads the counter synchronously
+ * copies; each wait is bounded (about a second), and a wait that runs out is counted
+ * here and the kernel goes on, so a copy that never completes cannot hang the GPU
+ * (that call's output is then not valid). Reads the counter synchronously
  * (cudaMemcpyFromSymbol); 0 on a device that ran none of those kernels. No paper
  * section defines this; it is the library's own failure report.
  */
