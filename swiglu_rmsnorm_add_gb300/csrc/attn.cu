@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
             float mx = sc;
             for (int o = BS >> 1; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
             const float m_new = fmaxf(m_old, mx);
-            const float pr = valid ? exp2f(sc - m_new) : 0.0f;
+            // PREFIX: a score of -inf weighs nothing, also where no score above it has been seen (a NaN stays NaN)
+            const float pr = valid && !(PREFIX && sc == -INFINITY) ? exp2f(sc - m_new) : 0.0f;
             float sum = pr;
             for (int o = BS >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
             __syncwarp();
@@ -335,11 +336,12 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
         float M = -INFINITY;
         for (int r = 0; r < S; ++r) M = fmaxf(M, cluster.map_shared_rank(m_run, r)[g]);
         float num = 0.0f, den = 0.0f;
-        if (M != -INFINITY) {
+        if (PREFIX || M != -INFINITY) {
             for (int r = 0; r < S; ++r) {
                 const float mr = cluster.map_shared_rank(m_run, r)[g];
-                if (mr == -INFINITY) continue;
-                const float w = exp2f(mr - M);
+                // PREFIX: a split without a score above -inf has no weight, unless NaN among its scores has left its sum NaN
+                if (mr == -INFINITY && !(PREFIX && cluster.map_shared_rank(l_run, r)[g] != 0.0f)) continue;
+                const float w = PREFIX && mr == -INFINITY ? 1.0f : exp2f(mr - M);
                 num = fmaf(w, cluster.map_shared_rank(pacc, r)[idx], num);
                 den = fmaf(w, cluster.map_shared_rank(l_run, r)[g], den);
             }

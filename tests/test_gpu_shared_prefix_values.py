@@ -1,0 +1,78 @@
+"""GPU: attention over a shared prefix where scores or values leave the ordinary range, in every form, against
+the formula in 64 bits with the tolerance of test_gpu_shared_prefix (it is relative to sum_t p_t |V_t|, so it holds for
+values of any size that sums of them in fp32 can hold).
+
+What the formula gives: a score of -inf has weight 0; a request with no score above -inf gets zeros; a NaN among a
+request's scores makes its output NaN."""
+import numpy as np
+import pytest
+import torch
+
+import swiglu_rmsnorm_add_gb300 as sra
+from tests.test_gpu_shared_prefix import DEV, Case, path, run  # noqa: F401  (path: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+KINDS = [(torch.bfloat16, 64), (torch.bfloat16, 128), (torch.bfloat16, 256), (torch.float16, 64), (torch.float16, 128),
+         (torch.float16, 256), (torch.float32, 64), (torch.float32, 128), (torch.float32, 256)]
+
+
+def set_tokens(c, which, fill):
+    """fill(plane K, page, row) for the tokens t of request b (None: of the prefix) in which(b)."""
+    for b in [None] + list(range(c.B)):
+        for t in which(b):
+            shared = t < c.P
+            if shared != (b is None) or (b is not None and t >= c.lens[b]):
+                continue
+            page = int(c.ptable[t // c.bs] if shared else c.table[b, t // c.bs])
+            fill(c.cache, page, t % c.bs)
+
+
+def close(c, got, what=""):
+    """As Case.check, but with zeros for a request without a score above -inf and NaN exactly where the formula has it."""
+    o, A = c.want()
+    u = torch.finfo(c.dtype).eps / 2
+    up = 0.0 if c.dtype == torch.float32 else u
+    nothing = torch.zeros(c.q.shape[:2], dtype=torch.bool, device=DEV)
+    G = c.q.shape[1] // c.n_kv
+    for b in range(c.B):
+        w = c.where(b)
+        if w:
+            k = c.cache.to(DEV).flatten(1, 2)[0, torch.tensor(w, device=DEV)].double()
+            for h in range(c.n_kv):
+                s = c.scale * c.q.to(DEV)[b, h * G:h * G + G].double() @ k[:, h].T
+                nothing[b, h * G:h * G + G] = (s == -torch.inf).all(-1)
+    o[nothing], A[nothing] = 0.0, 0.0
+    assert torch.equal(got.isnan(), o.isnan()), (what, int(got.isnan().sum()), int(o.isnan().sum()))
+    ok = ((got.double() - o).abs() <= u * o.abs() + (up + 6e-5) * A + 1e-30) | o.isnan()
+    assert bool(ok.all()), (what, int((~ok).sum()), [int(x) for x in (~ok).nonzero()[0]])
+
+
+@pytest.mark.parametrize("dtype,hd", KINDS)
+def test_scores_of_minus_infinity(dtype, hd, path):
+    """The first 40 tokens of the prefix, some later ones and the first 20 behind the prefix have no weight: whole
+    leading tiles without a score above -inf, requests that end among such tokens, a prefix that ends in a page."""
+    lens = [150, 160, 165, 300, 0, 7, 40, 41, 90, 151, 260, 171, 172, 400, 152, 149]
+    c = Case(16, 12, 2, hd, 16, 150, lens, dtype, 21 + hd)
+    c.q[..., 0] = c.q[..., 0].abs() + 0.5
+
+    def fill(cache, page, row):
+        cache[0, page, row, :, 0] = -torch.inf
+
+    set_tokens(c, lambda b: [*range(40), 64, 100, *range(128, 144)] if b is None else range(150, 170), fill)
+    d = c.dev()
+    close(c, sra.shared_prefix_attention(**d, scale=c.scale))
+    set_tokens(c, lambda b: range(150) if b is None else range(150, 172), fill)     # nothing in the prefix counts
+    close(c, sra.shared_prefix_attention(**c.dev(), scale=c.scale), "none of the prefix")
+
+
+@pytest.mark.parametrize("dtype,hd", KINDS)
+def test_nan_queries_and_keys(dtype, hd, path):
+    """NaN in one head of a request's query, or in a token that a request attends to, and nowhere else in the output."""
+    c = Case(20, 12, 2, hd, 16, 150, [150 + 5 * (b % 7) for b in range(20)], dtype, 31 + hd)
+    c.lens[9] = c.lens[10] = 33
+    c.q[3, 5, 7] = torch.nan
+    c.q[9, 0] = torch.nan
+    page = int(c.table[12, 150 // 16])
+    c.cache[0, page, 150 % 16, 1, 3] = torch.nan      # request 12's own first token, its second KV head
+    close(c, sra.shared_prefix_attention(**c.dev(), scale=c.scale))
