@@ -22,7 +22,7 @@ constexpr int kTok = 64;            // tokens of a K / V tile
 constexpr int kRows = 128;          // query rows of a tile (the MMA's M)
 constexpr int kThreads = 384;       // producer, MMA issuer, two warps that help to set up; two softmax warpgroups
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescale = 8.0f;    // base-2 headroom of the running maximum, see softmax below
+constexpr float kRescale = 8.0f;    // powers of two that a maximum may rise before its base moves, see softmax below
 
 template <int HD>
 struct Smem {
@@ -342,13 +342,14 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         }
         __syncwarp();
     } else if (warp >= 4) {
-        // softmax: thread = query row of stream x. The running maximum m (base 2, scaled) is moved only
-        // when a tile's maximum passes it by more than kRescale: o and l are sums of 2^(s - m) for one
-        // m, so any m will do as long as nothing overflows (2^8 times a row's sum of values does not),
-        // and O in tensor memory is scaled seldom. fp16 has few exponents: there m stays 7 below the maximum
-        // (p up to 2^15), so that probabilities down to 2^-21 of the largest are normal numbers and those to 2^-32
-        // are not lost.
-        constexpr float kUnder = kUnderMax<T>;
+        // softmax: thread = query row of stream x. The base m of the exponents (base 2, scaled) is moved only
+        // when a tile's maximum leaves the kRescale powers of two that the last move left room for: o and l are
+        // sums of 2^(s - m) for one m, so any m will do as long as nothing overflows or is lost, and O in tensor
+        // memory is scaled seldom. bf16 has fp32's exponents, for P and for V: there m is put 8 above the maximum, so
+        // that no p is above 1 and O stays within the sum of |V|. fp16 has few: there m is put 7 below the maximum (p up to
+        // 2^15 of V up to 2^16, far from fp32's end), so that probabilities down to 2^-21 of the largest are
+        // normal numbers and those to 2^-32 are not lost.
+        constexpr float kUnder = kBf16 ? -kRescale : kUnderMax<T>;
         const int x = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + lanes + kS + x * kTok, tP = tmem + lanes + kP + x * 64,

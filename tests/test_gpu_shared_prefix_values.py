@@ -76,3 +76,28 @@ def test_nan_queries_and_keys(dtype, hd, path):
     page = int(c.table[12, 150 // 16])
     c.cache[0, page, 150 % 16, 1, 3] = torch.nan      # request 12's own first token, its second KV head
     close(c, sra.shared_prefix_attention(**c.dev(), scale=c.scale))
+
+
+@pytest.mark.parametrize("B", [20, 130])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_values_near_the_end_of_the_range(hd, B, path):
+    """V of 1.5e36 and a maximum that rises by 2^7.875 in a later tile of a split. The 212 tokens' |V| add up to 3.2e38,
+    within fp32 and bf16, so sums of them with weights of at most 1 are finite whatever their signs; a weight of 2^7.875
+    would make one token's 3.5e38 infinite. (As many KV heads as SMs: a split has three tiles, of one row tile or two.)"""
+    n_kv = torch.cuda.get_device_properties(0).multi_processor_count
+    prefix, own = 192, 20
+    c = Case(B, n_kv, n_kv, hd, 16, prefix, [prefix + own if b < 3 else prefix + 1 for b in range(B)], torch.bfloat16, 5,
+             scale=float(np.log(2.0)))
+    c.q.zero_()
+    c.q[..., 0] = 1
+    some = ~c.cache[0].isnan().any(-1)
+    c.cache[0][some] = 0.0
+    c.cache[1][some] = 1.5e36 * c.cache[1][some].sign()
+
+    def fill(cache, page, row):
+        cache[0, page, row, :, 0] = 7.875
+
+    set_tokens(c, lambda b: [150] if b is None else [prefix + 15], fill)
+    got = sra.shared_prefix_attention(**c.dev(), scale=c.scale)
+    assert bool(got.isfinite().all())
+    close(c, got)
