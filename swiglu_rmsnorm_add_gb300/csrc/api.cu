@@ -6,6 +6,7 @@
 // the sizes, the alignment of every pointer and stride, and the SM count.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -1819,9 +1820,8 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     f.n_kv = n_kv_head;
     f.group = group;
     f.block_size = block_size;
-    // not 0: the kernel scales masked scores of -inf too (1e-37 times any score that is not itself near 1e37 is 0
-    // next to 1, the weight that a scale of 0 gives every token)
-    f.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-37f);
+    f.zero = scale == 0.0f;
+    f.scale_log2 = f.zero ? 1.0f : std::max(std::fabs(a.scale_log2), FLT_MIN);
     f.negate = scale < 0.0f;
     f.q16 = aligned16(q) && stride_aligned16(q_tok_stride, es);
     f.rows = pp.rows;

@@ -282,6 +282,16 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         }
         if (bad) s_ragged = 1;
         const uint32_t flip = a.negate ? 0x80008000u : 0u;
+        if (a.zero) {  // a query element counts as 0 times itself: 0, or NaN for infinities and NaN
+            auto half = [](uint32_t h) -> uint32_t {
+                constexpr uint32_t kExp = kBf16 ? 0x7f80u : 0x7c00u;
+                return (h & kExp) == kExp ? 0x7fffu : 0u;
+            };
+            auto word = [&](uint32_t w) { return half(w & 0xffffu) | half(w >> 16) << 16; };
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                qv[e] = make_uint4(word(qv[e].x), word(qv[e].y), word(qv[e].z), word(qv[e].w));
+        }
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int r = r0 + e * kStep, rr = r % kRows;
@@ -602,7 +612,7 @@ __global__ void __launch_bounds__(kF32Threads) prefix_f32_kernel(PrefixArgs a, c
                 const int b = row / a.group, g = row - b * a.group;
                 v = static_cast<const float*>(a.q)[b * a.qs + (kvh * a.group + g) * HD + d];
             }
-            qs[r * RS + d] = a.negate ? -v : v;
+            qs[r * RS + d] = a.zero ? 0.0f * v : a.negate ? -v : v;
         }
         __syncthreads();
         copy(ks, 0, 0);

@@ -206,8 +206,10 @@ struct PrefixArgs {
     void* out;
     int64_t B, qs, os, num_blocks, pblocks, cap;  // cap: the most tokens a request's row holds
     int n_kv, group, block_size;
-    float scale_log2;  // |softmax scale| * log2(e); a negative scale flips the queries' sign
-    bool negate, q16;  // q16: 16-byte aligned query rows
+    // |softmax scale| * log2(e), never 0: masked scores of -inf are scaled too. A negative scale flips the queries'
+    // sign; a scale of 0 (zero) makes them 0, with scale_log2 1
+    float scale_log2;
+    bool negate, zero, q16;  // q16: 16-byte aligned query rows
     // work: rows = B * group query rows of a KV head in tiles of 128. Two tiles share a CTA's K / V
     // tiles (a pair block); an odd last tile is a block of its own whose CTAs work on two K / V tiles
     // at a time. A block's K / V range is dealt to its splits, each split leaves one record per row.

@@ -101,3 +101,22 @@ def test_values_near_the_end_of_the_range(hd, B, path):
     got = sra.shared_prefix_attention(**c.dev(), scale=c.scale)
     assert bool(got.isfinite().all())
     close(c, got)
+
+
+@pytest.mark.parametrize("dtype,hd", KINDS)
+def test_a_scale_of_zero(dtype, hd, path):
+    """Every token has the same weight, whatever its score: also where scores are as large as the type allows; and
+    0 times an infinite score is NaN."""
+    c = Case(20, 12, 2, hd, 16, 150, [150 + 5 * (b % 7) for b in range(20)], dtype, 41 + hd, scale=0.0)
+    big = 2.0 ** 7 if dtype == torch.float16 else 2.0 ** 61
+    c.q[..., 0] = big
+    some = ~c.cache[0].isnan().any(-1)
+    c.cache[0][..., 0][some] = (torch.randint(0, 2, (int(some.sum()),), generator=torch.Generator().manual_seed(1)) * 2.0
+                                - 1.0).to(dtype) * big
+    close(c, sra.shared_prefix_attention(**c.dev(), scale=0.0))
+    page = int(c.ptable[2])
+    c.cache[0, page, 3, 1, 0] = -torch.inf      # token 35 of the prefix, for the second KV head
+    c.lens[4] = 20
+    close(c, sra.shared_prefix_attention(**c.dev(), scale=0.0), "an infinite score")
+    c.q[7, 2, 5] = torch.inf
+    close(c, sra.shared_prefix_attention(**c.dev(), scale=0.0), "an infinite query")
