@@ -282,23 +282,26 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
         }
         if (bad) s_ragged = 1;
         const uint32_t flip = a.negate ? 0x80008000u : 0u;
+        auto place = [&](int r) {
+            return reinterpret_cast<uint4*>(qs + (r / kRows) * L::kQBytes + (chunk / 8) * L::kQHalf + r % kRows * 128 +
+                                            (((chunk & 7) ^ (r & 7)) * 16));
+        };
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int r = r0 + e * kStep;
+            if (r < count) *place(r) = make_uint4(qv[e].x ^ flip, qv[e].y ^ flip, qv[e].z ^ flip, qv[e].w ^ flip);
+        }
         if (a.zero) {  // a query element counts as 0 times itself: 0, or NaN for infinities and NaN
             auto half = [](uint32_t h) -> uint32_t {
                 constexpr uint32_t kExp = kBf16 ? 0x7f80u : 0x7c00u;
                 return (h & kExp) == kExp ? 0x7fffu : 0u;
             };
             auto word = [&](uint32_t w) { return half(w & 0xffffu) | half(w >> 16) << 16; };
-#pragma unroll
-            for (int e = 0; e < kEach; ++e)
-                qv[e] = make_uint4(word(qv[e].x), word(qv[e].y), word(qv[e].z), word(qv[e].w));
-        }
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int r = r0 + e * kStep, rr = r % kRows;
-            if (r < count)
-                *reinterpret_cast<uint4*>(qs + (r / kRows) * L::kQBytes + (chunk / 8) * L::kQHalf + rr * 128 +
-                                          (((chunk & 7) ^ (rr & 7)) * 16)) =
-                    make_uint4(qv[e].x ^ flip, qv[e].y ^ flip, qv[e].z ^ flip, qv[e].w ^ flip);
+#pragma unroll 1
+            for (int r = r0; r < count; r += kStep) {  // (its own chunks, as stored above)
+                const uint4 u = *place(r);
+                *place(r) = make_uint4(word(u.x), word(u.y), word(u.z), word(u.w));
+            }
         }
         fence_proxy_async();  // before the tensor core reads them
         asm volatile("bar.sync 1, %0;" ::"r"(kSetup) : "memory");
