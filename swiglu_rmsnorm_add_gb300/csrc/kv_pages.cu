@@ -86,12 +86,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CacheList c, PageCop
     copy_items<V>(c, a.n, blockIdx.x, gridDim.x, [&](int64_t i, bool first) {
         const int32_t s = a.src[i], d = a.dst[i];
         Pair p{s, d, 0};
-        if (s < 0 || d < 0 || s == d) return p;  // padding, or nothing to move
+        if (s < 0 || d < 0) return p;  // padding
         if (s >= a.num_blocks || d >= a.num_blocks) {
             if (first && threadIdx.x == 0 && a.count_errors) count_error(a.err);
             return p;
         }
-        p.bytes = c.page_bytes;
+        if (s != d) p.bytes = c.page_bytes;
         return p;
     });
 }
