@@ -518,9 +518,10 @@ SRA_API int sra_kv_copy_pages(void* const* kv_caches, int64_t n_caches, const in
  *     that the child held;
  *   - the child's row becomes the parent's used entries, then -1; seq_lens[child] =
  *     seq_lens[parent] (0 frees the child's pages).
- * parents, children: device int32 [n]; a negative index in either is padding. One each is added
- * to err_count, and the entry does nothing, for: an index >= rows; a child that an earlier entry
- * names; a seq_len of the two rows outside [0, max_blocks_per_seq * block_size]. One each is
+ * parents, children: device int32 [n]; an entry with a negative index in either is padding and
+ * names nothing. One each is added to err_count, and the entry does nothing, for: an index >= rows;
+ * a child that an earlier entry (done or refused) names; a seq_len of the two rows outside [0,
+ * max_blocks_per_seq * block_size]. One each is
  * added for every used table entry outside [0, num_blocks) (the parent's is passed on as it is)
  * and for every holder that a count does not have (it stays at zero).
  */
@@ -546,7 +547,7 @@ SRA_API int64_t sra_kv_fork_workspace_size(int64_t n, int64_t max_blocks_per_seq
  * the call and its slot in the cache (page * block_size + offset), what sra_rope_kv_store
  * takes for a decode step's token; -1 for an empty row and an entry that does nothing.
  * row_idx, lens: device int32 [n]; a negative row is padding. One each is added to err_count, and
- * the entry does nothing, for: a row >= rows or one that an earlier entry names; a length (new
+ * the entry does nothing, for: a row >= rows or one that an earlier entry (done or refused) names; a length (new
  * or present) outside [0, max_blocks_per_seq * block_size]; a partly filled last page outside
  * [0, num_blocks) in a row that grows. One each is added for bad entries and missing holders among the
  * pages given up, as in sra_kv_fork_rows. New pages' contents are not cleared. n_caches >= 1.

@@ -100,11 +100,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CacheList c, PageCop
 constexpr int kRows = 8;        // entries of a call that one CTA takes together
 constexpr int kCols = 128;      // table columns of a CTA, one per thread
 
-// Whether an entry of idx[0 .. i) equals idx[i]; the whole warp asks.
-__device__ __forceinline__ bool named_before(const int32_t* idx, int64_t i, int lane) {
+// Whether an entry of idx[0 .. i) equals idx[i]; the whole warp asks. `other` (or null): an entry whose other
+// index is negative is padding and names nothing.
+__device__ __forceinline__ bool named_before(const int32_t* idx, const int32_t* other, int64_t i, int lane) {
     const int32_t me = idx[i];
     bool hit = false;
-    for (int64_t k = lane; k < i; k += 32) hit |= idx[k] == me;
+    for (int64_t k = lane; k < i; k += 32)
+        if (idx[k] == me) hit |= !other || other[k] >= 0;
     return __any_sync(FULL, hit);
 }
 
@@ -152,7 +154,7 @@ __device__ __forceinline__ void fork_take(const ForkArgs& a, const Group& q, int
                     prow = p;
                     bad = plen < 0 || plen > a.cap || clen < 0 || clen > a.cap;
                 }
-                bad = named_before(a.children, i, lane) || bad;
+                bad = named_before(a.children, a.parents, i, lane) || bad;
                 if (bad) {
                     plen = -1;
                     if (first && lane == 0) count_error(a.err);
@@ -288,7 +290,7 @@ __device__ __forceinline__ void resize_release(const ResizeArgs& a, const Group&
                     old = a.seq_lens[row];
                     bad = old < 0 || old > a.cap;
                 }
-                bad = named_before(a.row_idx, i, lane) || bad;
+                bad = named_before(a.row_idx, nullptr, i, lane) || bad;
                 if (bad) {
                     old = -1;
                     if (first && lane == 0) count_error(a.err);

@@ -25,3 +25,24 @@ def test_copy_counts_every_pair_out_of_range():
     sra.copy_kv_pages(cache, i32([nb, 0, BIG, 2, -1, nb + 1]), i32([nb, 3, BIG, 2, -1, -1]), err_count=err)
     assert torch.equal(cache, want)
     assert int(err.item()) == 2
+
+
+@pytest.mark.parametrize("cols", [4, 8192])     # all entries in one CTA, and a grid of them
+def test_a_padding_entry_names_no_child(cols):
+    """An entry with a negative index in either array does nothing, also to a later entry for the same child; one
+    that is refused for another reason has named its child."""
+    table = np.full((8, cols), -1)
+    table[0, :2], table[1, :1] = [0, 1], [2]
+    seq, ref = [7, 3, 0, 0, 0, 0, 0, 0], [1, 1, 1, 0, 0]
+    t, s, r = i32(table), i32(seq), i32(ref)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    #                            padding  done  refused: parent, then its child again  padding  done
+    sra.fork_kv_rows(t, s, r, i32([-1, 0, 8, 1, -7, 0]), i32([2, 2, 4, 4, 5, 5]), 4, err_count=err)
+    for row in (2, 5):
+        table[row, :2] = [0, 1]
+    assert t.cpu().tolist() == table.tolist()
+    assert s.tolist() == [7, 3, 7, 0, 0, 7, 0, 0] and r.tolist() == [3, 3, 1, 0, 0]
+    assert int(err.item()) == 2
+    # the same child twice: the first entry is done, the second refused
+    sra.fork_kv_rows(t, s, r, i32([1, 0]), i32([6, 6]), 4, err_count=err)
+    assert s.tolist() == [7, 3, 7, 0, 0, 7, 3, 0] and int(err.item()) == 3
