@@ -5,8 +5,9 @@ projection they feed.
 
 Every operator runs in the hand-written sm_103a CUDA kernels of ``libsra.so``
 (C ABI in ``include/sra.h``). This module only marshals torch tensors into that
-ABI: pointers, sizes, strides, dtype code and the current CUDA stream. There is
-no CPU or PyTorch fallback: without the built library every call raises.
+ABI: pointers, sizes, strides, dtype code and the CUDA stream (the current one unless
+``stream`` is given; results that a call makes are allocated for the stream it runs on).
+There is no CPU or PyTorch fallback: without the built library every call raises.
 """
 from ._binding import (  # noqa: F401
     SRAError,

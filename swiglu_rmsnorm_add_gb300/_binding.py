@@ -199,12 +199,38 @@ def _on(index: int):
     return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
+def _raw(stream) -> int:
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _stream(t: torch.Tensor, stream) -> int:
     if stream is None:
         if _raw_current_stream is not None:
             return _raw_current_stream(t.get_device())
         stream = torch.cuda.current_stream(t.device)
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    return _raw(stream)
+
+
+def _made_for(stream, dev: int, make):
+    """make() with its memory allocated for `stream` (None: the current one), where a call's kernels write it: what was
+    freed on the current stream may still be in use there."""
+    if stream is None or _raw(stream) == torch.cuda.current_stream(dev).cuda_stream:
+        return make()
+    s = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(_raw(stream), device=torch.device("cuda", dev))
+    with torch.cuda.stream(s):
+        return make()
+
+
+def _result(stream, dev: int, make):
+    """A call's result, made for its stream and kept, once dropped, until the current stream is done with what
+    it has queued by then (the caller reads it there)."""
+    t = _made_for(stream, dev, make)
+    if stream is not None:
+        here = torch.cuda.current_stream(dev)
+        if _raw(stream) != here.cuda_stream:
+            t.record_stream(here)
+    return t
 
 
 def _same_device(*ts):
@@ -220,7 +246,7 @@ def rmsnorm(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = None, e
     """out = x * rsqrt(mean(x^2, -1) + eps) * w (fp32 accumulation). out may be x."""
     _cuda(x, "x"), _cuda(w, "w")
     if out is None:
-        out = torch.empty_like(x)
+        out = _result(stream, x.get_device(), lambda: torch.empty_like(x))
     _cuda(out, "out")
     _same_device(x, w, out)
     if w.dtype != x.dtype or out.dtype != x.dtype:
@@ -242,7 +268,7 @@ def add_rmsnorm(x: torch.Tensor, res: torch.Tensor, w: torch.Tensor, out: torch.
     for t, n in ((x, "x"), (res, "res"), (w, "w")):
         _cuda(t, n)
     if out is None:
-        out = torch.empty_like(x)
+        out = _result(stream, x.get_device(), lambda: torch.empty_like(x))
     _cuda(out, "out")
     _same_device(x, res, w, out)
     if not (res.dtype == w.dtype == out.dtype == x.dtype):
@@ -345,7 +371,8 @@ def glu(gate_up: torch.Tensor, out: torch.Tensor | None = None, act: str = "silu
         raise ValueError("gate_up width must be even (gate | up)")
     I = W // 2
     if out is None:
-        out = torch.empty(*gate_up.shape[:-1], I, dtype=gate_up.dtype, device=gate_up.device)
+        out = _result(stream, gate_up.get_device(),
+                      lambda: torch.empty(*gate_up.shape[:-1], I, dtype=gate_up.dtype, device=gate_up.device))
     _cuda(out, "out")
     _same_device(gate_up, out)
     if out.dtype != gate_up.dtype:
@@ -393,7 +420,7 @@ def uclip(x: torch.Tensor, alpha: torch.Tensor, gamma: torch.Tensor, out: torch.
     _cuda(alpha, "alpha")
     _cuda(gamma, "gamma")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _result(stream, x.get_device(), lambda: torch.empty(x.shape, dtype=x.dtype, device=x.device))
     _cuda(out, "out")
     _same_device(x, alpha, gamma, out)
     if out.dtype != x.dtype:
@@ -432,12 +459,12 @@ def decode_attention_workspace(B: int, n_head: int, n_kv_head: int, head_dim: in
     return torch.zeros(int(n), dtype=torch.uint8, device=device) if n > 0 else None
 
 
-def _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count):
+def _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count, stream=None):
     """Checks and C arguments shared by the decode-attention entry points."""
     for t, n in ((q, "q"), (kv_cache, "kv_cache"), (block_table, "block_table"), (seq_lens, "seq_lens")):
         _cuda(t, n)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _result(stream, q.get_device(), lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
     _cuda(out, "out")
     _same_device(q, kv_cache, block_table, seq_lens, out, err_count)
     if not (q.dtype == kv_cache.dtype == out.dtype):
@@ -474,7 +501,7 @@ def paged_decode_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table:
     q: [B, n_head, head_dim]; kv_cache: [2, num_blocks, block_size, n_kv_head, head_dim] (the
     layout rope_kv_store writes); block_table: int32 [B, max_blocks]; seq_lens: int32 [B];
     scale defaults to 1 / sqrt(head_dim)."""
-    out, args, err = _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count)
+    out, args, err = _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count, stream)
     with torch.cuda.device(q.device):
         if workspace is None:
             st = lib().sra_paged_decode_attention(*args, err, _dtype(q), _stream(q, stream))
@@ -498,7 +525,7 @@ def paged_decode_attention_noalloc(q: torch.Tensor, kv_cache: torch.Tensor, bloc
     it before any stream capture."""
     if out is None:
         raise ValueError("out is required: this entry point allocates nothing")
-    out, args, err = _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count)
+    out, args, err = _attention_args(q, kv_cache, block_table, seq_lens, out, scale, err_count, stream)
     with torch.cuda.device(q.device):
         st = lib().sra_paged_decode_attention_noalloc(*args, err, _dtype(q), _stream(q, stream))
     _check("sra_paged_decode_attention_noalloc", st)
@@ -549,7 +576,7 @@ def rmsnorm_linear(x: torch.Tensor, w_ln: torch.Tensor, W: torch.Tensor, y: torc
     if w_ln.numel() != K or w_ln.dtype != x.dtype or not w_ln.is_contiguous():
         raise ValueError("w_ln must be a contiguous [K] tensor of x's dtype")
     if y is None:
-        y = torch.empty(*x.shape[:-1], N, dtype=x.dtype, device=x.device)
+        y = _result(stream, x.get_device(), lambda: torch.empty(*x.shape[:-1], N, dtype=x.dtype, device=x.device))
     _cuda(y, "y")
     _same_device(x, w_ln, W, y)
     yr, yn, ys = _as_rows(y, "y")
@@ -585,7 +612,8 @@ def glu_linear(gate_up: torch.Tensor, W: torch.Tensor, y: torch.Tensor | None = 
     if act not in ACT_CODE:
         raise ValueError("act must be 'silu' or 'relu'")
     if y is None:
-        y = torch.empty(*gate_up.shape[:-1], N, dtype=gate_up.dtype, device=gate_up.device)
+        y = _result(stream, gate_up.get_device(),
+                    lambda: torch.empty(*gate_up.shape[:-1], N, dtype=gate_up.dtype, device=gate_up.device))
     _cuda(y, "y")
     _same_device(gate_up, W, y)
     yr, yn, ys = _as_rows(y, "y")
@@ -706,13 +734,7 @@ def _workspace_args(workspace, make, dev, stream):
     here is allocated on the stream that the call runs on, so its memory is not used again before
     the call's kernels are done with it."""
     if workspace is None:
-        if stream is None:
-            workspace = make()
-        else:
-            s = stream if isinstance(stream, torch.cuda.Stream) else \
-                torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=torch.device("cuda", dev))
-            with torch.cuda.stream(s):
-                workspace = make()
+        workspace = _made_for(stream, dev, make)
     if not (isinstance(workspace, torch.Tensor) and workspace.is_cuda):
         _cuda(workspace, "workspace")
     if not workspace.is_contiguous():
@@ -804,11 +826,11 @@ def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts
     if dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
     if pos is None:
-        pos = torch.empty(n, dtype=torch.int64, device=rows.device)
+        pos = _result(stream, dev, lambda: torch.empty(n, dtype=torch.int64, device=rows.device))
     else:
         _int64_out(pos, "pos", n, dev)
     if slot_mapping is None:
-        slot_mapping = torch.empty(n, dtype=torch.int64, device=rows.device)
+        slot_mapping = _result(stream, dev, lambda: torch.empty(n, dtype=torch.int64, device=rows.device))
     else:
         _int64_out(slot_mapping, "slot_mapping", n, dev)
     if counts != nb:
@@ -838,7 +860,7 @@ def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_coun
     dev, rows, mb, counts = _page_state(block_table, seq_lens, ref_counts)
     (_, nb, bs, n_kv, hd), dtype, cache_dev, ptrs, count = _kv_caches(kv_caches)
     if num_live is None:
-        num_live = torch.empty(1, dtype=_I32, device=seq_lens.device)
+        num_live = _result(stream, dev, lambda: torch.empty(1, dtype=_I32, device=seq_lens.device))
     _int32(num_live, "num_live", 1, dev)
     if num_live.numel() != 1:
         raise ValueError("num_live must hold one entry")
@@ -892,7 +914,7 @@ def shared_prefix_attention(q: torch.Tensor, kv_cache: torch.Tensor, prefix_tabl
     if prefix_len.numel() != 1:
         raise ValueError("prefix_len must hold one entry")
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        out = _result(stream, dev, lambda: torch.empty(q.shape, dtype=dtype, device=q.device))
     if not (isinstance(kv_cache, torch.Tensor) and q.dim() == 3 and dtype in DTYPE_CODE and kv_cache.dtype is dtype
             and out.dtype is dtype and _kv_cache_ok(kv_cache) and kv_cache.get_device() == dev
             and out.get_device() == dev and out.shape == q.shape and kv_cache.shape[4] == q.shape[2]
