@@ -540,12 +540,15 @@ SRA_API int64_t sra_kv_fork_workspace_size(int64_t n, int64_t max_blocks_per_seq
  *      1 among them), each with count 1. A row whose partly filled last page has other
  *      holders (count > 1 after step 1) first gets a page in its place: that page's
  *      tokens up to the old length are copied, K and V, in every cache, and the old page's
- *      count falls by one. Entry i is served if the pages that entries 0 .. i need together
- *      are there; otherwise its row stays as it was and 1 is added to err_count.
+ *      count falls by one. An entry that needs no page (its row grows within a last page of its
+ *      own) is served. Any other entry i is served if the pages that entries 0 .. i need together
+ *      are there, refused ones among them; otherwise its row stays as it was and 1 is added to
+ *      err_count.
  *   3. seq_lens[row_idx[i]] = lens[i] where served or shrunk.
  * pos, slot_mapping: NULL, or device int64 [n]: the position of the row's last token after
  * the call and its slot in the cache (page * block_size + offset), what sra_rope_kv_store
- * takes for a decode step's token; -1 for an empty row and an entry that does nothing.
+ * takes for a decode step's token; -1 for an empty row and an entry that does nothing. (For a
+ * refused row they name the last token that it had: a new one is not to be stored there.)
  * row_idx, lens: device int32 [n]; a negative row is padding. One each is added to err_count, and
  * the entry does nothing, for: a row >= rows or one that an earlier entry (done or refused) names; a length (new
  * or present) outside [0, max_blocks_per_seq * block_size]; a partly filled last page outside

@@ -814,8 +814,9 @@ def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts
     fork_kv_rows and copy_kv_pages, changed in place.
 
     Returns (pos, slot_mapping), int64 [n]: position and cache slot of each row's last token, what
-    rope_kv_store takes for a decode step; -1 for an empty row or a refused entry. A row whose pages are
-    not there stays as it was and is counted in err_count."""
+    rope_kv_store takes for a decode step; -1 for an empty row and an entry that does nothing. A row
+    whose pages are not there stays as it was and is counted in err_count (its pos and slot are those of the last
+    token that it had, where no new one is to be stored); one that needs none is served whatever was refused before it."""
     dev, table_rows, mb, counts = _page_state(block_table, seq_lens, ref_counts, rows=rows, lens=lens)
     (_, nb, bs, n_kv, hd), dtype, cache_dev, ptrs, count = _kv_caches(kv_caches)
     n = rows.numel()

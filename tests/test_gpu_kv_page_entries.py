@@ -46,3 +46,18 @@ def test_a_padding_entry_names_no_child(cols):
     # the same child twice: the first entry is done, the second refused
     sra.fork_kv_rows(t, s, r, i32([1, 0]), i32([6, 6]), 4, err_count=err)
     assert s.tolist() == [7, 3, 7, 0, 0, 7, 3, 0] and int(err.item()) == 3
+
+
+def test_a_row_that_needs_no_page_is_served_behind_a_refused_one():
+    """Three free pages and rows that ask for five, for none (inside a last page of its own), for one, and, last, for none:
+    the first and the third are refused, the others grow."""
+    table = np.full((4, 8), -1)
+    table[0, :1], table[1, :2], table[2, :1], table[3, :1] = [6], [0, 1], [2], [3]
+    seq, ref = [4, 5, 4, 2], [1, 1, 1, 1, 0, 0, 1, 0]
+    t, s, r = i32(table), i32(seq), i32(ref)
+    cache = torch.zeros(2, 8, 4, 1, 8, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pos, slot = sra.resize_kv_rows(t, s, r, i32([0, 1, 2, 3]), i32([24, 6, 5, 4]), cache, err_count=err)
+    assert t.cpu().tolist() == table.tolist() and r.tolist() == ref
+    assert s.tolist() == [4, 6, 4, 4] and int(err.item()) == 2
+    assert pos.tolist() == [3, 5, 3, 3] and slot.tolist() == [6 * 4 + 3, 1 * 4 + 1, 2 * 4 + 3, 3 * 4 + 3]
