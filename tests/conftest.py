@@ -15,6 +15,9 @@ def pytest_configure(config):
 def pytest_collection_modifyitems(config, items):
     import torch
 
+    # The count of waits that ran out is the process's, and one test lets a wait run out on purpose: it comes behind all
+    # that read the count, some of which expect 0.
+    items.sort(key=lambda item: item.name.startswith("test_bounded_wait_gives_up"))
     if torch.cuda.is_available():
         return
     skip = pytest.mark.skip(reason="no CUDA device")
