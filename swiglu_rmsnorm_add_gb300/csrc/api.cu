@@ -1768,7 +1768,7 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     plan.smem = plan.tensor_cores ? decode_attention_mma_smem(head_dim, 8)
                                   : decode_attention_smem(group, head_dim, block_size, 2, es);
     if (static_cast<int64_t>(plan.smem) > limit) return SRA_ERR_SHAPE;
-    AttnArgs a;
+    PrefixAttnArgs a;
     a.q = q;
     a.cache = kv_cache;
     a.table = block_table;

@@ -34,6 +34,8 @@
 // scale * log2(e) and exponentials are exp2.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tma.cuh"
@@ -90,13 +92,16 @@ __device__ __forceinline__ T from_f32(float v) {
     }
 }
 
+template <bool PREFIX>
+using ArgsOf = std::conditional_t<PREFIX, PrefixAttnArgs, AttnArgs>;
+
 // The shared prefix of a PREFIX launch: tokens below P come through the prefix's table. A
 // request's part of the work is [lo, len): all of its tokens, or, when another kernel takes the
 // prefix's whole pages (a.tail_only) for the requests that reach past them, those behind them.
 struct PrefixRange {
     int64_t P, lo;
 };
-__device__ __forceinline__ PrefixRange prefix_range(const AttnArgs& a, int64_t len) {
+__device__ __forceinline__ PrefixRange prefix_range(const PrefixAttnArgs& a, int64_t len) {
     int64_t P = __ldcg(a.plen);
     const int64_t cap = a.pblocks * a.block_size;
     P = P < 0 ? 0 : (P > cap ? cap : P);
@@ -109,7 +114,7 @@ __device__ __forceinline__ float quotient(float num, float den) {
     return (PREFIX ? den != 0.0f : den > 0.0f) ? num / den : 0.0f;
 }
 // One CTA of a call: a prefix length out of range and bad entries of the prefix's table, counted once.
-__device__ __forceinline__ void count_prefix_errors(const AttnArgs& a, int64_t P) {
+__device__ __forceinline__ void count_prefix_errors(const PrefixAttnArgs& a, int64_t P) {
     if (!a.err) return;
     int n = threadIdx.x == 0 && __ldcg(a.plen) != P ? 1 : 0;
     for (int64_t j = threadIdx.x; j * a.block_size < P; j += blockDim.x) {
@@ -120,7 +125,7 @@ __device__ __forceinline__ void count_prefix_errors(const AttnArgs& a, int64_t P
 }
 
 template <typename T, int HD, int STAGES, bool PREFIX>
-__global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads) decode_kernel(ArgsOf<PREFIX> a) {
     constexpr int IPT = HD / 64;                                  // (head, 4-dim) slices per thread, G <= 8
     constexpr int EPC = 16 / static_cast<int>(sizeof(T));         // elements per 16-byte copy
     constexpr int CPR = HD / EPC;                                 // copies per row
@@ -174,12 +179,16 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(AttnArgs a) {
     auto block_ok = [&](int32_t blk) { return blk >= 0 && blk < a.num_blocks; };
     // PREFIX: the rows of block j that count, as a mask: those below P through the prefix's entry, the
     // others (below len) through the request's own
-    auto row_mask = [&](int64_t j) -> unsigned {
-        const int64_t left = len - j * BS, pre = P - j * BS;
-        const int nl = left < BS ? static_cast<int>(left) : BS;
-        const int np = pre <= 0 ? 0 : (pre < nl ? static_cast<int>(pre) : nl);
-        const unsigned all = static_cast<unsigned>((1ull << nl) - 1), first = static_cast<unsigned>((1ull << np) - 1);
-        return (np > 0 && block_ok(a.ptable[j]) ? first : 0u) | (np < nl && block_ok(table[j]) ? all & ~first : 0u);
+    [[maybe_unused]] auto row_mask = [&](int64_t j) -> unsigned {
+        if constexpr (PREFIX) {
+            const int64_t left = len - j * BS, pre = P - j * BS;
+            const int nl = left < BS ? static_cast<int>(left) : BS;
+            const int np = pre <= 0 ? 0 : (pre < nl ? static_cast<int>(pre) : nl);
+            const unsigned all = static_cast<unsigned>((1ull << nl) - 1), first = static_cast<unsigned>((1ull << np) - 1);
+            return (np > 0 && block_ok(a.ptable[j]) ? first : 0u) | (np < nl && block_ok(table[j]) ? all & ~first : 0u);
+        } else {
+            return 0u;
+        }
     };
     auto issue = [&](int64_t j) {
         if constexpr (PREFIX) {
@@ -660,7 +669,7 @@ __device__ __forceinline__ void finish_mma(const AttnArgs& a, unsigned char* sme
 // PREFIX: tokens below the shared prefix's length come through the prefix's table; the splits
 // divide the request's own range of tokens (prefix_range), which is known after the wait only.
 template <typename T, int HD, bool GMERGE, int NW, bool PREFIX>
-__global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(ArgsOf<PREFIX> a) {
     constexpr int CPR = HD * 2 / 16;      // 16-byte chunks per row
     constexpr int KS = HD / 16;           // k-steps of Q K^T
     constexpr int NB = HD / 8;            // 8-dim blocks of O
@@ -778,7 +787,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) decode_mma_kernel(At
             if (tok < t_end) {
                 if (block_ok(blk)) {
                     off = ((static_cast<int64_t>(blk) << bs_log2) + (tok & (BS - 1))) * tok_stride + kvh_off;
-                } else if (kvh == 0 && ((tok & (BS - 1)) == 0 || (PREFIX && tok == P)) && tok >= P && a.err) {
+                } else if (kvh == 0 && ((tok & (BS - 1)) == 0 || (PREFIX && tok == P)) && (!PREFIX || tok >= P) && a.err) {
                     atomicAdd(a.err, 1);  // a bad block entry, counted once (kv head 0, its first token)
                 }
             }
@@ -1078,7 +1087,7 @@ __host__ __device__ constexpr size_t tail_smem(int HD) {
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(PrefixAttnArgs a) {
     constexpr int CPR = HD * 2 / 16, KS = HD / 16, TE = kTailTok * HD;
     constexpr int RPI = 32 / CPR;  // rows per copy instruction (CPR lanes per row)
     extern __shared__ __align__(16) unsigned char smem[];
@@ -1357,7 +1366,7 @@ __global__ void __launch_bounds__(kTailThreads, HD > 128 ? 2 : 4) tail_kernel(At
 }
 
 template <typename T, int HD>
-cudaError_t launch_tail(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+cudaError_t launch_tail(const PrefixAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     auto kernel = tail_kernel<T, HD>;
     constexpr size_t smem = tail_smem(HD);
     static std::atomic<uint64_t> done{0};
@@ -1370,7 +1379,7 @@ cudaError_t launch_tail(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
 }
 
 template <typename T, int HD, int NW, bool PREFIX = false>
-cudaError_t launch_mma(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+cudaError_t launch_mma(const ArgsOf<PREFIX>& a, const AttnPlan& p, cudaStream_t s) {
     const size_t smem = mma_smem(HD, NW);
     if (!PREFIX && a.gsplits > 0) {
         auto kg = decode_mma_kernel<T, HD, true, NW, false>;
@@ -1651,7 +1660,7 @@ cudaError_t launch_tma(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
 }
 
 template <typename T, int HD, int STAGES, bool PREFIX = false>
-cudaError_t launch_hd(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+cudaError_t launch_hd(const ArgsOf<PREFIX>& a, const AttnPlan& p, cudaStream_t s) {
     auto kernel = decode_kernel<T, HD, STAGES, PREFIX>;
     const size_t smem = layout(a.group, HD, a.block_size, STAGES, sizeof(T)).total;
     if (smem > 48 * 1024) {
@@ -1676,7 +1685,7 @@ cudaError_t launch_stages(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) 
 }
 
 template <typename T>
-cudaError_t launch_prefix_typed(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+cudaError_t launch_prefix_typed(const PrefixAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     if constexpr (sizeof(T) == 2) {
         if (a.tail_only)
             return p.head_dim == 64    ? launch_tail<T, 64>(a, p, s)
@@ -1723,7 +1732,7 @@ cudaError_t launch_decode_attention(const AttnArgs& a, const AttnPlan& p, int dt
     }
 }
 
-cudaError_t launch_prefix_tail(const AttnArgs& a, const AttnPlan& p, int dtype, cudaStream_t s) {
+cudaError_t launch_prefix_tail(const PrefixAttnArgs& a, const AttnPlan& p, int dtype, cudaStream_t s) {
     switch (dtype) {
         case DT_F32: return attn::launch_prefix_typed<float>(a, p, s);
         case DT_F16: return attn::launch_prefix_typed<__half>(a, p, s);
