@@ -86,12 +86,15 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CacheList c, PageCop
     copy_items<V>(c, a.n, blockIdx.x, gridDim.x, [&](int64_t i, bool first) {
         const int32_t s = a.src[i], d = a.dst[i];
         Pair p{s, d, 0};
-        if (s < 0 || d < 0) return p;  // padding
+        if (s < 0 || d < 0 || s == d) {  // padding, or nothing to move
+            if (s == d && s >= a.num_blocks && first && threadIdx.x == 0 && a.count_errors) count_error(a.err);
+            return p;
+        }
         if (s >= a.num_blocks || d >= a.num_blocks) {
             if (first && threadIdx.x == 0 && a.count_errors) count_error(a.err);
             return p;
         }
-        if (s != d) p.bytes = c.page_bytes;
+        p.bytes = c.page_bytes;
         return p;
     });
 }
@@ -105,8 +108,11 @@ constexpr int kCols = 128;      // table columns of a CTA, one per thread
 __device__ __forceinline__ bool named_before(const int32_t* idx, const int32_t* other, int64_t i, int lane) {
     const int32_t me = idx[i];
     bool hit = false;
-    for (int64_t k = lane; k < i; k += 32)
-        if (idx[k] == me) hit |= !other || other[k] >= 0;
+    for (int64_t k = lane; k < i; k += 32) hit |= idx[k] == me;
+    if (!__any_sync(FULL, hit)) return false;
+    if (!other) return true;
+    hit = false;
+    for (int64_t k = lane; k < i; k += 32) hit |= idx[k] == me && other[k] >= 0;
     return __any_sync(FULL, hit);
 }
 
