@@ -857,7 +857,8 @@ def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_coun
                      num_live: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                      err_count: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Move the live pages (count > 0) to the front of the caches; tables and counts follow.
-    Returns num_live, int32 [1]: the pages from there on are free."""
+    Returns num_live, int32 [1]: the pages from there on are free. A page list kept apart from
+    block_table (a prefix_table) has to be taken from a row of it again."""
     dev, rows, mb, counts = _page_state(block_table, seq_lens, ref_counts)
     (_, nb, bs, n_kv, hd), dtype, cache_dev, ptrs, count = _kv_caches(kv_caches)
     if num_live is None:
@@ -905,7 +906,9 @@ def shared_prefix_attention(q: torch.Tensor, kv_cache: torch.Tensor, prefix_tabl
     q: [B, n_head, head_dim]; kv_cache, block_table [B, max_blocks] and seq_lens [B] (all of a
     request's tokens) as in paged_decode_attention; prefix_table: int32 [prefix_blocks], the pages of
     the prefix (a row of block_table that reaches past it will do); prefix_len: int32 [1] on the
-    device. workspace: from shared_prefix_workspace; one is made for the call where none is given."""
+    device. workspace: from shared_prefix_workspace; one is made for the call where None is given. With
+    an empty tensor (torch.empty(0, device=...)) the call has none: every request reads the prefix for
+    itself, and probabilities keep 16 bits or more instead of one rounding to bf16 / fp16."""
     if not (isinstance(q, torch.Tensor) and q.is_cuda):
         _cuda(q, "q")
     dev, dtype = q.get_device(), q.dtype

@@ -120,3 +120,25 @@ def test_a_scale_of_zero(dtype, hd, path):
     close(c, sra.shared_prefix_attention(**c.dev(), scale=0.0), "an infinite score")
     c.q[7, 2, 5] = torch.inf
     close(c, sra.shared_prefix_attention(**c.dev(), scale=0.0), "an infinite query")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_an_empty_workspace_keeps_the_probabilities(dtype):
+    """The form without a workspace, from Python: the forced decode form's result, with probabilities of 16 bits (2^-16 of
+    A instead of the half step of the dtype that one rounding costs; a residual that is subnormal in fp16 is off by
+    half a step of 2^-24, 2^-25 of the largest probability each)."""
+    c = Case(70, 12, 2, 128, 16, 2000, [2000 + b % 50 for b in range(70)], dtype, 8)
+    d = c.dev()
+    got = sra.shared_prefix_attention(**d, scale=c.scale, workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+    sra.force_variant("shared_prefix", 0)
+    try:
+        want = sra.shared_prefix_attention(**d, scale=c.scale)
+    finally:
+        sra.force_variant("shared_prefix", -1)
+    assert torch.equal(got, want)
+    assert not torch.equal(got, sra.shared_prefix_attention(**d, scale=c.scale))     # (this size is taken together)
+    o, A = c.want()
+    V = c.cache.to(DEV).float().nan_to_num().abs().max().double()
+    tiny = 2.0 ** -25 * 2050 * V if dtype == torch.float16 else 0.0
+    tol = torch.finfo(dtype).eps / 2 * o.abs() + (2.0 ** -16 + 6e-5) * A + tiny + 1e-30
+    assert bool(((got.double() - o).abs() <= tol).all())
