@@ -1646,8 +1646,14 @@ PrefixPlan plan_prefix(int64_t B, int group, int n_kv, int head_dim, int64_t pre
     // What every request reading the prefix for itself would move (L2 to SM) decides: up to 70 MB that is as
     // fast as the two or three kernels of the other path, whose fixed part is 14 to 16 us (measured at
     // 67 MB: 32 requests x 2048 tokens of 12 / 2 heads of 128 16.4 against 18.5 us, 64 x 1024 of 32 / 4 heads of
-    // 64 20.5 against 18.5; at 134 MB 24.6 and 26.7 against 19.6 and 21.6; at 34 MB 12.3 against 16.4). With
-    // head_dim 256 or fp32 the other form runs on the CUDA cores, at 0.9 to 1.5 TB/s of those reads.
+    // 64 20.5 against 18.5; at 134 MB 24.6 and 26.7 against 19.6 and 21.6; at 34 MB 12.3 against 16.4). A few
+    // requests have 16 CTAs per (request, KV head) and do not fill the card, so there the rule is late (12 / 2 heads
+    // of 128, decode form against the other: 1 x 8192 10.1 and 13.5 us, 1 x 32768 22.8 and 20.6, 4 x 8192 19.1 and
+    // 16.4, 8 x 8192 26.3 and 16.7; 32 / 8 heads, 8 x 2048 14.1 and 16.0). With head_dim 256 or fp32 that form runs
+    // on the CUDA cores, slower per byte, and up to 12 MB are read by it: right for 16 and more requests (at 12 MB,
+    // in us: fp32, 12 / 2 heads of 64, 16 requests 20.0 and 21.7, 64 16.7 and 22.0; bf16, 8 / 2 heads of 256, 16
+    // requests 22.0 and 19.1, 64 26.9 and 19.7), far too late for few with a long prefix (1 x 5856, 8 / 2 heads of
+    // 256 in bf16, 211 and 18; 1 x 11712, 12 / 2 heads of 64 in fp32, 186 and 36; 4 requests 60 and 20, 53 and 21).
     const int forced = g_force_prefix.load(std::memory_order_relaxed);
     const double moved = static_cast<double>(B) * prefix_blocks * block_size * n_kv * head_dim * 2.0 * elem_bytes(dtype);
     const bool cores = head_dim > 128 || dtype == DT_F32;

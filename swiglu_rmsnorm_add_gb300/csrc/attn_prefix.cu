@@ -5,8 +5,8 @@
 // K and V, so S = Q K^T and O = P V are matrix products of up to some thousand rows with the prefix's
 // tokens: 4 * rows * head_dim operations per token against 4 * head_dim bytes, tensor-core work from
 // about 280 rows on. prefix_tc_kernel below does them on the fifth-generation tensor cores; each
-// request's own tokens go through the decode kernels of attn.cu (launch_prefix_tail), and merge_kernel
-// joins the parts: with (m_i, l_i, o_i) the maximum, sum of exponentials and weighted V of part i,
+// request's own tokens go through tail_kernel of attn.cu (fp32: its decode_kernel; launch_prefix_tail), and
+// merge_kernel joins the parts: with (m_i, l_i, o_i) the maximum, sum of exponentials and weighted V of part i,
 // out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, M = max m_i.
 #include <type_traits>
 
@@ -131,11 +131,15 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 // S, P and O never share columns, so the next tile's S needs only that this one's has been read: the
 // product S runs under the softmax, and the tensor cores have work of one stream while the other's
 // softmax is under way. (With P over S in 128-token tiles the chain S -> softmax -> P V -> next S has no
-// such overlap: measured 4700 clocks per 128 tokens of both streams, against 2070 of tensor-core work.
+// such overlap within a stream: measured 4700 clocks per 128 tokens of both streams, against 2070 of tensor-core
+// work, in a form whose one warp also issued for both streams from a branch of one lane, at 75 clocks an instruction;
+// what the tile alone costs or gives has not been measured apart from that.
 // The price is that S in tiles of 64 tokens reads Q from shared memory twice as often: 48 clocks per
 // K step of 16 instead of 2 x 32, shared-memory bandwidth, so a tile cannot run above 81 % of the peak.)
-// With head_dim 256 O alone would fill tensor memory for two row tiles, so the streams share a row tile and a
-// CTA's S and take half of V's dims each; S is computed twice (62 % of the work is needed work).
+// With head_dim 256 O alone would fill tensor memory for two row tiles, so a CTA has one, and its streams take half
+// of V's dims each with an S and P of their own, which are the same: S is computed twice (62 % of the work is needed
+// work; batch 100 x 12000 with 16 / 2 heads 57 us, the needed products 10.3 at the measured peak). One O of 256
+// columns beside two S and two P, 448 columns in all, would fit and need S once; it has not been built.
 template <typename T, int HD>
 __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_constant__ CUtensorMap tmC) {
     using L = Smem<HD>;
@@ -420,8 +424,9 @@ __global__ void __maxnreg__(120) prefix_tc_kernel(PrefixArgs a, const __grid_con
                     tc::wait_st();
                 }
             }
-            // p = 2^(c s - m), summed in fp32, rounded once to T: a relative error of half a step of T
-            // per probability, which the product with V averages over the tokens. Pairs of fp32 go
+            // p = 2^(c s - m), summed in fp32, rounded once to T: a relative error of up to half a step of T
+            // per probability, so that O is off by about as much again as its own rounding to T costs (batch 64 and
+            // 256, bf16: 2.3e-3 of the exact result's norm where that rounding alone is 1.7e-3). Pairs of fp32 go
             // through the packed multiply-add and add.
             const float base = m == -INFINITY ? 0.0f : m;
             const uint64_t c2 = f32x2(c, c), b2 = f32x2(-base, -base);
@@ -559,8 +564,10 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* cache, bool pdl, cudaStre
 }
 
 // ------------------------------------------------------------------ fp32
-// The same cut for fp32, on the CUDA cores (the tensor cores have no fp32 products, and parts of fewer bits
-// would have to be paid for six times): a CTA takes 64 query rows through its split's K / V tiles of 64
+// The same cut for fp32, on the CUDA cores (the tensor cores have no fp32 products. Three bf16 parts of each operand
+// and the six products of them that matter would be a sixth of the bf16 rate, 317 TFLOP/s at the measured peak, more
+// than the CUDA cores have: not built, and so not known is whether that holds the error. Batch 100 x 4800, 16 / 2
+// heads of 128: 171 us, 23 TFLOP/s): a CTA takes 64 query rows through its split's K / V tiles of 64
 // tokens. A thread holds 4 rows x 4 tokens of S and 4 rows x head_dim / 16 dims of O, so that a load of 16
 // bytes from shared memory feeds 5 (S) to 6 (O) FMAs a lane; the rows of its operands are padded by 16 bytes, so
 // that the lanes of a load meet different banks. K of the next tile is copied under P V, V under Q K^T.
