@@ -216,8 +216,12 @@ def _made_for(stream, dev: int, make):
     freed on the current stream may still be in use there."""
     if stream is None or _raw(stream) == torch.cuda.current_stream(dev).cuda_stream:
         return make()
-    s = stream if isinstance(stream, torch.cuda.Stream) else \
-        torch.cuda.ExternalStream(_raw(stream), device=torch.device("cuda", dev))
+    if isinstance(stream, torch.cuda.Stream):
+        s = stream
+    elif _raw(stream) in (0, 1):    # CUDA's handles of the default stream (an ExternalStream of 0 is some other stream)
+        s = torch.cuda.default_stream(dev)
+    else:
+        s = torch.cuda.ExternalStream(_raw(stream), device=torch.device("cuda", dev))
     with torch.cuda.stream(s):
         return make()
 

@@ -82,6 +82,21 @@ def test_a_dropped_result_waits_for_the_current_stream(call):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("which", ["object", "integer", "default object", "default integer"])
+def test_memory_is_filed_under_the_calls_stream(call, which):
+    """What the allocator has on record: results belong to the stream that the call was given, also where that is the
+    default stream (whose handle is 0) and another one is current."""
+    side, here = torch.cuda.Stream(), torch.cuda.Stream()
+    s = torch.cuda.default_stream() if which.startswith("default") else side
+    with torch.cuda.stream(here):
+        got = call(s if which.endswith("object") else s.cuda_stream)
+    torch.cuda.synchronize()
+    segments = torch.cuda.memory_snapshot()
+    for t in got:
+        (owner,) = [g["stream"] for g in segments if g["address"] <= t.data_ptr() < g["address"] + g["total_size"]]
+        assert owner == s.cuda_stream
+
+
 def test_values_on_another_stream_without_its_context():
     """The same results as on the current stream, outputs and workspaces made by the call."""
     torch.manual_seed(2)
