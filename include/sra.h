@@ -17,6 +17,8 @@
  *   sra_kv_copy_pages / sra_kv_fork_rows / sra_kv_resize_rows / sra_kv_compact_pages  the pages of the
  *                      cache: copied, shared, grown with copy on write, given back, moved together
  *   sra_shared_prefix_attention  decode attention of a batch that shares a prefix, read once for it
+ *   sra_rope_kv_store_quant / sra_kv_quant_read / sra_paged_decode_attention_quant  the paged cache held in
+ *                      4 or 8 bits: written, read back, and attended to
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -80,8 +82,14 @@ extern "C" {
 typedef enum sra_dtype {
     SRA_F32 = 0,  /* IEEE binary32 */
     SRA_F16 = 1,  /* IEEE binary16 */
-    SRA_BF16 = 2  /* bfloat16 */
+    SRA_BF16 = 2,  /* bfloat16 */
+    SRA_BYTES = 8  /* the page operators' caches only: a cache held in 4 or 8 bits */
 } sra_dtype_t;
+
+typedef enum sra_kv_format {
+    SRA_KV_E2M1 = 0, /* 4 bits: a sign and 0, .5, 1, 1.5, 2, 3, 4 or 6, times the group's scale */
+    SRA_KV_INT8 = 1  /* 8 bits: an integer of [-127, 127], times the group's scale */
+} sra_kv_format_t;
 
 typedef enum sra_status {
     SRA_OK = 0,
@@ -485,6 +493,8 @@ SRA_API int sra_uclip(const void* x, const float* alpha, const float* gamma, voi
  * [2, num_blocks, block_size, n_kv_head, head_dim] of `dtype`, aligned to the dtype; read
  * during the call only (the pointers go into the kernels' parameters). The caches must not
  * overlap one another or any other argument. Any head_dim and block_size.
+ * A cache held in 4 or 8 bits (sra_rope_kv_store_quant) is passed with dtype SRA_BYTES and its row bytes
+ * as head_dim (a multiple of 4, the caches aligned to 4); of a shared last page the whole is copied.
  * err_count: NULL, or a device int32 to which each call adds what it found wrong, as said
  * at each; the caller zeroes it. Nothing is read or written out of range for any contents of
  * the device arrays.
@@ -636,6 +646,83 @@ SRA_API int sra_shared_prefix_attention(const void* q, const void* kv_cache, con
 SRA_API int64_t sra_shared_prefix_workspace_size(int64_t B, int n_head, int n_kv_head, int head_dim,
                                                  int64_t prefix_blocks, int64_t max_blocks_per_seq, int block_size,
                                                  int dtype);
+
+/*
+ * The paged cache held in 4 or 8 bits.
+ *
+ * kv_cache: uint8 [2, num_blocks, n_kv_head, block_size, row_bytes], contiguous, 16-byte aligned; plane 0 = K,
+ * plane 1 = V; row_bytes = sra_kv_quant_row_bytes(head_dim, format). (A head's rows of a page lie in a row; blocks, slots,
+ * tables and lengths are those of the cache in 16 or 32 bits.) head_dim 64, 128 or 256.
+ * A row holds the codes of its head_dim values, then one scale byte for each 16 dims in a row. Scale byte u is the fp16
+ * number with the bits u << 7 (a 5-bit exponent and 3 bits of mantissa); 255, a NaN, marks a group that held an infinity
+ * or a NaN, all of whose values read as NaN.
+ *   SRA_KV_E2M1  value = (-1)^(c >> 3) * {0, .5, 1, 1.5, 2, 3, 4, 6}[c & 7] * scale; dim 2i is the low half of byte i.
+ *                scale = amax / 6 rounded to nearest (ties to an even byte), at most 10240.
+ *   SRA_KV_INT8  value = n * scale, byte i = n of dim i. scale = amax / 127 rounded up, at most 512.
+ * amax is the group's largest magnitude; a code is the nearest to x / scale, ties to the even code, saturating (values
+ * above 61440 or 65024 are held as those). A group whose scale rounds to 0 (amax up to 6 * 2^-18, 4 bits) holds zeros.
+ * Every value is an fp16 number. The bytes follow from the inputs alone.
+ */
+
+/* Bytes of a row, or a negative sra_status. */
+SRA_API int64_t sra_kv_quant_row_bytes(int head_dim, int format);
+
+/*
+ * sra_rope_kv_store_quant — sra_rope_kv_store_ex (all of q_alpha .. k_gamma NULL) or sra_rope_kv_store_qk_uclip (all
+ * given) into a cache held in 4 or 8 bits: q is rotated in place with their result, bit for bit; K after the rotation,
+ * rounded correctly to `dtype`, and V are quantised into the token's slot. Token rules and err_count are theirs.
+ * Errors: theirs; an unknown format -> SRA_ERR_ARG; a cache not 16-byte aligned -> SRA_ERR_ARG; some but not all of the four
+ * parameters -> SRA_ERR_NULL; head_dim other than 64, 128 and 256 -> SRA_ERR_SHAPE; pos, slot_mapping, a table or a
+ * parameter that overlaps q or the cache -> SRA_ERR_ALIAS.
+ */
+SRA_API int sra_rope_kv_store_quant(void* q, const void* k, const void* v, const float* cos, const float* sin,
+                                    const int64_t* pos, const int64_t* slot_mapping, void* kv_cache, int64_t T, int n_head,
+                                    int n_kv_head, int head_dim, int64_t q_tok_stride, int64_t k_tok_stride,
+                                    int64_t v_tok_stride, int64_t max_pos, int64_t num_blocks, int block_size,
+                                    int32_t* err_count, int style, const float* q_alpha, const float* q_gamma,
+                                    const float* k_alpha, const float* k_gamma, float clip_min, float clip_max, int format,
+                                    int dtype, void* stream);
+
+/*
+ * sra_kv_quant_read — tokens of a cache held in 4 or 8 bits as dense K and V, row after row (the history that a
+ * prompt's next chunk attends to).
+ *
+ *   k[cu_lens[r] + i, h, :] = the K of row r's token starts[r] + i, kv head h, for 0 <= i < cu_lens[r + 1] - cu_lens[r]
+ *
+ * and v likewise, each value rounded once to `dtype` (exact in fp16 and fp32, and in bf16 for 4 bits).
+ * block_table: int32 [rows, max_blocks_per_seq]; cu_lens: int32 [rows + 1], not falling; starts: NULL (zeros) or int32
+ * [rows]; k, v: [total, n_kv_head, head_dim], token strides k_tok_stride and v_tok_stride (views of one buffer
+ * will do). What lies outside [cu_lens[0], cu_lens[rows]) is left as it was.
+ * err_count: nullable device int32, incremented once for each entry outside [0, num_blocks) that holds a token asked
+ * for and once for each row that asks for tokens outside [0, max_blocks_per_seq * block_size); those tokens are zeros.
+ * Nothing is read or written out of range for any contents of the device arrays.
+ * Errors: bad sizes -> SRA_ERR_SHAPE; short strides -> SRA_ERR_STRIDE; NULL -> SRA_ERR_NULL; unknown dtype or format, a
+ * misaligned cache -> SRA_ERR_DTYPE, SRA_ERR_ARG; overlap -> SRA_ERR_ALIAS. total == 0 is a no-op.
+ */
+SRA_API int sra_kv_quant_read(const void* kv_cache, const int32_t* block_table, const int32_t* cu_lens, const int32_t* starts,
+                              void* k, void* v, int64_t rows, int64_t max_blocks_per_seq, int64_t total, int n_kv_head,
+                              int head_dim, int64_t k_tok_stride, int64_t v_tok_stride, int64_t num_blocks, int block_size,
+                              int32_t* err_count, int format, int dtype, void* stream);
+
+/*
+ * sra_paged_decode_attention_quant — sra_paged_decode_attention over a cache held in 4 or 8 bits, K_t and V_t the values
+ * that the cache stands for. q, out, block_table, seq_lens, scale and err_count are those of
+ * sra_paged_decode_attention. A request without tokens, or with none whose score is above -inf, gets zeros; NaN in
+ * what a request attends to gives NaN.
+ * workspace: NULL, or device memory of at least sra_paged_decode_attention_quant_workspace_size bytes (same sizes,
+ * current device), 16-byte aligned, contents without meaning; calls that share one must not overlap on the GPU.
+ * Supported shapes: head_dim 64, 128 or 256; block_size 8, 16 or 32; n_head / n_kv_head <= 8.
+ * Errors: as sra_paged_decode_attention_ws; an unknown format -> SRA_ERR_ARG.
+ */
+SRA_API int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const int32_t* block_table,
+                                             const int32_t* seq_lens, void* out, int64_t B, int n_head, int n_kv_head,
+                                             int head_dim, int64_t q_tok_stride, int64_t out_tok_stride, int64_t num_blocks,
+                                             int block_size, int64_t max_blocks_per_seq, float scale, void* workspace,
+                                             int64_t workspace_bytes, int32_t* err_count, int format, int dtype, void* stream);
+/* Workspace bytes that call uses on the current device (0: none); a negative sra_status for bad sizes. */
+SRA_API int64_t sra_paged_decode_attention_quant_workspace_size(int64_t B, int n_head, int n_kv_head, int head_dim,
+                                                                int64_t max_blocks_per_seq, int block_size, int format,
+                                                                int dtype);
 
 /* Static text for a status code (never NULL). */
 SRA_API const char* sra_status_string(int status);

@@ -1,7 +1,7 @@
 """GB300-native fused per-token decoder path: RMSNorm, residual-add + RMSNorm,
 RoPE (neox or interleaved) with paged KV-cache store, SwiGLU / ReGLU, UClip / DyHT,
-the decode-attention read of the paged cache, and RMSNorm / GLU fused into the
-projection they feed.
+the decode-attention read of the paged cache, the same cache held in 4 or 8 bits, and
+RMSNorm / GLU fused into the projection they feed.
 
 Every operator runs in the hand-written sm_103a CUDA kernels of ``libsra.so``
 (C ABI in ``include/sra.h``). This module only marshals torch tensors into that
@@ -14,6 +14,7 @@ from ._binding import (  # noqa: F401
     add_rmsnorm,
     compact_kv_pages,
     copy_kv_pages,
+    decode_attention_quant_workspace,
     decode_attention_workspace,
     dyht,
     force_variant,
@@ -27,12 +28,16 @@ from ._binding import (  # noqa: F401
     linear_workspace,
     paged_decode_attention,
     paged_decode_attention_noalloc,
+    paged_decode_attention_quant,
     pick_variant,
+    quant_kv_cache,
+    read_kv_quant,
     reglu,
     resize_kv_rows,
     rmsnorm,
     rmsnorm_linear,
     rope_kv_store,
+    rope_kv_store_quant,
     set_pdl,
     shared_prefix_attention,
     shared_prefix_workspace,
@@ -50,7 +55,9 @@ __all__ = ["rmsnorm", "add_rmsnorm", "rope_kv_store", "swiglu", "reglu", "glu", 
            "rmsnorm_linear", "glu_linear", "linear_workspace",
            "copy_kv_pages", "fork_kv_rows", "resize_kv_rows", "compact_kv_pages",
            "kv_fork_workspace", "kv_resize_workspace", "kv_compact_workspace",
-           "shared_prefix_attention", "shared_prefix_workspace", "lib",
+           "shared_prefix_attention", "shared_prefix_workspace",
+           "quant_kv_cache", "rope_kv_store_quant", "read_kv_quant", "paged_decode_attention_quant",
+           "decode_attention_quant_workspace", "lib",
            "SRAError",
            "force_variant", "set_pdl", "variant_count", "variant_name", "pick_variant", "status_string",
            "wait_timeouts", "wait_selftest"]

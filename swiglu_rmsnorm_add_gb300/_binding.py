@@ -16,6 +16,8 @@ _lib = None
 
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ACT_CODE = {"silu": 0, "relu": 1}
+PAGE_DTYPE_CODE = {**DTYPE_CODE, torch.uint8: 8}    # of the page operators' caches
+KV_FORMAT = {"e2m1": 0, "int8": 1}
 
 
 class SRAError(RuntimeError):
@@ -85,6 +87,18 @@ def lib() -> ctypes.CDLL:
             L.sra_shared_prefix_attention.restype = i32
             L.sra_shared_prefix_workspace_size.argtypes = [i64, i32, i32, i32, i64, i64, i32, i32]
             L.sra_shared_prefix_workspace_size.restype = i64
+            L.sra_kv_quant_row_bytes.argtypes = [i32, i32]
+            L.sra_kv_quant_row_bytes.restype = i64
+            L.sra_rope_kv_store_quant.argtypes = L.sra_rope_kv_store_qk_uclip.argtypes[:-2] + [i32, i32, vp]
+            L.sra_rope_kv_store_quant.restype = i32
+            L.sra_kv_quant_read.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i64, i64, i64, i32, vp, i32,
+                                            i32, vp]
+            L.sra_kv_quant_read.restype = i32
+            L.sra_paged_decode_attention_quant.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, i64, i64, i32, i64,
+                                                           f32, vp, i64, vp, i32, i32, vp]
+            L.sra_paged_decode_attention_quant.restype = i32
+            L.sra_paged_decode_attention_quant_workspace_size.argtypes = [i64, i32, i32, i32, i64, i32, i32, i32]
+            L.sra_paged_decode_attention_quant_workspace_size.restype = i64
             L.sra_status_string.argtypes = [i32]
             L.sra_status_string.restype = ctypes.c_char_p
             L.sra_version.restype = i32
@@ -648,7 +662,15 @@ def _kv_cache_ok(c: torch.Tensor) -> bool:
 def _kv_caches(kv_caches):
     """(shape, dtype, device index, pointers, count) of one cache [2, num_blocks, block_size, n_kv_head,
     head_dim], a [layers, 2, ...] tensor of them, or a sequence of caches of one shape and dtype. The
-    pointers are an array that has to live until the call returns."""
+    pointers are an array that has to live until the call returns. A cache in 4 or 8 bits (quant_kv_cache)
+    is uint8 [2, num_blocks, n_kv_head, block_size, row_bytes]; its shape is given in the order of the others."""
+    shape, dtype, *rest = _caches_given(kv_caches)
+    if dtype is torch.uint8:
+        shape = [shape[0], shape[1], shape[3], shape[2], shape[4]]
+    return (shape, dtype, *rest)
+
+
+def _caches_given(kv_caches):
     if isinstance(kv_caches, torch.Tensor):
         if kv_caches.dim() == 6 and kv_caches.is_cuda and kv_caches.shape[0] > 0 and kv_caches.shape[1] == 2 \
                 and kv_caches.is_contiguous():
@@ -763,11 +785,11 @@ def copy_kv_pages(kv_caches, src: torch.Tensor, dst: torch.Tensor, err_count: to
     n = src.numel()
     if dst.numel() != n:
         raise ValueError("src and dst must have the same length")
-    if dtype not in DTYPE_CODE:
+    if dtype not in PAGE_DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
     with _on(dev):
         st = lib().sra_kv_copy_pages(ptrs.buffer_info()[0], count, src.data_ptr(), dst.data_ptr(), n, nb, bs, n_kv, hd,
-                                     _err_ptr(err_count, dev), DTYPE_CODE[dtype], _stream(src, stream))
+                                     _err_ptr(err_count, dev), PAGE_DTYPE_CODE[dtype], _stream(src, stream))
     _check("sra_kv_copy_pages", st)
 
 
@@ -828,7 +850,7 @@ def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts
         raise ValueError("rows and lens must have the same length")
     if cache_dev != dev:
         raise ValueError("all tensors must be on the same CUDA device")
-    if dtype not in DTYPE_CODE:
+    if dtype not in PAGE_DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
     if pos is None:
         pos = _result(stream, dev, lambda: torch.empty(n, dtype=torch.int64, device=rows.device))
@@ -846,7 +868,7 @@ def resize_kv_rows(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts
         st = lib().sra_kv_resize_rows(block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
                                       rows.data_ptr(), lens.data_ptr(), n, table_rows, mb,
                                       ptrs.buffer_info()[0], count, nb, bs, n_kv, hd, pos.data_ptr(),
-                                      slot_mapping.data_ptr(), wp, wb, _err_ptr(err_count, dev), DTYPE_CODE[dtype],
+                                      slot_mapping.data_ptr(), wp, wb, _err_ptr(err_count, dev), PAGE_DTYPE_CODE[dtype],
                                       _stream(block_table, stream))
     _check("sra_kv_resize_rows", st)
     return pos, slot_mapping
@@ -872,7 +894,7 @@ def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_coun
         raise ValueError("num_live must hold one entry")
     if cache_dev != dev:
         raise ValueError("all tensors must be on the same CUDA device")
-    if dtype not in DTYPE_CODE:
+    if dtype not in PAGE_DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
     if counts != nb:
         raise ValueError("ref_counts must have one entry per page of the caches")
@@ -881,7 +903,7 @@ def compact_kv_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_coun
         st = lib().sra_kv_compact_pages(block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
                                         rows, mb, ptrs.buffer_info()[0], count, nb, bs,
                                         n_kv, hd, num_live.data_ptr(), wp, wb, _err_ptr(err_count, dev),
-                                        DTYPE_CODE[dtype], _stream(block_table, stream))
+                                        PAGE_DTYPE_CODE[dtype], _stream(block_table, stream))
     _check("sra_kv_compact_pages", st)
     return num_live
 
@@ -950,4 +972,176 @@ def shared_prefix_attention(q: torch.Tensor, kv_cache: torch.Tensor, prefix_tabl
             bs, pb, mb, float(scale) if scale is not None else 1.0 / float(hd) ** 0.5, wp, wb, _err_ptr(err_count, dev),
             code, _stream(q, stream))
     _check("sra_shared_prefix_attention", st)
+    return out
+
+
+# ------------------------------------------------------------------- a cache held in 4 or 8 bits
+def _row_bytes(fmt: str, head_dim: int) -> int:
+    if fmt not in KV_FORMAT:
+        raise ValueError("fmt must be 'e2m1' (4 bits) or 'int8'")
+    n = lib().sra_kv_quant_row_bytes(int(head_dim), KV_FORMAT[fmt])
+    if n < 0:
+        _check("sra_kv_quant_row_bytes", int(n))
+    return int(n)
+
+
+def quant_kv_cache(num_blocks: int, block_size: int, n_kv_head: int, head_dim: int, fmt: str = "e2m1",
+                   layers: int | None = None, device="cuda") -> torch.Tensor:
+    """An empty cache held in 4 ("e2m1") or 8 ("int8") bits: uint8 [2, num_blocks, n_kv_head, block_size, row_bytes],
+    with `layers` one [layers, 2, ...] tensor of them. head_dim 64, 128 or 256."""
+    shape = (2, num_blocks, n_kv_head, block_size, _row_bytes(fmt, head_dim))
+    return torch.zeros(shape if layers is None else (layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _quant_cache(kv_cache, head_dim, n_kv=None):
+    """(num_blocks, n_kv_head, block_size, format code) of a quantised cache; the format follows from its rows' bytes."""
+    _cuda(kv_cache, "kv_cache")
+    if kv_cache.dtype is not torch.uint8 or kv_cache.dim() != 5 or kv_cache.shape[0] != 2 or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be contiguous uint8 [2, num_blocks, n_kv_head, block_size, row_bytes]")
+    _, nb, kv, bs, row = kv_cache.shape
+    if head_dim not in (64, 128, 256):
+        raise ValueError("head_dim must be 64, 128 or 256")
+    for code in (0, 1):
+        if row == (head_dim * (1 + code)) // 2 + head_dim // 16:
+            break
+    else:
+        raise ValueError(f"kv_cache: rows of {row} bytes hold no {head_dim} values in 4 or 8 bits")
+    if n_kv is not None and kv != n_kv:
+        raise ValueError("shape mismatch")
+    return nb, kv, bs, code
+
+
+def rope_kv_store_quant(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
+                        pos: torch.Tensor, slot_mapping: torch.Tensor, kv_cache: torch.Tensor,
+                        err_count: torch.Tensor | None = None, max_pos: int | None = None, stream=None,
+                        style: str = "neox", qk_uclip=None, clip: tuple[float, float] = (-1.0, 1.0)) -> None:
+    """rope_kv_store into a cache held in 4 or 8 bits (quant_kv_cache): q is rotated in place as there; the rotated k,
+    rounded to its dtype, and v are quantised into their slots."""
+    if style not in ROPE_STYLE:
+        raise ValueError("style must be 'neox' or 'interleaved'")
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (cos, "cos"), (sin, "sin"), (pos, "pos"), (slot_mapping, "slot_mapping")):
+        _cuda(t, n)
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [T, heads, head_dim]")
+    T, n_head, hd = q.shape
+    n_kv = k.shape[1]
+    nb, _, bs, fmt = _quant_cache(kv_cache, hd, n_kv)
+    params = (None,) * 4 if qk_uclip is None else tuple(qk_uclip)
+    _same_device(q, k, v, cos, sin, pos, slot_mapping, kv_cache, *params)
+    if not (k.dtype == v.dtype == q.dtype):
+        raise ValueError("q, k and v must share one dtype")
+    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("cos and sin must be contiguous float32 [max_pos, head_dim // 2]")
+    if pos.dtype != torch.int64 or slot_mapping.dtype != torch.int64 or not pos.is_contiguous() \
+            or not slot_mapping.is_contiguous():
+        raise ValueError("pos and slot_mapping must be contiguous int64")
+    if k.shape != (T, n_kv, hd) or v.shape != (T, n_kv, hd) or pos.numel() != T or slot_mapping.numel() != T:
+        raise ValueError("shape mismatch")
+    if max_pos is None:
+        max_pos = cos.shape[0]
+    if cos.dim() != 2 or cos.shape[-1] != hd // 2 or sin.shape != cos.shape or max_pos > cos.shape[0]:
+        raise ValueError("cos / sin tables must be [>= max_pos, head_dim // 2]")
+    if qk_uclip is not None:
+        if len(params) != 4:
+            raise ValueError("qk_uclip is (q_alpha, q_gamma, k_alpha, k_gamma)")
+        for t, n in zip(params, ("q_alpha", "q_gamma", "k_alpha", "k_gamma")):
+            _cuda(t, n)
+            if t.dtype != torch.float32 or t.numel() != hd or not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous float32 tensor of head_dim entries")
+    dev = q.get_device()
+    with _on(dev):
+        st = lib().sra_rope_kv_store_quant(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(),
+            slot_mapping.data_ptr(), kv_cache.data_ptr(), T, n_head, n_kv, hd, _tok_stride(q, "q"), _tok_stride(k, "k"),
+            _tok_stride(v, "v"), int(max_pos), nb, bs, _err_ptr(err_count, dev), ROPE_STYLE[style],
+            *(t.data_ptr() if t is not None else None for t in params), float(clip[0]), float(clip[1]), fmt, _dtype(q),
+            _stream(q, stream))
+    _check("sra_rope_kv_store_quant", st)
+
+
+def read_kv_quant(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_lens: torch.Tensor, total: int, head_dim: int,
+                  dtype=torch.bfloat16, starts: torch.Tensor | None = None,
+                  out: tuple[torch.Tensor, torch.Tensor] | None = None, err_count: torch.Tensor | None = None,
+                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(k, v), [total, n_kv_head, head_dim] each: the tokens starts[r] (default 0) and on of every row r of block_table, at
+    k[cu_lens[r]:cu_lens[r + 1]].
+
+    kv_cache: from quant_kv_cache; block_table: int32 [rows, max_blocks]; cu_lens: int32 [rows + 1]; starts: int32 [rows].
+    total is the rows of the results; those outside of [cu_lens[0], cu_lens[-1]) are not written."""
+    nb, n_kv, bs, fmt = _quant_cache(kv_cache, head_dim)
+    dev = kv_cache.get_device()
+    _int32(block_table, "block_table", 2, dev)
+    _int32(cu_lens, "cu_lens", 1, dev)
+    rows, mb = block_table.shape
+    if cu_lens.numel() != rows + 1:
+        raise ValueError("cu_lens must have one entry more than block_table has rows")
+    if starts is not None:
+        _int32(starts, "starts", 1, dev)
+        if starts.numel() != rows:
+            raise ValueError("starts must have one entry per row of block_table")
+    if out is None:
+        if dtype not in DTYPE_CODE:
+            raise ValueError(f"unsupported dtype {dtype}")
+        shape = (int(total), n_kv, head_dim)
+        out = tuple(_result(stream, dev, lambda: torch.empty(shape, dtype=dtype, device=kv_cache.device)) for _ in "kv")
+    k, v = out
+    for t, n in ((k, "k"), (v, "v")):
+        _cuda(t, n)
+        if t.shape != (total, n_kv, head_dim) or t.dtype != k.dtype:
+            raise ValueError("the results must be [total, n_kv_head, head_dim] of one dtype")
+    _same_device(kv_cache, k, v)
+    with _on(dev):
+        st = lib().sra_kv_quant_read(kv_cache.data_ptr(), block_table.data_ptr(), cu_lens.data_ptr(),
+                                     starts.data_ptr() if starts is not None else None, k.data_ptr(), v.data_ptr(), rows,
+                                     mb, int(total), n_kv, head_dim, _tok_stride(k, "k"), _tok_stride(v, "v"), nb, bs,
+                                     _err_ptr(err_count, dev), fmt, _dtype(k), _stream(kv_cache, stream))
+    _check("sra_kv_quant_read", st)
+    return k, v
+
+
+def decode_attention_quant_workspace(B: int, n_head: int, n_kv_head: int, head_dim: int, max_blocks: int, block_size: int,
+                                     fmt: str = "e2m1", dtype=torch.bfloat16, device="cuda") -> torch.Tensor | None:
+    """A workspace for paged_decode_attention_quant, or None where these sizes use none. Reuse it across calls (each
+    call writes what it reads)."""
+    if fmt not in KV_FORMAT:
+        raise ValueError("fmt must be 'e2m1' (4 bits) or 'int8'")
+    with torch.cuda.device(device):
+        n = lib().sra_paged_decode_attention_quant_workspace_size(B, n_head, n_kv_head, head_dim, max_blocks, block_size,
+                                                                  KV_FORMAT[fmt], DTYPE_CODE[dtype])
+    if n < 0:
+        _check("sra_paged_decode_attention_quant_workspace_size", int(n))
+    return torch.empty(int(n), dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def paged_decode_attention_quant(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                                 out: torch.Tensor | None = None, scale: float | None = None,
+                                 err_count: torch.Tensor | None = None, stream=None,
+                                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """paged_decode_attention over a cache held in 4 or 8 bits (quant_kv_cache).
+
+    q: [B, n_head, head_dim]; block_table: int32 [B, max_blocks]; seq_lens: int32 [B]; scale defaults to
+    1 / sqrt(head_dim). workspace: from decode_attention_quant_workspace, or None."""
+    _cuda(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, n_head, head_dim]")
+    dev, (B, n_head, hd) = q.get_device(), q.shape
+    nb, n_kv, bs, fmt = _quant_cache(kv_cache, hd)
+    _int32(block_table, "block_table", 2, dev)
+    _int32(seq_lens, "seq_lens", 1, dev)
+    if out is None:
+        out = _result(stream, dev, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+    _cuda(out, "out")
+    _same_device(q, kv_cache, out)
+    if out.shape != q.shape or out.dtype != q.dtype or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("shape mismatch")
+    wp, wb = None, 0
+    if workspace is not None:
+        workspace, wp, wb = _workspace_args(workspace, None, dev, stream)
+    with _on(dev):
+        st = lib().sra_paged_decode_attention_quant(
+            q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), B, n_head, n_kv,
+            hd, _tok_stride(q, "q"), _tok_stride(out, "out"), nb, bs, block_table.shape[1],
+            float(scale) if scale is not None else 1.0 / float(hd) ** 0.5, wp, wb, _err_ptr(err_count, dev), fmt, _dtype(q),
+            _stream(q, stream))
+    _check("sra_paged_decode_attention_quant", st)
     return out

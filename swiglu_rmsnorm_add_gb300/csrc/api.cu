@@ -1292,6 +1292,7 @@ namespace {
 // Sizes of a call on the caches' pages, and the spans it writes and reads for the overlap checks.
 struct PageCall {
     int64_t page_bytes = 0, plane_bytes = 0;
+    bool by_head = false;  // SRA_BYTES
     Span spans[kMaxCacheList + 16];
     int n = 0, written = 0;  // spans[0 .. written) are written, the others only read
     void add(const void* p, int64_t bytes) {
@@ -1310,7 +1311,13 @@ constexpr int64_t kMaxEntries = 65535 * 8;  // entries of one fork or resize (th
 
 bool int32_size(int64_t v) { return v >= 0 && v <= 0x7fffffff; }
 
+// The caches of a quantised cache's page calls are bytes, in words of 4.
+bool page_dtype(int dt) { return valid_dtype(dt) || dt == SRA_BYTES; }
+int page_elem_bytes(int dt) { return dt == SRA_BYTES ? 1 : elem_bytes(dt); }
+
 int page_sizes(int64_t num_blocks, int block_size, int n_kv_head, int head_dim, int es, PageCall* c) {
+    c->by_head = es == 1;
+    if (c->by_head && head_dim % 4 != 0) return SRA_ERR_SHAPE;
     if (!int32_size(num_blocks) || block_size <= 0 || n_kv_head <= 0 || head_dim <= 0) return SRA_ERR_SHAPE;
     int64_t b = block_size;
     if (__builtin_mul_overflow(b, static_cast<int64_t>(n_kv_head), &b) ||
@@ -1336,7 +1343,7 @@ int check_caches(void* const* caches, int64_t n, int64_t plane_bytes, int es) {
     if (!caches) return SRA_ERR_NULL;
     for (int64_t i = 0; i < n; ++i) {
         if (!caches[i]) return SRA_ERR_NULL;
-        if (reinterpret_cast<uintptr_t>(caches[i]) % es) return SRA_ERR_ARG;
+        if (reinterpret_cast<uintptr_t>(caches[i]) % (es == 1 ? 4 : es)) return SRA_ERR_ARG;
     }
     // in ascending order neighbours are all that can meet
     bool apart = true;
@@ -1378,6 +1385,7 @@ CacheList cache_list(void* const* caches, int64_t first, int64_t n, const PageCa
     for (int i = 0; i < kMaxCacheList; ++i) l.p[i] = i < l.n && c.plane_bytes > 0 ? caches[first + i] : nullptr;
     l.page_bytes = c.page_bytes;
     l.plane_bytes = c.plane_bytes;
+    l.by_head = c.by_head;
     return l;
 }
 
@@ -1394,8 +1402,8 @@ int64_t round_up256(int64_t v) { return (v + 255) / 256 * 256; }
 int sra_kv_copy_pages(void* const* kv_caches, int64_t n_caches, const int32_t* src, const int32_t* dst, int64_t n,
                       int64_t num_blocks, int block_size, int n_kv_head, int head_dim, int32_t* err_count, int dtype,
                       void* stream) {
-    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
-    const int es = elem_bytes(dtype);
+    if (!page_dtype(dtype)) return SRA_ERR_DTYPE;
+    const int es = page_elem_bytes(dtype);
     PageCall c;
     if (n_caches < 0 || n < 0 || n > (int64_t(1) << 40)) return SRA_ERR_SHAPE;
     int st = page_sizes(num_blocks, block_size, n_kv_head, head_dim, es, &c);
@@ -1492,8 +1500,8 @@ int sra_kv_resize_rows(int32_t* block_table, int32_t* seq_lens, int32_t* ref_cou
                        void* const* kv_caches, int64_t n_caches, int64_t num_blocks, int block_size, int n_kv_head,
                        int head_dim, int64_t* pos, int64_t* slot_mapping, void* workspace, int64_t workspace_bytes,
                        int32_t* err_count, int dtype, void* stream) {
-    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
-    const int es = elem_bytes(dtype);
+    if (!page_dtype(dtype)) return SRA_ERR_DTYPE;
+    const int es = page_elem_bytes(dtype);
     PageCall c;
     if (n < 0 || n > kMaxEntries || n_caches <= 0 || !table_sizes_ok(rows, max_blocks_per_seq)) return SRA_ERR_SHAPE;
     int st = page_sizes(num_blocks, block_size, n_kv_head, head_dim, es, &c);
@@ -1522,7 +1530,8 @@ int sra_kv_resize_rows(int32_t* block_table, int32_t* seq_lens, int32_t* ref_cou
     PagePlan plan;
     plan.num_sms = current_sm_count(&dev);
     if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
-    plan.vec = c.plane_bytes ? page_vec(kv_caches, n_caches, c.page_bytes / block_size) : 2;  // whole tokens are copied
+    // whole tokens are copied (whole pages where a page is not in the order of its tokens)
+    plan.vec = c.plane_bytes ? page_vec(kv_caches, n_caches, c.by_head ? c.page_bytes : c.page_bytes / block_size) : 2;
     // a page's and a plane's start are multiples of a token's bytes
     plan.pdl = g_pdl;
     ResizeArgs a;
@@ -1564,8 +1573,8 @@ int sra_kv_compact_pages(int32_t* block_table, const int32_t* seq_lens, int32_t*
                          int64_t max_blocks_per_seq, void* const* kv_caches, int64_t n_caches, int64_t num_blocks,
                          int block_size, int n_kv_head, int head_dim, int32_t* num_live, void* workspace,
                          int64_t workspace_bytes, int32_t* err_count, int dtype, void* stream) {
-    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
-    const int es = elem_bytes(dtype);
+    if (!page_dtype(dtype)) return SRA_ERR_DTYPE;
+    const int es = page_elem_bytes(dtype);
     PageCall c;
     if (n_caches <= 0 || !table_sizes_ok(rows, max_blocks_per_seq)) return SRA_ERR_SHAPE;
     int st = page_sizes(num_blocks, block_size, n_kv_head, head_dim, es, &c);
@@ -1861,6 +1870,228 @@ int sra_shared_prefix_attention(const void* q, const void* kv_cache, const int32
     plan.tail_ctas = head_dim > 128 ? 1 : tail_us > prefix_us ? 3 : 1;
     rs = status_from(launch_prefix_tail(a, plan, dtype, s));
     return rs != SRA_OK ? rs : status_from(launch_prefix_merge(f, head_dim, dtype, s));
+}
+
+// ------------------------------------------------------------------- a cache held in 4 or 8 bits
+namespace {
+
+bool quant_head_dim(int hd) { return hd == 64 || hd == 128 || hd == 256; }
+
+// Bytes of a plane of the cache; false where the sizes overflow.
+bool quant_plane(int64_t num_blocks, int block_size, int n_kv, int format, int head_dim, int64_t* bytes) {
+    int64_t b = kv_row_bytes(format, head_dim), whole;
+    if (__builtin_mul_overflow(b, static_cast<int64_t>(block_size), &b) || __builtin_mul_overflow(b, static_cast<int64_t>(n_kv), &b) ||
+        __builtin_mul_overflow(b, num_blocks, &b) || __builtin_mul_overflow(b, int64_t(2), &whole))
+        return false;
+    *bytes = b;
+    return true;
+}
+
+}  // namespace
+
+int64_t sra_kv_quant_row_bytes(int head_dim, int format) {
+    if (!valid_kv_format(format)) return SRA_ERR_ARG;
+    if (!quant_head_dim(head_dim)) return SRA_ERR_SHAPE;
+    return kv_row_bytes(format, head_dim);
+}
+
+int sra_rope_kv_store_quant(void* q, const void* k, const void* v, const float* cos, const float* sin, const int64_t* pos,
+                            const int64_t* slot_mapping, void* kv_cache, int64_t T, int n_head, int n_kv_head, int head_dim,
+                            int64_t q_tok_stride, int64_t k_tok_stride, int64_t v_tok_stride, int64_t max_pos,
+                            int64_t num_blocks, int block_size, int32_t* err_count, int style, const float* q_alpha,
+                            const float* q_gamma, const float* k_alpha, const float* k_gamma, float clip_min, float clip_max,
+                            int format, int dtype, void* stream) {
+    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
+    if (!valid_kv_format(format) || (style != SRA_ROPE_NEOX && style != SRA_ROPE_INTERLEAVED)) return SRA_ERR_ARG;
+    const bool norm = q_alpha || q_gamma || k_alpha || k_gamma;
+    if (norm && (std::isnan(clip_min) || std::isnan(clip_max) || clip_min > clip_max)) return SRA_ERR_ARG;
+    int64_t plane = 0;
+    if (T < 0 || n_head <= 0 || n_kv_head <= 0 || n_head % n_kv_head != 0 || n_head > (1 << 20) || !quant_head_dim(head_dim) ||
+        block_size <= 0 || num_blocks < 0 || max_pos < 0 || !quant_plane(num_blocks, block_size, n_kv_head, format, head_dim, &plane))
+        return SRA_ERR_SHAPE;
+    const int64_t qw = static_cast<int64_t>(n_head) * head_dim, kw = static_cast<int64_t>(n_kv_head) * head_dim;
+    if (q_tok_stride < qw || k_tok_stride < kw || v_tok_stride < kw) return SRA_ERR_STRIDE;
+    if (T == 0) return SRA_OK;
+    if (!q || !k || !v || !cos || !sin || !pos || !slot_mapping || !kv_cache) return SRA_ERR_NULL;
+    if (norm && (!q_alpha || !q_gamma || !k_alpha || !k_gamma)) return SRA_ERR_NULL;
+    if (!aligned16(kv_cache)) return SRA_ERR_ARG;
+    const int es = elem_bytes(dtype);
+    const Span sq = span_of(q, T, q_tok_stride, qw, es), sc = span_of(kv_cache, 1, 0, 2 * plane, 1);
+    if (rows_overlap(q, T, q_tok_stride, qw, k, T, k_tok_stride, kw, es) ||
+        rows_overlap(q, T, q_tok_stride, qw, v, T, v_tok_stride, kw, es) || overlap(sc, sq) ||
+        overlap(sc, span_of(k, T, k_tok_stride, kw, es)) || overlap(sc, span_of(v, T, v_tok_stride, kw, es)))
+        return SRA_ERR_ALIAS;
+    // what is read while q and the cache are written
+    const Span reads[] = {span_of(pos, 1, 0, T, 8),
+                          span_of(slot_mapping, 1, 0, T, 8),
+                          span_of(cos, 1, 0, max_pos * (head_dim / 2), 4),
+                          span_of(sin, 1, 0, max_pos * (head_dim / 2), 4),
+                          span_of(q_alpha, norm, 0, head_dim, 4),
+                          span_of(q_gamma, norm, 0, head_dim, 4),
+                          span_of(k_alpha, norm, 0, head_dim, 4),
+                          span_of(k_gamma, norm, 0, head_dim, 4)};
+    for (const Span& r : reads)
+        if (overlap(r, sq) || overlap(r, sc)) return SRA_ERR_ALIAS;
+    KvQuantPlan plan;
+    int dev = 0;
+    plan.num_sms = current_sm_count(&dev);
+    if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
+    plan.format = format;
+    plan.style = style;
+    plan.qk_norm = norm;
+    plan.pdl = g_pdl;
+    plan.wide = aligned16(q) && aligned16(k) && aligned16(v) && aligned16(cos) && aligned16(sin) &&
+                stride_aligned16(q_tok_stride, es) && stride_aligned16(k_tok_stride, es) && stride_aligned16(v_tok_stride, es) &&
+                aligned16(q_alpha) && aligned16(q_gamma) && aligned16(k_alpha) && aligned16(k_gamma);
+    RopeArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.cos = cos;
+    a.sin = sin;
+    a.pos = pos;
+    a.slot = slot_mapping;
+    a.cache = kv_cache;
+    a.err = err_count;
+    a.T = T;
+    a.n_head = n_head;
+    a.n_kv = n_kv_head;
+    a.head_dim = head_dim;
+    a.qs = q_tok_stride;
+    a.ks = k_tok_stride;
+    a.vs = v_tok_stride;
+    a.max_pos = max_pos;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.qa = q_alpha, a.qg = q_gamma, a.ka = k_alpha, a.kg = k_gamma;
+    a.clip_lo = clip_min, a.clip_hi = clip_max;
+    return status_from(launch_rope_kv_store_quant(a, plan, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int sra_kv_quant_read(const void* kv_cache, const int32_t* block_table, const int32_t* cu_lens, const int32_t* starts, void* k,
+                      void* v, int64_t rows, int64_t max_blocks_per_seq, int64_t total, int n_kv_head, int head_dim,
+                      int64_t k_tok_stride, int64_t v_tok_stride, int64_t num_blocks, int block_size, int32_t* err_count,
+                      int format, int dtype, void* stream) {
+    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
+    if (!valid_kv_format(format)) return SRA_ERR_ARG;
+    int64_t plane = 0, table = 0;
+    if (rows < 0 || rows > 0x7fffffff || max_blocks_per_seq < 0 || total < 0 || total > 0x7fffffff || n_kv_head <= 0 ||
+        n_kv_head > (1 << 20) || !quant_head_dim(head_dim) || block_size <= 0 || num_blocks < 0 ||
+        !quant_plane(num_blocks, block_size, n_kv_head, format, head_dim, &plane) ||
+        __builtin_mul_overflow(rows * 4, max_blocks_per_seq, &table))
+        return SRA_ERR_SHAPE;
+    const int64_t w = static_cast<int64_t>(n_kv_head) * head_dim;
+    if (k_tok_stride < w || v_tok_stride < w) return SRA_ERR_STRIDE;
+    if (total == 0) return SRA_OK;
+    if (!k || !v || !cu_lens || (rows > 0 && max_blocks_per_seq > 0 && !block_table) || (plane > 0 && !kv_cache))
+        return SRA_ERR_NULL;
+    if (!aligned16(kv_cache)) return SRA_ERR_ARG;
+    const int es = elem_bytes(dtype);
+    const Span outs[] = {span_of(k, total, k_tok_stride, w, es), span_of(v, total, v_tok_stride, w, es)};
+    const Span reads[] = {span_of(kv_cache, 1, 0, 2 * plane, 1), span_of(block_table, 1, 0, table, 1),
+                          span_of(cu_lens, 1, 0, rows + 1, 4), span_of(starts, starts ? 1 : 0, 0, rows, 4)};
+    for (const Span& o : outs)
+        for (const Span& r : reads)
+            if (overlap(o, r)) return SRA_ERR_ALIAS;
+    if (rows_overlap(k, total, k_tok_stride, w, v, total, v_tok_stride, w, es)) return SRA_ERR_ALIAS;
+    KvQuantPlan plan;
+    int dev = 0;
+    plan.num_sms = current_sm_count(&dev);
+    if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
+    plan.format = format;
+    plan.pdl = g_pdl;
+    plan.wide = aligned16(k) && aligned16(v) && stride_aligned16(k_tok_stride, es) && stride_aligned16(v_tok_stride, es);
+    KvReadArgs a;
+    a.cache = kv_cache;
+    a.table = block_table;
+    a.cu = cu_lens;
+    a.starts = starts;
+    a.k = k;
+    a.v = v;
+    a.err = err_count;
+    a.rows = rows;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.total = total;
+    a.ks = k_tok_stride;
+    a.vs = v_tok_stride;
+    a.plane_bytes = plane;
+    a.n_kv = n_kv_head;
+    a.head_dim = head_dim;
+    a.block_size = block_size;
+    return status_from(launch_kv_quant_read(a, plan, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+int quant_attention_sizes(int64_t B, int n_head, int n_kv_head, int head_dim, int64_t max_blocks, int block_size) {
+    int64_t b;
+    return B < 0 || n_head <= 0 || n_kv_head <= 0 || n_head % n_kv_head != 0 || n_head / n_kv_head > 8 || !quant_head_dim(head_dim) ||
+                   (block_size != 8 && block_size != 16 && block_size != 32) || max_blocks < 0 ||
+                   __builtin_mul_overflow(B, static_cast<int64_t>(n_kv_head), &b) || b > 0x7fffffff ||
+                   __builtin_mul_overflow(max_blocks, static_cast<int64_t>(block_size), &b) || b > 0x7fffffff ||
+                   __builtin_mul_overflow(B * 4, max_blocks, &b)
+               ? SRA_ERR_SHAPE
+               : SRA_OK;
+}
+
+}  // namespace
+
+int64_t sra_paged_decode_attention_quant_workspace_size(int64_t B, int n_head, int n_kv_head, int head_dim,
+                                                        int64_t max_blocks_per_seq, int block_size, int format, int dtype) {
+    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
+    if (!valid_kv_format(format)) return SRA_ERR_ARG;
+    return quant_attention_sizes(B, n_head, n_kv_head, head_dim, max_blocks_per_seq, block_size);
+}
+
+int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                                     void* out, int64_t B, int n_head, int n_kv_head, int head_dim, int64_t q_tok_stride,
+                                     int64_t out_tok_stride, int64_t num_blocks, int block_size, int64_t max_blocks_per_seq,
+                                     float scale, void* workspace, int64_t workspace_bytes, int32_t* err_count, int format,
+                                     int dtype, void* stream) {
+    if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
+    if (!valid_kv_format(format)) return SRA_ERR_ARG;
+    const int st = quant_attention_sizes(B, n_head, n_kv_head, head_dim, max_blocks_per_seq, block_size);
+    int64_t plane = 0;
+    if (st != SRA_OK || num_blocks < 0 || num_blocks > 0x7fffffff ||
+        !quant_plane(num_blocks, block_size, n_kv_head, format, head_dim, &plane))
+        return SRA_ERR_SHAPE;
+    const int64_t w = static_cast<int64_t>(n_head) * head_dim;
+    if (q_tok_stride < w || out_tok_stride < w) return SRA_ERR_STRIDE;
+    if (!std::isfinite(scale) || workspace_bytes < 0) return SRA_ERR_ARG;
+    if (B == 0) return SRA_OK;
+    if (!q || !kv_cache || !block_table || !seq_lens || !out) return SRA_ERR_NULL;
+    if (!aligned16(kv_cache)) return SRA_ERR_ARG;
+    const int es = elem_bytes(dtype);
+    const Span so = span_of(out, B, out_tok_stride, w, es), sc = span_of(kv_cache, 1, 0, 2 * plane, 1),
+               st_ = span_of(block_table, 1, 0, B * max_blocks_per_seq, 4), sl = span_of(seq_lens, 1, 0, B, 4);
+    if (rows_overlap(out, B, out_tok_stride, w, q, B, q_tok_stride, w, es) || overlap(so, sc) || overlap(so, st_) || overlap(so, sl))
+        return SRA_ERR_ALIAS;
+    QuantAttnPlan plan;
+    int dev = 0;
+    plan.num_sms = current_sm_count(&dev);
+    if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
+    plan.format = format;
+    plan.head_dim = head_dim;
+    plan.pdl = g_pdl;
+    QuantAttnArgs a;
+    a.q = q;
+    a.cache = kv_cache;
+    a.table = block_table;
+    a.seq_lens = seq_lens;
+    a.out = out;
+    a.err = err_count;
+    a.B = B;
+    a.qs = q_tok_stride;
+    a.os = out_tok_stride;
+    a.num_blocks = num_blocks;
+    a.max_blocks = max_blocks_per_seq;
+    a.plane_bytes = plane;
+    a.n_kv = n_kv_head;
+    a.group = n_head / n_kv_head;
+    a.block_size = block_size;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return status_from(launch_attention_quant(a, plan, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int sra_force_variant(const char* op, int variant) {

@@ -107,6 +107,38 @@ struct RopePlan {
 
 cudaError_t launch_rope_kv_store(const RopeArgs& a, const RopePlan& p, int dtype, cudaStream_t s);
 
+// ------------------------------------------------- a cache held in 4 or 8 bits (kv_format.cuh)
+enum KvFormat { KV_E2M1 = 0, KV_INT8 = 1 };
+inline bool valid_kv_format(int f) { return f == KV_E2M1 || f == KV_INT8; }
+inline SRA_HD int kv_row_bytes(int format, int head_dim) {
+    return (format == KV_E2M1 ? head_dim / 2 : head_dim) + head_dim / 16;
+}
+
+struct KvQuantPlan {
+    int format;
+    int style = 0;         // store: 0 = neox, 1 = interleaved
+    bool qk_norm = false;  // store: UClip Q and K heads before rotating
+    bool wide;             // 16-byte accesses of the tensors of `dtype`
+    bool pdl;
+    int num_sms;
+};
+
+// RopeArgs::cache: [2, num_blocks, n_kv, block_size, row bytes]
+cudaError_t launch_rope_kv_store_quant(const RopeArgs& a, const KvQuantPlan& p, int dtype, cudaStream_t s);
+
+struct KvReadArgs {
+    const void* cache;
+    const int32_t* table;   // [rows, max_blocks]
+    const int32_t* cu;      // [rows + 1]
+    const int32_t* starts;  // [rows], nullable: 0
+    void* k;                // [total, n_kv, head_dim], token strides ks, vs
+    void* v;
+    int32_t* err;
+    int64_t rows, max_blocks, num_blocks, total, ks, vs, plane_bytes;
+    int n_kv, head_dim, block_size;
+};
+cudaError_t launch_kv_quant_read(const KvReadArgs& a, const KvQuantPlan& p, int dtype, cudaStream_t s);
+
 // ------------------------------------------------------------------- GLU
 struct GluArgs {
     const void* gate_up;  // [T, 2I]
@@ -188,6 +220,25 @@ size_t decode_attention_tma_smem(int head_dim);
 constexpr int kMaxGsplits = 256;
 int decode_attention_gsplits(int64_t B, int n_kv, int64_t max_blocks, int block_size, int num_sms);
 int64_t decode_attention_ws_bytes(int64_t B, int n_kv, int head_dim, int gsplits);
+
+// Decode attention over a cache held in 4 or 8 bits.
+struct QuantAttnArgs {
+    const void* q;            // [B, n_head, head_dim] of the dtype, token stride qs
+    const void* cache;        // [2, num_blocks, n_kv, block_size, row bytes]
+    const int32_t* table;     // [B, max_blocks]
+    const int32_t* seq_lens;  // [B]
+    void* out;                // [B, n_head, head_dim] of the dtype, token stride os
+    int32_t* err;             // nullable
+    int64_t B, qs, os, num_blocks, max_blocks, plane_bytes;
+    int n_kv, group, block_size;
+    float scale_log2;  // softmax scale * log2(e)
+};
+struct QuantAttnPlan {
+    int format, head_dim;
+    bool pdl;
+    int num_sms;
+};
+cudaError_t launch_attention_quant(const QuantAttnArgs& a, const QuantAttnPlan& p, int dtype, cudaStream_t s);
 
 // ------------------------------------------------------------------- shared prefix
 // The requests' own tokens: tiles of kTailTok tokens of all requests in a row, cut into parts for the
@@ -300,6 +351,7 @@ constexpr int kMaxCacheList = 128;
 struct CacheList {
     void* p[kMaxCacheList];  // [2, num_blocks, block_size, n_kv, head_dim] each
     int n;
+    bool by_head;  // bytes [2, num_blocks, n_kv, block_size, row]: the first tokens of a page are no run of its bytes
     int64_t page_bytes;   // one page of one plane
     int64_t plane_bytes;  // num_blocks pages
 };

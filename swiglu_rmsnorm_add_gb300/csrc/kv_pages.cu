@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kCols) resize_assign_kernel(CacheList c, Resiz
             Pair p{a.ws_from[i], 0, 0};
             if (p.src >= 0 && served(i)) {
                 p.dst = a.ws_free[a.ws_first[i]];
-                p.bytes = a.ws_old[i] % a.block_size * token_bytes;
+                p.bytes = c.by_head ? c.page_bytes : a.ws_old[i] % a.block_size * token_bytes;
             }
             return p;
         });

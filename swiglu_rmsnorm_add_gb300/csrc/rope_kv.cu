@@ -22,17 +22,10 @@
 // ulps of the RESULT even under cancellation; one RNE to the dtype follows.
 #include "common.cuh"
 #include "internal.h"
+#include "rope_math.cuh"
 
 namespace sra {
 namespace rope {
-
-// a * b - c * d, accurate to a few ulps of the result (W. Kahan).
-__device__ __forceinline__ float diff_of_products(float a, float b, float c, float d) {
-    const float w = c * d;
-    const float e = fmaf(-c, d, w);  // w - c * d, exactly
-    const float f = fmaf(a, b, -w);
-    return f + e;
-}
 
 // The per-channel parameters of the dimensions a task's lo[j] / hi[j] hold:
 // neox lo = i0 + j, hi = h + i0 + j; interleaved lo = 2 (i0 + j), hi = lo + 1.
@@ -63,12 +56,6 @@ __device__ __forceinline__ void load_pair_params(const float* p, int i0, int h, 
             for (int q = 0; q < CW; ++q) lo[j + q] = fl[q], hi[j + q] = fh[q];
         }
     }
-}
-
-// clamp(a x, lo, hi) * g in fp32; a NaN product takes the lower bound (fmaxf
-// returns its non-NaN operand), as in the separate UClip kernel.
-__device__ __forceinline__ float uclip1(float x, float a, float g, float lo, float hi) {
-    return fminf(fmaxf(a * x, lo), hi) * g;
 }
 
 // One Q or K task: unpack the two accesses (r0, r1) into the pair halves, UClip
