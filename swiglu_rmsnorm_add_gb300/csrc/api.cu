@@ -713,7 +713,7 @@ int sra_version(void) { return SRA_VERSION; }
 
 int sra_last_cuda_error(void) { return g_last_cuda_error; }
 
-unsigned int sra_wait_timeouts(void) { return linear_wait_timeouts() + attn_wait_timeouts() + prefix_wait_timeouts(); }
+unsigned int sra_wait_timeouts(void) { return linear_wait_timeouts() + attn_wait_timeouts() + prefix_wait_timeouts() + quant_attn_wait_timeouts(); }
 
 int sra_wait_selftest(int32_t* result, void* stream) {
     if (!result) return SRA_ERR_NULL;
@@ -2074,6 +2074,10 @@ int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const 
     plan.format = format;
     plan.head_dim = head_dim;
     plan.pdl = g_pdl;
+    const int64_t pairs = B * n_kv_head, part = 32 * static_cast<int64_t>(quant_attn_warps(format, head_dim));
+    plan.splits = 1;
+    while (plan.splits < 16 && pairs * plan.splits <= plan.num_sms && max_blocks_per_seq * block_size >= 2 * part * plan.splits)
+        plan.splits *= 2;
     QuantAttnArgs a;
     a.q = q;
     a.cache = kv_cache;
@@ -2091,6 +2095,7 @@ int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const 
     a.group = n_head / n_kv_head;
     a.block_size = block_size;
     a.scale_log2 = scale * 1.4426950408889634f;
+    a.wide_q = aligned16(q) && stride_aligned16(q_tok_stride, es);
     return status_from(launch_attention_quant(a, plan, dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -2,123 +2,621 @@
 //
 //   o = sum_t softmax_t(scale * q . K_t) V_t over a request's tokens, K_t and V_t the values that the cache holds.
 //
-// A CTA takes a (request, kv head) pair, 16 tokens at a time: codes become fp32 in shared memory, a thread takes
-// a (query head, token) score, the running maximum and sum of the softmax are kept for each head, and the threads
-// that own output columns add p V.
+// A CTA takes a (request, kv head) pair, or a split of it, 32 tokens (a tile) a warp at a time. A head's rows of a page
+// lie in a row, so a tile is one to four bulk copies for K and as many for V into the warp's own ring in shared
+// memory; the warp that reads a stage asks for its next tile, and waits for nobody else.
+//
+// Codes become fp16 in registers, in the layout of the matrix instruction's operand: a value times its scale is an fp16
+// number exactly, so this is one conversion (or byte permutation) and one multiplication for two values, and nothing is
+// rounded. The products have the tokens (S^T = K Q^T) or the dims (O^T = V^T P^T) as their 16 rows and the up to eight
+// query heads as their eight columns. V's operand holds two tokens' values of a dim side by side: for e2m1 the
+// nibbles of two tokens are merged first (four bitwise operations for 16 values) and one conversion then makes the pair.
+// Which dims and tokens a lane takes is free, as long as both sides of a product agree: a lane's K is one scale group of
+// 16 dims in a row, its V a run of head_dim / 8 dims of four tokens in a row.
+//
+// q is fp16, or bf16 / fp32 times a power of two that takes its row's largest element to [2^14, 2^15) (elements below 2^-39
+// of it are lost); fp32 goes in as three fp16 numbers. Probabilities are fp16 at 2^14 times their size relative to the running
+// maximum (normal numbers down to 2^-28 of the largest), rounded once, 2^-11 of each; two fp16 numbers for fp32. Sums, maxima
+// and outputs are fp32; for fp32 each tile's products are added to them by ordinary additions, because the matrix
+// instruction's own accumulation truncates.
+//
+// The splits of a pair are the CTAs of a cluster, which merge through distributed shared memory.
+#include <cooperative_groups.h>
+
 #include "kv_format.cuh"
+#include "tma.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace sra {
 namespace qattn {
 
-constexpr int kThreads = 128, kTok = 16;
+constexpr int kTile = 32;     // tokens of a warp's tile
+constexpr float kUnder = 14;  // the probabilities' base lies 2^14 under the maximum
 
+template <int FMT, int HD>
+struct Shape {
+    static constexpr int R = kvq::row_bytes(FMT, HD), CODES = kvq::code_bytes(FMT, HD);
+    static constexpr int STAGE = 2 * kTile * R;  // bytes of a stage: K rows, V rows
+    static constexpr int STAGES = FMT == KV_E2M1 && HD == 64 ? 4 : 3;
+    // warps per CTA and CTAs per SM: what the rings leave of an SM's shared memory
+    static constexpr int WARPS = STAGE <= 4608 ? 8 : 4;
+    static constexpr int CTAS = FMT == KV_INT8 && HD == 256 ? 1 : 2;
+    static constexpr int KS = HD / 16;  // steps of 16 dims
+};
+__host__ __device__ constexpr int up16(int n) { return (n + 15) / 16 * 16; }
+template <typename T> constexpr int kQParts = sizeof(T) == 4 ? 3 : 1;
+template <typename T> constexpr int kPParts = sizeof(T) == 4 ? 2 : 1;
+template <typename T, int HD> constexpr bool kQShared = sizeof(T) == 4 || HD == 256;  // q's fragments in shared memory
+
+// Shared memory: rings, then q's fragments, barriers and masks. The merge runs over the drained rings: the warps'
+// partial outputs [WARPS][8][HD + 4] and statistics, then the CTA's result.
 template <typename T, int FMT, int HD>
-__global__ void __launch_bounds__(kThreads) decode_kernel(QuantAttnArgs a) {
-    constexpr int R = kvq::row_bytes(FMT, HD), CODES = kvq::code_bytes(FMT, HD), WORDS = FMT == KV_E2M1 ? 1 : 2;
-    constexpr int COLS = HD > kThreads ? HD / kThreads : 1;
-    __shared__ float qs[8][HD], ks[kTok][HD + 1], vs[kTok][HD], ps[8][kTok], m_run[8], l_run[8], corr[8];
-    pdl_enter();
-    const int64_t b = blockIdx.x / a.n_kv;
-    const int kvh = static_cast<int>(blockIdx.x - b * a.n_kv), G = a.group, BS = a.block_size;
-    int64_t len = a.seq_lens[b];
-    const int64_t cap = a.max_blocks * BS;
-    if ((len < 0 || len > cap) && kvh == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
-    len = len < 0 ? 0 : (len > cap ? cap : len);
-    for (int i = threadIdx.x; i < G * HD; i += kThreads)
-        qs[i / HD][i % HD] = to_f32(static_cast<const T*>(a.q)[b * a.qs + static_cast<int64_t>(kvh) * G * HD + i]);
-    if (threadIdx.x < 8) m_run[threadIdx.x] = -INFINITY, l_run[threadIdx.x] = 0.0f;
-    float acc[8][COLS];
+struct Mem {
+    using S = Shape<FMT, HD>;
+    static constexpr int ring = S::WARPS * S::STAGES * S::STAGE;
+    static constexpr int q_at = ring;
+    static constexpr int factor_at = q_at + (kQShared<T, HD> ? kQParts<T> * S::KS * 32 * 8 : 0);
+    static constexpr int bar_at = factor_at + 8 * 4;
+    static constexpr int mask_at = bar_at + S::WARPS * S::STAGES * 8;
+    static constexpr int total = up16(mask_at + S::WARPS * S::STAGES * 4);
+    static constexpr int HS = HD + 4;  // floats between heads
+    static constexpr int part_ml = S::WARPS * 8 * HS * 4;
+    static constexpr int res_ml = part_ml + S::WARPS * 16 * 4;
+    static constexpr int res_o = res_ml + 16 * 4;
+    static_assert(res_o + 8 * HD * 4 <= ring, "the merge fits over the rings");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) {
+    __half2 h;
+    memcpy(&h, &v, 4);
+    return __half22float2(h);
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {  // an 8 x 8 matrix of 16-bit values, a row's pairs over four lanes
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A bulk copy of a page's rows (16-byte aligned on both sides, a multiple of 16 bytes) that completes on `bar`.
+__device__ __forceinline__ void copy_rows(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// N words from shared memory at a multiple of ALIGN bytes.
+template <int N, int ALIGN>
+__device__ __forceinline__ void words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (ALIGN % 8 == 0 && N % 2 == 0) {
 #pragma unroll
-    for (int g = 0; g < 8; ++g)
+        for (int i = 0; i < N; i += 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * i);
+            w[i] = v.x, w[i + 1] = v.y;
+        }
+    } else {
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) acc[g][c] = 0.0f;
-    for (int64_t t0 = 0; t0 < len; t0 += kTok) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * kTok * (HD / 8); i += kThreads) {
-            const int plane = i / (kTok * (HD / 8)), rest = i - plane * kTok * (HD / 8);
-            const int t = rest / (HD / 8), d = (rest - t * (HD / 8)) * 8;
-            const int64_t tok = t0 + t;
-            const int32_t page = tok < len ? a.table[b * a.max_blocks + tok / BS] : -1;
-            const bool ok = page >= 0 && page < a.num_blocks;
-            if (!ok && tok < len && tok % BS == 0 && i == t * (HD / 8) && kvh == 0 && a.err) atomicAdd(a.err, 1);
-            uint32_t v[4] = {0, 0, 0, 0};
-            if (ok) {
-                const uint8_t* row = static_cast<const uint8_t*>(a.cache) + plane * a.plane_bytes +
-                                     ((static_cast<int64_t>(page) * a.n_kv + kvh) * BS + tok % BS) * R;
-                uint32_t w[WORDS];
+        for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+    }
+}
+// Byte i (a constant once unrolled) of e2m1 codes, or bytes 2 (i & 1) and 2 (i & 1) + 1 of flipped integers, as two fp16 numbers.
+__device__ __forceinline__ uint32_t e2m1_byte(uint32_t w, int i) {
+    return i == 0 ? kvq::e2m1_pair<0>(w) : i == 1 ? kvq::e2m1_pair<1>(w) : i == 2 ? kvq::e2m1_pair<2>(w) : kvq::e2m1_pair<3>(w);
+}
+__device__ __forceinline__ uint32_t int8_half(uint32_t w, int i) { return i == 0 ? kvq::int8_pair<0, 1>(w) : kvq::int8_pair<2, 3>(w); }
+
+// Q as B fragments: step e = 4 j + i holds dims 64 j + 16 ft + 4 i + {0, 1} (b0) and {2, 3} (b1) of head fg.
+template <typename T, int HD>
+struct Query {
+    static constexpr int KS = HD / 16, QP = kQParts<T>;
+    uint32_t reg[kQShared<T, HD> ? 1 : KS][2];
+    const uint2* shared;
+    float factor[2];  // of the scores of heads 2 ft and 2 ft + 1: the softmax scale in base 2 and q's power of two
+
+    // Every warp loads it into its registers or, where it is kept in shared memory, warp 0 into that (the CTA's barrier and
+    // shared_factors() follow).
+    __device__ __forceinline__ void load(const T* row, bool there, bool wide, float scale_log2, uint2* keep, float* factors,
+                                         int warp, int lane) {
+        const int fg = lane >> 2, ft = lane & 3;
+        shared = keep + lane;
+        if (kQShared<T, HD> && warp != 0) return;
+        float x[HD / 4];
 #pragma unroll
-                for (int j = 0; j < WORDS; ++j) w[j] = reinterpret_cast<const uint32_t*>(row + d * WORDS / 2)[j];
-                kvq::decode8<FMT>(w, kvq::scale_pair(row[CODES + d / kvq::kGroup]), v);
+        for (int j = 0; j < HD / 64; ++j) {
+            const T* p = row + static_cast<int64_t>(fg) * HD + 64 * j + 16 * ft;
+            if (!there) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[16 * j + k] = 0.0f;
+            } else if (wide) {
+                constexpr int V = vec16<T>();
+#pragma unroll
+                for (int k = 0; k < 16; k += V) {
+                    float f[V];
+                    Vec<T, V>::unpack(Vec<T, V>::load(p + k), f);
+#pragma unroll
+                    for (int c = 0; c < V; ++c) x[16 * j + k + c] = f[c];
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[16 * j + k] = to_f32(p[k]);
             }
-            float* dst = plane ? &vs[t][d] : &ks[t][d];
+        }
+        float back = 1.0f;
+        if constexpr (!std::is_same_v<T, __half>) {
+            float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                __half2 h;
-                memcpy(&h, &v[j], 4);
-                const float2 f = __half22float2(h);
-                dst[2 * j] = f.x, dst[2 * j + 1] = f.y;
+            for (int k = 0; k < HD / 4; ++k) {
+                const float a = fabsf(x[k]);
+                top = a < INFINITY ? fmaxf(top, a) : top;
             }
-        }
-        __syncthreads();
-        const int g = threadIdx.x / kTok, t = threadIdx.x % kTok;
-        const int64_t tok = t0 + t;
-        bool valid = tok < len && g < G;
-        if (valid) {
-            const int32_t page = a.table[b * a.max_blocks + tok / BS];
-            valid = page >= 0 && page < a.num_blocks;
-        }
-        float s = -INFINITY;
-        if (valid) {
-            float d0 = 0.0f;
-            for (int d = 0; d < HD; ++d) d0 = fmaf(qs[g][d], ks[t][d], d0);
-            s = d0 * a.scale_log2;
-        }
-        float mx = s;
-        for (int o = kTok / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m_old = m_run[g], m_new = fmaxf(m_old, mx);
-        // (no score above -inf yet: those weigh nothing; a NaN stays one)
-        const float p = valid ? exp2f(s - (m_new == -INFINITY ? 0.0f : m_new)) : 0.0f;
-        float sum = p;
-        for (int o = kTok / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        __syncwarp();
-        ps[g][t] = p;
-        if (t == 0) {
-            const float c = m_new == -INFINITY ? 1.0f : exp2f(m_old - m_new);
-            corr[g] = c;
-            l_run[g] = l_run[g] * c + sum;
-            m_run[g] = m_new;
-        }
-        __syncthreads();
-        const int n = static_cast<int>(len - t0 < kTok ? len - t0 : kTok);
-        for (int gg = 0; gg < G; ++gg)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127: 0 or subnormal
+            const int up = top == 0.0f ? 0 : min(14 - e, 126);
+            const float to = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-                const int d = threadIdx.x + c * kThreads;
-                if (d < HD) {
-                    float x = acc[gg][c] * corr[gg];
-                    for (int k = 0; k < n; ++k) x = fmaf(ps[gg][k], vs[k][d], x);
-                    acc[gg][c] = x;
+            for (int k = 0; k < HD / 4; ++k) x[k] *= to;
+        }
+#pragma unroll
+        for (int part = 0; part < QP; ++part)
+#pragma unroll
+            for (int e = 0; e < KS; ++e) {
+                float* y = x + 4 * e;
+                const uint32_t b0 = pack_h2(y[0], y[1]), b1 = pack_h2(y[2], y[3]);
+                if constexpr (kQShared<T, HD>) keep[(part * KS + e) * 32 + lane] = make_uint2(b0, b1);
+                else reg[e][0] = b0, reg[e][1] = b1;
+                if constexpr (QP > 1) {  // what is left (nothing of infinities and NaN)
+                    const float2 f0 = unpack_h2(b0), f1 = unpack_h2(b1);
+                    const float f[4] = {f0.x, f0.y, f1.x, f1.y};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = fabsf(f[k]) < INFINITY ? y[k] - f[k] : 0.0f;
                 }
             }
+        const float f = back * scale_log2;
+        if constexpr (kQShared<T, HD>) {
+            if (ft == 0) factors[fg] = f;
+        } else {
+            factor[0] = __shfl_sync(0xffffffffu, f, 8 * ft);
+            factor[1] = __shfl_sync(0xffffffffu, f, 8 * ft + 4);
+        }
+    }
+    __device__ __forceinline__ void shared_factors(const float* factors, int lane) {
+        factor[0] = factors[2 * (lane & 3)], factor[1] = factors[2 * (lane & 3) + 1];
+    }
+    __device__ __forceinline__ uint2 get(int part, int e) const {
+        if constexpr (kQShared<T, HD>) return shared[(part * KS + e) * 32];
+        else return make_uint2(reg[e][0], reg[e][1]);
+    }
+};
+
+// S^T of a tile: lane (fg, ft) gets the scores of tokens 16 u + 4 (fg / 2) + fg % 2 (k < 2) and those two further (k >= 2) for heads
+// 2 ft + k % 2 in s[u][k].
+template <typename T, int FMT, int HD>
+__device__ __forceinline__ void scores(const uint8_t* kt, const Query<T, HD>& q, float (&s)[2][4], int lane) {
+    using S = Shape<FMT, HD>;
+    constexpr int WORDS = FMT == KV_E2M1 ? 2 : 4, KS = S::KS;  // words of a group of 16 codes
+    const int fg = lane >> 2, ft = lane & 3;
+    const uint8_t* r0 = kt + (4 * (fg >> 1) + (fg & 1)) * S::R;
+    float fine[2][4];  // fp32: the products with the lower parts of q
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[u][k] = fine[u][k] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < HD / 64; ++j) {
+        uint32_t w[2][2][WORDS], sc[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* r = r0 + (16 * u + 2 * h) * S::R;
+                words<WORDS, S::R>(r + (ft + 4 * j) * WORDS * 4, w[u][h]);
+                sc[u][h] = kvq::scale_pair(r[S::CODES + ft + 4 * j]);
+                if constexpr (FMT == KV_INT8) {
+#pragma unroll
+                    for (int i = 0; i < WORDS; ++i) w[u][h][i] ^= 0x80808080u;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 b = q.get(0, 4 * j + i);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t a[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        a[h + 2 * c] = kvq::mul2(FMT == KV_E2M1 ? e2m1_byte(w[u][h][i >> 1], (2 * i + c) & 3)
+                                                                : int8_half(w[u][h][i], c),
+                                                 sc[u][h]);
+                if constexpr (sizeof(T) == 4) {
+                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma(part, a, b.x, b.y);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s[u][k] += part[k];
+                    const uint2 b1 = q.get(1, 4 * j + i), b2 = q.get(2, 4 * j + i);
+                    mma(fine[u], a, b1.x, b1.y);
+                    mma(fine[u], a, b2.x, b2.y);
+                } else {
+                    mma(s[u], a, b.x, b.y);
+                }
+            }
+        }
+    }
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[u][k] += fine[u][k];
+    }
+}
+
+// The running softmax over those scores (valid: a bit per token): maxima m of the lane's two heads, this lane's tokens' part l of
+// their sums, corr = 2^(old m - new m); the probabilities, relative to 2^(m - kUnder), as l, as B fragments of the next
+// product.
+template <int PP>
+__device__ __forceinline__ void softmax(float (&p)[2][4], unsigned valid, const float (&factor)[2], float (&m)[2], float (&l)[2],
+                                        float (&corr)[2], uint32_t (&pb)[PP][2][2], int lane) {
+    const unsigned FULL = 0xffffffffu;
+    const int fg = lane >> 2;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[u][k] *= factor[k & 1];
+    if (valid != FULL) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (!((valid >> (16 * u + 4 * (fg >> 1) + (fg & 1) + (k & 2))) & 1u)) p[u][k] = -INFINITY;
+    }
+    float mx[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) mx[h] = fmaxf(fmaxf(p[0][h], p[0][h + 2]), fmaxf(p[1][h], p[1][h + 2]));
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+        const float a = __shfl_xor_sync(FULL, mx[0], x), b = __shfl_xor_sync(FULL, mx[1], x);
+        mx[0] = fmaxf(mx[0], a), mx[1] = fmaxf(mx[1], b);
+    }
+    float base[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float now = fmaxf(m[h], mx[h]);
+        base[h] = now == -INFINITY ? 0.0f : now - kUnder;  // (no score above -inf yet: those weigh nothing)
+        corr[h] = now == -INFINITY ? 1.0f : ex2(m[h] - now);
+        m[h] = now;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[u][k] = ex2(p[u][k] - base[k & 1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t hi = pack_h2(p[u][2 * c], p[u][2 * c + 1]);
+            pb[0][u][c] = transpose8(hi);
+            if constexpr (PP > 1) {
+                const float2 f = unpack_h2(hi);
+                pb[1][u][c] = transpose8(pack_h2(p[u][2 * c] - f.x, p[u][2 * c + 1] - f.y));
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) l[h] = fmaf(l[h], corr[h], (p[0][h] + p[0][h + 2]) + (p[1][h] + p[1][h + 2]));
+}
+
+// O^T = O^T corr + V^T P^T: o[d] holds dim fg * HD / 8 + 2 d (k < 2) and the next one (k >= 2) of heads 2 ft + k % 2. Tokens that
+// do not count get a scale of 0.
+template <typename T, int FMT, int HD>
+__device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[kPParts<T>][2][2], const float (&corr)[2],
+                                       unsigned valid, float (&o)[HD / 16][4], int lane) {
+    using S = Shape<FMT, HD>;
+    constexpr int RUN = HD / 8;                         // dims of a lane
+    constexpr int PER = FMT == KV_E2M1 ? 8 : 4;         // codes in a word
+    constexpr int WORDS = RUN / PER;
+    constexpr int GROUPS = RUN > kvq::kGroup ? RUN / kvq::kGroup : 1;
+    const int fg = lane >> 2, ft = lane & 3;
+    if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) o[d][0] *= corr[0], o[d][1] *= corr[1], o[d][2] *= corr[0], o[d][3] *= corr[1];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const uint8_t* r0 = vt + (16 * u + 4 * ft) * S::R;
+        uint32_t w[4][WORDS], sc[2][GROUPS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) words<WORDS, S::R>(r0 + i * S::R + fg * WORDS * 4, w[i]);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const int at = S::CODES + fg * RUN / kvq::kGroup + g;
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                b[i] = r0[i * S::R + at];
+                if (valid != 0xffffffffu && !((valid >> (16 * u + 4 * ft + i)) & 1u)) b[i] = 0;
+            }
+            sc[0][g] = (b[0] | b[1] << 16) << 7;
+            sc[1][g] = (b[2] | b[3] << 16) << 7;
+        }
+#pragma unroll
+        for (int c = 0; c < WORDS; ++c) {
+            const uint32_t* s2[2] = {&sc[0][c * PER / kvq::kGroup], &sc[1][c * PER / kvq::kGroup]};
+            // pair[e][k]: tokens 2 e and 2 e + 1, the codes of dims k of this word (a byte, or a half, a pair)
+            uint32_t even[2], odd[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t x = w[2 * e][c], y = w[2 * e + 1][c];
+                if constexpr (FMT == KV_E2M1) {
+                    even[e] = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
+                    odd[e] = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+                } else {
+                    even[e] = __byte_perm(x, y, 0x6240) ^ 0x80808080u;  // x0 y0 x2 y2
+                    odd[e] = __byte_perm(x, y, 0x7351) ^ 0x80808080u;   // x1 y1 x3 y3
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < PER / 2; ++k) {
+                uint32_t a[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    a[2 * e] = kvq::mul2(FMT == KV_E2M1 ? e2m1_byte(even[e], k) : int8_half(even[e], k), *s2[e]);
+                    a[2 * e + 1] = kvq::mul2(FMT == KV_E2M1 ? e2m1_byte(odd[e], k) : int8_half(odd[e], k), *s2[e]);
+                }
+                const int d = c * (PER / 2) + k;
+                if constexpr (sizeof(T) == 4) {
+                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma(part, a, pb[kPParts<T> - 1][u][0], pb[kPParts<T> - 1][u][1]);
+                    mma(part, a, pb[0][u][0], pb[0][u][1]);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) o[d][n] += part[n];
+                } else {
+                    mma(o[d], a, pb[0][u][0], pb[0][u][1]);
+                }
+            }
+        }
+    }
+}
+
+// Tiles [t0, t1) of a pair. Leaves the CTA's maxima and sums (res_ml) and unnormalised output (res_o) in shared memory.
+template <typename T, int FMT, int HD>
+__device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* smem, int64_t b, int kvh, int len, int t0, int t1,
+                                        uint32_t* turn) {
+    using S = Shape<FMT, HD>;
+    using M = Mem<T, FMT, HD>;
+    constexpr int W = S::WARPS, ST = S::STAGES;
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, fg = lane >> 2, ft = lane & 3;
+    const int G = a.group, bs_log2 = __ffs(a.block_size) - 1, per_tile = kTile >> bs_log2;
+    const uint32_t page_bytes = static_cast<uint32_t>(S::R) << bs_log2;
+    unsigned char* ring = smem + warp * ST * S::STAGE;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + M::bar_at) + warp * ST;
+    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + M::mask_at) + warp * ST;
+    const uint8_t* cache = static_cast<const uint8_t*>(a.cache) + static_cast<int64_t>(kvh) * page_bytes;
+    const int64_t page_step = static_cast<int64_t>(a.n_kv) * page_bytes;
+    const int32_t* table = a.table + b * a.max_blocks;
+    const int pages = (len + a.block_size - 1) >> bs_log2;
+
+    // Lane k < per_tile has the entry of page k of a tile; asked for a tile ahead of the copies.
+    auto entry = [&](int t) -> int32_t {
+        const int j = t * per_tile + lane;
+        return t < t1 && lane < per_tile && j < pages ? __ldg(table + j) : -1;
+    };
+    auto issue = [&](int t, int32_t page, int stage) {
+        const bool used = lane < per_tile && t * per_tile + lane < pages;
+        const bool ok = page >= 0 && page < a.num_blocks;  // (-1 where unused)
+        if (used && !ok && kvh == 0 && a.err) atomicAdd(a.err, 1);
+        const unsigned good = __ballot_sync(FULL, ok);
+        if (lane == 0) {
+            const int left = len - t * kTile;
+            uint32_t m = 0;
+            for (int k = 0; k < per_tile; ++k)
+                if ((good >> k) & 1u) m |= (a.block_size == 32 ? FULL : (1u << a.block_size) - 1u) << (k << bs_log2);
+            mask[stage] = left >= kTile ? m : m & ((1u << left) - 1u);
+            mbar_arrive_expect_tx(bar + stage, 2 * page_bytes * __popc(good));
+        }
+        __syncwarp();
+        if (ok) {
+            const uint32_t dst = smem_u32(ring + stage * S::STAGE) + lane * page_bytes;
+            const uint8_t* src = cache + page * page_step;
+            copy_rows(dst, src, page_bytes, bar + stage);
+            copy_rows(dst + kTile * S::R, src + a.plane_bytes, page_bytes, bar + stage);
+        }
+    };
+
+    int32_t page[ST];
+#pragma unroll
+    for (int s = 0; s < ST; ++s) page[s] = entry(t0 + warp + s * W);
+    int32_t next = entry(t0 + warp + ST * W);
+    // q's fragments come in while the first tiles do
+    Query<T, HD> q;
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+        if (t0 + warp + s * W < t1) issue(t0 + warp + s * W, page[s], s);
+    {
+        const T* row = static_cast<const T*>(a.q) + b * a.qs + static_cast<int64_t>(kvh) * G * HD;
+        float* factors = reinterpret_cast<float*>(smem + M::factor_at);
+        q.load(row, fg < G, a.wide_q, a.scale_log2, reinterpret_cast<uint2*>(smem + M::q_at), factors, warp, lane);
+        if constexpr (kQShared<T, HD>) {
+            __syncthreads();
+            q.shared_factors(factors, lane);
+        }
+    }
+    float o[HD / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.0f;
+    int stage = 0;
+    uint32_t phase = *turn;  // parity of the stages' next phases, a bit each
+    for (int t = t0 + warp; t < t1; t += W) {
+        mbar_wait(bar + stage, (phase >> stage) & 1u);
+        phase ^= 1u << stage;
+        const unsigned valid = mask[stage];
+        const uint8_t* kt = ring + stage * S::STAGE;
+        float s[2][4], corr[2];
+        uint32_t pb[kPParts<T>][2][2];
+        scores<T, FMT, HD>(kt, q, s, lane);
+        softmax<kPParts<T>>(s, valid, q.factor, m, l, corr, pb, lane);
+        values<T, FMT, HD>(kt + kTile * S::R, pb, corr, valid, o, lane);
+        __syncwarp();  // every lane is done with the stage
+        const int32_t p = next;
+        next = entry(t + (ST + 1) * W);
+        if (t + ST * W < t1) issue(t + ST * W, p, stage);
+        stage = stage + 1 == ST ? 0 : stage + 1;
+    }
+    *turn = phase;
+    // the warps' parts
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+        l[0] += __shfl_xor_sync(FULL, l[0], x);
+        l[1] += __shfl_xor_sync(FULL, l[1], x);
+    }
+    __syncthreads();  // all rings are drained
+    float* po = reinterpret_cast<float*>(smem) + warp * 8 * M::HS;
+    float* ml = reinterpret_cast<float*>(smem + M::part_ml);
+    if (fg == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) ml[warp * 16 + 2 * ft + h] = m[h], ml[warp * 16 + 8 + 2 * ft + h] = l[h];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float* row = po + (2 * ft + h) * M::HS + fg * (HD / 8);
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) *reinterpret_cast<float2*>(row + 2 * d) = make_float2(o[d][h], o[d][2 + h]);
     }
     __syncthreads();
-    for (int g = 0; g < G; ++g)
+    float* res = reinterpret_cast<float*>(smem + M::res_ml);
+    float* ro = reinterpret_cast<float*>(smem + M::res_o);
+    const float* all = reinterpret_cast<const float*>(smem);
+    for (int i = threadIdx.x; i < G * HD; i += W * 32) {
+        const int g = i / HD, d = i - g * HD;
+        float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) {
-            const int d = threadIdx.x + c * kThreads;
-            if (d < HD)
-                static_cast<T*>(a.out)[b * a.os + (static_cast<int64_t>(kvh) * G + g) * HD + d] =
-                    from_f32<T>(l_run[g] != 0.0f ? acc[g][c] / l_run[g] : 0.0f);
+        for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * 16 + g]);
+        float sum = 0.0f, acc = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float lw = ml[w * 16 + 8 + g];
+            // (a part without scores above -inf has a sum of 0, or NaN)
+            const float f = ml[w * 16 + g] == -INFINITY ? 1.0f : ex2(ml[w * 16 + g] - top);
+            sum = fmaf(f, lw, sum);
+            acc = fmaf(f, all[w * 8 * M::HS + g * M::HS + d], acc);
         }
+        ro[i] = acc;
+        if (d == 0) res[g] = top, res[8 + g] = sum;
+    }
+}
+
+template <typename T, int FMT, int HD>
+__global__ void __launch_bounds__(Shape<FMT, HD>::WARPS * 32, Shape<FMT, HD>::CTAS) cluster_kernel(QuantAttnArgs a) {
+    using S = Shape<FMT, HD>;
+    using M = Mem<T, FMT, HD>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int64_t pair = blockIdx.x / splits, b = pair / a.n_kv;
+    const int kvh = static_cast<int>(pair - b * a.n_kv), G = a.group;
+    if (threadIdx.x < S::WARPS * S::STAGES) {
+        mbar_init(reinterpret_cast<uint64_t*>(smem + M::bar_at) + threadIdx.x, 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    pdl_enter();
+    int64_t n = a.seq_lens[b];
+    const int64_t cap = a.max_blocks * a.block_size;
+    if ((n < 0 || n > cap) && kvh == 0 && rank == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
+    const int len = static_cast<int>(n < 0 ? 0 : (n > cap ? cap : n));
+    const int tiles = (len + kTile - 1) / kTile, per = (tiles + splits - 1) / splits;
+    const int t0 = min(rank * per, tiles), t1 = min(t0 + per, tiles);
+    uint32_t turn = 0;
+    segment<T, FMT, HD>(a, smem, b, kvh, len, t0, t1, &turn);
+    T* out = static_cast<T*>(a.out) + b * a.os + static_cast<int64_t>(kvh) * G * HD;
+    const float* res = reinterpret_cast<const float*>(smem + M::res_ml);
+    const float* ro = reinterpret_cast<const float*>(smem + M::res_o);
+    if (splits == 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < G * HD; i += S::WARPS * 32) {
+            const float l = res[8 + i / HD];
+            out[i] = from_f32<T>(l != 0.0f ? ro[i] / l : 0.0f);
+        }
+        return;
+    }
+    cluster.sync();
+    const int slice = (G * HD + splits - 1) / splits, i0 = rank * slice, i1 = min(i0 + slice, G * HD);
+    for (int i = i0 + threadIdx.x; i < i1; i += S::WARPS * 32) {
+        const int g = i / HD;
+        float top = -INFINITY, sum = 0.0f, acc = 0.0f;
+        for (int r = 0; r < splits; ++r) top = fmaxf(top, cluster.map_shared_rank(res, r)[g]);
+        for (int r = 0; r < splits; ++r) {
+            const float* o = cluster.map_shared_rank(res, r);
+            const float f = o[g] == -INFINITY ? 1.0f : ex2(o[g] - top);
+            sum = fmaf(f, o[8 + g], sum);
+            acc = fmaf(f, o[16 + i], acc);
+        }
+        out[i] = from_f32<T>(sum != 0.0f ? acc / sum : 0.0f);
+    }
+    cluster.sync();  // nobody reads this CTA's part any more
+}
+
+template <typename T, int FMT, int HD>
+cudaError_t launch_cluster(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
+    using M = Mem<T, FMT, HD>;
+    auto kernel = cluster_kernel<T, FMT, HD>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = set_smem_once(kernel, M::total, true, &done);
+    if (e != cudaSuccess) return e;
+    if (p.splits > 8) {
+        static std::atomic<uint64_t> wide{0};
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+        if (!(wide.load(std::memory_order_acquire) & bit)) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            wide.fetch_or(bit, std::memory_order_release);
+        }
+    }
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(a.B * a.n_kv * p.splits)), dim3(Shape<FMT, HD>::WARPS * 32), M::total, s,
+                         p.pdl, p.splits, a);
 }
 
 template <typename T, int FMT>
 cudaError_t launch(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
-    auto kernel = p.head_dim == 64 ? decode_kernel<T, FMT, 64> : p.head_dim == 128 ? decode_kernel<T, FMT, 128> : decode_kernel<T, FMT, 256>;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(a.B * a.n_kv)), dim3(kThreads), 0, s, p.pdl, 1, a);
+    switch (p.head_dim) {
+        case 64: return launch_cluster<T, FMT, 64>(a, p, s);
+        case 128: return launch_cluster<T, FMT, 128>(a, p, s);
+        default: return launch_cluster<T, FMT, 256>(a, p, s);
+    }
 }
 
 }  // namespace qattn
+
+int quant_attn_warps(int format, int head_dim) {
+    return 2 * qattn::kTile * kv_row_bytes(format, head_dim) <= 4608 ? 8 : 4;  // Shape::WARPS
+}
+
+unsigned int quant_attn_wait_timeouts() {
+    unsigned int n = 0;
+    if (cudaMemcpyFromSymbol(&n, g_wait_timeouts, sizeof(n)) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
 
 cudaError_t launch_attention_quant(const QuantAttnArgs& a, const QuantAttnPlan& p, int dtype, cudaStream_t s) {
     using namespace qattn;

@@ -232,13 +232,17 @@ struct QuantAttnArgs {
     int64_t B, qs, os, num_blocks, max_blocks, plane_bytes;
     int n_kv, group, block_size;
     float scale_log2;  // softmax scale * log2(e)
+    bool wide_q;       // 16-byte aligned query rows
 };
 struct QuantAttnPlan {
     int format, head_dim;
+    int splits;  // CTAs per (request, kv head): the cluster size
     bool pdl;
     int num_sms;
 };
 cudaError_t launch_attention_quant(const QuantAttnArgs& a, const QuantAttnPlan& p, int dtype, cudaStream_t s);
+int quant_attn_warps(int format, int head_dim);  // per CTA
+unsigned int quant_attn_wait_timeouts();
 
 // ------------------------------------------------------------------- shared prefix
 // The requests' own tokens: tiles of kTailTok tokens of all requests in a row, cut into parts for the

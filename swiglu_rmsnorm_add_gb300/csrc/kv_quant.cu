@@ -6,10 +6,9 @@
 // pairs, V as 16 dims in a row. In the neox pairing a K task holds half of two groups, whose other halves the
 // neighbouring thread has (one shuffle each); otherwise a task is a group.
 //
-// K's rotation is rounded to the dtype correctly: the product difference is kept as a sum of two fp32 numbers and
-// rounded to odd before the one rounding to 16 bits. A code can hang on the last place of its value, and with
-// this the cache's bytes follow from the definition, whoever evaluates it. (Q is rotated exactly as
-// sra_rope_kv_store does it.)
+// K's rotation is the correctly rounded fp32 number (the product difference is kept as a sum of two fp32 numbers), rounded
+// once more to the dtype. A code can hang on the last place of its value, and with this the cache's bytes
+// follow from the definition, whoever evaluates it. (Q is rotated exactly as sra_rope_kv_store does it.)
 //
 // Read. A CTA takes a tile of output tokens, finds each one's row of the cache once, and its threads turn eight codes
 // into one 16-byte store (two in fp32).
@@ -21,29 +20,14 @@ namespace kvq {
 
 constexpr int kThreads = 256;
 
-// a * c - b * s as hi + lo, hi the nearest fp32 number (relative error of the sum about 2^-46 of the products).
-__device__ __forceinline__ void rotate_exact(float a, float c, float b, float s, float* hi, float* lo) {
+// The fp32 number nearest to a * c - b * s (of a sum that is known to about 2^-46 of the products).
+__device__ __forceinline__ float rotate_exact(float a, float c, float b, float s) {
     const float p = a * c, q = b * s;
     const float ep = fmaf(a, c, -p), eq = fmaf(b, s, -q);
     const float d = p - q, bb = d - p;
     const float e = (p - (d - bb)) + (-q - bb);  // p - q = d + e, exactly (Knuth's two-sum)
-    const float l = e + (ep - eq);
-    *hi = d + l;
-    *lo = l - (*hi - d);
+    return d + (e + (ep - eq));
 }
-// hi + lo rounded once to T, as fp32. For 16 bits through the fp32 neighbour whose last bit is odd: what lies
-// strictly between two fp32 numbers can then not be taken for a tie.
-template <typename T>
-__device__ __forceinline__ float round_sum(float hi, float lo) {
-    if constexpr (sizeof(T) == 4) {
-        return hi;
-    } else {
-        uint32_t b = __float_as_uint(hi);
-        if (lo != 0.0f && !(b & 1u)) b += (lo > 0.0f) == (hi > 0.0f) ? 1u : ~0u;
-        return round_trip<T>(__uint_as_float(b));
-    }
-}
-
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, bool wide, float (&f)[8]) {
     if (wide) {
@@ -166,11 +150,8 @@ __global__ void __launch_bounds__(kThreads) store_kernel(RopeArgs a, int tokens_
                             y0 = rope::diff_of_products(lo, c[j], hi, s[j]);
                             y1 = rope::diff_of_products(hi, c[j], -lo, s[j]);
                         } else {
-                            float u0, l0, u1, l1;
-                            rotate_exact(lo, c[j], hi, s[j], &u0, &l0);
-                            rotate_exact(hi, c[j], -lo, s[j], &u1, &l1);
-                            y0 = round_sum<T>(u0, l0);
-                            y1 = round_sum<T>(u1, l1);
+                            y0 = round_trip<T>(rotate_exact(lo, c[j], hi, s[j]));
+                            y1 = round_trip<T>(rotate_exact(hi, c[j], -lo, s[j]));
                         }
                         lo = y0, hi = y1;
                     }

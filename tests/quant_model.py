@@ -91,3 +91,8 @@ def rotated(x: np.ndarray, c: np.ndarray, s: np.ndarray, style: str) -> np.ndarr
     y[..., a] = x[..., a] * c - x[..., b] * s
     y[..., b] = x[..., b] * c + x[..., a] * s
     return y
+
+
+def held_k(x, c, s, style, dtype):
+    """The rotated K that is quantised: rounded to fp32, and from there to the dtype."""
+    return rounded(rounded(rotated(x, c, s, style), torch.float32), dtype)

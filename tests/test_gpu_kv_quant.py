@@ -50,7 +50,7 @@ def want_store(before, k, v, cos, sin, pos, slot, fmt, style, dtype, norm=None, 
     P = cos.shape[0]
     ok = (pos >= 0) & (pos < P)
     p = np.where(ok, pos, 0)
-    kk = qm.rounded(qm.rotated(kk, cos.double().numpy()[p], sin.double().numpy()[p], style), dtype)
+    kk = qm.held_k(kk, cos.double().numpy()[p], sin.double().numpy()[p], style, dtype)
     rows = qm.encode(kk, fmt), qm.encode(f64(v), fmt)
     for t in range(len(pos)):
         if ok[t] and 0 <= slot[t] < nb * bs:

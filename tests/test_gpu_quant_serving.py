@@ -36,8 +36,8 @@ class Server:
         """A token for each (row, pos) at its slot, in every layer; the rows' models grow by them."""
         for layer, cache in enumerate(self.caches):
             q, k, v = self.qkv(len(rows))
-            kk = qm.rounded(qm.rotated(k.double().cpu().numpy(), self.cos.double().cpu().numpy()[pos.cpu()],
-                                       self.sin.double().cpu().numpy()[pos.cpu()], "neox"), self.dtype)
+            kk = qm.held_k(k.double().cpu().numpy(), self.cos.double().cpu().numpy()[pos.cpu()],
+                           self.sin.double().cpu().numpy()[pos.cpu()], "neox", self.dtype)
             new = np.stack([qm.encode(kk, self.fmt), qm.encode(v.double().cpu().numpy(), self.fmt)])
             sra.rope_kv_store_quant(q, k, v, self.cos, self.sin, pos, slot, cache)
             for i, r in enumerate(rows):
