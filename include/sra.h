@@ -790,7 +790,9 @@ SRA_API int sra_set_pdl(int enable);
  * decode-batch projection kernel of the fused entry points, up to 16 rows: variant 0,
  * OR-ed with (s << 8), s in 1..8, forces the CTAs of its cluster along K),
  * "shared_prefix" (0 = a decode call per request, 1 = the prefix for all requests at once, given a
- * workspace; it also sets what sra_shared_prefix_workspace_size answers).
+ * workspace; it also sets what sra_shared_prefix_workspace_size answers), "decode_attention_quant" (0 = a
+ * cluster of CTAs for each (request, kv head), 1 = the batch as one stream of tiles, given a workspace; it also sets
+ * what sra_paged_decode_attention_quant_workspace_size answers).
  * variant: -1 = automatic per-shape choice (the default); otherwise an index
  * < sra_variant_count(op), optionally OR-ed with (nv << 8) to also force the
  * number of 16-byte accesses each thread holds in the register variants of
@@ -812,7 +814,7 @@ SRA_API const char* sra_variant_name(const char* op, int variant);
  * rope_kv_store: a = T, b = n_head, c = n_kv_head, d = head_dim; glu: a = T, b = I,
  * c = act (0 = SiLU, 1 = ReLU);
  * decode_attention: a = B, b = n_head, c = n_kv_head, d = head_dim ("linear",
- * "linear_narrow" and "shared_prefix" have no pick: SRA_ERR_ARG).
+ * "linear_narrow", "shared_prefix" and "decode_attention_quant" have no pick: SRA_ERR_ARG).
  * Negative sra_status on bad arguments. Enqueues nothing.
  */
 SRA_API int sra_pick_variant(const char* op, int64_t a, int64_t b, int64_t c, int64_t d, int dtype,

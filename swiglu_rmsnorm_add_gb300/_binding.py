@@ -976,6 +976,23 @@ def shared_prefix_attention(q: torch.Tensor, kv_cache: torch.Tensor, prefix_tabl
 
 
 # ------------------------------------------------------------------- a cache held in 4 or 8 bits
+# The checks of these calls come twice, as those of the page operators: all in one cheap test, and one by one where it fails.
+_U8, _I64, _F32 = torch.uint8, torch.int64, torch.float32
+_FORMAT_OF = {(hd, hd * (1 + code) // 2 + hd // 16): code for hd in (64, 128, 256) for code in (0, 1)}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call_on(dev: int, fn: str, *args) -> None:
+    """A C call with that device current."""
+    if _current_device() == dev:
+        st = getattr(_lib or lib(), fn)(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib(), fn)(*args)
+    if st != 0:
+        _check(fn, st)
+
+
 def _row_bytes(fmt: str, head_dim: int) -> int:
     if fmt not in KV_FORMAT:
         raise ValueError("fmt must be 'e2m1' (4 bits) or 'int8'")
@@ -993,22 +1010,37 @@ def quant_kv_cache(num_blocks: int, block_size: int, n_kv_head: int, head_dim: i
     return torch.zeros(shape if layers is None else (layers, *shape), dtype=torch.uint8, device=device)
 
 
-def _quant_cache(kv_cache, head_dim, n_kv=None):
+def _quant_cache(kv_cache, head_dim):
     """(num_blocks, n_kv_head, block_size, format code) of a quantised cache; the format follows from its rows' bytes."""
-    _cuda(kv_cache, "kv_cache")
-    if kv_cache.dtype is not torch.uint8 or kv_cache.dim() != 5 or kv_cache.shape[0] != 2 or not kv_cache.is_contiguous():
+    if not isinstance(kv_cache, torch.Tensor) or not kv_cache.is_cuda:
+        _cuda(kv_cache, "kv_cache")
+    if kv_cache.dtype is not _U8 or kv_cache.dim() != 5 or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous uint8 [2, num_blocks, n_kv_head, block_size, row_bytes]")
-    _, nb, kv, bs, row = kv_cache.shape
-    if head_dim not in (64, 128, 256):
-        raise ValueError("head_dim must be 64, 128 or 256")
-    for code in (0, 1):
-        if row == (head_dim * (1 + code)) // 2 + head_dim // 16:
-            break
-    else:
-        raise ValueError(f"kv_cache: rows of {row} bytes hold no {head_dim} values in 4 or 8 bits")
-    if n_kv is not None and kv != n_kv:
-        raise ValueError("shape mismatch")
-    return nb, kv, bs, code
+    planes, nb, n_kv, bs, row = kv_cache.shape
+    code = _FORMAT_OF.get((head_dim, row))
+    if planes != 2:
+        raise ValueError("kv_cache must be contiguous uint8 [2, num_blocks, n_kv_head, block_size, row_bytes]")
+    if code is None:
+        raise ValueError(f"kv_cache: rows of {row} bytes hold no {head_dim} values in 4 or 8 bits (of 64, 128 or 256)")
+    return nb, n_kv, bs, code
+
+
+def _heads_ok(t, dev, shape, dtype) -> bool:
+    """Whether t is a contiguous [T, heads, head_dim] of that shape and dtype."""
+    return isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape \
+        and t.is_contiguous()
+
+
+def _heads_stride(t, dev, shape, dtype, name) -> int:
+    """The token stride of a [T, heads, head_dim] view of that shape and dtype."""
+    _cuda(t, name)
+    if t.get_device() != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"shape mismatch: {name} must be {list(shape)}")
+    return _tok_stride(t, name)
 
 
 def rope_kv_store_quant(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
@@ -1017,46 +1049,57 @@ def rope_kv_store_quant(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: 
                         style: str = "neox", qk_uclip=None, clip: tuple[float, float] = (-1.0, 1.0)) -> None:
     """rope_kv_store into a cache held in 4 or 8 bits (quant_kv_cache): q is rotated in place as there; the rotated k,
     rounded to its dtype, and v are quantised into their slots."""
-    if style not in ROPE_STYLE:
-        raise ValueError("style must be 'neox' or 'interleaved'")
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (cos, "cos"), (sin, "sin"), (pos, "pos"), (slot_mapping, "slot_mapping")):
-        _cuda(t, n)
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k and v must be [T, heads, head_dim]")
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        _cuda(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, n_head, head_dim]")
+    dev, dtype = q.get_device(), q.dtype
     T, n_head, hd = q.shape
-    n_kv = k.shape[1]
-    nb, _, bs, fmt = _quant_cache(kv_cache, hd, n_kv)
-    params = (None,) * 4 if qk_uclip is None else tuple(qk_uclip)
-    _same_device(q, k, v, cos, sin, pos, slot_mapping, kv_cache, *params)
-    if not (k.dtype == v.dtype == q.dtype):
-        raise ValueError("q, k and v must share one dtype")
-    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or not cos.is_contiguous() or not sin.is_contiguous():
-        raise ValueError("cos and sin must be contiguous float32 [max_pos, head_dim // 2]")
-    if pos.dtype != torch.int64 or slot_mapping.dtype != torch.int64 or not pos.is_contiguous() \
-            or not slot_mapping.is_contiguous():
-        raise ValueError("pos and slot_mapping must be contiguous int64")
-    if k.shape != (T, n_kv, hd) or v.shape != (T, n_kv, hd) or pos.numel() != T or slot_mapping.numel() != T:
-        raise ValueError("shape mismatch")
+    nb, n_kv, bs, fmt = _quant_cache(kv_cache, hd)
+    kv_shape = (T, n_kv, hd)
+    qs, ks = n_head * hd, n_kv * hd
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if kv_cache.get_device() != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
+    vs = ks
+    if not (_heads_ok(k, dev, kv_shape, dtype) and _heads_ok(v, dev, kv_shape, dtype) and q.is_contiguous()):
+        qs = _tok_stride(q, "q")
+        ks = _heads_stride(k, dev, kv_shape, dtype, "k")
+        vs = _heads_stride(v, dev, kv_shape, dtype, "v")
+    for t, n in ((pos, "pos"), (slot_mapping, "slot_mapping")):
+        if not (isinstance(t, torch.Tensor) and t.dtype is _I64 and t.get_device() == dev and t.numel() == T
+                and t.is_contiguous()):
+            _int64_out(t, n, T, dev)
+    rows = cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() else 0
+    for t, n in ((cos, "cos"), (sin, "sin")):
+        if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.get_device() == dev and t.shape == (rows, hd // 2)
+                and t.is_contiguous()):
+            _cuda(t, n)
+            if t.get_device() != dev:
+                raise ValueError("all tensors must be on the same CUDA device")
+            raise ValueError("cos and sin must be contiguous float32 [max_pos, head_dim // 2]")
     if max_pos is None:
-        max_pos = cos.shape[0]
-    if cos.dim() != 2 or cos.shape[-1] != hd // 2 or sin.shape != cos.shape or max_pos > cos.shape[0]:
+        max_pos = rows
+    elif max_pos > rows:
         raise ValueError("cos / sin tables must be [>= max_pos, head_dim // 2]")
+    params = (None, None, None, None)
     if qk_uclip is not None:
+        params = tuple(qk_uclip)
         if len(params) != 4:
             raise ValueError("qk_uclip is (q_alpha, q_gamma, k_alpha, k_gamma)")
         for t, n in zip(params, ("q_alpha", "q_gamma", "k_alpha", "k_gamma")):
             _cuda(t, n)
             if t.dtype != torch.float32 or t.numel() != hd or not t.is_contiguous():
                 raise ValueError(f"{n} must be a contiguous float32 tensor of head_dim entries")
-    dev = q.get_device()
-    with _on(dev):
-        st = lib().sra_rope_kv_store_quant(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(),
-            slot_mapping.data_ptr(), kv_cache.data_ptr(), T, n_head, n_kv, hd, _tok_stride(q, "q"), _tok_stride(k, "k"),
-            _tok_stride(v, "v"), int(max_pos), nb, bs, _err_ptr(err_count, dev), ROPE_STYLE[style],
-            *(t.data_ptr() if t is not None else None for t in params), float(clip[0]), float(clip[1]), fmt, _dtype(q),
-            _stream(q, stream))
-    _check("sra_rope_kv_store_quant", st)
+        _same_device(q, *params)
+        params = tuple(t.data_ptr() for t in params)
+    if style not in ROPE_STYLE:
+        raise ValueError("style must be 'neox' or 'interleaved'")
+    _call_on(dev, "sra_rope_kv_store_quant", q.data_ptr(), k.data_ptr(), v.data_ptr(), cos.data_ptr(), sin.data_ptr(),
+             pos.data_ptr(), slot_mapping.data_ptr(), kv_cache.data_ptr(), T, n_head, n_kv, hd, qs, ks, vs, max_pos, nb, bs,
+             None if err_count is None else _err_ptr(err_count, dev), ROPE_STYLE[style], *params, clip[0], clip[1], fmt,
+             DTYPE_CODE[dtype], _stream(q, stream))
 
 
 def read_kv_quant(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_lens: torch.Tensor, total: int, head_dim: int,
@@ -1075,27 +1118,33 @@ def read_kv_quant(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_lens: to
     rows, mb = block_table.shape
     if cu_lens.numel() != rows + 1:
         raise ValueError("cu_lens must have one entry more than block_table has rows")
+    sp = None
     if starts is not None:
         _int32(starts, "starts", 1, dev)
         if starts.numel() != rows:
             raise ValueError("starts must have one entry per row of block_table")
+        sp = starts.data_ptr()
+    ks = vs = n_kv * head_dim
     if out is None:
         if dtype not in DTYPE_CODE:
             raise ValueError(f"unsupported dtype {dtype}")
-        shape = (int(total), n_kv, head_dim)
-        out = tuple(_result(stream, dev, lambda: torch.empty(shape, dtype=dtype, device=kv_cache.device)) for _ in "kv")
-    k, v = out
-    for t, n in ((k, "k"), (v, "v")):
-        _cuda(t, n)
-        if t.shape != (total, n_kv, head_dim) or t.dtype != k.dtype:
-            raise ValueError("the results must be [total, n_kv_head, head_dim] of one dtype")
-    _same_device(kv_cache, k, v)
-    with _on(dev):
-        st = lib().sra_kv_quant_read(kv_cache.data_ptr(), block_table.data_ptr(), cu_lens.data_ptr(),
-                                     starts.data_ptr() if starts is not None else None, k.data_ptr(), v.data_ptr(), rows,
-                                     mb, int(total), n_kv, head_dim, _tok_stride(k, "k"), _tok_stride(v, "v"), nb, bs,
-                                     _err_ptr(err_count, dev), fmt, _dtype(k), _stream(kv_cache, stream))
-    _check("sra_kv_quant_read", st)
+        shape = (total, n_kv, head_dim)
+        if stream is None:
+            k, v = (torch.empty(shape, dtype=dtype, device=kv_cache.device),
+                    torch.empty(shape, dtype=dtype, device=kv_cache.device))
+        else:
+            k, v = (_result(stream, dev, lambda: torch.empty(shape, dtype=dtype, device=kv_cache.device)) for _ in "kv")
+    else:
+        k, v = out
+        _cuda(k, "k")
+        dtype = k.dtype
+        if dtype not in DTYPE_CODE:
+            raise ValueError(f"unsupported dtype {dtype}")
+        shape = (total, n_kv, head_dim)
+        ks, vs = _heads_stride(k, dev, shape, dtype, "k"), _heads_stride(v, dev, shape, dtype, "v")
+    _call_on(dev, "sra_kv_quant_read", kv_cache.data_ptr(), block_table.data_ptr(), cu_lens.data_ptr(), sp, k.data_ptr(),
+             v.data_ptr(), rows, mb, total, n_kv, head_dim, ks, vs, nb, bs,
+             None if err_count is None else _err_ptr(err_count, dev), fmt, DTYPE_CODE[dtype], _stream(kv_cache, stream))
     return k, v
 
 
@@ -1121,27 +1170,36 @@ def paged_decode_attention_quant(q: torch.Tensor, kv_cache: torch.Tensor, block_
 
     q: [B, n_head, head_dim]; block_table: int32 [B, max_blocks]; seq_lens: int32 [B]; scale defaults to
     1 / sqrt(head_dim). workspace: from decode_attention_quant_workspace, or None."""
-    _cuda(q, "q")
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        _cuda(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [B, n_head, head_dim]")
-    dev, (B, n_head, hd) = q.get_device(), q.shape
+    dev, dtype = q.get_device(), q.dtype
+    shape = q.shape
+    B, n_head, hd = shape
     nb, n_kv, bs, fmt = _quant_cache(kv_cache, hd)
     _int32(block_table, "block_table", 2, dev)
     _int32(seq_lens, "seq_lens", 1, dev)
+    rows, mb = block_table.shape
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if kv_cache.get_device() != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if rows != B or seq_lens.numel() != B:
+        raise ValueError("shape mismatch: block_table and seq_lens must have a row for each of q")
+    qs = os_ = n_head * hd
+    if not q.is_contiguous():
+        qs = _tok_stride(q, "q")
     if out is None:
-        out = _result(stream, dev, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
-    _cuda(out, "out")
-    _same_device(q, kv_cache, out)
-    if out.shape != q.shape or out.dtype != q.dtype or block_table.shape[0] != B or seq_lens.numel() != B:
-        raise ValueError("shape mismatch")
+        out = torch.empty(shape, dtype=dtype, device=q.device) if stream is None else \
+            _result(stream, dev, lambda: torch.empty(shape, dtype=dtype, device=q.device))
+    elif not _heads_ok(out, dev, shape, dtype):
+        os_ = _heads_stride(out, dev, shape, dtype, "out")
     wp, wb = None, 0
     if workspace is not None:
         workspace, wp, wb = _workspace_args(workspace, None, dev, stream)
-    with _on(dev):
-        st = lib().sra_paged_decode_attention_quant(
-            q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), B, n_head, n_kv,
-            hd, _tok_stride(q, "q"), _tok_stride(out, "out"), nb, bs, block_table.shape[1],
-            float(scale) if scale is not None else 1.0 / float(hd) ** 0.5, wp, wb, _err_ptr(err_count, dev), fmt, _dtype(q),
-            _stream(q, stream))
-    _check("sra_paged_decode_attention_quant", st)
+    _call_on(dev, "sra_paged_decode_attention_quant", q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+             seq_lens.data_ptr(), out.data_ptr(), B, n_head, n_kv, hd, qs, os_, nb, bs, mb,
+             hd ** -0.5 if scale is None else scale, wp, wb, None if err_count is None else _err_ptr(err_count, dev), fmt,
+             DTYPE_CODE[dtype], _stream(q, stream))
     return out

@@ -20,7 +20,7 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
 std::atomic<int> g_smem_optin[kMaxDevices];
 std::atomic<int> g_force_norm{-1}, g_force_rope{-1}, g_force_glu{-1}, g_force_attn{-1}, g_force_lin{-1},
-    g_force_narrow{-1}, g_force_prefix{-1};
+    g_force_narrow{-1}, g_force_prefix{-1}, g_force_quant_attn{-1};
 thread_local bool g_pdl = false;  // programmatic dependent launch for this thread's calls
 thread_local int g_force_nv = 0;  // accesses per thread forced for A/B measurement (0 = planner's)
 thread_local int g_force_g = 0;   // warps per row forced for warps_row A/B measurement (0 = planner's)
@@ -547,6 +547,7 @@ std::atomic<int>* force_slot(const char* op) {
     if (std::strcmp(op, "glu") == 0) return &g_force_glu;
     if (std::strcmp(op, "decode_attention") == 0) return &g_force_attn;
     if (std::strcmp(op, "shared_prefix") == 0) return &g_force_prefix;
+    if (std::strcmp(op, "decode_attention_quant") == 0) return &g_force_quant_attn;
     if (std::strcmp(op, "linear") == 0) return &g_force_lin;
     if (std::strcmp(op, "linear_narrow") == 0) return &g_force_narrow;
     return nullptr;
@@ -558,6 +559,7 @@ int variant_count(const char* op) {
     if (std::strcmp(op, "rope_kv_store") == 0) return ROPE_NUM_VARIANTS;
     if (std::strcmp(op, "glu") == 0) return GLU_NUM_VARIANTS;
     if (std::strcmp(op, "shared_prefix") == 0) return 2;
+    if (std::strcmp(op, "decode_attention_quant") == 0) return 2;  // a cluster for each pair, the batch as one stream
     if (std::strcmp(op, "decode_attention") == 0) return 3;  // CUDA cores, mma.sync, mma.sync fed by TMA
     if (std::strcmp(op, "linear") == 0) return 2;            // mma.sync, tcgen05 (projection over h)
     if (std::strcmp(op, "linear_narrow") == 0) return 1;     // the decode-batch kernel (K split forced)
@@ -1907,7 +1909,9 @@ int sra_rope_kv_store_quant(void* q, const void* k, const void* v, const float* 
     if (norm && (std::isnan(clip_min) || std::isnan(clip_max) || clip_min > clip_max)) return SRA_ERR_ARG;
     int64_t plane = 0;
     if (T < 0 || n_head <= 0 || n_kv_head <= 0 || n_head % n_kv_head != 0 || n_head > (1 << 20) || !quant_head_dim(head_dim) ||
-        block_size <= 0 || num_blocks < 0 || max_pos < 0 || !quant_plane(num_blocks, block_size, n_kv_head, format, head_dim, &plane))
+        block_size <= 0 || num_blocks < 0 || max_pos < 0 ||
+        !quant_plane(num_blocks, block_size, n_kv_head, format, head_dim, &plane) ||
+        T > (int64_t(1) << 38) / ((n_head + 2 * static_cast<int64_t>(n_kv_head)) * (head_dim / 16)))  // tasks of 256-thread CTAs
         return SRA_ERR_SHAPE;
     const int64_t qw = static_cast<int64_t>(n_head) * head_dim, kw = static_cast<int64_t>(n_kv_head) * head_dim;
     if (q_tok_stride < qw || k_tok_stride < kw || v_tok_stride < kw) return SRA_ERR_STRIDE;
@@ -2000,7 +2004,6 @@ int sra_kv_quant_read(const void* kv_cache, const int32_t* block_table, const in
     if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
     plan.format = format;
     plan.pdl = g_pdl;
-    plan.wide = aligned16(k) && aligned16(v) && stride_aligned16(k_tok_stride, es) && stride_aligned16(v_tok_stride, es);
     KvReadArgs a;
     a.cache = kv_cache;
     a.table = block_table;
@@ -2035,13 +2038,32 @@ int quant_attention_sizes(int64_t B, int n_head, int n_kv_head, int head_dim, in
                : SRA_OK;
 }
 
+// CTAs of the stream form (0: the cluster form), and its workspace: the sums, then two records a CTA.
+int quant_stream_ctas(int64_t B, int n_kv, int64_t tokens, int format, int head_dim, int num_sms) {
+    const int forced = g_force_quant_attn.load(std::memory_order_relaxed);
+    if (forced == 0) return 0;
+    const int ctas = num_sms * quant_attn_ctas_per_sm(format, head_dim);
+    // (a thread sums B / 256 requests; the tiles of a kv head are counted in 32 bits)
+    if (B > 65536 || B * ((tokens + 31) / 32) > 0x7fffffff) return 0;
+    return ctas;
+}
+int64_t quant_stream_at_bytes(int64_t B) { return round_up256((B + 1) * 4); }
+int64_t quant_stream_bytes(int64_t B, int ctas, int head_dim) {
+    return ctas > 0 ? quant_stream_at_bytes(B) + static_cast<int64_t>(ctas) * 2 * (16 + 8 * head_dim) * 4 : 0;
+}
+
 }  // namespace
 
 int64_t sra_paged_decode_attention_quant_workspace_size(int64_t B, int n_head, int n_kv_head, int head_dim,
                                                         int64_t max_blocks_per_seq, int block_size, int format, int dtype) {
     if (!valid_dtype(dtype)) return SRA_ERR_DTYPE;
     if (!valid_kv_format(format)) return SRA_ERR_ARG;
-    return quant_attention_sizes(B, n_head, n_kv_head, head_dim, max_blocks_per_seq, block_size);
+    const int st = quant_attention_sizes(B, n_head, n_kv_head, head_dim, max_blocks_per_seq, block_size);
+    if (st != SRA_OK || B == 0) return st;
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
+    if (sms <= 0) return SRA_ERR_DEVICE;
+    return quant_stream_bytes(B, quant_stream_ctas(B, n_kv_head, max_blocks_per_seq * block_size, format, head_dim, sms), head_dim);
 }
 
 int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
@@ -2079,6 +2101,21 @@ int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const 
     while (plan.splits < 16 && pairs * plan.splits <= plan.num_sms && max_blocks_per_seq * block_size >= 2 * part * plan.splits)
         plan.splits *= 2;
     QuantAttnArgs a;
+    plan.stream_ctas = 0;
+    const int ctas = quant_stream_ctas(B, n_kv_head, max_blocks_per_seq * block_size, format, head_dim, plan.num_sms);
+    if (workspace && ctas > 0) {
+        const int64_t need = quant_stream_bytes(B, ctas, head_dim);
+        if (workspace_bytes < need || !aligned16(workspace)) return SRA_ERR_ARG;
+        const Span sws = span_of(workspace, 1, 0, need, 1);
+        if (overlap(sws, so) || overlap(sws, sc) || overlap(sws, st_) || overlap(sws, sl) ||
+            overlap(sws, span_of(q, B, q_tok_stride, w, es)))
+            return SRA_ERR_ALIAS;
+        plan.stream_ctas = ctas;
+        a.ws_at = static_cast<int32_t*>(workspace);
+        a.ws_rec = reinterpret_cast<float*>(static_cast<char*>(workspace) + quant_stream_at_bytes(B));
+    } else if (g_force_quant_attn.load(std::memory_order_relaxed) == 1) {
+        return SRA_ERR_VARIANT;
+    }
     a.q = q;
     a.cache = kv_cache;
     a.table = block_table;
@@ -2118,6 +2155,7 @@ const char* sra_variant_name(const char* op, int variant) {
     static const char* const attn_names[] = {"cuda_cores", "mma_sync", "mma_sync_tma"};
     static const char* const lin_names[] = {"mma_sync", "tcgen05"};
     static const char* const prefix_names[] = {"decode", "batched"};
+    static const char* const quant_names[] = {"cluster", "stream"};
     static const char* const narrow_names[] = {"cluster_k_split"};
     const int n = variant_count(op);
     if (n < 0 || variant < 0 || variant >= n) return nullptr;
@@ -2125,6 +2163,7 @@ const char* sra_variant_name(const char* op, int variant) {
     if (std::strcmp(op, "rope_kv_store") == 0) return rope_names[variant];
     if (std::strcmp(op, "decode_attention") == 0) return attn_names[variant];
     if (std::strcmp(op, "shared_prefix") == 0) return prefix_names[variant];
+    if (std::strcmp(op, "decode_attention_quant") == 0) return quant_names[variant];
     if (std::strcmp(op, "linear") == 0) return lin_names[variant];
     if (std::strcmp(op, "linear_narrow") == 0) return narrow_names[variant];
     return glu_names[variant];

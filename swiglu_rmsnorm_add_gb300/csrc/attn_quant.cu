@@ -20,7 +20,8 @@
 // and outputs are fp32; for fp32 each tile's products are added to them by ordinary additions, because the matrix
 // instruction's own accumulation truncates.
 //
-// The splits of a pair are the CTAs of a cluster, which merge through distributed shared memory.
+// Without a workspace the splits of a pair are the CTAs of a cluster, which merge through distributed shared memory; with one the
+// batch is a stream of tiles cut into equal parts (stream_kernel), whose records a second kernel merges.
 #include <cooperative_groups.h>
 
 #include "kv_format.cuh"
@@ -34,11 +35,12 @@ namespace qattn {
 constexpr int kTile = 32;     // tokens of a warp's tile
 constexpr float kUnder = 14;  // the probabilities' base lies 2^14 under the maximum
 
-template <int FMT, int HD>
+template <typename T, int FMT, int HD>
 struct Shape {
     static constexpr int R = kvq::row_bytes(FMT, HD), CODES = kvq::code_bytes(FMT, HD);
     static constexpr int STAGE = 2 * kTile * R;  // bytes of a stage: K rows, V rows
-    static constexpr int STAGES = FMT == KV_E2M1 && HD == 64 ? 4 : 3;
+    // (fp32 queries' fragments take a stage's room)
+    static constexpr int STAGES = FMT == KV_E2M1 && HD == 64 ? 4 : FMT == KV_E2M1 && sizeof(T) == 4 ? 2 : 3;
     // warps per CTA and CTAs per SM: what the rings leave of an SM's shared memory
     static constexpr int WARPS = STAGE <= 4608 ? 8 : 4;
     static constexpr int CTAS = FMT == KV_INT8 && HD == 256 ? 1 : 2;
@@ -53,7 +55,7 @@ template <typename T, int HD> constexpr bool kQShared = sizeof(T) == 4 || HD == 
 // partial outputs [WARPS][8][HD + 4] and statistics, then the CTA's result.
 template <typename T, int FMT, int HD>
 struct Mem {
-    using S = Shape<FMT, HD>;
+    using S = Shape<T, FMT, HD>;
     static constexpr int ring = S::WARPS * S::STAGES * S::STAGE;
     static constexpr int q_at = ring;
     static constexpr int factor_at = q_at + (kQShared<T, HD> ? kQParts<T> * S::KS * 32 * 8 : 0);
@@ -208,8 +210,8 @@ struct Query {
 // 2 ft + k % 2 in s[u][k].
 template <typename T, int FMT, int HD>
 __device__ __forceinline__ void scores(const uint8_t* kt, const Query<T, HD>& q, float (&s)[2][4], int lane) {
-    using S = Shape<FMT, HD>;
-    constexpr int WORDS = FMT == KV_E2M1 ? 2 : 4, KS = S::KS;  // words of a group of 16 codes
+    using S = Shape<T, FMT, HD>;
+    constexpr int WORDS = FMT == KV_E2M1 ? 2 : 4;  // words of a group of 16 codes
     const int fg = lane >> 2, ft = lane & 3;
     const uint8_t* r0 = kt + (4 * (fg >> 1) + (fg & 1)) * S::R;
     float fine[2][4];  // fp32: the products with the lower parts of q
@@ -325,7 +327,7 @@ __device__ __forceinline__ void softmax(float (&p)[2][4], unsigned valid, const 
 template <typename T, int FMT, int HD>
 __device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[kPParts<T>][2][2], const float (&corr)[2],
                                        unsigned valid, float (&o)[HD / 16][4], int lane) {
-    using S = Shape<FMT, HD>;
+    using S = Shape<T, FMT, HD>;
     constexpr int RUN = HD / 8;                         // dims of a lane
     constexpr int PER = FMT == KV_E2M1 ? 8 : 4;         // codes in a word
     constexpr int WORDS = RUN / PER;
@@ -396,7 +398,7 @@ __device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[k
 template <typename T, int FMT, int HD>
 __device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* smem, int64_t b, int kvh, int len, int t0, int t1,
                                         uint32_t* turn) {
-    using S = Shape<FMT, HD>;
+    using S = Shape<T, FMT, HD>;
     using M = Mem<T, FMT, HD>;
     constexpr int W = S::WARPS, ST = S::STAGES;
     const unsigned FULL = 0xffffffffu;
@@ -414,19 +416,23 @@ __device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* s
     // Lane k < per_tile has the entry of page k of a tile; asked for a tile ahead of the copies.
     auto entry = [&](int t) -> int32_t {
         const int j = t * per_tile + lane;
-        return t < t1 && lane < per_tile && j < pages ? __ldg(table + j) : -1;
+        return t < t1 && lane < per_tile && j < pages ? __ldcg(table + j) : -1;
     };
+    const unsigned all_pages = FULL >> (32 - per_tile);
     auto issue = [&](int t, int32_t page, int stage) {
-        const bool used = lane < per_tile && t * per_tile + lane < pages;
-        const bool ok = page >= 0 && page < a.num_blocks;  // (-1 where unused)
-        if (used && !ok && kvh == 0 && a.err) atomicAdd(a.err, 1);
+        const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_blocks);  // (-1 where unused)
         const unsigned good = __ballot_sync(FULL, ok);
-        if (lane == 0) {
-            const int left = len - t * kTile;
-            uint32_t m = 0;
+        uint32_t count = FULL;
+        if (good != all_pages || len - t * kTile < kTile) {
+            count = 0;
             for (int k = 0; k < per_tile; ++k)
-                if ((good >> k) & 1u) m |= (a.block_size == 32 ? FULL : (1u << a.block_size) - 1u) << (k << bs_log2);
-            mask[stage] = left >= kTile ? m : m & ((1u << left) - 1u);
+                if ((good >> k) & 1u) count |= (FULL >> (32 - a.block_size)) << (k << bs_log2);
+            const int left = len - t * kTile;
+            if (left < kTile) count &= (1u << left) - 1u;
+            if (!ok && lane < per_tile && t * per_tile + lane < pages && kvh == 0 && a.err) atomicAdd(a.err, 1);
+        }
+        if (lane == 0) {
+            mask[stage] = count;
             mbar_arrive_expect_tx(bar + stage, 2 * page_bytes * __popc(good));
         }
         __syncwarp();
@@ -521,8 +527,8 @@ __device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* s
 }
 
 template <typename T, int FMT, int HD>
-__global__ void __launch_bounds__(Shape<FMT, HD>::WARPS * 32, Shape<FMT, HD>::CTAS) cluster_kernel(QuantAttnArgs a) {
-    using S = Shape<FMT, HD>;
+__global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, HD>::CTAS) cluster_kernel(QuantAttnArgs a) {
+    using S = Shape<T, FMT, HD>;
     using M = Mem<T, FMT, HD>;
     extern __shared__ __align__(128) unsigned char smem[];
     cg::cluster_group cluster = cg::this_cluster();
@@ -535,7 +541,7 @@ __global__ void __launch_bounds__(Shape<FMT, HD>::WARPS * 32, Shape<FMT, HD>::CT
     }
     __syncthreads();
     pdl_enter();
-    int64_t n = a.seq_lens[b];
+    int64_t n = __ldcg(a.seq_lens + b);
     const int64_t cap = a.max_blocks * a.block_size;
     if ((n < 0 || n > cap) && kvh == 0 && rank == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
     const int len = static_cast<int>(n < 0 ? 0 : (n > cap ? cap : n));
@@ -571,6 +577,200 @@ __global__ void __launch_bounds__(Shape<FMT, HD>::WARPS * 32, Shape<FMT, HD>::CT
     cluster.sync();  // nobody reads this CTA's part any more
 }
 
+// The whole batch as one stream of tiles (requests, their kv heads, their tiles), cut into equal parts for as many CTAs as
+// the GPU holds. A CTA writes the outputs of the pairs that it holds whole, and leaves a record [8 max][8 sum][8 x HD] of
+// the one that began before its part (slot 0) and of the one that goes on behind it (slot 1). Every CTA sums the
+// requests' tiles to find its part; CTA 0 leaves the sums for the merge.
+template <typename T, int FMT, int HD>
+__global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, HD>::CTAS) stream_kernel(QuantAttnArgs a) {
+    using S = Shape<T, FMT, HD>;
+    using M = Mem<T, FMT, HD>;
+    constexpr int NT = S::WARPS * 32;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int warp_sum[S::WARPS], found[2];
+    if (threadIdx.x == 0) found[0] = 0x7fffffff;
+    if (threadIdx.x < S::WARPS * S::STAGES) {
+        mbar_init(reinterpret_cast<uint64_t*>(smem + M::bar_at) + threadIdx.x, 1);
+        mbar_init_fence();
+    }
+    pdl_enter();
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = static_cast<int>(a.B), G = a.group;
+    const int64_t cap = a.max_blocks * a.block_size;
+    auto length = [&](int b) -> int {
+        if (b >= B) return 0;
+        const int64_t n = __ldcg(a.seq_lens + b);
+        return static_cast<int>(n < 0 ? 0 : (n > cap ? cap : n));
+    };
+    auto tiles_of = [](int len) { return (len + kTile - 1) / kTile; };
+    // thread t sums requests [t * each, (t + 1) * each)
+    const int each = (B + NT - 1) / NT, mine0 = threadIdx.x * each;
+    int mine = 0;
+    for (int k = 0; k < each; ++k) {
+        const int b = mine0 + k;
+        if (blockIdx.x == 0 && a.err && b < B) {
+            const int32_t n = __ldcg(a.seq_lens + b);
+            if (n < 0 || n > cap) atomicAdd(a.err, 1);
+        }
+        mine += tiles_of(length(b));
+    }
+    int inc = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int t = __shfl_up_sync(FULL, inc, x);
+        if (lane >= x) inc += t;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < S::WARPS; ++w) {
+        before += w < warp ? warp_sum[w] : 0;
+        total += warp_sum[w];
+    }
+    const int at0 = before + inc - mine;  // tiles before this thread's requests
+    // (tiles of all kv heads are counted in 64 bits)
+    const int64_t all = static_cast<int64_t>(total) * a.n_kv;
+    const int64_t part = stream_part(all, gridDim.x, S::WARPS);
+    if (blockIdx.x == 0) {
+        int at = at0;
+        for (int k = 0; k < each; ++k) {
+            if (mine0 + k < B) a.ws_at[mine0 + k] = at;
+            at += tiles_of(length(mine0 + k));
+        }
+        if (threadIdx.x == 0) a.ws_at[B] = total;
+    }
+    int64_t g0 = blockIdx.x * part;
+    const int64_t g1 = g0 + part < all ? g0 + part : all;
+    if (g0 >= g1) return;
+    // the request that tile g0 belongs to
+    {
+        int at = at0;
+        for (int k = 0; k < each; ++k) {
+            const int n = tiles_of(length(mine0 + k));
+            const int64_t lo = static_cast<int64_t>(at) * a.n_kv, hi = static_cast<int64_t>(at + n) * a.n_kv;
+            if (lo <= g0 && g0 < hi) found[0] = mine0 + k, found[1] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    int b = found[0];
+    int64_t begin = static_cast<int64_t>(found[1]) * a.n_kv;  // the request's first tile in the stream
+    uint32_t turn = 0;
+    int window = b, lens = length(b + lane);  // lane k: request window + k
+    while (g0 < g1 && b < B) {
+        if (b - window >= 32) window = b, lens = length(b + lane);
+        const int len = __shfl_sync(FULL, lens, b - window), n = tiles_of(len);
+        if (g0 >= begin + static_cast<int64_t>(n) * a.n_kv) {
+            begin += static_cast<int64_t>(n) * a.n_kv;
+            ++b;
+            continue;
+        }
+        const int kvh = static_cast<int>((g0 - begin) / n);
+        const int t0 = static_cast<int>(g0 - begin - static_cast<int64_t>(kvh) * n);
+        const int t1 = g1 - g0 < n - t0 ? t0 + static_cast<int>(g1 - g0) : n;
+        segment<T, FMT, HD>(a, smem, b, kvh, len, t0, t1, &turn);
+        __syncthreads();
+        const float* res = reinterpret_cast<const float*>(smem + M::res_ml);
+        const float* ro = reinterpret_cast<const float*>(smem + M::res_o);
+        if (t0 == 0 && t1 == n) {
+            T* out = static_cast<T*>(a.out) + b * a.os + static_cast<int64_t>(kvh) * G * HD;
+            for (int i = threadIdx.x; i < G * HD; i += NT) {
+                const float l = res[8 + i / HD];
+                out[i] = from_f32<T>(l != 0.0f ? ro[i] / l : 0.0f);
+            }
+        } else {
+            float* rec = a.ws_rec + (static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * (16 + 8 * HD);
+            for (int i = threadIdx.x; i < 16 + G * HD; i += NT) rec[i] = res[i];
+        }
+        g0 += t1 - t0;
+        fence_proxy_async();  // the merge's accesses come before the copies that fill the rings again
+        __syncthreads();
+    }
+}
+
+// out of a pair whose tiles several parts share, and zeros for a request without tokens. A CTA takes 256 / LANES columns; LANES
+// threads share a column's records. The sums meet in a fixed order.
+template <typename T, int HD, int LANES>
+__global__ void __launch_bounds__(256) merge_kernel(QuantAttnArgs a, int ctas, int warps) {
+    constexpr int COLS = 256 / LANES;
+    __shared__ float s_acc[LANES][COLS], s_sum[LANES][COLS], s_top[LANES][COLS];
+    pdl_enter();
+    const int chunks = (a.group * HD + COLS - 1) / COLS;
+    const int64_t pair = blockIdx.x / chunks, b = pair / a.n_kv;
+    const int kvh = static_cast<int>(pair - b * a.n_kv);
+    const int col = threadIdx.x % COLS, p = threadIdx.x / COLS;
+    const int i = static_cast<int>(blockIdx.x - pair * chunks) * COLS + col, g = i / HD;
+    const bool there = i < a.group * HD;
+    const int at = a.ws_at[b], n = a.ws_at[b + 1] - at;
+    const int64_t part = stream_part(static_cast<int64_t>(a.ws_at[a.B]) * a.n_kv, ctas, warps);
+    T* out = static_cast<T*>(a.out) + b * a.os + static_cast<int64_t>(kvh) * a.group * HD;
+    if (n == 0) {
+        if (p == 0 && there) out[i] = from_f32<T>(0.0f);
+        return;
+    }
+    const int64_t first = static_cast<int64_t>(at) * a.n_kv + static_cast<int64_t>(kvh) * n;
+    const int64_t c0 = first / part, c1 = (first + n - 1) / part;
+    if (c0 == c1) return;  // written by that part
+    float top = -INFINITY, sum = 0.0f, acc = 0.0f;
+    if (there) {
+        constexpr int MANY = 4;
+        for (int64_t c = c0 + p; c <= c1; c += LANES * MANY) {
+            float m[MANY], l[MANY], o[MANY];
+#pragma unroll
+            for (int k = 0; k < MANY; ++k) {
+                const int64_t ck = c + k * LANES;
+                const bool ok = ck <= c1;
+                const float* rec = a.ws_rec + (ck * 2 + (ck == c0 ? 1 : 0)) * (16 + 8 * HD);
+                m[k] = ok ? __ldcg(rec + g) : -INFINITY;
+                l[k] = ok ? __ldcg(rec + 8 + g) : 0.0f;
+                o[k] = ok ? __ldcg(rec + 16 + i) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < MANY; ++k) {
+                const float now = fmaxf(top, m[k]);
+                // (a record without scores above -inf has a sum of 0, or NaN)
+                const float f0 = top == -INFINITY ? 1.0f : ex2(top - now), f1 = m[k] == -INFINITY ? 1.0f : ex2(m[k] - now);
+                sum = sum * f0 + l[k] * f1;
+                acc = acc * f0 + o[k] * f1;
+                top = now;
+            }
+        }
+    }
+    if constexpr (LANES > 1) {
+        s_top[p][col] = top, s_sum[p][col] = sum, s_acc[p][col] = acc;
+        __syncthreads();
+        if (p != 0) return;
+#pragma unroll
+        for (int k = 0; k < LANES; ++k) top = fmaxf(top, s_top[k][col]);
+        sum = acc = 0.0f;
+#pragma unroll
+        for (int k = 0; k < LANES; ++k) {
+            const float f = s_top[k][col] == -INFINITY ? 1.0f : ex2(s_top[k][col] - top);
+            sum = fmaf(f, s_sum[k][col], sum);
+            acc = fmaf(f, s_acc[k][col], acc);
+        }
+    }
+    if (there) out[i] = from_f32<T>(sum != 0.0f ? acc / sum : 0.0f);
+}
+
+template <typename T, int FMT, int HD>
+cudaError_t launch_stream(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
+    using M = Mem<T, FMT, HD>;
+    using S = Shape<T, FMT, HD>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = set_smem_once(stream_kernel<T, FMT, HD>, M::total, true, &done);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(stream_kernel<T, FMT, HD>, dim3(static_cast<unsigned>(p.stream_ctas)), dim3(S::WARPS * 32), M::total, s, p.pdl, 1, a);
+    if (e != cudaSuccess) return e;
+    // pairs that many parts share: eight threads to a column
+    const bool many = a.B * a.n_kv * 8 < p.stream_ctas;
+    const int cols = many ? 32 : 256;
+    const int64_t grid = a.B * a.n_kv * ((a.group * HD + cols - 1) / cols);
+    return launch_kernel(many ? merge_kernel<T, HD, 8> : merge_kernel<T, HD, 1>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, true,
+                         1, a, p.stream_ctas, S::WARPS);
+}
+
 template <typename T, int FMT, int HD>
 cudaError_t launch_cluster(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
     using M = Mem<T, FMT, HD>;
@@ -590,16 +790,16 @@ cudaError_t launch_cluster(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaS
             wide.fetch_or(bit, std::memory_order_release);
         }
     }
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(a.B * a.n_kv * p.splits)), dim3(Shape<FMT, HD>::WARPS * 32), M::total, s,
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(a.B * a.n_kv * p.splits)), dim3(Shape<T, FMT, HD>::WARPS * 32), M::total, s,
                          p.pdl, p.splits, a);
 }
 
 template <typename T, int FMT>
 cudaError_t launch(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
     switch (p.head_dim) {
-        case 64: return launch_cluster<T, FMT, 64>(a, p, s);
-        case 128: return launch_cluster<T, FMT, 128>(a, p, s);
-        default: return launch_cluster<T, FMT, 256>(a, p, s);
+        case 64: return p.stream_ctas ? launch_stream<T, FMT, 64>(a, p, s) : launch_cluster<T, FMT, 64>(a, p, s);
+        case 128: return p.stream_ctas ? launch_stream<T, FMT, 128>(a, p, s) : launch_cluster<T, FMT, 128>(a, p, s);
+        default: return p.stream_ctas ? launch_stream<T, FMT, 256>(a, p, s) : launch_cluster<T, FMT, 256>(a, p, s);
     }
 }
 
@@ -608,6 +808,7 @@ cudaError_t launch(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t 
 int quant_attn_warps(int format, int head_dim) {
     return 2 * qattn::kTile * kv_row_bytes(format, head_dim) <= 4608 ? 8 : 4;  // Shape::WARPS
 }
+int quant_attn_ctas_per_sm(int format, int head_dim) { return format == KV_INT8 && head_dim == 256 ? 1 : 2; }  // Shape::CTAS
 
 unsigned int quant_attn_wait_timeouts() {
     unsigned int n = 0;

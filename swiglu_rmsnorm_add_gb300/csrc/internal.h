@@ -118,7 +118,7 @@ struct KvQuantPlan {
     int format;
     int style = 0;         // store: 0 = neox, 1 = interleaved
     bool qk_norm = false;  // store: UClip Q and K heads before rotating
-    bool wide;             // 16-byte accesses of the tensors of `dtype`
+    bool wide = false;     // store: 16-byte accesses of the tensors
     bool pdl;
     int num_sms;
 };
@@ -233,15 +233,25 @@ struct QuantAttnArgs {
     int n_kv, group, block_size;
     float scale_log2;  // softmax scale * log2(e)
     bool wide_q;       // 16-byte aligned query rows
+    // workspace of the stream form
+    int32_t* ws_at = nullptr;   // [B + 1] tiles (of a kv head) before each request
+    float* ws_rec = nullptr;    // [CTAs][2][16 + 8 * head_dim]
 };
+// The tiles of a CTA's part of the stream: equal parts, but no less than a tile for each warp.
+inline SRA_HD int64_t stream_part(int64_t all, int64_t ctas, int warps) {
+    const int64_t part = (all + ctas - 1) / ctas;
+    return part < warps ? warps : part;
+}
 struct QuantAttnPlan {
     int format, head_dim;
-    int splits;  // CTAs per (request, kv head): the cluster size
+    int splits;       // CTAs per (request, kv head): the cluster size
+    int stream_ctas;  // > 0: the stream form, with that many CTAs
     bool pdl;
     int num_sms;
 };
 cudaError_t launch_attention_quant(const QuantAttnArgs& a, const QuantAttnPlan& p, int dtype, cudaStream_t s);
 int quant_attn_warps(int format, int head_dim);  // per CTA
+int quant_attn_ctas_per_sm(int format, int head_dim);
 unsigned int quant_attn_wait_timeouts();
 
 // ------------------------------------------------------------------- shared prefix

@@ -2,16 +2,16 @@
 // (format: kv_format.cuh). Cache layout [2, num_blocks, n_kv_head, block_size, row_bytes]: a head's rows of a
 // page lie in a row, so the attention copies them as one piece.
 //
-// Store. A token's work is (n_head + 2 n_kv_head) * head_dim / 16 tasks of 16 values: Q and K as eight rotation
-// pairs, V as 16 dims in a row. In the neox pairing a K task holds half of two groups, whose other halves the
-// neighbouring thread has (one shuffle each); otherwise a task is a group.
+// Store. A thread takes a task of 16 values of one head: of Q and K eight rotation pairs, of V 16 dims in a row. In the
+// neox pairing a K task holds half of two groups, whose other halves the neighbouring thread has (one shuffle
+// each); otherwise a task is a group.
 //
 // K's rotation is the correctly rounded fp32 number (the product difference is kept as a sum of two fp32 numbers), rounded
 // once more to the dtype. A code can hang on the last place of its value, and with this the cache's bytes
 // follow from the definition, whoever evaluates it. (Q is rotated exactly as sra_rope_kv_store does it.)
 //
-// Read. A CTA takes a tile of output tokens, finds each one's row of the cache once, and its threads turn eight codes
-// into one 16-byte store (two in fp32).
+// Read. A CTA takes a tile of output tokens, finds each one's place in the cache once, and its threads turn groups of 16
+// codes into one 32-byte store each (two in fp32).
 #include "kv_format.cuh"
 #include "rope_math.cuh"
 
@@ -79,162 +79,197 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[W]) 
     for (int j = 0; j < W; ++j) reinterpret_cast<uint32_t*>(p)[j] = w[j];  // rows are multiples of 4 bytes
 }
 
-template <typename T, int FMT, bool IL, bool NORM>
-__global__ void __launch_bounds__(kThreads) store_kernel(RopeArgs a, int tokens_per_cta, bool wide) {
+// Which tensor a CTA's tasks come from; each has CTAs of its own (K's first: they have the most to do), so that no warp
+// walks through two kinds' code.
+struct StoreGrid {
+    int64_t k_ctas, v_ctas;
+    bool wide;
+};
+
+template <typename T, int FMT, bool IL, bool NORM, int KIND>  // KIND: 0 Q, 1 K, 2 V
+__device__ __forceinline__ void store_task(const RopeArgs& a, int64_t cta, bool wide) {
     constexpr int CB = FMT == KV_E2M1 ? 4 : 8;  // bits per code
-    pdl_enter();
-    const int D = a.head_dim, h = D >> 1, per_head = D / kGroup;
-    const int U = (a.n_head + 2 * a.n_kv) * per_head;
-    const int R = row_bytes(FMT, D), codes = code_bytes(FMT, D);
-    const int64_t capacity = a.num_blocks * static_cast<int64_t>(a.block_size);
-    const int tasks = U * tokens_per_cta;  // of a CTA at a time; more than kThreads only for one token
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_cta; t0 < a.T;
-         t0 += static_cast<int64_t>(gridDim.x) * tokens_per_cta) {
-        for (int base = 0; base < tasks; base += kThreads) {
-            const int i = base + threadIdx.x;
-            const int lt = tokens_per_cta == 1 ? 0 : i / U, u = i - lt * U;
-            const int64_t t = t0 + lt;
-            bool live = i < tasks && t < a.T;
-            const int unit = u / per_head, g = u - unit * per_head;
-            const int kind = unit < a.n_head ? 0 : (unit < a.n_head + a.n_kv ? 1 : 2);  // Q, K, V head
-            const int head = kind == 0 ? unit : (kind == 1 ? unit - a.n_head : unit - a.n_head - a.n_kv);
-            int64_t p = 0, slot = -1;
-            if (live) {
-                p = a.pos[t];
-                slot = a.slot[t];
-                const bool pos_ok = p >= 0 && p < a.max_pos, past = slot >= capacity;
-                if (u == 0 && a.err != nullptr) {
-                    const int bad = (pos_ok ? 0 : 1) + (past ? 1 : 0);
-                    if (bad) atomicAdd(a.err, bad);
-                }
-                live = pos_ok && (kind == 0 || (slot >= 0 && !past));
+    constexpr bool ROW = IL || KIND == 2;       // 16 dims in a row
+    const int D = a.head_dim, h = D >> 1, lg = __ffs(D) - 5;  // 2^lg tasks a head
+    const int U = (KIND == 0 ? a.n_head : a.n_kv) << lg;
+    // tasks are numbered over tokens, heads, groups
+    const int64_t first = cta * kThreads, t0 = first / U;
+    const unsigned i = static_cast<unsigned>(first - t0 * U) + threadIdx.x, lt = i / static_cast<unsigned>(U);
+    const int64_t t = t0 + lt;
+    const int u = static_cast<int>(i - lt * U), head = u >> lg, g = u & ((1 << lg) - 1);
+    bool live = t < a.T;
+    int64_t p = 0, slot = -1;
+    float x0[8], x1[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x0[j] = x1[j] = 0.0f;
+    // offsets of the task's two runs of eight values
+    const int o0 = ROW ? 16 * g : 8 * g, o1 = ROW ? 16 * g + 8 : h + 8 * g;
+    T* q = nullptr;
+    if (live) {
+        const int64_t capacity = a.num_blocks * static_cast<int64_t>(a.block_size), ho = static_cast<int64_t>(head) * D;
+        p = a.pos[t];
+        if (KIND != 0) slot = a.slot[t];
+        const T* src;
+        if (KIND == 0) src = q = static_cast<T*>(a.q) + t * a.qs + ho;
+        else src = KIND == 1 ? static_cast<const T*>(a.k) + t * a.ks + ho : static_cast<const T*>(a.v) + t * a.vs + ho;
+        load8(src + o0, wide, x0);
+        load8(src + o1, wide, x1);
+        const bool pos_ok = p >= 0 && p < a.max_pos, past = slot >= capacity;
+        if (KIND == 1 && u == 0 && a.err != nullptr) {
+            const int bad = (pos_ok ? 0 : 1) + (past ? 1 : 0);
+            if (bad) atomicAdd(a.err, bad);
+        }
+        live = pos_ok && (KIND == 0 || (slot >= 0 && !past));
+    }
+    if (KIND != 2 && live) {
+        float c[8], s[8];
+        load8(a.cos + p * h + 8 * g, wide, c);
+        load8(a.sin + p * h + 8 * g, wide, s);
+        if constexpr (NORM) {
+            const float* pa = KIND == 0 ? a.qa : a.ka;
+            const float* pg = KIND == 0 ? a.qg : a.kg;
+            float al[8], ga[8];
+            load8(pa + o0, wide, al);
+            load8(pg + o0, wide, ga);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x0[j] = round_trip<T>(rope::uclip1(x0[j], al[j], ga[j], a.clip_lo, a.clip_hi));
+            load8(pa + o1, wide, al);
+            load8(pg + o1, wide, ga);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x1[j] = round_trip<T>(rope::uclip1(x1[j], al[j], ga[j], a.clip_lo, a.clip_hi));
+        }
+        // pair j: neox (x0[j], x1[j]); interleaved elements 2j and 2j + 1 of the two runs
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float& lo = IL ? (j < 4 ? x0[2 * j & 7] : x1[2 * j & 7]) : x0[j];
+            float& hi = IL ? (j < 4 ? x0[(2 * j + 1) & 7] : x1[(2 * j + 1) & 7]) : x1[j];
+            float y0, y1;
+            if constexpr (KIND == 0) {
+                y0 = rope::diff_of_products(lo, c[j], hi, s[j]);
+                y1 = rope::diff_of_products(hi, c[j], -lo, s[j]);
+            } else {
+                y0 = round_trip<T>(rotate_exact(lo, c[j], hi, s[j]));
+                y1 = round_trip<T>(rotate_exact(hi, c[j], -lo, s[j]));
             }
-            // offsets of the task's two runs of eight values
-            const bool in_a_row = IL || kind == 2;
-            const int o0 = in_a_row ? 16 * g : 8 * g, o1 = in_a_row ? 16 * g + 8 : h + 8 * g;
-            float x0[8], x1[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x0[j] = x1[j] = 0.0f;
-            T* q = nullptr;
-            if (live) {
-                const int64_t ho = static_cast<int64_t>(head) * D;
-                q = static_cast<T*>(a.q) + t * a.qs + ho;
-                const T* src = kind == 0 ? q : kind == 1 ? static_cast<const T*>(a.k) + t * a.ks + ho
-                                                        : static_cast<const T*>(a.v) + t * a.vs + ho;
-                load8(src + o0, wide, x0);
-                load8(src + o1, wide, x1);
-                if (kind != 2) {
-                    float c[8], s[8];
-                    load8(a.cos + p * h + 8 * g, wide, c);
-                    load8(a.sin + p * h + 8 * g, wide, s);
-                    if constexpr (NORM) {
-                        const float* pa = kind == 0 ? a.qa : a.ka;
-                        const float* pg = kind == 0 ? a.qg : a.kg;
-                        float al[8], ga[8];
-                        load8(pa + o0, wide, al);
-                        load8(pg + o0, wide, ga);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x0[j] = round_trip<T>(rope::uclip1(x0[j], al[j], ga[j], a.clip_lo, a.clip_hi));
-                        load8(pa + o1, wide, al);
-                        load8(pg + o1, wide, ga);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x1[j] = round_trip<T>(rope::uclip1(x1[j], al[j], ga[j], a.clip_lo, a.clip_hi));
-                    }
-                    // pair j: neox (x0[j], x1[j]); interleaved elements 2j and 2j + 1 of the two runs
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float& lo = IL ? (j < 4 ? x0[2 * j & 7] : x1[2 * j & 7]) : x0[j];
-                        float& hi = IL ? (j < 4 ? x0[(2 * j + 1) & 7] : x1[(2 * j + 1) & 7]) : x1[j];
-                        float y0, y1;
-                        if (kind == 0) {
-                            y0 = rope::diff_of_products(lo, c[j], hi, s[j]);
-                            y1 = rope::diff_of_products(hi, c[j], -lo, s[j]);
-                        } else {
-                            y0 = round_trip<T>(rotate_exact(lo, c[j], hi, s[j]));
-                            y1 = round_trip<T>(rotate_exact(hi, c[j], -lo, s[j]));
-                        }
-                        lo = y0, hi = y1;
-                    }
-                    if (kind == 0) {
-                        store8(q + o0, wide, x0);
-                        store8(q + o1, wide, x1);
-                    }
-                }
-            }
-            // a warp's lanes meet here for the groups' maxima
-            uint32_t m0 = amax_bits(x0), m1 = amax_bits(x1);
-            const uint32_t n0 = __shfl_xor_sync(0xffffffffu, m0, 1), n1 = __shfl_xor_sync(0xffffffffu, m1, 1);
-            if (in_a_row) m0 = m1 = max(m0, m1);
-            else m0 = max(m0, n0), m1 = max(m1, n1);
-            if (!live || kind == 0) continue;
-            const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
-            uint8_t* row = static_cast<uint8_t*>(a.cache) +
-                           ((((kind == 2 ? a.num_blocks : 0) + blk) * a.n_kv + head) * a.block_size + off) * R;
-            const uint32_t c0 = scale_of<FMT>(m0), c1 = in_a_row ? c0 : scale_of<FMT>(m1);
-            uint32_t w0[CB / 4], w1[CB / 4];
-            encode<FMT>(x0, c0, w0);
-            encode<FMT>(x1, c1, w1);
-            store_words(row + o0 * CB / 8, w0);
-            store_words(row + o1 * CB / 8, w1);
-            if (in_a_row) {
-                row[codes + g] = static_cast<uint8_t>(c0);
-            } else if (!(g & 1)) {
-                row[codes + (g >> 1)] = static_cast<uint8_t>(c0);
-                row[codes + h / kGroup + (g >> 1)] = static_cast<uint8_t>(c1);
-            }
+            lo = y0, hi = y1;
         }
     }
+    if constexpr (KIND == 0) {
+        if (live) {
+            store8(q + o0, wide, x0);
+            store8(q + o1, wide, x1);
+        }
+    } else {
+        uint32_t m0 = amax_bits(x0), m1 = amax_bits(x1);
+        if constexpr (ROW) {
+            m0 = m1 = max(m0, m1);
+        } else {  // a warp's lanes meet here: the neighbour holds the groups' other halves
+            m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
+            m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
+        }
+        if (!live) return;
+        const int R = row_bytes(FMT, D), codes = code_bytes(FMT, D);
+        const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
+        uint8_t* row = static_cast<uint8_t*>(a.cache) +
+                       ((((KIND == 2 ? a.num_blocks : 0) + blk) * a.n_kv + head) * a.block_size + off) * R;
+        const uint32_t c0 = scale_of<FMT>(m0), c1 = ROW ? c0 : scale_of<FMT>(m1);
+        uint32_t w0[CB / 4], w1[CB / 4];
+        encode<FMT>(x0, c0, w0);
+        encode<FMT>(x1, c1, w1);
+        store_words(row + o0 * CB / 8, w0);
+        store_words(row + o1 * CB / 8, w1);
+        if constexpr (ROW) {
+            row[codes + g] = static_cast<uint8_t>(c0);
+        } else if (!(g & 1)) {
+            row[codes + (g >> 1)] = static_cast<uint8_t>(c0);
+            row[codes + h / kGroup + (g >> 1)] = static_cast<uint8_t>(c1);
+        }
+    }
+}
+
+template <typename T, int FMT, bool IL, bool NORM>
+__global__ void __launch_bounds__(kThreads, 4) store_kernel(RopeArgs a, StoreGrid grid) {
+    pdl_enter();
+    const int64_t cta = blockIdx.x;
+    if (cta < grid.k_ctas) store_task<T, FMT, IL, NORM, 1>(a, cta, grid.wide);
+    else if (cta < grid.k_ctas + grid.v_ctas) store_task<T, FMT, IL, NORM, 2>(a, cta - grid.k_ctas, grid.wide);
+    else store_task<T, FMT, IL, NORM, 0>(a, cta - grid.k_ctas - grid.v_ctas, grid.wide);
 }
 
 template <typename T, int FMT>
 cudaError_t launch_store(const RopeArgs& a, const KvQuantPlan& p, cudaStream_t s) {
-    void (*kernel)(RopeArgs, int, bool) =
+    void (*kernel)(RopeArgs, StoreGrid) =
         p.style == 0 ? (p.qk_norm ? store_kernel<T, FMT, false, true> : store_kernel<T, FMT, false, false>)
                      : (p.qk_norm ? store_kernel<T, FMT, true, true> : store_kernel<T, FMT, true, false>);
-    const int U = (a.n_head + 2 * a.n_kv) * (a.head_dim / kGroup);
-    const int tokens = U < kThreads ? kThreads / U : 1;
-    const dim3 grid(persistent_grid(kernel, kThreads, 0, p.num_sms, (a.T + tokens - 1) / tokens));
-    return launch_kernel(kernel, grid, dim3(kThreads), 0, s, p.pdl, 1, a, tokens, p.wide);
+    const int64_t per_head = a.T * (a.head_dim / kGroup);
+    StoreGrid g;
+    g.k_ctas = g.v_ctas = (per_head * a.n_kv + kThreads - 1) / kThreads;
+    g.wide = p.wide;
+    const int64_t all = g.k_ctas + g.v_ctas + (per_head * a.n_head + kThreads - 1) / kThreads;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(all)), dim3(kThreads), 0, s, p.pdl, 1, a, g);
 }
 
 // ------------------------------------------------------------------- read back
-constexpr int kReadTokens = 32;   // of a CTA's tile, at most
-constexpr int kReadRows = 1024;   // cu_lens entries kept in shared memory
+constexpr int kReadTokens = 32;  // of a CTA's tile, at most
+constexpr int kReadRows = 1024;  // cu_lens entries kept in shared memory
 
-// The pair of fp16 numbers as T.
+// 16 values (pairs of fp16 numbers) as T, in stores of 32 bytes where `wide` is 2, of 16 where it is 1.
 template <typename T>
-__device__ __forceinline__ void store_pairs(T* p, bool wide, const uint32_t (&h)[4]) {
-    if constexpr (std::is_same_v<T, __half>) {
-        if (wide) {
-            *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
-            return;
+__device__ __forceinline__ void store16(T* p, int wide, const uint32_t (&h)[8]) {
+    constexpr int W = static_cast<int>(sizeof(T)) * 4;  // words
+    uint32_t w[W];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (std::is_same_v<T, __half>) {
+            w[j] = h[j];
+        } else {
+            __half2 v;
+            memcpy(&v, &h[j], 4);
+            const float2 x = __half22float2(v);
+            if constexpr (sizeof(T) == 4) {
+                w[2 * j] = __float_as_uint(x.x), w[2 * j + 1] = __float_as_uint(x.y);
+            } else {
+                const float f[2] = {x.x, x.y};
+                w[j] = Elem<T>::pack_word(f);
+            }
         }
     }
-    float f[8];
+    if (wide == 2) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        __half2 v;
-        memcpy(&v, &h[j], 4);
-        const float2 x = __half22float2(v);
-        f[2 * j] = x.x, f[2 * j + 1] = x.y;
+        for (int j = 0; j < W; j += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t*>(p) + j),
+                         "r"(w[j]), "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]), "r"(w[j + 5]), "r"(w[j + 6]),
+                         "r"(w[j + 7])
+                         : "memory");
+    } else if (wide == 1) {
+#pragma unroll
+        for (int j = 0; j < W; j += 4) reinterpret_cast<uint4*>(p)[j / 4] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) p[j] = __uint_as_float(w[j]);
+    } else {
+        unsigned short* q = reinterpret_cast<unsigned short*>(p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[2 * j] = static_cast<unsigned short>(w[j]), q[2 * j + 1] = static_cast<unsigned short>(w[j] >> 16);
     }
-    store8(p, wide, f);
 }
 
+// A thread's items are groups of 16 values: four at a time, whose bytes are all asked for before the first is used.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads) read_kernel(KvReadArgs a, int tile, bool wide) {
-    constexpr int WORDS = FMT == KV_E2M1 ? 1 : 2;  // of eight codes
+__global__ void __launch_bounds__(kThreads) read_kernel(KvReadArgs a, int tile, int wide) {
+    constexpr int WORDS = FMT == KV_E2M1 ? 2 : 4;  // of sixteen codes
+    constexpr int MANY = 4;
     __shared__ int32_t s_cu[kReadRows + 1];
-    __shared__ int64_t s_at[kReadTokens];  // (page * n_kv * block_size + offset) of each token; -1: zeros, -2: not written
+    __shared__ int64_t s_at[kReadTokens];  // page * n_kv * block_size + offset of each token; -1: zeros, -2: not written
     pdl_enter();
-    const int D = a.head_dim, per_head = D / 8, R = row_bytes(FMT, D), codes = code_bytes(FMT, D);
+    const int D = a.head_dim, lg = __ffs(D) - 5, R = row_bytes(FMT, D), codes = code_bytes(FMT, D);
     const bool cached = a.rows <= kReadRows;
     if (cached) {
         for (int64_t i = threadIdx.x; i <= a.rows; i += kThreads) s_cu[i] = a.cu[i];
         __syncthreads();
     }
-    auto cu = [&](int64_t r) { return cached ? s_cu[r] : __ldg(a.cu + r); };
-    const int per_token = 2 * a.n_kv * per_head;  // items: both planes
+    auto cu = [&](int64_t r) { return cached ? s_cu[r] : a.cu[r]; };
+    const int per_token = 2 * a.n_kv << lg;  // items: planes, heads, groups
     for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tile; t0 < a.total; t0 += static_cast<int64_t>(gridDim.x) * tile) {
         if (threadIdx.x < tile) {
             const int64_t i = t0 + threadIdx.x;
@@ -262,25 +297,52 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvReadArgs a, int tile, 
         }
         __syncthreads();
         const int n = static_cast<int>(a.total - t0 < tile ? a.total - t0 : tile) * per_token;
-        for (int it = threadIdx.x; it < n; it += kThreads) {
-            const int lt = it / per_token;
-            int rest = it - lt * per_token;
-            const int plane = rest >= per_token / 2 ? 1 : 0;
-            rest -= plane * (per_token / 2);
-            const int head = rest / per_head, d = (rest - head * per_head) * 8;
-            const int64_t at = s_at[lt];
-            if (at == -2) continue;
-            uint32_t v[4] = {0, 0, 0, 0};
-            if (at >= 0) {
-                const uint8_t* row = static_cast<const uint8_t*>(a.cache) + plane * a.plane_bytes +
-                                     (at + static_cast<int64_t>(head) * a.block_size) * R;
-                uint32_t w[WORDS];
+        for (int base = threadIdx.x; base < n; base += MANY * kThreads) {
+            uint32_t w[MANY][WORDS];
+            uint32_t scale[MANY];
+            T* out[MANY];
 #pragma unroll
-                for (int j = 0; j < WORDS; ++j) w[j] = reinterpret_cast<const uint32_t*>(row + d * WORDS / 2)[j];
-                decode8<FMT>(w, scale_pair(row[codes + d / kGroup]), v);
+            for (int k = 0; k < MANY; ++k) {
+                const unsigned it = base + k * kThreads;
+                out[k] = nullptr;
+                scale[k] = 0;
+#pragma unroll
+                for (int j = 0; j < WORDS; ++j) w[k][j] = 0;
+                if (it < static_cast<unsigned>(n)) {
+                    const unsigned lt = it / static_cast<unsigned>(per_token), rest = it - lt * per_token;
+                    const int g = rest & ((1 << lg) - 1);
+                    int head = rest >> lg;
+                    const bool plane = head >= a.n_kv;
+                    if (plane) head -= a.n_kv;
+                    const int64_t at = s_at[lt];
+                    if (at != -2)
+                        out[k] = static_cast<T*>(plane ? a.v : a.k) + (t0 + lt) * (plane ? a.vs : a.ks) + head * D + g * kGroup;
+                    if (at >= 0) {
+                        const uint8_t* row = static_cast<const uint8_t*>(a.cache) + (plane ? a.plane_bytes : 0) +
+                                             (at + static_cast<int64_t>(head) * a.block_size) * R;
+                        scale[k] = row[codes + g];
+                        if (R % 8 == 0) {  // rows of head_dim 64 are multiples of 4 bytes only
+#pragma unroll
+                            for (int j = 0; j < WORDS; j += 2) {
+                                const uint2 v = *reinterpret_cast<const uint2*>(row + (g * WORDS + j) * 4);
+                                w[k][j] = v.x, w[k][j + 1] = v.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < WORDS; ++j) w[k][j] = reinterpret_cast<const uint32_t*>(row)[g * WORDS + j];
+                        }
+                    }
+                }
             }
-            T* out = static_cast<T*>(plane ? a.v : a.k) + (t0 + lt) * (plane ? a.vs : a.ks) + head * D + d;
-            store_pairs(out, wide, v);
+#pragma unroll
+            for (int k = 0; k < MANY; ++k) {
+                if (!out[k]) continue;
+                uint32_t lo[4], hi[4];
+                decode8<FMT>(w[k], scale_pair(scale[k]), lo);
+                decode8<FMT>(w[k] + WORDS / 2, scale_pair(scale[k]), hi);
+                const uint32_t h[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                store16(out[k], wide, h);
+            }
         }
         __syncthreads();
     }
@@ -289,11 +351,15 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvReadArgs a, int tile, 
 template <typename T, int FMT>
 cudaError_t launch_read(const KvReadArgs& a, const KvQuantPlan& p, cudaStream_t s) {
     auto kernel = read_kernel<T, FMT>;
-    // few tokens: a CTA for each; many: up to 32 in a tile
+    // up to 32 tokens in a tile; for few tokens as many as give every thread of a CTA an item
+    const int per_token = 2 * a.n_kv * (a.head_dim / kGroup);
     int tile = kReadTokens;
-    while (tile > 1 && (a.total + tile - 1) / tile < 4 * static_cast<int64_t>(p.num_sms)) tile >>= 1;
+    while (tile > 1 && tile / 2 * per_token >= kThreads && (a.total + tile - 1) / tile < 4 * static_cast<int64_t>(p.num_sms)) tile >>= 1;
     const dim3 grid(persistent_grid(kernel, kThreads, 0, p.num_sms, (a.total + tile - 1) / tile));
-    return launch_kernel(kernel, grid, dim3(kThreads), 0, s, p.pdl, 1, a, tile, p.wide);
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                           static_cast<uintptr_t>((a.ks | a.vs) * static_cast<int64_t>(sizeof(T)));
+    const int wide = bits % 32 == 0 ? 2 : bits % 16 == 0 ? 1 : 0;
+    return launch_kernel(kernel, grid, dim3(kThreads), 0, s, p.pdl, 1, a, tile, wide);
 }
 
 }  // namespace kvq
