@@ -22,7 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsra.so")
 
 SOURCES = ["api.cu", "norm_rms.cu", "norm_add.cu", "rope_kv.cu", "glu.cu", "uclip.cu", "attn.cu", "attn_noalloc.cu", "linear.cu",
-           "kv_pages.cu", "attn_prefix.cu", "kv_quant.cu", "attn_quant.cu"]
+           "kv_pages.cu", "attn_prefix.cu", "kv_quant.cu", "attn_quant_e2m1.cu",
+           "attn_quant_int8.cu", "attn_quant_e2m1_f32.cu", "attn_quant_int8_f32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-Wall,-fvisibility=hidden", "-I" + INCLUDE,
                  "-I" + CSRC]

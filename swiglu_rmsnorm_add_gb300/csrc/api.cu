@@ -2038,18 +2038,37 @@ int quant_attention_sizes(int64_t B, int n_head, int n_kv_head, int head_dim, in
                : SRA_OK;
 }
 
-// CTAs of the stream form (0: the cluster form), and its workspace: the sums, then two records a CTA.
-int quant_stream_ctas(int64_t B, int n_kv, int64_t tokens, int format, int head_dim, int num_sms) {
+// How a call runs: the cluster form's CTAs for each pair, or the stream form's CTAs (0: the cluster form) with its workspace: the
+// sums, then two records a CTA.
+// How a call runs: the cluster form's CTAs for each pair, or the stream form's CTAs (0: the cluster form) with its workspace: the
+// sums, then two records a CTA.
+struct QuantAttnForm {
+    int splits = 1, stream_ctas = 0;
+    int64_t at_bytes = 0, bytes = 0;
+};
+QuantAttnForm quant_attn_form(int64_t B, int n_kv, int64_t tokens, int format, int head_dim, int dtype, int num_sms) {
+    QuantAttnForm f;
+    const int warps = quant_attn_warps(format, head_dim);
+    const int64_t slots = static_cast<int64_t>(num_sms) * quant_attn_ctas(format, head_dim), pairs = B * n_kv;
+    // A cluster takes as many CTAs as fill the SMs, with a tile for each warp. One of 16 only where all of them have an SM for themselves:
+    // 8 requests x 4096 of 2 heads 9.8 us with 8 CTAs, 13.7 with 16; 1 x 8192 10.2 and 8.1.
+    while (f.splits < 16 && pairs * f.splits * 2 <= (f.splits < 8 ? slots : num_sms) &&
+           tokens >= 2 * 32 * warps * static_cast<int64_t>(f.splits))
+        f.splits *= 2;
+    // The stream form has a second launch and a search for its parts (6 us), and every SM the same to do: for long parts, and sooner
+    // where the clusters leave SMs without work. bf16, e2m1, head_dim 128, both (cluster, stream), lengths alike and from 1 on: batch 64 x 8192 41,
+    // 46 and 38, 42 us, x 16384 72, 72 and 65, 54, x 65536 253, 227 and 227, 132; 8 x 16384 21, 22 and 17, 18, x 32768 38, 32 and 28, 22;
+    // 1 x 65536 25, 19. fp32 does more for each token: 24 x 4096 of 4 heads 33, 33 and 29, 34, x 8192 57, 49 and 51, 45.
+    const int64_t part = tokens / f.splits * (dtype == DT_F32 ? 2 : 1);
+    const bool longer = part >= 3072 && part * slots >= 6144 * std::min<int64_t>(slots, pairs * f.splits);
     const int forced = g_force_quant_attn.load(std::memory_order_relaxed);
-    if (forced == 0) return 0;
-    const int ctas = num_sms * quant_attn_ctas_per_sm(format, head_dim);
+    if (forced >= 0 ? (forced & 0xff) == 0 : !longer) return f;
     // (a thread sums B / 256 requests; the tiles of a kv head are counted in 32 bits)
-    if (B > 65536 || B * ((tokens + 31) / 32) > 0x7fffffff) return 0;
-    return ctas;
-}
-int64_t quant_stream_at_bytes(int64_t B) { return round_up256((B + 1) * 4); }
-int64_t quant_stream_bytes(int64_t B, int ctas, int head_dim) {
-    return ctas > 0 ? quant_stream_at_bytes(B) + static_cast<int64_t>(ctas) * 2 * (16 + 8 * head_dim) * 4 : 0;
+    if (B > 65536 || B * ((tokens + 31) / 32) > 0x7fffffff) return f;
+    f.stream_ctas = static_cast<int>(slots);
+    f.at_bytes = round_up256((B + 1) * 4);
+    f.bytes = f.at_bytes + slots * 2 * (16 + 8 * head_dim) * 4;
+    return f;
 }
 
 }  // namespace
@@ -2063,7 +2082,7 @@ int64_t sra_paged_decode_attention_quant_workspace_size(int64_t B, int n_head, i
     int dev = 0;
     const int sms = current_sm_count(&dev);
     if (sms <= 0) return SRA_ERR_DEVICE;
-    return quant_stream_bytes(B, quant_stream_ctas(B, n_kv_head, max_blocks_per_seq * block_size, format, head_dim, sms), head_dim);
+    return quant_attn_form(B, n_kv_head, max_blocks_per_seq * block_size, format, head_dim, dtype, sms).bytes;
 }
 
 int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
@@ -2093,28 +2112,29 @@ int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const 
     int dev = 0;
     plan.num_sms = current_sm_count(&dev);
     if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
-    plan.format = format;
     plan.head_dim = head_dim;
     plan.pdl = g_pdl;
-    const int64_t pairs = B * n_kv_head, part = 32 * static_cast<int64_t>(quant_attn_warps(format, head_dim));
-    plan.splits = 1;
-    while (plan.splits < 16 && pairs * plan.splits <= plan.num_sms && max_blocks_per_seq * block_size >= 2 * part * plan.splits)
-        plan.splits *= 2;
-    QuantAttnArgs a;
+    const QuantAttnForm form = quant_attn_form(B, n_kv_head, max_blocks_per_seq * block_size, format, head_dim, dtype, plan.num_sms);
     plan.stream_ctas = 0;
-    const int ctas = quant_stream_ctas(B, n_kv_head, max_blocks_per_seq * block_size, format, head_dim, plan.num_sms);
-    if (workspace && ctas > 0) {
-        const int64_t need = quant_stream_bytes(B, ctas, head_dim);
-        if (workspace_bytes < need || !aligned16(workspace)) return SRA_ERR_ARG;
-        const Span sws = span_of(workspace, 1, 0, need, 1);
+    QuantAttnArgs a;
+    if (workspace && form.stream_ctas > 0) {
+        if (workspace_bytes < form.bytes || !aligned16(workspace)) return SRA_ERR_ARG;
+        const Span sws = span_of(workspace, 1, 0, form.bytes, 1);
         if (overlap(sws, so) || overlap(sws, sc) || overlap(sws, st_) || overlap(sws, sl) ||
             overlap(sws, span_of(q, B, q_tok_stride, w, es)))
             return SRA_ERR_ALIAS;
-        plan.stream_ctas = ctas;
+        plan.stream_ctas = form.stream_ctas;
         a.ws_at = static_cast<int32_t*>(workspace);
-        a.ws_rec = reinterpret_cast<float*>(static_cast<char*>(workspace) + quant_stream_at_bytes(B));
-    } else if (g_force_quant_attn.load(std::memory_order_relaxed) == 1) {
+        a.ws_rec = reinterpret_cast<float*>(static_cast<char*>(workspace) + form.at_bytes);
+    } else if ((g_force_quant_attn.load(std::memory_order_relaxed) & 0xff) == 1) {
         return SRA_ERR_VARIANT;
+    }
+    plan.splits = form.splits;
+    const int forced = g_force_quant_attn.load(std::memory_order_relaxed);
+    if (forced > 0 && (forced >> 8) != 0) {
+        const int f = forced >> 8;
+        if (f > 16 || (f & (f - 1)) != 0) return SRA_ERR_VARIANT;
+        plan.splits = f;
     }
     a.q = q;
     a.cache = kv_cache;
@@ -2133,7 +2153,10 @@ int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const 
     a.block_size = block_size;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.wide_q = aligned16(q) && stride_aligned16(q_tok_stride, es);
-    return status_from(launch_attention_quant(a, plan, dtype, static_cast<cudaStream_t>(stream)));
+    a.bf16 = dtype == DT_BF16;
+    auto launch = format == KV_E2M1 ? (dtype == DT_F32 ? launch_attn_quant_e2m1_f32 : launch_attn_quant_e2m1)
+                                    : (dtype == DT_F32 ? launch_attn_quant_int8_f32 : launch_attn_quant_int8);
+    return status_from(launch(a, plan, static_cast<cudaStream_t>(stream)));
 }
 
 int sra_force_variant(const char* op, int variant) {

@@ -2,9 +2,10 @@
 //
 //   o = sum_t softmax_t(scale * q . K_t) V_t over a request's tokens, K_t and V_t the values that the cache holds.
 //
-// A CTA takes a (request, kv head) pair, or a split of it, 32 tokens (a tile) a warp at a time. A head's rows of a page
-// lie in a row, so a tile is one to four bulk copies for K and as many for V into the warp's own ring in shared
-// memory; the warp that reads a stage asks for its next tile, and waits for nobody else.
+// A CTA takes a (request, kv head) pair, or a part of it, 32 tokens (a tile) a warp at a time. A head's rows of a page lie in a row,
+// so a tile is one to four bulk copies for K and as many for V into the warp's own ring in shared memory, where it alone reads
+// them: warps wait for nobody. (The same rings filled by the lanes, 16 bytes a cp.async: batch 64 x 16384 72.0 -> 75.7 us, in 8 bits
+// 101 -> 118. A ring that warps of their own fill for twelve that compute: 94; these could not keep up.)
 //
 // Codes become fp16 in registers, in the layout of the matrix instruction's operand: a value times its scale is an fp16
 // number exactly, so this is one conversion (or byte permutation) and one multiplication for two values, and nothing is
@@ -21,7 +22,13 @@
 // instruction's own accumulation truncates.
 //
 // Without a workspace the splits of a pair are the CTAs of a cluster, which merge through distributed shared memory; with one the
-// batch is a stream of tiles cut into equal parts (stream_kernel), whose records a second kernel merges.
+// batch may be a stream of tiles cut into equal parts (stream_kernel), whose records a second kernel merges.
+//
+// What bounds it: the arithmetic beside the products, not HBM. A tile of head_dim 128 in 4 bits takes 128 conversions and 128
+// multiplications (two cycles each, on different pipes) and 32 products, each of which holds the scheduler's dispatch for some
+// six cycles (measured: a product with four conversions and four multiplications takes 14 cycles, not nine).
+#pragma once
+
 #include <cooperative_groups.h>
 
 #include "kv_format.cuh"
@@ -32,39 +39,37 @@ namespace cg = cooperative_groups;
 namespace sra {
 namespace qattn {
 
-constexpr int kTile = 32;     // tokens of a warp's tile
-constexpr float kUnder = 14;  // the probabilities' base lies 2^14 under the maximum
+constexpr int kTile = 32;       // tokens of a warp's tile
+constexpr int kHalves = 2;      // of 16 tokens
+constexpr float kUnder = 14;    // the probabilities' base lies 2^14 under the maximum
 
-template <typename T, int FMT, int HD>
+// F32: fp32 queries (three parts, probabilities in two); otherwise bf16 or fp16 (QuantAttnArgs::bf16).
+template <bool F32, int FMT, int HD, int BS>
 struct Shape {
     static constexpr int R = kvq::row_bytes(FMT, HD), CODES = kvq::code_bytes(FMT, HD);
-    static constexpr int STAGE = 2 * kTile * R;  // bytes of a stage: K rows, V rows
-    // (fp32 queries' fragments take a stage's room)
-    static constexpr int STAGES = FMT == KV_E2M1 && HD == 64 ? 4 : FMT == KV_E2M1 && sizeof(T) == 4 ? 2 : 3;
-    // warps per CTA and CTAs per SM: what the rings leave of an SM's shared memory
-    static constexpr int WARPS = STAGE <= 4608 ? 8 : 4;
-    static constexpr int CTAS = FMT == KV_INT8 && HD == 256 ? 1 : 2;
     static constexpr int KS = HD / 16;  // steps of 16 dims
-};
-__host__ __device__ constexpr int up16(int n) { return (n + 15) / 16 * 16; }
-template <typename T> constexpr int kQParts = sizeof(T) == 4 ? 3 : 1;
-template <typename T> constexpr int kPParts = sizeof(T) == 4 ? 2 : 1;
-template <typename T, int HD> constexpr bool kQShared = sizeof(T) == 4 || HD == 256;  // q's fragments in shared memory
-
-// Shared memory: rings, then q's fragments, barriers and masks. The merge runs over the drained rings: the warps'
-// partial outputs [WARPS][8][HD + 4] and statistics, then the CTA's result.
-template <typename T, int FMT, int HD>
-struct Mem {
-    using S = Shape<T, FMT, HD>;
-    static constexpr int ring = S::WARPS * S::STAGES * S::STAGE;
+    static constexpr int QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;
+    // q's fragments in shared memory, one copy for the CTA: where the registers do not hold them
+    static constexpr bool Q_SHARED = F32 || HD == 256;
+    static constexpr int Q_BYTES = Q_SHARED ? QP * KS * 32 * 8 : 0;
+    static constexpr int PAGES = kTile / BS;        // of a tile
+    static constexpr int STAGE = 2 * kTile * R;     // bytes of a stage: K rows, V rows
+    static constexpr int WARPS = STAGE <= 4608 ? 8 : 4;
+    static constexpr int CTAS = FMT == KV_INT8 && HD == 256 ? 1 : 2;  // per SM
+    static constexpr int FIT = (233472 / CTAS - 1024 - 1536 - Q_BYTES) / (WARPS * STAGE);
+    static constexpr int STAGES = FIT > 4 ? 4 : FIT;
+    static_assert(STAGES >= 2, "a tile under way beside the one at work");
+    // shared memory: rings, q's fragments and their factors, the stages' barriers and masks
+    static constexpr int ring = WARPS * STAGES * STAGE;
     static constexpr int q_at = ring;
-    static constexpr int factor_at = q_at + (kQShared<T, HD> ? kQParts<T> * S::KS * 32 * 8 : 0);
+    static constexpr int factor_at = q_at + Q_BYTES;
     static constexpr int bar_at = factor_at + 8 * 4;
-    static constexpr int mask_at = bar_at + S::WARPS * S::STAGES * 8;
-    static constexpr int total = up16(mask_at + S::WARPS * S::STAGES * 4);
+    static constexpr int mask_at = bar_at + WARPS * STAGES * 8;
+    static constexpr int total = (mask_at + WARPS * STAGES * 4 + 15) / 16 * 16;
+    // the merge, over the drained rings: the warps' partial outputs and statistics, then the CTA's result
     static constexpr int HS = HD + 4;  // floats between heads
-    static constexpr int part_ml = S::WARPS * 8 * HS * 4;
-    static constexpr int res_ml = part_ml + S::WARPS * 16 * 4;
+    static constexpr int part_ml = WARPS * 8 * HS * 4;
+    static constexpr int res_ml = part_ml + WARPS * 16 * 4;
     static constexpr int res_o = res_ml + 16 * 4;
     static_assert(res_o + 8 * HD * 4 <= ring, "the merge fits over the rings");
 };
@@ -94,13 +99,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// A bulk copy of a page's rows (16-byte aligned on both sides, a multiple of 16 bytes) that completes on `bar`.
-__device__ __forceinline__ void copy_rows(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 // N words from shared memory at a multiple of ALIGN bytes.
 template <int N, int ALIGN>
 __device__ __forceinline__ void words(const uint8_t* p, uint32_t (&w)[N]) {
@@ -121,109 +119,140 @@ __device__ __forceinline__ uint32_t e2m1_byte(uint32_t w, int i) {
 }
 __device__ __forceinline__ uint32_t int8_half(uint32_t w, int i) { return i == 0 ? kvq::int8_pair<0, 1>(w) : kvq::int8_pair<2, 3>(w); }
 
-// Q as B fragments: step e = 4 j + i holds dims 64 j + 16 ft + 4 i + {0, 1} (b0) and {2, 3} (b1) of head fg.
-template <typename T, int HD>
-struct Query {
-    static constexpr int KS = HD / 16, QP = kQParts<T>;
-    uint32_t reg[kQShared<T, HD> ? 1 : KS][2];
-    const uint2* shared;
-    float factor[2];  // of the scores of heads 2 ft and 2 ft + 1: the softmax scale in base 2 and q's power of two
+__device__ __forceinline__ float from_16(uint32_t bits, bool bf16) {
+    return bf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+// Element i of an output row.
+template <bool F32>
+__device__ __forceinline__ void put(void* out, int64_t i, float v, bool bf16) {
+    if constexpr (F32) static_cast<float*>(out)[i] = v;
+    else static_cast<unsigned short*>(out)[i] = bf16 ? Elem<__nv_bfloat16>::to_bits16(v) : Elem<__half>::to_bits16(v);
+}
 
-    // Every warp loads it into its registers or, where it is kept in shared memory, warp 0 into that (the CTA's barrier and
-    // shared_factors() follow).
-    __device__ __forceinline__ void load(const T* row, bool there, bool wide, float scale_log2, uint2* keep, float* factors,
-                                         int warp, int lane) {
+// Q as B fragments: step e = 4 j + i holds dims 64 j + 16 ft + 4 i + {0, 1} (b0) and {2, 3} (b1) of head fg.
+template <typename S, bool F32, int HD>
+struct Query {
+    static constexpr int KS = S::KS, QP = S::QP;
+    uint32_t reg[S::Q_SHARED ? 1 : KS][2];
+    const uint2* shared;
+    float factor[2];  // of the scores of heads 2 ft and 2 ft + 1: the softmax scale's size in base 2 and q's power of two
+
+    // Every warp loads it into its registers or, where it is kept in shared memory, warp 0 into that, and the CTA's warps meet.
+    // row: the pair's first element in q.
+    __device__ __forceinline__ void load(const QuantAttnArgs& a, int64_t row, unsigned char* smem, int warp, int lane) {
         const int fg = lane >> 2, ft = lane & 3;
-        shared = keep + lane;
-        if (kQShared<T, HD> && warp != 0) return;
-        float x[HD / 4];
+        uint2* keep = reinterpret_cast<uint2*>(smem + S::q_at) + lane;
+        float* factors = reinterpret_cast<float*>(smem + S::factor_at);
+        shared = keep;
+        if (!S::Q_SHARED || warp == 0) {
+            float x[HD / 4];
 #pragma unroll
-        for (int j = 0; j < HD / 64; ++j) {
-            const T* p = row + static_cast<int64_t>(fg) * HD + 64 * j + 16 * ft;
-            if (!there) {
+            for (int j = 0; j < HD / 64; ++j) {
+                const int64_t at = row + static_cast<int64_t>(fg) * HD + 64 * j + 16 * ft;
+                if (fg >= a.group) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[16 * j + k] = 0.0f;
-            } else if (wide) {
-                constexpr int V = vec16<T>();
+                    for (int k = 0; k < 16; ++k) x[16 * j + k] = 0.0f;
+                } else if constexpr (F32) {
+                    const float* p = static_cast<const float*>(a.q) + at;
 #pragma unroll
-                for (int k = 0; k < 16; k += V) {
-                    float f[V];
-                    Vec<T, V>::unpack(Vec<T, V>::load(p + k), f);
+                    for (int k = 0; k < 16; k += 4) {
+                        if (a.wide_q) {
+                            const float4 v = *reinterpret_cast<const float4*>(p + k);
+                            x[16 * j + k] = v.x, x[16 * j + k + 1] = v.y, x[16 * j + k + 2] = v.z, x[16 * j + k + 3] = v.w;
+                        } else {
 #pragma unroll
-                    for (int c = 0; c < V; ++c) x[16 * j + k + c] = f[c];
+                            for (int c = 0; c < 4; ++c) x[16 * j + k + c] = p[k + c];
+                        }
+                    }
+                } else {
+                    const unsigned short* p = static_cast<const unsigned short*>(a.q) + at;
+#pragma unroll
+                    for (int k = 0; k < 16; k += 8) {
+                        if (a.wide_q) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(p + k);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) x[16 * j + k + c] = from_16((word(v, c / 2) >> (16 * (c & 1))) & 0xffffu, a.bf16);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) x[16 * j + k + c] = from_16(p[k + c], a.bf16);
+                        }
+                    }
                 }
+            }
+            if (a.scale_log2 < 0.0f) {  // the sign goes to q: the scores' factor is not negative
+#pragma unroll
+                for (int k = 0; k < HD / 4; ++k) x[k] = -x[k];
+            }
+            float back = 1.0f;
+            if (F32 || a.bf16) {
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < HD / 4; ++k) {
+                    const float v = fabsf(x[k]);
+                    top = v < INFINITY ? fmaxf(top, v) : top;
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127: 0 or subnormal
+                const int up = top == 0.0f ? 0 : min(14 - e, 126);
+                const float to = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+                for (int k = 0; k < HD / 4; ++k) x[k] *= to;
+            }
+#pragma unroll
+            for (int part = 0; part < QP; ++part)
+#pragma unroll
+                for (int e = 0; e < KS; ++e) {
+                    float* y = x + 4 * e;
+                    const uint32_t b0 = pack_h2(y[0], y[1]), b1 = pack_h2(y[2], y[3]);
+                    if constexpr (S::Q_SHARED) keep[(part * KS + e) * 32] = make_uint2(b0, b1);
+                    else reg[e][0] = b0, reg[e][1] = b1;
+                    if constexpr (QP > 1) {  // what is left (nothing of infinities and NaN)
+                        const float2 f0 = unpack_h2(b0), f1 = unpack_h2(b1);
+                        const float f[4] = {f0.x, f0.y, f1.x, f1.y};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[k] = fabsf(f[k]) < INFINITY ? y[k] - f[k] : 0.0f;
+                    }
+                }
+            const float f = back * fabsf(a.scale_log2);
+            if constexpr (S::Q_SHARED) {
+                if (ft == 0) factors[fg] = f;
             } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) x[16 * j + k] = to_f32(p[k]);
+                factor[0] = __shfl_sync(0xffffffffu, f, 8 * ft);
+                factor[1] = __shfl_sync(0xffffffffu, f, 8 * ft + 4);
             }
         }
-        float back = 1.0f;
-        if constexpr (!std::is_same_v<T, __half>) {
-            float top = 0.0f;
-#pragma unroll
-            for (int k = 0; k < HD / 4; ++k) {
-                const float a = fabsf(x[k]);
-                top = a < INFINITY ? fmaxf(top, a) : top;
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127: 0 or subnormal
-            const int up = top == 0.0f ? 0 : min(14 - e, 126);
-            const float to = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-            back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-#pragma unroll
-            for (int k = 0; k < HD / 4; ++k) x[k] *= to;
+        if constexpr (S::Q_SHARED) {
+            __syncthreads();
+            factor[0] = factors[2 * ft], factor[1] = factors[2 * ft + 1];
         }
-#pragma unroll
-        for (int part = 0; part < QP; ++part)
-#pragma unroll
-            for (int e = 0; e < KS; ++e) {
-                float* y = x + 4 * e;
-                const uint32_t b0 = pack_h2(y[0], y[1]), b1 = pack_h2(y[2], y[3]);
-                if constexpr (kQShared<T, HD>) keep[(part * KS + e) * 32 + lane] = make_uint2(b0, b1);
-                else reg[e][0] = b0, reg[e][1] = b1;
-                if constexpr (QP > 1) {  // what is left (nothing of infinities and NaN)
-                    const float2 f0 = unpack_h2(b0), f1 = unpack_h2(b1);
-                    const float f[4] = {f0.x, f0.y, f1.x, f1.y};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = fabsf(f[k]) < INFINITY ? y[k] - f[k] : 0.0f;
-                }
-            }
-        const float f = back * scale_log2;
-        if constexpr (kQShared<T, HD>) {
-            if (ft == 0) factors[fg] = f;
-        } else {
-            factor[0] = __shfl_sync(0xffffffffu, f, 8 * ft);
-            factor[1] = __shfl_sync(0xffffffffu, f, 8 * ft + 4);
-        }
-    }
-    __device__ __forceinline__ void shared_factors(const float* factors, int lane) {
-        factor[0] = factors[2 * (lane & 3)], factor[1] = factors[2 * (lane & 3) + 1];
     }
     __device__ __forceinline__ uint2 get(int part, int e) const {
-        if constexpr (kQShared<T, HD>) return shared[(part * KS + e) * 32];
+        if constexpr (S::Q_SHARED) return shared[(part * KS + e) * 32];
         else return make_uint2(reg[e][0], reg[e][1]);
     }
 };
 
 // S^T of a tile: lane (fg, ft) gets the scores of tokens 16 u + 4 (fg / 2) + fg % 2 (k < 2) and those two further (k >= 2) for heads
 // 2 ft + k % 2 in s[u][k].
-template <typename T, int FMT, int HD>
-__device__ __forceinline__ void scores(const uint8_t* kt, const Query<T, HD>& q, float (&s)[2][4], int lane) {
-    using S = Shape<T, FMT, HD>;
-    constexpr int WORDS = FMT == KV_E2M1 ? 2 : 4;  // words of a group of 16 codes
+template <typename S, bool F32, int FMT, int HD>
+__device__ __forceinline__ void scores(const uint8_t* kt, const Query<S, F32, HD>& q, float (&s)[kHalves][4], int lane) {
+        constexpr int WORDS = FMT == KV_E2M1 ? 2 : 4;  // words of a group of 16 codes
     const int fg = lane >> 2, ft = lane & 3;
     const uint8_t* r0 = kt + (4 * (fg >> 1) + (fg & 1)) * S::R;
-    float fine[2][4];  // fp32: the products with the lower parts of q
+    // fp32: the products with the lower parts of q; otherwise those of every other step, so that four chains of products
+    // are under way instead of two
+    float fine[kHalves][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kHalves; ++u)
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[u][k] = fine[u][k] = 0.0f;
 #pragma unroll
     for (int j = 0; j < HD / 64; ++j) {
-        uint32_t w[2][2][WORDS], sc[2][2];
+        uint32_t w[kHalves][2][WORDS], sc[kHalves][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kHalves; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint8_t* r = r0 + (16 * u + 2 * h) * S::R;
@@ -238,7 +267,7 @@ __device__ __forceinline__ void scores(const uint8_t* kt, const Query<T, HD>& q,
         for (int i = 0; i < 4; ++i) {
             const uint2 b = q.get(0, 4 * j + i);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < kHalves; ++u) {
                 uint32_t a[4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -247,7 +276,7 @@ __device__ __forceinline__ void scores(const uint8_t* kt, const Query<T, HD>& q,
                         a[h + 2 * c] = kvq::mul2(FMT == KV_E2M1 ? e2m1_byte(w[u][h][i >> 1], (2 * i + c) & 3)
                                                                 : int8_half(w[u][h][i], c),
                                                  sc[u][h]);
-                if constexpr (sizeof(T) == 4) {
+                if constexpr (F32) {
                     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                     mma(part, a, b.x, b.y);
 #pragma unroll
@@ -256,41 +285,43 @@ __device__ __forceinline__ void scores(const uint8_t* kt, const Query<T, HD>& q,
                     mma(fine[u], a, b1.x, b1.y);
                     mma(fine[u], a, b2.x, b2.y);
                 } else {
-                    mma(s[u], a, b.x, b.y);
+                    mma(i & 1 ? fine[u] : s[u], a, b.x, b.y);
                 }
             }
         }
     }
-    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kHalves; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[u][k] += fine[u][k];
-    }
+        for (int k = 0; k < 4; ++k) s[u][k] += fine[u][k];
 }
 
 // The running softmax over those scores (valid: a bit per token): maxima m of the lane's two heads, this lane's tokens' part l of
 // their sums, corr = 2^(old m - new m); the probabilities, relative to 2^(m - kUnder), as l, as B fragments of the next
 // product.
 template <int PP>
-__device__ __forceinline__ void softmax(float (&p)[2][4], unsigned valid, const float (&factor)[2], float (&m)[2], float (&l)[2],
-                                        float (&corr)[2], uint32_t (&pb)[PP][2][2], int lane) {
+__device__ __forceinline__ void softmax(float (&p)[kHalves][4], uint32_t valid, bool whole, const float (&factor)[2], float (&m)[2], float (&l)[2],
+                                        float (&corr)[2], uint32_t (&pb)[PP][kHalves][2], int lane) {
     const unsigned FULL = 0xffffffffu;
     const int fg = lane >> 2;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kHalves; ++u)
 #pragma unroll
         for (int k = 0; k < 4; ++k) p[u][k] *= factor[k & 1];
-    if (valid != FULL) {
+    if (!whole) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kHalves; ++u)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (!((valid >> (16 * u + 4 * (fg >> 1) + (fg & 1) + (k & 2))) & 1u)) p[u][k] = -INFINITY;
     }
     float mx[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) mx[h] = fmaxf(fmaxf(p[0][h], p[0][h + 2]), fmaxf(p[1][h], p[1][h + 2]));
+    for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(p[0][h], p[0][h + 2]);
+#pragma unroll
+        for (int u = 1; u < kHalves; ++u) mx[h] = fmaxf(mx[h], fmaxf(p[u][h], p[u][h + 2]));
+    }
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
         const float a = __shfl_xor_sync(FULL, mx[0], x), b = __shfl_xor_sync(FULL, mx[1], x);
@@ -305,7 +336,7 @@ __device__ __forceinline__ void softmax(float (&p)[2][4], unsigned valid, const 
         m[h] = now;
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kHalves; ++u) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) p[u][k] = ex2(p[u][k] - base[k & 1]);
 #pragma unroll
@@ -319,15 +350,19 @@ __device__ __forceinline__ void softmax(float (&p)[2][4], unsigned valid, const 
         }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) l[h] = fmaf(l[h], corr[h], (p[0][h] + p[0][h + 2]) + (p[1][h] + p[1][h + 2]));
+    for (int h = 0; h < 2; ++h) {
+        float sum = p[0][h] + p[0][h + 2];
+#pragma unroll
+        for (int u = 1; u < kHalves; ++u) sum += p[u][h] + p[u][h + 2];
+        l[h] = fmaf(l[h], corr[h], sum);
+    }
 }
 
 // O^T = O^T corr + V^T P^T: o[d] holds dim fg * HD / 8 + 2 d (k < 2) and the next one (k >= 2) of heads 2 ft + k % 2. Tokens that
 // do not count get a scale of 0.
-template <typename T, int FMT, int HD>
-__device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[kPParts<T>][2][2], const float (&corr)[2],
-                                       unsigned valid, float (&o)[HD / 16][4], int lane) {
-    using S = Shape<T, FMT, HD>;
+template <typename S, bool F32, int FMT, int HD>
+__device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[S::PP][kHalves][2], const float (&corr)[2],
+                                       uint32_t valid, bool whole, float (&o)[HD / 16][4], int lane) {
     constexpr int RUN = HD / 8;                         // dims of a lane
     constexpr int PER = FMT == KV_E2M1 ? 8 : 4;         // codes in a word
     constexpr int WORDS = RUN / PER;
@@ -338,7 +373,7 @@ __device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[k
         for (int d = 0; d < HD / 16; ++d) o[d][0] *= corr[0], o[d][1] *= corr[1], o[d][2] *= corr[0], o[d][3] *= corr[1];
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kHalves; ++u) {
         const uint8_t* r0 = vt + (16 * u + 4 * ft) * S::R;
         uint32_t w[4][WORDS], sc[2][GROUPS];
 #pragma unroll
@@ -348,12 +383,14 @@ __device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[k
             const int at = S::CODES + fg * RUN / kvq::kGroup + g;
             uint32_t b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                b[i] = r0[i * S::R + at];
-                if (valid != 0xffffffffu && !((valid >> (16 * u + 4 * ft + i)) & 1u)) b[i] = 0;
+            for (int i = 0; i < 4; ++i) b[i] = r0[i * S::R + at];
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!((valid >> (16 * u + 4 * ft + i)) & 1u)) b[i] = 0;
             }
-            sc[0][g] = (b[0] | b[1] << 16) << 7;
-            sc[1][g] = (b[2] | b[3] << 16) << 7;
+            sc[0][g] = b[0] * 0x80u + b[1] * 0x800000u;
+            sc[1][g] = b[2] * 0x80u + b[3] * 0x800000u;
         }
 #pragma unroll
         for (int c = 0; c < WORDS; ++c) {
@@ -380,9 +417,9 @@ __device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[k
                     a[2 * e + 1] = kvq::mul2(FMT == KV_E2M1 ? e2m1_byte(odd[e], k) : int8_half(odd[e], k), *s2[e]);
                 }
                 const int d = c * (PER / 2) + k;
-                if constexpr (sizeof(T) == 4) {
+                if constexpr (F32) {
                     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma(part, a, pb[kPParts<T> - 1][u][0], pb[kPParts<T> - 1][u][1]);
+                    mma(part, a, pb[S::PP - 1][u][0], pb[S::PP - 1][u][1]);
                     mma(part, a, pb[0][u][0], pb[0][u][1]);
 #pragma unroll
                     for (int n = 0; n < 4; ++n) o[d][n] += part[n];
@@ -394,118 +431,28 @@ __device__ __forceinline__ void values(const uint8_t* vt, const uint32_t (&pb)[k
     }
 }
 
-// Tiles [t0, t1) of a pair. Leaves the CTA's maxima and sums (res_ml) and unnormalised output (res_o) in shared memory.
-template <typename T, int FMT, int HD>
-__device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* smem, int64_t b, int kvh, int len, int t0, int t1,
-                                        uint32_t* turn) {
-    using S = Shape<T, FMT, HD>;
-    using M = Mem<T, FMT, HD>;
-    constexpr int W = S::WARPS, ST = S::STAGES;
-    const unsigned FULL = 0xffffffffu;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, fg = lane >> 2, ft = lane & 3;
-    const int G = a.group, bs_log2 = __ffs(a.block_size) - 1, per_tile = kTile >> bs_log2;
-    const uint32_t page_bytes = static_cast<uint32_t>(S::R) << bs_log2;
-    unsigned char* ring = smem + warp * ST * S::STAGE;
-    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + M::bar_at) + warp * ST;
-    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + M::mask_at) + warp * ST;
-    const uint8_t* cache = static_cast<const uint8_t*>(a.cache) + static_cast<int64_t>(kvh) * page_bytes;
-    const int64_t page_step = static_cast<int64_t>(a.n_kv) * page_bytes;
-    const int32_t* table = a.table + b * a.max_blocks;
-    const int pages = (len + a.block_size - 1) >> bs_log2;
-
-    // Lane k < per_tile has the entry of page k of a tile; asked for a tile ahead of the copies.
-    auto entry = [&](int t) -> int32_t {
-        const int j = t * per_tile + lane;
-        return t < t1 && lane < per_tile && j < pages ? __ldcg(table + j) : -1;
-    };
-    const unsigned all_pages = FULL >> (32 - per_tile);
-    auto issue = [&](int t, int32_t page, int stage) {
-        const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_blocks);  // (-1 where unused)
-        const unsigned good = __ballot_sync(FULL, ok);
-        uint32_t count = FULL;
-        if (good != all_pages || len - t * kTile < kTile) {
-            count = 0;
-            for (int k = 0; k < per_tile; ++k)
-                if ((good >> k) & 1u) count |= (FULL >> (32 - a.block_size)) << (k << bs_log2);
-            const int left = len - t * kTile;
-            if (left < kTile) count &= (1u << left) - 1u;
-            if (!ok && lane < per_tile && t * per_tile + lane < pages && kvh == 0 && a.err) atomicAdd(a.err, 1);
-        }
-        if (lane == 0) {
-            mask[stage] = count;
-            mbar_arrive_expect_tx(bar + stage, 2 * page_bytes * __popc(good));
-        }
-        __syncwarp();
-        if (ok) {
-            const uint32_t dst = smem_u32(ring + stage * S::STAGE) + lane * page_bytes;
-            const uint8_t* src = cache + page * page_step;
-            copy_rows(dst, src, page_bytes, bar + stage);
-            copy_rows(dst + kTile * S::R, src + a.plane_bytes, page_bytes, bar + stage);
-        }
-    };
-
-    int32_t page[ST];
-#pragma unroll
-    for (int s = 0; s < ST; ++s) page[s] = entry(t0 + warp + s * W);
-    int32_t next = entry(t0 + warp + ST * W);
-    // q's fragments come in while the first tiles do
-    Query<T, HD> q;
-#pragma unroll
-    for (int s = 0; s < ST; ++s)
-        if (t0 + warp + s * W < t1) issue(t0 + warp + s * W, page[s], s);
-    {
-        const T* row = static_cast<const T*>(a.q) + b * a.qs + static_cast<int64_t>(kvh) * G * HD;
-        float* factors = reinterpret_cast<float*>(smem + M::factor_at);
-        q.load(row, fg < G, a.wide_q, a.scale_log2, reinterpret_cast<uint2*>(smem + M::q_at), factors, warp, lane);
-        if constexpr (kQShared<T, HD>) {
-            __syncthreads();
-            q.shared_factors(factors, lane);
-        }
-    }
-    float o[HD / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int d = 0; d < HD / 16; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.0f;
-    int stage = 0;
-    uint32_t phase = *turn;  // parity of the stages' next phases, a bit each
-    for (int t = t0 + warp; t < t1; t += W) {
-        mbar_wait(bar + stage, (phase >> stage) & 1u);
-        phase ^= 1u << stage;
-        const unsigned valid = mask[stage];
-        const uint8_t* kt = ring + stage * S::STAGE;
-        float s[2][4], corr[2];
-        uint32_t pb[kPParts<T>][2][2];
-        scores<T, FMT, HD>(kt, q, s, lane);
-        softmax<kPParts<T>>(s, valid, q.factor, m, l, corr, pb, lane);
-        values<T, FMT, HD>(kt + kTile * S::R, pb, corr, valid, o, lane);
-        __syncwarp();  // every lane is done with the stage
-        const int32_t p = next;
-        next = entry(t + (ST + 1) * W);
-        if (t + ST * W < t1) issue(t + ST * W, p, stage);
-        stage = stage + 1 == ST ? 0 : stage + 1;
-    }
-    *turn = phase;
-    // the warps' parts
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) {
-        l[0] += __shfl_xor_sync(FULL, l[0], x);
-        l[1] += __shfl_xor_sync(FULL, l[1], x);
-    }
-    __syncthreads();  // all rings are drained
-    float* po = reinterpret_cast<float*>(smem) + warp * 8 * M::HS;
-    float* ml = reinterpret_cast<float*>(smem + M::part_ml);
+// The warps' maxima, sums (of all their lanes) and outputs of one pair, merged over the drained rings: the CTA's maxima and sums (res_ml) and
+// unnormalised output (res_o) in shared memory.
+template <typename S, int HD>
+__device__ __forceinline__ void merge_warps(unsigned char* smem, const float (&o)[HD / 16][4], const float (&m)[2], const float (&l)[2],
+                                            int G, int warp, int lane) {
+    constexpr int W = S::WARPS;
+    const int fg = lane >> 2, ft = lane & 3;
+    float* po = reinterpret_cast<float*>(smem) + warp * 8 * S::HS;
+    float* ml = reinterpret_cast<float*>(smem + S::part_ml);
     if (fg == 0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) ml[warp * 16 + 2 * ft + h] = m[h], ml[warp * 16 + 8 + 2 * ft + h] = l[h];
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float* row = po + (2 * ft + h) * M::HS + fg * (HD / 8);
+        float* row = po + (2 * ft + h) * S::HS + fg * (HD / 8);
 #pragma unroll
         for (int d = 0; d < HD / 16; ++d) *reinterpret_cast<float2*>(row + 2 * d) = make_float2(o[d][h], o[d][2 + h]);
     }
     __syncthreads();
-    float* res = reinterpret_cast<float*>(smem + M::res_ml);
-    float* ro = reinterpret_cast<float*>(smem + M::res_o);
+    float* res = reinterpret_cast<float*>(smem + S::res_ml);
+    float* ro = reinterpret_cast<float*>(smem + S::res_o);
     const float* all = reinterpret_cast<const float*>(smem);
     for (int i = threadIdx.x; i < G * HD; i += W * 32) {
         const int g = i / HD, d = i - g * HD;
@@ -519,44 +466,147 @@ __device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* s
             // (a part without scores above -inf has a sum of 0, or NaN)
             const float f = ml[w * 16 + g] == -INFINITY ? 1.0f : ex2(ml[w * 16 + g] - top);
             sum = fmaf(f, lw, sum);
-            acc = fmaf(f, all[w * 8 * M::HS + g * M::HS + d], acc);
+            acc = fmaf(f, all[w * 8 * S::HS + g * S::HS + d], acc);
         }
         ro[i] = acc;
         if (d == 0) res[g] = top, res[8 + g] = sum;
     }
 }
 
-template <typename T, int FMT, int HD>
-__global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, HD>::CTAS) cluster_kernel(QuantAttnArgs a) {
-    using S = Shape<T, FMT, HD>;
-    using M = Mem<T, FMT, HD>;
+// A bulk copy of a page's rows (16-byte aligned on both sides, a multiple of 16 bytes) that completes on `bar`.
+__device__ __forceinline__ void copy_rows(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+template <typename S>
+__device__ __forceinline__ void init_barriers(unsigned char* smem) {  // each warp its own
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane < S::STAGES) {
+        mbar_init(reinterpret_cast<uint64_t*>(smem + S::bar_at) + warp * S::STAGES + lane, 1);
+        mbar_init_fence();
+    }
+    __syncwarp();
+}
+
+// The tiles first + warp, first + warp + stride, ... below `end` of a pair whose request has `len` tokens. Leaves the CTA's
+// maxima and sums (res_ml) and unnormalised output (res_o) in shared memory; the CTA's warps meet before they are read.
+template <typename S, bool F32, int FMT, int HD, int BS>
+__device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* smem, int64_t b, int kvh, int len, int first, int stride,
+                                        int end, uint32_t* turn) {
+    constexpr int ST = S::STAGES, PAGES = S::PAGES;
+    constexpr uint32_t PAGE_BYTES = BS * S::R;
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.group;
+    unsigned char* ring = smem + warp * ST * S::STAGE;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::bar_at) + warp * ST;
+    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + S::mask_at) + warp * ST;
+    const int64_t page_step = static_cast<int64_t>(a.n_kv) * PAGE_BYTES;
+    const uint8_t* cache = static_cast<const uint8_t*>(a.cache) + static_cast<int64_t>(kvh) * PAGE_BYTES;
+    const int32_t* table = a.table + b * a.max_blocks;
+
+    // Lane k < PAGES has the entry of page k of a tile, asked for a tile ahead of the copies. (The entries of the first tiles are asked
+    // for together with the request's length: whether they are in use shows when the copies are made.)
+    auto entry = [&](int t) -> int32_t {
+        const int64_t j = static_cast<int64_t>(t) * PAGES + lane;
+        return lane < PAGES && j < a.max_blocks ? __ldcg(table + j) : -1;
+    };
+    auto issue = [&](int t, int32_t page, int stage) {
+        const int left = len - t * kTile;  // tokens from here on
+        const bool used = lane * BS < left && lane < PAGES;
+        const bool ok = used && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_blocks);
+        const unsigned good = __ballot_sync(FULL, ok);
+        uint32_t valid = FULL;
+        if (good != FULL >> (32 - PAGES) || left < kTile) {  // the last tile of a request, or bad entries
+            valid = 0;
+#pragma unroll
+            for (int k = 0; k < PAGES; ++k)
+                if ((good >> k) & 1u) valid |= (FULL >> (32 - BS)) << (k * BS & 31);
+            if (left < kTile) valid &= (1u << left) - 1u;
+            if (used && !ok && kvh == 0 && a.err) atomicAdd(a.err, 1);
+        }
+        if (lane == 0) {
+            mask[stage] = valid;
+            mbar_arrive_expect_tx(bar + stage, 2 * PAGE_BYTES * __popc(good));
+        }
+        __syncwarp();
+        if (ok) {
+            const uint32_t dst = smem_u32(ring + stage * S::STAGE) + lane * PAGE_BYTES;
+            const uint8_t* src = cache + page * page_step;
+            copy_rows(dst, src, PAGE_BYTES, bar + stage);
+            copy_rows(dst + kTile * S::R, src + a.plane_bytes, PAGE_BYTES, bar + stage);
+        }
+    };
+
+    const int t0 = first + warp;
+    int32_t page[ST];
+#pragma unroll
+    for (int s = 0; s < ST; ++s) page[s] = entry(t0 + s * stride);
+    int32_t next = entry(t0 + ST * stride);
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+        if (t0 + s * stride < end) issue(t0 + s * stride, page[s], s);
+    }
+    Query<S, F32, HD> q;  // comes in while the first tiles do
+    q.load(a, b * a.qs + static_cast<int64_t>(kvh) * G * HD, smem, warp, lane);
+    float o[HD / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.0f;
+    int stage = 0;
+    uint32_t phase = *turn;  // parity of the stages' next phases, a bit each
+    for (int t = t0; t < end; t += stride) {
+        mbar_wait(bar + stage, (phase >> stage) & 1u);
+        phase ^= 1u << stage;
+        const uint32_t valid = mask[stage];
+        const bool whole = valid == FULL;
+        const uint8_t* kt = ring + stage * S::STAGE;
+        float s[kHalves][4], corr[2];
+        uint32_t pb[S::PP][kHalves][2];
+        scores<S, F32, FMT, HD>(kt, q, s, lane);
+        softmax<S::PP>(s, valid, whole, q.factor, m, l, corr, pb, lane);
+        values<S, F32, FMT, HD>(kt + kTile * S::R, pb, corr, valid, whole, o, lane);
+        __syncwarp();  // every lane is done with the stage
+        const int32_t now = next;
+        next = entry(t + (ST + 1) * stride);
+        if (t + ST * stride < end) issue(t + ST * stride, now, stage);
+        stage = stage + 1 == ST ? 0 : stage + 1;
+    }
+    *turn = phase;
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+        l[0] += __shfl_xor_sync(FULL, l[0], x);
+        l[1] += __shfl_xor_sync(FULL, l[1], x);
+    }
+    __syncthreads();  // all rings are drained
+    merge_warps<S, HD>(smem, o, m, l, G, warp, lane);
+}
+
+__device__ __forceinline__ int tokens_of(const QuantAttnArgs& a, int64_t b) {
+    const int64_t n = __ldcg(a.seq_lens + b), cap = a.max_blocks * a.block_size;
+    return static_cast<int>(n < 0 ? 0 : (n > cap ? cap : n));
+}
+
+template <bool F32, int FMT, int HD, int BS>
+__global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32, FMT, HD, BS>::CTAS) cluster_kernel(QuantAttnArgs a) {
+    using S = Shape<F32, FMT, HD, BS>;
     extern __shared__ __align__(128) unsigned char smem[];
     cg::cluster_group cluster = cg::this_cluster();
     const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int64_t pair = blockIdx.x / splits, b = pair / a.n_kv;
     const int kvh = static_cast<int>(pair - b * a.n_kv), G = a.group;
-    if (threadIdx.x < S::WARPS * S::STAGES) {
-        mbar_init(reinterpret_cast<uint64_t*>(smem + M::bar_at) + threadIdx.x, 1);
-        mbar_init_fence();
-    }
-    __syncthreads();
+    init_barriers<S>(smem);
     pdl_enter();
-    int64_t n = __ldcg(a.seq_lens + b);
-    const int64_t cap = a.max_blocks * a.block_size;
-    if ((n < 0 || n > cap) && kvh == 0 && rank == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
-    const int len = static_cast<int>(n < 0 ? 0 : (n > cap ? cap : n));
-    const int tiles = (len + kTile - 1) / kTile, per = (tiles + splits - 1) / splits;
-    const int t0 = min(rank * per, tiles), t1 = min(t0 + per, tiles);
+    const int len = tokens_of(a, b);
     uint32_t turn = 0;
-    segment<T, FMT, HD>(a, smem, b, kvh, len, t0, t1, &turn);
-    T* out = static_cast<T*>(a.out) + b * a.os + static_cast<int64_t>(kvh) * G * HD;
-    const float* res = reinterpret_cast<const float*>(smem + M::res_ml);
-    const float* ro = reinterpret_cast<const float*>(smem + M::res_o);
+    if (kvh == 0 && rank == 0 && threadIdx.x == 0 && a.err && a.seq_lens[b] != len) atomicAdd(a.err, 1);
+    segment<S, F32, FMT, HD, BS>(a, smem, b, kvh, len, rank * S::WARPS, splits * S::WARPS, (len + kTile - 1) / kTile, &turn);
+    const int64_t out = b * a.os + static_cast<int64_t>(kvh) * G * HD;
+    const float* res = reinterpret_cast<const float*>(smem + S::res_ml);
     if (splits == 1) {
         __syncthreads();
         for (int i = threadIdx.x; i < G * HD; i += S::WARPS * 32) {
             const float l = res[8 + i / HD];
-            out[i] = from_f32<T>(l != 0.0f ? ro[i] / l : 0.0f);
+            put<F32>(a.out, out + i, l != 0.0f ? res[16 + i] / l : 0.0f, a.bf16);
         }
         return;
     }
@@ -572,7 +622,7 @@ __global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, H
             sum = fmaf(f, o[8 + g], sum);
             acc = fmaf(f, o[16 + i], acc);
         }
-        out[i] = from_f32<T>(sum != 0.0f ? acc / sum : 0.0f);
+        put<F32>(a.out, out + i, sum != 0.0f ? acc / sum : 0.0f, a.bf16);
     }
     cluster.sync();  // nobody reads this CTA's part any more
 }
@@ -581,26 +631,20 @@ __global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, H
 // the GPU holds. A CTA writes the outputs of the pairs that it holds whole, and leaves a record [8 max][8 sum][8 x HD] of
 // the one that began before its part (slot 0) and of the one that goes on behind it (slot 1). Every CTA sums the
 // requests' tiles to find its part; CTA 0 leaves the sums for the merge.
-template <typename T, int FMT, int HD>
-__global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, HD>::CTAS) stream_kernel(QuantAttnArgs a) {
-    using S = Shape<T, FMT, HD>;
-    using M = Mem<T, FMT, HD>;
+template <bool F32, int FMT, int HD, int BS>
+__global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32, FMT, HD, BS>::CTAS) stream_kernel(QuantAttnArgs a) {
+    using S = Shape<F32, FMT, HD, BS>;
     constexpr int NT = S::WARPS * 32;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int warp_sum[S::WARPS], found[2];
     if (threadIdx.x == 0) found[0] = 0x7fffffff;
-    if (threadIdx.x < S::WARPS * S::STAGES) {
-        mbar_init(reinterpret_cast<uint64_t*>(smem + M::bar_at) + threadIdx.x, 1);
-        mbar_init_fence();
-    }
+    init_barriers<S>(smem);
+    uint32_t turn = 0;
     pdl_enter();
     const unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = static_cast<int>(a.B), G = a.group;
-    const int64_t cap = a.max_blocks * a.block_size;
     auto length = [&](int b) -> int {
-        if (b >= B) return 0;
-        const int64_t n = __ldcg(a.seq_lens + b);
-        return static_cast<int>(n < 0 ? 0 : (n > cap ? cap : n));
+        return b < B ? tokens_of(a, b) : 0;
     };
     auto tiles_of = [](int len) { return (len + kTile - 1) / kTile; };
     // thread t sums requests [t * each, (t + 1) * each)
@@ -609,8 +653,7 @@ __global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, H
     for (int k = 0; k < each; ++k) {
         const int b = mine0 + k;
         if (blockIdx.x == 0 && a.err && b < B) {
-            const int32_t n = __ldcg(a.seq_lens + b);
-            if (n < 0 || n > cap) atomicAdd(a.err, 1);
+            if (__ldcg(a.seq_lens + b) != tokens_of(a, b)) atomicAdd(a.err, 1);
         }
         mine += tiles_of(length(b));
     }
@@ -656,7 +699,6 @@ __global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, H
     __syncthreads();
     int b = found[0];
     int64_t begin = static_cast<int64_t>(found[1]) * a.n_kv;  // the request's first tile in the stream
-    uint32_t turn = 0;
     int window = b, lens = length(b + lane);  // lane k: request window + k
     while (g0 < g1 && b < B) {
         if (b - window >= 32) window = b, lens = length(b + lane);
@@ -669,15 +711,14 @@ __global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, H
         const int kvh = static_cast<int>((g0 - begin) / n);
         const int t0 = static_cast<int>(g0 - begin - static_cast<int64_t>(kvh) * n);
         const int t1 = g1 - g0 < n - t0 ? t0 + static_cast<int>(g1 - g0) : n;
-        segment<T, FMT, HD>(a, smem, b, kvh, len, t0, t1, &turn);
+        segment<S, F32, FMT, HD, BS>(a, smem, b, kvh, len, t0, S::WARPS, t1, &turn);
         __syncthreads();
-        const float* res = reinterpret_cast<const float*>(smem + M::res_ml);
-        const float* ro = reinterpret_cast<const float*>(smem + M::res_o);
+        const float* res = reinterpret_cast<const float*>(smem + S::res_ml);
         if (t0 == 0 && t1 == n) {
-            T* out = static_cast<T*>(a.out) + b * a.os + static_cast<int64_t>(kvh) * G * HD;
+            const int64_t out = b * a.os + static_cast<int64_t>(kvh) * G * HD;
             for (int i = threadIdx.x; i < G * HD; i += NT) {
                 const float l = res[8 + i / HD];
-                out[i] = from_f32<T>(l != 0.0f ? ro[i] / l : 0.0f);
+                put<F32>(a.out, out + i, l != 0.0f ? res[16 + i] / l : 0.0f, a.bf16);
             }
         } else {
             float* rec = a.ws_rec + (static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * (16 + 8 * HD);
@@ -691,7 +732,7 @@ __global__ void __launch_bounds__(Shape<T, FMT, HD>::WARPS * 32, Shape<T, FMT, H
 
 // out of a pair whose tiles several parts share, and zeros for a request without tokens. A CTA takes 256 / LANES columns; LANES
 // threads share a column's records. The sums meet in a fixed order.
-template <typename T, int HD, int LANES>
+template <bool F32, int HD, int LANES>
 __global__ void __launch_bounds__(256) merge_kernel(QuantAttnArgs a, int ctas, int warps) {
     constexpr int COLS = 256 / LANES;
     __shared__ float s_acc[LANES][COLS], s_sum[LANES][COLS], s_top[LANES][COLS];
@@ -702,11 +743,11 @@ __global__ void __launch_bounds__(256) merge_kernel(QuantAttnArgs a, int ctas, i
     const int col = threadIdx.x % COLS, p = threadIdx.x / COLS;
     const int i = static_cast<int>(blockIdx.x - pair * chunks) * COLS + col, g = i / HD;
     const bool there = i < a.group * HD;
-    const int at = a.ws_at[b], n = a.ws_at[b + 1] - at;
-    const int64_t part = stream_part(static_cast<int64_t>(a.ws_at[a.B]) * a.n_kv, ctas, warps);
-    T* out = static_cast<T*>(a.out) + b * a.os + static_cast<int64_t>(kvh) * a.group * HD;
+    const int at = __ldcg(a.ws_at + b), n = __ldcg(a.ws_at + b + 1) - at;
+    const int64_t part = stream_part(static_cast<int64_t>(__ldcg(a.ws_at + a.B)) * a.n_kv, ctas, warps);
+    const int64_t out = b * a.os + static_cast<int64_t>(kvh) * a.group * HD;
     if (n == 0) {
-        if (p == 0 && there) out[i] = from_f32<T>(0.0f);
+        if (p == 0 && there) put<F32>(a.out, out + i, 0.0f, a.bf16);
         return;
     }
     const int64_t first = static_cast<int64_t>(at) * a.n_kv + static_cast<int64_t>(kvh) * n;
@@ -751,32 +792,42 @@ __global__ void __launch_bounds__(256) merge_kernel(QuantAttnArgs a, int ctas, i
             acc = fmaf(f, s_acc[k][col], acc);
         }
     }
-    if (there) out[i] = from_f32<T>(sum != 0.0f ? acc / sum : 0.0f);
+    if (there) put<F32>(a.out, out + i, sum != 0.0f ? acc / sum : 0.0f, a.bf16);
 }
 
-template <typename T, int FMT, int HD>
+// Bounded waits of this translation unit that ran out, on the current device.
+static unsigned int unit_wait_timeouts() {
+    unsigned int n = 0;
+    if (cudaMemcpyFromSymbol(&n, g_wait_timeouts, sizeof(n)) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+template <bool F32, int FMT, int HD, int BS>
 cudaError_t launch_stream(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
-    using M = Mem<T, FMT, HD>;
-    using S = Shape<T, FMT, HD>;
+    using S = Shape<F32, FMT, HD, BS>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = set_smem_once(stream_kernel<T, FMT, HD>, M::total, true, &done);
+    cudaError_t e = set_smem_once(stream_kernel<F32, FMT, HD, BS>, S::total, true, &done);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(stream_kernel<T, FMT, HD>, dim3(static_cast<unsigned>(p.stream_ctas)), dim3(S::WARPS * 32), M::total, s, p.pdl, 1, a);
+    e = launch_kernel(stream_kernel<F32, FMT, HD, BS>, dim3(static_cast<unsigned>(p.stream_ctas)), dim3(S::WARPS * 32), S::total, s, p.pdl,
+                      1, a);
     if (e != cudaSuccess) return e;
     // pairs that many parts share: eight threads to a column
-    const bool many = a.B * a.n_kv * 8 < p.stream_ctas;
+    const bool many = a.B * a.n_kv * 4 < p.stream_ctas;
     const int cols = many ? 32 : 256;
     const int64_t grid = a.B * a.n_kv * ((a.group * HD + cols - 1) / cols);
-    return launch_kernel(many ? merge_kernel<T, HD, 8> : merge_kernel<T, HD, 1>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, true,
-                         1, a, p.stream_ctas, S::WARPS);
+    return launch_kernel(many ? merge_kernel<F32, HD, 8> : merge_kernel<F32, HD, 1>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s,
+                         true, 1, a, p.stream_ctas, S::WARPS);
 }
 
-template <typename T, int FMT, int HD>
+template <bool F32, int FMT, int HD, int BS>
 cudaError_t launch_cluster(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
-    using M = Mem<T, FMT, HD>;
-    auto kernel = cluster_kernel<T, FMT, HD>;
+    using S = Shape<F32, FMT, HD, BS>;
+    auto kernel = cluster_kernel<F32, FMT, HD, BS>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = set_smem_once(kernel, M::total, true, &done);
+    cudaError_t e = set_smem_once(kernel, S::total, true, &done);
     if (e != cudaSuccess) return e;
     if (p.splits > 8) {
         static std::atomic<uint64_t> wide{0};
@@ -790,44 +841,25 @@ cudaError_t launch_cluster(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaS
             wide.fetch_or(bit, std::memory_order_release);
         }
     }
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(a.B * a.n_kv * p.splits)), dim3(Shape<T, FMT, HD>::WARPS * 32), M::total, s,
-                         p.pdl, p.splits, a);
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(a.B * a.n_kv * p.splits)), dim3(S::WARPS * 32), S::total, s, p.pdl, p.splits, a);
 }
 
-template <typename T, int FMT>
-cudaError_t launch(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
+template <bool F32, int FMT, int HD>
+cudaError_t launch_sized(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
+    switch (a.block_size) {
+        case 8: return p.stream_ctas ? launch_stream<F32, FMT, HD, 8>(a, p, s) : launch_cluster<F32, FMT, HD, 8>(a, p, s);
+        case 16: return p.stream_ctas ? launch_stream<F32, FMT, HD, 16>(a, p, s) : launch_cluster<F32, FMT, HD, 16>(a, p, s);
+        default: return p.stream_ctas ? launch_stream<F32, FMT, HD, 32>(a, p, s) : launch_cluster<F32, FMT, HD, 32>(a, p, s);
+    }
+}
+template <bool F32, int FMT>
+cudaError_t launch_format(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s) {
     switch (p.head_dim) {
-        case 64: return p.stream_ctas ? launch_stream<T, FMT, 64>(a, p, s) : launch_cluster<T, FMT, 64>(a, p, s);
-        case 128: return p.stream_ctas ? launch_stream<T, FMT, 128>(a, p, s) : launch_cluster<T, FMT, 128>(a, p, s);
-        default: return p.stream_ctas ? launch_stream<T, FMT, 256>(a, p, s) : launch_cluster<T, FMT, 256>(a, p, s);
+        case 64: return launch_sized<F32, FMT, 64>(a, p, s);
+        case 128: return launch_sized<F32, FMT, 128>(a, p, s);
+        default: return launch_sized<F32, FMT, 256>(a, p, s);
     }
 }
 
 }  // namespace qattn
-
-int quant_attn_warps(int format, int head_dim) {
-    return 2 * qattn::kTile * kv_row_bytes(format, head_dim) <= 4608 ? 8 : 4;  // Shape::WARPS
-}
-int quant_attn_ctas_per_sm(int format, int head_dim) { return format == KV_INT8 && head_dim == 256 ? 1 : 2; }  // Shape::CTAS
-
-unsigned int quant_attn_wait_timeouts() {
-    unsigned int n = 0;
-    if (cudaMemcpyFromSymbol(&n, g_wait_timeouts, sizeof(n)) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
-}
-
-cudaError_t launch_attention_quant(const QuantAttnArgs& a, const QuantAttnPlan& p, int dtype, cudaStream_t s) {
-    using namespace qattn;
-    const bool e = p.format == KV_E2M1;
-    switch (dtype) {
-        case DT_F32: return e ? launch<float, KV_E2M1>(a, p, s) : launch<float, KV_INT8>(a, p, s);
-        case DT_F16: return e ? launch<__half, KV_E2M1>(a, p, s) : launch<__half, KV_INT8>(a, p, s);
-        case DT_BF16: return e ? launch<__nv_bfloat16, KV_E2M1>(a, p, s) : launch<__nv_bfloat16, KV_INT8>(a, p, s);
-        default: return cudaErrorInvalidValue;
-    }
-}
-
 }  // namespace sra

@@ -233,6 +233,7 @@ struct QuantAttnArgs {
     int n_kv, group, block_size;
     float scale_log2;  // softmax scale * log2(e)
     bool wide_q;       // 16-byte aligned query rows
+    bool bf16;         // of the 16-bit dtypes
     // workspace of the stream form
     int32_t* ws_at = nullptr;   // [B + 1] tiles (of a kv head) before each request
     float* ws_rec = nullptr;    // [CTAs][2][16 + 8 * head_dim]
@@ -243,16 +244,20 @@ inline SRA_HD int64_t stream_part(int64_t all, int64_t ctas, int warps) {
     return part < warps ? warps : part;
 }
 struct QuantAttnPlan {
-    int format, head_dim;
+    int head_dim;
     int splits;       // CTAs per (request, kv head): the cluster size
     int stream_ctas;  // > 0: the stream form, with that many CTAs
     bool pdl;
     int num_sms;
 };
-cudaError_t launch_attention_quant(const QuantAttnArgs& a, const QuantAttnPlan& p, int dtype, cudaStream_t s);
-int quant_attn_warps(int format, int head_dim);  // per CTA
-int quant_attn_ctas_per_sm(int format, int head_dim);
+// Warps per CTA and CTAs per SM (alike for all dtypes and block sizes).
+inline int quant_attn_warps(int format, int head_dim) { return 64 * kv_row_bytes(format, head_dim) <= 4608 ? 8 : 4; }
+inline int quant_attn_ctas(int format, int head_dim) { return format == KV_INT8 && head_dim == 256 ? 1 : 2; }
 unsigned int quant_attn_wait_timeouts();
+cudaError_t launch_attn_quant_e2m1(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s);
+cudaError_t launch_attn_quant_int8(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s);
+cudaError_t launch_attn_quant_e2m1_f32(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s);
+cudaError_t launch_attn_quant_int8_f32(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s);
 
 // ------------------------------------------------------------------- shared prefix
 // The requests' own tokens: tiles of kTailTok tokens of all requests in a row, cut into parts for the

@@ -83,16 +83,35 @@ class Case:
         assert not bad.any(), (what, int(bad.sum()), np.nanmax(np.abs(g - o)), np.argwhere(bad)[0].tolist())
 
 
-def workspace(c, dtype=None):
+FORM = ["auto"]
+
+
+@pytest.fixture(params=["auto", "cluster", "stream"], autouse=True)
+def form(request):
+    """The automatic choice, and each of the two forms forced."""
+    sra.force_variant("decode_attention_quant", {"auto": -1, "cluster": 0, "stream": 1}[request.param])
+    FORM[0] = request.param
+    yield request.param
+    sra.force_variant("decode_attention_quant", -1)
+
+
+def workspace(c):
     return sra.decode_attention_quant_workspace(len(c.lens), c.q.shape[1], c.n_kv, c.hd, c.table.shape[1], c.bs, c.fmt, c.dtype, DEV)
 
 
-def run(c, what="", errors=0, ws=True, **kw):
+def spaces(c):
+    """The workspaces to run with: none (the stream form, forced, is refused then), and the one that the form uses."""
+    w = workspace(c)
+    assert (w is None) if FORM[0] == "cluster" else (w is not None or FORM[0] == "auto")
+    return ([] if FORM[0] == "stream" else [None]) + ([] if w is None else [w])
+
+
+def run(c, what="", errors=0, **kw):
     d = c.dev()
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
     before = sra.wait_timeouts()
     outs = []
-    for w in ([None, workspace(c)] if ws else [None]):
+    for w in spaces(c):
         if w is not None:
             w.fill_(255)
         err.zero_()
@@ -188,7 +207,7 @@ def test_no_score_above_minus_infinity():
     c.q[0] = 0.0
     c.q[0, :, 0] = -float("inf")
     d = c.dev()
-    for w in (None, workspace(c)):
+    for w in spaces(c):
         got = sra.paged_decode_attention_quant(**d, workspace=w)
         # -inf * 1 + 0 * 1 ... = -inf for every token: nothing weighs
         assert (got[0] == 0).all()
@@ -218,7 +237,7 @@ def test_views():
             q.copy_(d["q"])
             obuf = torch.full((3 * (W + 9) + shift,), 7.0, dtype=dtype, device=DEV)
             out = obuf[shift:].view(3, W + 9)[:, :W].unflatten(1, (6, 128))
-            got = sra.paged_decode_attention_quant(q, d["kv_cache"], d["block_table"], d["seq_lens"], out=out)
+            got = sra.paged_decode_attention_quant(q, d["kv_cache"], d["block_table"], d["seq_lens"], out=out, workspace=spaces(c)[-1])
             assert got is out
             c.check(got)
             out.fill_(7.0)
@@ -256,6 +275,28 @@ def test_graph_and_streams():
     got = sra.paged_decode_attention_quant(**d, workspace=w, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_forced_forms(form):
+    """Clusters of any size; the stream form without a workspace is refused."""
+    c = Case(6, 2, 128, 16, [1500, 0, 33], "e2m1", BF, seed=17)
+    d = c.dev()
+    for splits in (1, 2, 4, 8, 16):
+        sra.force_variant("decode_attention_quant", splits << 8)
+        c.check(sra.paged_decode_attention_quant(**d), splits)
+    for variant, w in ((3 << 8, None), (32 << 8, None), (1, None)):
+        sra.force_variant("decode_attention_quant", variant)
+        with pytest.raises(sra.SRAError) as e:
+            sra.paged_decode_attention_quant(**d, workspace=w)
+        assert e.value.status == -7
+    sra.force_variant("decode_attention_quant", 1)
+    w = workspace(c)
+    with pytest.raises(sra.SRAError) as e:      # too small
+        sra.paged_decode_attention_quant(**d, workspace=w[:-16])
+    assert e.value.status == -6
+    with pytest.raises(sra.SRAError) as e:      # misaligned
+        sra.paged_decode_attention_quant(**d, workspace=torch.empty(w.numel() + 16, dtype=torch.uint8, device=DEV)[8:])
+    assert e.value.status == -6
 
 
 def test_pdl_chain():
