@@ -791,7 +791,7 @@ SRA_API int sra_set_pdl(int enable);
  * OR-ed with (s << 8), s in 1..8, forces the CTAs of its cluster along K),
  * "shared_prefix" (0 = a decode call per request, 1 = the prefix for all requests at once, given a
  * workspace; it also sets what sra_shared_prefix_workspace_size answers), "decode_attention_quant" (0 = a
- * cluster of CTAs for each (request, kv head), OR-ed with (s << 8), s in 1, 2, 4, 8, 16, of that many, 1 = the batch as
+ * cluster of CTAs for each (request, kv head), OR-ed with (s << 8), s in 1..16, of that many, 1 = the batch as
  * one stream of tiles, given a workspace; it also sets what sra_paged_decode_attention_quant_workspace_size answers).
  * variant: -1 = automatic per-shape choice (the default); otherwise an index
  * < sra_variant_count(op), optionally OR-ed with (nv << 8) to also force the

@@ -982,15 +982,9 @@ _FORMAT_OF = {(hd, hd * (1 + code) // 2 + hd // 16): code for hd in (64, 128, 25
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call_on(dev: int, fn: str, *args) -> None:
-    """A C call with that device current."""
-    if _current_device() == dev:
-        st = getattr(_lib or lib(), fn)(*args)
-    else:
-        with torch.cuda.device(dev):
-            st = getattr(lib(), fn)(*args)
-    if st != 0:
-        _check(fn, st)
+def _with(dev: int):
+    """A guard for the CUDA device of that index, as _on."""
+    return _HERE if _current_device() == dev else torch.cuda.device(dev)
 
 
 def _row_bytes(fmt: str, head_dim: int) -> int:
@@ -1096,10 +1090,14 @@ def rope_kv_store_quant(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: 
         params = tuple(t.data_ptr() for t in params)
     if style not in ROPE_STYLE:
         raise ValueError("style must be 'neox' or 'interleaved'")
-    _call_on(dev, "sra_rope_kv_store_quant", q.data_ptr(), k.data_ptr(), v.data_ptr(), cos.data_ptr(), sin.data_ptr(),
-             pos.data_ptr(), slot_mapping.data_ptr(), kv_cache.data_ptr(), T, n_head, n_kv, hd, qs, ks, vs, max_pos, nb, bs,
-             None if err_count is None else _err_ptr(err_count, dev), ROPE_STYLE[style], *params, clip[0], clip[1], fmt,
-             DTYPE_CODE[dtype], _stream(q, stream))
+    with _with(dev):
+        st = (_lib or lib()).sra_rope_kv_store_quant(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(),
+            slot_mapping.data_ptr(), kv_cache.data_ptr(), T, n_head, n_kv, hd, qs, ks, vs, max_pos, nb, bs,
+            None if err_count is None else _err_ptr(err_count, dev), ROPE_STYLE[style], *params, clip[0], clip[1], fmt,
+            DTYPE_CODE[dtype], _stream(q, stream))
+    if st:
+        _check("sra_rope_kv_store_quant", st)
 
 
 def read_kv_quant(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_lens: torch.Tensor, total: int, head_dim: int,
@@ -1142,9 +1140,13 @@ def read_kv_quant(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_lens: to
             raise ValueError(f"unsupported dtype {dtype}")
         shape = (total, n_kv, head_dim)
         ks, vs = _heads_stride(k, dev, shape, dtype, "k"), _heads_stride(v, dev, shape, dtype, "v")
-    _call_on(dev, "sra_kv_quant_read", kv_cache.data_ptr(), block_table.data_ptr(), cu_lens.data_ptr(), sp, k.data_ptr(),
-             v.data_ptr(), rows, mb, total, n_kv, head_dim, ks, vs, nb, bs,
-             None if err_count is None else _err_ptr(err_count, dev), fmt, DTYPE_CODE[dtype], _stream(kv_cache, stream))
+    with _with(dev):
+        st = (_lib or lib()).sra_kv_quant_read(
+            kv_cache.data_ptr(), block_table.data_ptr(), cu_lens.data_ptr(), sp, k.data_ptr(), v.data_ptr(), rows, mb, total,
+            n_kv, head_dim, ks, vs, nb, bs, None if err_count is None else _err_ptr(err_count, dev), fmt, DTYPE_CODE[dtype],
+            _stream(kv_cache, stream))
+    if st:
+        _check("sra_kv_quant_read", st)
     return k, v
 
 
@@ -1174,8 +1176,7 @@ def paged_decode_attention_quant(q: torch.Tensor, kv_cache: torch.Tensor, block_
         _cuda(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [B, n_head, head_dim]")
-    dev, dtype = q.get_device(), q.dtype
-    shape = q.shape
+    dev, dtype, shape, plain = q.get_device(), q.dtype, q.shape, q.is_contiguous()
     B, n_head, hd = shape
     nb, n_kv, bs, fmt = _quant_cache(kv_cache, hd)
     _int32(block_table, "block_table", 2, dev)
@@ -1188,18 +1189,23 @@ def paged_decode_attention_quant(q: torch.Tensor, kv_cache: torch.Tensor, block_
     if rows != B or seq_lens.numel() != B:
         raise ValueError("shape mismatch: block_table and seq_lens must have a row for each of q")
     qs = os_ = n_head * hd
-    if not q.is_contiguous():
+    if not plain:
         qs = _tok_stride(q, "q")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device) if stream is None else \
-            _result(stream, dev, lambda: torch.empty(shape, dtype=dtype, device=q.device))
+        if stream is None:
+            out = torch.empty_like(q) if plain else torch.empty(shape, dtype=dtype, device=q.device)
+        else:
+            out = _result(stream, dev, lambda: torch.empty(shape, dtype=dtype, device=q.device))
     elif not _heads_ok(out, dev, shape, dtype):
         os_ = _heads_stride(out, dev, shape, dtype, "out")
     wp, wb = None, 0
     if workspace is not None:
         workspace, wp, wb = _workspace_args(workspace, None, dev, stream)
-    _call_on(dev, "sra_paged_decode_attention_quant", q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
-             seq_lens.data_ptr(), out.data_ptr(), B, n_head, n_kv, hd, qs, os_, nb, bs, mb,
-             hd ** -0.5 if scale is None else scale, wp, wb, None if err_count is None else _err_ptr(err_count, dev), fmt,
-             DTYPE_CODE[dtype], _stream(q, stream))
+    with _with(dev):
+        st = (_lib or lib()).sra_paged_decode_attention_quant(
+            q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), B, n_head, n_kv,
+            hd, qs, os_, nb, bs, mb, hd ** -0.5 if scale is None else scale, wp, wb,
+            None if err_count is None else _err_ptr(err_count, dev), fmt, DTYPE_CODE[dtype], _stream(q, stream))
+    if st:
+        _check("sra_paged_decode_attention_quant", st)
     return out

@@ -2050,8 +2050,9 @@ QuantAttnForm quant_attn_form(int64_t B, int n_kv, int64_t tokens, int format, i
     QuantAttnForm f;
     const int warps = quant_attn_warps(format, head_dim);
     const int64_t slots = static_cast<int64_t>(num_sms) * quant_attn_ctas(format, head_dim), pairs = B * n_kv;
-    // A cluster takes as many CTAs as fill the SMs, with a tile for each warp. One of 16 only where all of them have an SM for themselves:
-    // 8 requests x 4096 of 2 heads 9.8 us with 8 CTAs, 13.7 with 16; 1 x 8192 10.2 and 8.1.
+    // A cluster takes as many CTAs as fill the SMs, with a tile for each warp. 16 only where all of them have an SM for themselves:
+    // 8 requests x 4096 of 2 heads 9.8 us with 8 CTAs, 13.7 with 16; 1 x 8192 10.2 and 8.1. Powers of two: 4 x 2000 of 8 heads
+    // 7.7 us with 4 CTAs, 9.9 with 7, 7.8 with 8.
     while (f.splits < 16 && pairs * f.splits * 2 <= (f.splits < 8 ? slots : num_sms) &&
            tokens >= 2 * 32 * warps * static_cast<int64_t>(f.splits))
         f.splits *= 2;
@@ -2133,7 +2134,7 @@ int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const 
     const int forced = g_force_quant_attn.load(std::memory_order_relaxed);
     if (forced > 0 && (forced >> 8) != 0) {
         const int f = forced >> 8;
-        if (f > 16 || (f & (f - 1)) != 0) return SRA_ERR_VARIANT;
+        if (f > 16) return SRA_ERR_VARIANT;
         plan.splits = f;
     }
     a.q = q;
