@@ -2032,14 +2032,13 @@ int quant_attention_sizes(int64_t B, int n_head, int n_kv_head, int head_dim, in
     return B < 0 || n_head <= 0 || n_kv_head <= 0 || n_head % n_kv_head != 0 || n_head / n_kv_head > 8 || !quant_head_dim(head_dim) ||
                    (block_size != 8 && block_size != 16 && block_size != 32) || max_blocks < 0 ||
                    __builtin_mul_overflow(B, static_cast<int64_t>(n_kv_head), &b) || b > 0x7fffffff ||
-                   __builtin_mul_overflow(max_blocks, static_cast<int64_t>(block_size), &b) || b > 0x7fffffff ||
+                   // (tokens are rounded up to tiles of 32 in 32 bits)
+                   __builtin_mul_overflow(max_blocks, static_cast<int64_t>(block_size), &b) || b > 0x7fffffff - 31 ||
                    __builtin_mul_overflow(B * 4, max_blocks, &b)
                ? SRA_ERR_SHAPE
                : SRA_OK;
 }
 
-// How a call runs: the cluster form's CTAs for each pair, or the stream form's CTAs (0: the cluster form) with its workspace: the
-// sums, then two records a CTA.
 // How a call runs: the cluster form's CTAs for each pair, or the stream form's CTAs (0: the cluster form) with its workspace: the
 // sums, then two records a CTA.
 struct QuantAttnForm {
@@ -2056,16 +2055,17 @@ QuantAttnForm quant_attn_form(int64_t B, int n_kv, int64_t tokens, int format, i
     while (f.splits < 16 && pairs * f.splits * 2 <= (f.splits < 8 ? slots : num_sms) &&
            tokens >= 2 * 32 * warps * static_cast<int64_t>(f.splits))
         f.splits *= 2;
-    // The stream form has a second launch and a search for its parts (6 us), and every SM the same to do: for long parts, and sooner
-    // where the clusters leave SMs without work. bf16, e2m1, head_dim 128, both (cluster, stream), lengths alike and from 1 on: batch 64 x 8192 41,
-    // 46 and 38, 42 us, x 16384 72, 72 and 65, 54, x 65536 253, 227 and 227, 132; 8 x 16384 21, 22 and 17, 18, x 32768 38, 32 and 28, 22;
-    // 1 x 65536 25, 19. fp32 does more for each token: 24 x 4096 of 4 heads 33, 33 and 29, 34, x 8192 57, 49 and 51, 45.
-    const int64_t part = tokens / f.splits * (dtype == DT_F32 ? 2 : 1);
-    const bool longer = part >= 3072 && part * slots >= 6144 * std::min<int64_t>(slots, pairs * f.splits);
+    // The stream form has a second launch and a search for its parts (some 5 us), and gives every SM the same to do: for CTAs with many
+    // tokens. Both (cluster, stream), lengths alike and from 1 on: bf16, e2m1, head_dim 128, 2 heads, batch 64 x 4096 26, 31 and 21, 22 us,
+    // x 8192 41, 45 and 38, 32, x 16384 72, 71 and 65, 46; 256 x 4096 75, 78 and 55, 54, x 16384 254, 231 and 173, 137; 8 x 16384 21, 19
+    // and 17, 16; int8, 16 x 4096 of 8 heads 32, 37 and 30, 27, x 8192 53, 58 and 49, 38; head_dim 256, 32 x 16384 of one 41, 46 and
+    // 38, 35, x 32768 68, 70 and 64, 48. fp32 does twice as much for a token: 24 x 2048 of 4 heads 18, 22 and 17, 18, x 4096 30, 30
+    // and 26, 23.
+    const bool longer = tokens / f.splits >= (dtype == DT_F32 ? 2048 : 4096);
     const int forced = g_force_quant_attn.load(std::memory_order_relaxed);
     if (forced >= 0 ? (forced & 0xff) == 0 : !longer) return f;
-    // (a thread sums B / 256 requests; the tiles of a kv head are counted in 32 bits)
-    if (B > 65536 || B * ((tokens + 31) / 32) > 0x7fffffff) return f;
+    // (a thread sums B / 256 requests; the tiles of a kv head are counted in 32 bits; up to eight CTAs merge a pair)
+    if (B > 65536 || pairs > 0x7fffffff / 8 || B * ((tokens + 31) / 32 + kStreamPair) > 0x7fffffff) return f;
     f.stream_ctas = static_cast<int>(slots);
     f.at_bytes = round_up256((B + 1) * 4);
     f.bytes = f.at_bytes + slots * 2 * (16 + 8 * head_dim) * 4;

@@ -16,10 +16,11 @@
 // 16 dims in a row, its V a run of head_dim / 8 dims of four tokens in a row.
 //
 // q is fp16, or bf16 / fp32 times a power of two that takes its row's largest element to [2^14, 2^15) (elements below 2^-39
-// of it are lost); fp32 goes in as three fp16 numbers. Probabilities are fp16 at 2^14 times their size relative to the running
-// maximum (normal numbers down to 2^-28 of the largest), rounded once, 2^-11 of each; two fp16 numbers for fp32. Sums, maxima
-// and outputs are fp32; for fp32 each tile's products are added to them by ordinary additions, because the matrix
-// instruction's own accumulation truncates.
+// of it are lost); fp32 goes in as two fp16 numbers, which hold 23 of its 24 bits (2^-23 of an element off at most: what is left
+// of it behind the first is up to 2^12 units of its last place, the second holds even ones from 2^11 on). Probabilities are fp16
+// at 2^14 times their size relative to the running maximum (normal numbers down to 2^-28 of the largest), rounded once, 2^-11 of
+// each; two fp16 numbers for fp32. Sums, maxima and outputs are fp32; for fp32 each tile's products are added to them by ordinary
+// additions, because the matrix instruction's own accumulation truncates.
 //
 // Without a workspace the splits of a pair are the CTAs of a cluster, which merge through distributed shared memory; with one the
 // batch may be a stream of tiles cut into equal parts (stream_kernel), whose records a second kernel merges.
@@ -43,12 +44,12 @@ constexpr int kTile = 32;       // tokens of a warp's tile
 constexpr int kHalves = 2;      // of 16 tokens
 constexpr float kUnder = 14;    // the probabilities' base lies 2^14 under the maximum
 
-// F32: fp32 queries (three parts, probabilities in two); otherwise bf16 or fp16 (QuantAttnArgs::bf16).
+// F32: fp32 queries (in two parts, and probabilities in two); otherwise bf16 or fp16 (QuantAttnArgs::bf16).
 template <bool F32, int FMT, int HD, int BS>
 struct Shape {
     static constexpr int R = kvq::row_bytes(FMT, HD), CODES = kvq::code_bytes(FMT, HD);
     static constexpr int KS = HD / 16;  // steps of 16 dims
-    static constexpr int QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;
+    static constexpr int QP = F32 ? 2 : 1, PP = F32 ? 2 : 1;
     // q's fragments in shared memory, one copy for the CTA: where the registers do not hold them
     static constexpr bool Q_SHARED = F32 || HD == 256;
     static constexpr int Q_BYTES = Q_SHARED ? QP * KS * 32 * 8 : 0;
@@ -56,7 +57,7 @@ struct Shape {
     static constexpr int STAGE = 2 * kTile * R;     // bytes of a stage: K rows, V rows
     static constexpr int WARPS = STAGE <= 4608 ? 8 : 4;
     static constexpr int CTAS = FMT == KV_INT8 && HD == 256 ? 1 : 2;  // per SM
-    static constexpr int FIT = (233472 / CTAS - 1024 - 1536 - Q_BYTES) / (WARPS * STAGE);
+    static constexpr int FIT = (233472 / CTAS - 1024 - 512 - Q_BYTES) / (WARPS * STAGE);
     static constexpr int STAGES = FIT > 4 ? 4 : FIT;
     static_assert(STAGES >= 2, "a tile under way beside the one at work");
     // shared memory: rings, q's fragments and their factors, the stages' barriers and masks
@@ -238,10 +239,10 @@ struct Query {
 // 2 ft + k % 2 in s[u][k].
 template <typename S, bool F32, int FMT, int HD>
 __device__ __forceinline__ void scores(const uint8_t* kt, const Query<S, F32, HD>& q, float (&s)[kHalves][4], int lane) {
-        constexpr int WORDS = FMT == KV_E2M1 ? 2 : 4;  // words of a group of 16 codes
+    constexpr int WORDS = FMT == KV_E2M1 ? 2 : 4;  // words of a group of 16 codes
     const int fg = lane >> 2, ft = lane & 3;
     const uint8_t* r0 = kt + (4 * (fg >> 1) + (fg & 1)) * S::R;
-    // fp32: the products with the lower parts of q; otherwise those of every other step, so that four chains of products
+    // fp32: the products with the lower part of q; otherwise those of every other step, so that four chains of products
     // are under way instead of two
     float fine[kHalves][4];
 #pragma unroll
@@ -281,9 +282,8 @@ __device__ __forceinline__ void scores(const uint8_t* kt, const Query<S, F32, HD
                     mma(part, a, b.x, b.y);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) s[u][k] += part[k];
-                    const uint2 b1 = q.get(1, 4 * j + i), b2 = q.get(2, 4 * j + i);
+                    const uint2 b1 = q.get(1, 4 * j + i);
                     mma(fine[u], a, b1.x, b1.y);
-                    mma(fine[u], a, b2.x, b2.y);
                 } else {
                     mma(i & 1 ? fine[u] : s[u], a, b.x, b.y);
                 }
@@ -646,7 +646,8 @@ __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32
     auto length = [&](int b) -> int {
         return b < B ? tokens_of(a, b) : 0;
     };
-    auto tiles_of = [](int len) { return (len + kTile - 1) / kTile; };
+    // a pair's room in the stream: its tiles, and kStreamPair for what it costs beside them
+    auto tiles_of = [](int len) { return len > 0 ? (len + kTile - 1) / kTile + kStreamPair : 0; };
     // thread t sums requests [t * each, (t + 1) * each)
     const int each = (B + NT - 1) / NT, mine0 = threadIdx.x * each;
     int mine = 0;
@@ -711,20 +712,22 @@ __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32
         const int kvh = static_cast<int>((g0 - begin) / n);
         const int t0 = static_cast<int>(g0 - begin - static_cast<int64_t>(kvh) * n);
         const int t1 = g1 - g0 < n - t0 ? t0 + static_cast<int>(g1 - g0) : n;
-        segment<S, F32, FMT, HD, BS>(a, smem, b, kvh, len, t0, S::WARPS, t1, &turn);
+        g0 += t1 - t0;
+        if (t1 <= kStreamPair) continue;  // (the pair's first tile is another CTA's)
+        const int first = t0 > kStreamPair ? t0 - kStreamPair : 0, end = t1 - kStreamPair;
+        segment<S, F32, FMT, HD, BS>(a, smem, b, kvh, len, first, S::WARPS, end, &turn);
         __syncthreads();
         const float* res = reinterpret_cast<const float*>(smem + S::res_ml);
-        if (t0 == 0 && t1 == n) {
+        if (first == 0 && t1 == n) {
             const int64_t out = b * a.os + static_cast<int64_t>(kvh) * G * HD;
             for (int i = threadIdx.x; i < G * HD; i += NT) {
                 const float l = res[8 + i / HD];
                 put<F32>(a.out, out + i, l != 0.0f ? res[16 + i] / l : 0.0f, a.bf16);
             }
         } else {
-            float* rec = a.ws_rec + (static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * (16 + 8 * HD);
+            float* rec = a.ws_rec + (static_cast<int64_t>(blockIdx.x) * 2 + (first == 0 ? 1 : 0)) * (16 + 8 * HD);
             for (int i = threadIdx.x; i < 16 + G * HD; i += NT) rec[i] = res[i];
         }
-        g0 += t1 - t0;
         fence_proxy_async();  // the merge's accesses come before the copies that fill the rings again
         __syncthreads();
     }
@@ -751,7 +754,7 @@ __global__ void __launch_bounds__(256) merge_kernel(QuantAttnArgs a, int ctas, i
         return;
     }
     const int64_t first = static_cast<int64_t>(at) * a.n_kv + static_cast<int64_t>(kvh) * n;
-    const int64_t c0 = first / part, c1 = (first + n - 1) / part;
+    const int64_t c0 = (first + kStreamPair) / part, c1 = (first + n - 1) / part;
     if (c0 == c1) return;  // written by that part
     float top = -INFINITY, sum = 0.0f, acc = 0.0f;
     if (there) {

@@ -238,7 +238,9 @@ struct QuantAttnArgs {
     int32_t* ws_at = nullptr;   // [B + 1] tiles (of a kv head) before each request
     float* ws_rec = nullptr;    // [CTAs][2][16 + 8 * head_dim]
 };
-// The tiles of a CTA's part of the stream: equal parts, but no less than a tile for each warp.
+// A CTA's part of the stream, and the room that a pair has there beside its tiles: a CTA that goes on to another pair loses some 5 us
+// with it (its sums merged, its first tiles waited for).
+constexpr int kStreamPair = 16;
 inline SRA_HD int64_t stream_part(int64_t all, int64_t ctas, int warps) {
     const int64_t part = (all + ctas - 1) / ctas;
     return part < warps ? warps : part;
