@@ -1171,7 +1171,7 @@ def paged_decode_attention_quant(q: torch.Tensor, kv_cache: torch.Tensor, block_
     """paged_decode_attention over a cache held in 4 or 8 bits (quant_kv_cache).
 
     q: [B, n_head, head_dim]; block_table: int32 [B, max_blocks]; seq_lens: int32 [B]; scale defaults to
-    1 / sqrt(head_dim). workspace: from decode_attention_quant_workspace, or None."""
+    1 / sqrt(head_dim). workspace: from decode_attention_quant_workspace, or None (slower for batches with many tokens)."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         _cuda(q, "q")
     if q.dim() != 3:
