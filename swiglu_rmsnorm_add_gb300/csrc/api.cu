@@ -2055,13 +2055,16 @@ QuantAttnForm quant_attn_form(int64_t B, int n_kv, int64_t tokens, int format, i
     while (f.splits < 16 && pairs * f.splits * 2 <= (f.splits < 8 ? slots : num_sms) &&
            tokens >= 2 * 32 * warps * static_cast<int64_t>(f.splits))
         f.splits *= 2;
-    // The stream form has a second launch and a search for its parts (some 5 us), and gives every SM the same to do: for CTAs with many
-    // tokens. Both (cluster, stream), lengths alike and from 1 on: bf16, e2m1, head_dim 128, 2 heads, batch 64 x 4096 26, 31 and 21, 22 us,
-    // x 8192 41, 45 and 38, 32, x 16384 72, 71 and 65, 46; 256 x 4096 75, 78 and 55, 54, x 16384 254, 231 and 173, 137; 8 x 16384 21, 19
-    // and 17, 16; int8, 16 x 4096 of 8 heads 32, 37 and 30, 27, x 8192 53, 58 and 49, 38; head_dim 256, 32 x 16384 of one 41, 46 and
-    // 38, 35, x 32768 68, 70 and 64, 48. fp32 does twice as much for a token: 24 x 2048 of 4 heads 18, 22 and 17, 18, x 4096 30, 30
-    // and 26, 23.
-    const bool longer = tokens / f.splits >= (dtype == DT_F32 ? 2048 : 4096);
+    // The stream form has a second launch and a search for its parts (some 4 us), and gives every SM the same to do: for CTAs with many
+    // tokens. Both (cluster, stream), lengths alike and from 1 on: bf16, e2m1, head_dim 128, 2 heads, batch 64 x 4096 26, 30 and 21, 21 us,
+    // x 8192 41, 44 and 38, 31, x 16384 72, 70 and 65, 45; 256 x 4096 75, 77 and 55, 54, x 16384 254, 228 and 173, 134; int8, 16 x 4096 of
+    // 8 heads 32, 37 and 30, 27, x 8192 53, 58 and 49, 38; head_dim 256, 32 x 16384 of one 41, 46 and 38, 35, x 32768 68, 70 and 64, 48.
+    // fp32 does twice as much for a token: 16 x 2048 of 8 heads 16, 22 and 16, 17, x 4096 29, 32 and 25, 22.
+    // Where clusters of 16 or 8 CTAs leave half of the GPU empty, from eight tiles a warp on: bf16, e2m1, 1 x 16384 of 2 heads 10.7, 10.9,
+    // x 32768 15.6, 12.7; 8 x 8192 14.0, 15.5, x 16384 21.8, 19.4; int8, 1 x 8192 of 8 heads 11.2, 10.8, x 16384 16.3, 14.0; head_dim
+    // 256, 1 x 8192 of one 12.7, 11.7, x 16384 17.4, 13.3.
+    const bool sparse = pairs * f.splits * 2 <= slots;
+    const bool longer = tokens / f.splits >= (sparse ? 8 * 32 * warps : dtype == DT_F32 ? 2048 : 4096);
     const int forced = g_force_quant_attn.load(std::memory_order_relaxed);
     if (forced >= 0 ? (forced & 0xff) == 0 : !longer) return f;
     // (a thread sums B / 256 requests; the tiles of a kv head are counted in 32 bits; up to eight CTAs merge a pair)

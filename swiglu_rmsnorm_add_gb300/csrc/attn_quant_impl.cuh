@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32
     using S = Shape<F32, FMT, HD, BS>;
     constexpr int NT = S::WARPS * 32;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int warp_sum[S::WARPS], found[2];
+    __shared__ int warp_sum[S::WARPS], found[3];
     if (threadIdx.x == 0) found[0] = 0x7fffffff;
     init_barriers<S>(smem);
     uint32_t turn = 0;
@@ -648,16 +648,12 @@ __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32
     };
     // a pair's room in the stream: its tiles, and kStreamPair for what it costs beside them
     auto tiles_of = [](int len) { return len > 0 ? (len + kTile - 1) / kTile + kStreamPair : 0; };
-    // thread t sums requests [t * each, (t + 1) * each)
+    // thread t sums requests [t * each, (t + 1) * each); the first one's length is kept
     const int each = (B + NT - 1) / NT, mine0 = threadIdx.x * each;
+    const int len0 = length(mine0);
+    auto own = [&](int k) { return k == 0 ? len0 : length(mine0 + k); };
     int mine = 0;
-    for (int k = 0; k < each; ++k) {
-        const int b = mine0 + k;
-        if (blockIdx.x == 0 && a.err && b < B) {
-            if (__ldcg(a.seq_lens + b) != tokens_of(a, b)) atomicAdd(a.err, 1);
-        }
-        mine += tiles_of(length(b));
-    }
+    for (int k = 0; k < each; ++k) mine += tiles_of(own(k));
     int inc = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -679,8 +675,11 @@ __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32
     if (blockIdx.x == 0) {
         int at = at0;
         for (int k = 0; k < each; ++k) {
-            if (mine0 + k < B) a.ws_at[mine0 + k] = at;
-            at += tiles_of(length(mine0 + k));
+            if (mine0 + k < B) {
+                a.ws_at[mine0 + k] = at;
+                if (a.err && __ldcg(a.seq_lens + mine0 + k) != own(k)) atomicAdd(a.err, 1);
+            }
+            at += tiles_of(own(k));
         }
         if (threadIdx.x == 0) a.ws_at[B] = total;
     }
@@ -691,19 +690,20 @@ __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32
     {
         int at = at0;
         for (int k = 0; k < each; ++k) {
-            const int n = tiles_of(length(mine0 + k));
+            const int len = own(k), n = tiles_of(len);
             const int64_t lo = static_cast<int64_t>(at) * a.n_kv, hi = static_cast<int64_t>(at + n) * a.n_kv;
-            if (lo <= g0 && g0 < hi) found[0] = mine0 + k, found[1] = at;
+            if (lo <= g0 && g0 < hi) found[0] = mine0 + k, found[1] = at, found[2] = len;
             at += n;
         }
     }
     __syncthreads();
     int b = found[0];
     int64_t begin = static_cast<int64_t>(found[1]) * a.n_kv;  // the request's first tile in the stream
-    int window = b, lens = length(b + lane);  // lane k: request window + k
+    const int b0 = b, first_len = found[2];
+    int window = b, lens = length(b + lane);  // lane k: request window + k (asked for now; the first one's length is known)
     while (g0 < g1 && b < B) {
         if (b - window >= 32) window = b, lens = length(b + lane);
-        const int len = __shfl_sync(FULL, lens, b - window), n = tiles_of(len);
+        const int len = b == b0 ? first_len : __shfl_sync(FULL, lens, b - window), n = tiles_of(len);
         if (g0 >= begin + static_cast<int64_t>(n) * a.n_kv) {
             begin += static_cast<int64_t>(n) * a.n_kv;
             ++b;
