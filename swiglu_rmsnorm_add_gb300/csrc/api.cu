@@ -2114,11 +2114,11 @@ int sra_paged_decode_attention_quant(const void* q, const void* kv_cache, const 
         return SRA_ERR_ALIAS;
     QuantAttnPlan plan;
     int dev = 0;
-    plan.num_sms = current_sm_count(&dev);
-    if (plan.num_sms <= 0) return SRA_ERR_DEVICE;
+    const int sms = current_sm_count(&dev);
+    if (sms <= 0) return SRA_ERR_DEVICE;
     plan.head_dim = head_dim;
     plan.pdl = g_pdl;
-    const QuantAttnForm form = quant_attn_form(B, n_kv_head, max_blocks_per_seq * block_size, format, head_dim, dtype, plan.num_sms);
+    const QuantAttnForm form = quant_attn_form(B, n_kv_head, max_blocks_per_seq * block_size, format, head_dim, dtype, sms);
     plan.stream_ctas = 0;
     QuantAttnArgs a;
     if (workspace && form.stream_ctas > 0) {

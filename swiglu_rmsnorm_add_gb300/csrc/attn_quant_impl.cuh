@@ -25,9 +25,14 @@
 // Without a workspace the splits of a pair are the CTAs of a cluster, which merge through distributed shared memory; with one the
 // batch may be a stream of tiles cut into equal parts (stream_kernel), whose records a second kernel merges.
 //
-// What bounds it: the arithmetic beside the products, not HBM. A tile of head_dim 128 in 4 bits takes 128 conversions and 128
-// multiplications (two cycles each, on different pipes) and 32 products, each of which holds the scheduler's dispatch for some
-// six cycles (measured: a product with four conversions and four multiplications takes 14 cycles, not nine).
+// What bounds it: the issue of instructions, not HBM. A tile of head_dim 128 in 4 bits is some 600 instructions a warp: 128 conversions and
+// 128 multiplications (two cycles each, on different pipes), 32 products, each of which holds the scheduler's dispatch for some six
+// cycles (measured: a product with four conversions and four multiplications takes 14 cycles, not nine), the softmax, the copies. The
+// four warps of a scheduler that registers and rings leave room for issue in 0.62 of its cycles: batch 256 x 16384 of 2 heads (from 4000
+// tokens on, 755 MB) 156 us, 112 at the copy rate; long streams run at 5.9 TB/s, a call's start, changes of pair and merge take some
+// 20 us. 8 bits have half the instructions for a byte: 16 x 32768 of 8 heads 178 us, 169 at the copy rate.
+// Measured and left: the next tile's scores beside a tile's values (64 x 16384 72 -> 75 us), a third CTA an SM in 80 registers (81), tiles of 64
+// tokens (73.5), a running maximum that follows only a score of twice its weight (157.7 -> 157.3).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -55,8 +60,8 @@ struct Shape {
     static constexpr int Q_BYTES = Q_SHARED ? QP * KS * 32 * 8 : 0;
     static constexpr int PAGES = kTile / BS;        // of a tile
     static constexpr int STAGE = 2 * kTile * R;     // bytes of a stage: K rows, V rows
-    static constexpr int WARPS = STAGE <= 4608 ? 8 : 4;
-    static constexpr int CTAS = FMT == KV_INT8 && HD == 256 ? 1 : 2;  // per SM
+    static constexpr int WARPS = quant_attn_warps(FMT, HD);
+    static constexpr int CTAS = quant_attn_ctas(FMT, HD);  // per SM
     static constexpr int FIT = (233472 / CTAS - 1024 - 512 - Q_BYTES) / (WARPS * STAGE);
     static constexpr int STAGES = FIT > 4 ? 4 : FIT;
     static_assert(STAGES >= 2, "a tile under way beside the one at work");
@@ -628,9 +633,10 @@ __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32
 }
 
 // The whole batch as one stream of tiles (requests, their kv heads, their tiles), cut into equal parts for as many CTAs as
-// the GPU holds. A CTA writes the outputs of the pairs that it holds whole, and leaves a record [8 max][8 sum][8 x HD] of
-// the one that began before its part (slot 0) and of the one that goes on behind it (slot 1). Every CTA sums the
-// requests' tiles to find its part; CTA 0 leaves the sums for the merge.
+// the GPU holds. Before its tiles a pair has kStreamPair places of none, for what a CTA loses with it. A CTA writes the outputs of the
+// pairs that it holds whole, and leaves a record [8 max][8 sum][8 x HD] of the one that began before its part (slot 0) and of the
+// one that goes on behind it (slot 1). Every CTA sums the requests' places to find its part; CTA 0 leaves the sums for the
+// merge.
 template <bool F32, int FMT, int HD, int BS>
 __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32, FMT, HD, BS>::CTAS) stream_kernel(QuantAttnArgs a) {
     using S = Shape<F32, FMT, HD, BS>;

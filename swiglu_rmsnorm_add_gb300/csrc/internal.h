@@ -110,7 +110,7 @@ cudaError_t launch_rope_kv_store(const RopeArgs& a, const RopePlan& p, int dtype
 // ------------------------------------------------- a cache held in 4 or 8 bits (kv_format.cuh)
 enum KvFormat { KV_E2M1 = 0, KV_INT8 = 1 };
 inline bool valid_kv_format(int f) { return f == KV_E2M1 || f == KV_INT8; }
-inline SRA_HD int kv_row_bytes(int format, int head_dim) {
+constexpr SRA_HD int kv_row_bytes(int format, int head_dim) {
     return (format == KV_E2M1 ? head_dim / 2 : head_dim) + head_dim / 16;
 }
 
@@ -235,11 +235,12 @@ struct QuantAttnArgs {
     bool wide_q;       // 16-byte aligned query rows
     bool bf16;         // of the 16-bit dtypes
     // workspace of the stream form
-    int32_t* ws_at = nullptr;   // [B + 1] tiles (of a kv head) before each request
+    int32_t* ws_at = nullptr;   // [B + 1] places (of a kv head) before each request
     float* ws_rec = nullptr;    // [CTAs][2][16 + 8 * head_dim]
 };
-// A CTA's part of the stream, and the room that a pair has there beside its tiles: a CTA that goes on to another pair loses some 5 us
-// with it (its sums merged, its first tiles waited for).
+// A CTA's part of the stream (no less than a tile for each warp), and the places that a pair has there beside its tiles: a CTA that goes on
+// to another pair loses some 5 us with it (its sums merged, its first tiles waited for). Without them 64 requests of 1 to 16384 tokens
+// of 2 heads took 53 us instead of 46, 300 of 300 tokens 41 instead of 24, 256 x 16384 162 instead of 158.
 constexpr int kStreamPair = 16;
 inline SRA_HD int64_t stream_part(int64_t all, int64_t ctas, int warps) {
     const int64_t part = (all + ctas - 1) / ctas;
@@ -250,11 +251,10 @@ struct QuantAttnPlan {
     int splits;       // CTAs per (request, kv head): the cluster size
     int stream_ctas;  // > 0: the stream form, with that many CTAs
     bool pdl;
-    int num_sms;
 };
 // Warps per CTA and CTAs per SM (alike for all dtypes and block sizes).
-inline int quant_attn_warps(int format, int head_dim) { return 64 * kv_row_bytes(format, head_dim) <= 4608 ? 8 : 4; }
-inline int quant_attn_ctas(int format, int head_dim) { return format == KV_INT8 && head_dim == 256 ? 1 : 2; }
+constexpr int quant_attn_warps(int format, int head_dim) { return 64 * kv_row_bytes(format, head_dim) <= 4608 ? 8 : 4; }
+constexpr int quant_attn_ctas(int format, int head_dim) { return format == KV_INT8 && head_dim == 256 ? 1 : 2; }
 unsigned int quant_attn_wait_timeouts();
 cudaError_t launch_attn_quant_e2m1(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s);
 cudaError_t launch_attn_quant_int8(const QuantAttnArgs& a, const QuantAttnPlan& p, cudaStream_t s);
