@@ -25,12 +25,13 @@
 // Without a workspace the splits of a pair are the CTAs of a cluster, which merge through distributed shared memory; with one the
 // batch may be a stream of tiles cut into equal parts (stream_kernel), whose records a second kernel merges.
 //
-// What bounds it: the issue of instructions, not HBM. A tile of head_dim 128 in 4 bits is some 600 instructions a warp: 128 conversions and
-// 128 multiplications (two cycles each, on different pipes), 32 products, each of which holds the scheduler's dispatch for some six
-// cycles (measured: a product with four conversions and four multiplications takes 14 cycles, not nine), the softmax, the copies. The
-// four warps of a scheduler that registers and rings leave room for issue in 0.62 of its cycles: batch 256 x 16384 of 2 heads (from 4000
-// tokens on, 755 MB) 156 us, 112 at the copy rate; long streams run at 5.9 TB/s, a call's start, changes of pair and merge take some
-// 20 us. 8 bits have half the instructions for a byte: 16 x 32768 of 8 heads 178 us, 169 at the copy rate.
+// What bounds it: the issue of instructions, a little before HBM. A tile of head_dim 128 in 4 bits is some 600 instructions a warp: 128
+// conversions and 128 multiplications (two cycles each, on different pipes), 32 products, each of which holds the scheduler's dispatch
+// for some six cycles (measured: a product with four conversions and four multiplications takes 14 cycles, not nine), the softmax, the
+// copies. A scheduler takes 0.48 us for a tile with four warps (0.64 with two; registers and rings leave room for four), where HBM's
+// copy rate would give it one in 0.41: long streams run at 5.9 TB/s. A call's start, its changes of pair and the merge come to some 20 us:
+// batch 256 x 16384 of 2 heads (from 4000 tokens on, 755 MB) 156 us, 112 at the copy rate. 8 bits have half the instructions for a
+// byte: 16 x 32768 of 8 heads 178 us, 169 at the copy rate.
 // Measured and left: the next tile's scores beside a tile's values (64 x 16384 72 -> 75 us), a third CTA an SM in 80 registers (81), tiles of 64
 // tokens (73.5), a running maximum that follows only a score of twice its weight (157.7 -> 157.3).
 #pragma once
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(Shape<F32, FMT, HD, BS>::WARPS * 32, Shape<F32
     constexpr int NT = S::WARPS * 32;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int warp_sum[S::WARPS], found[3];
-    if (threadIdx.x == 0) found[0] = 0x7fffffff;
+    if (threadIdx.x == 0) found[0] = 0x40000000;  // (nobody: above every request)
     init_barriers<S>(smem);
     uint32_t turn = 0;
     pdl_enter();
