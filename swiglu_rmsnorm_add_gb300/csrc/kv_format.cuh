@@ -15,9 +15,9 @@
 // the step (a third) that it sits in, and the other values gain. int8's is rounded up: its steps at amax
 // are 16 times finer than such a clip.
 //
-// Borders between codes are compared, not computed by a division: a border is a multiple of the scale with
-// at most 7 (e2m1) or 12 (int8) bits, so it is an fp32 number, and the bytes follow from the inputs exactly, for
-// every dtype.
+// A border between codes is a multiple of the scale with at most 7 (e2m1) or 12 (int8) bits, so it is an fp32 number, and the
+// correctly rounded quotient of a value and its scale lies on the same side of it: the bytes follow from the inputs exactly,
+// for every dtype.
 #pragma once
 
 #include "common.cuh"
@@ -59,45 +59,43 @@ __device__ __forceinline__ uint32_t scale_code(float amax) {
     }
 }
 
+// x / s, correctly rounded, with inv the correctly rounded 1 / s: the remainder of x * inv is exact, and adding it once gives the quotient
+// (Markstein's theorem; s is at least 2^-17, and what underflows is far below the first border).
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+    const float q = x * inv;
+    return fmaf(fmaf(-q, s, x), inv, q);
+}
+
 // N values of one group as codes in 32-bit words (8 or 4 codes each); `code` is the group's scale byte. A group
-// whose scale is 0 or NaN has codes of 0.
+// whose scale is 0 or NaN has codes of 0. The quotient decides as x itself would: where x is a border times the scale it is the border, and
+// an x one place further is off by more than 2^-24 of it, half a place of a border or more, so its quotient lies beyond.
 template <int FMT, int N>
 __device__ __forceinline__ void encode(const float (&x)[N], uint32_t code, uint32_t* w) {
-    const float s = scale_value(code);
+    const float s = scale_value(code), inv = 1.0f / s;
     const bool live = code != 0 && code != kScaleNaN;
     if constexpr (FMT == KV_E2M1) {
-        // the borders' ties go to the even code: >= where the upper one is even
-        const float s175 = 1.75f * s, s075 = 0.75f * s, s35 = 3.5f * s, s025 = 0.25f * s, s125 = 1.25f * s, s25 = 2.5f * s,
-                    s5 = 5.0f * s;
 #pragma unroll
         for (int j = 0; j < N / 8; ++j) {
-            uint32_t v = 0;
+            float q[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float a = fabsf(x[8 * j + k]);
-                const bool c4 = a >= s175;
-                const bool c2 = a >= (c4 ? s35 : s075);
-                const bool c1 = a > (c4 ? (c2 ? s5 : s25) : (c2 ? s125 : s025));
-                const uint32_t sign = (__float_as_uint(x[8 * j + k]) >> 28) & 8u;
-                v |= (sign | (c4 ? 4u : 0u) | (c2 ? 2u : 0u) | (c1 ? 1u : 0u)) << (4 * k);
-            }
+            for (int k = 0; k < 8; ++k) q[k] = copysignf(quotient(x[8 * j + k], s, inv), x[8 * j + k]);  // (-0 has lost its sign)
+            uint32_t v;  // to nearest, ties to the even code, saturating
+            asm("{.reg .b8 a, b, c, d; cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3; "
+                "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7; mov.b32 %0, {a, b, c, d};}"
+                : "=r"(v)
+                : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
             w[j] = live ? v : 0u;
         }
     } else {
-        const float top = 127.0f * s, half = 0.5f * s, inv = 1.0f / s;
 #pragma unroll
         for (int j = 0; j < N / 4; ++j) {
-            uint32_t v = 0;
+            uint32_t n[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float a = fminf(fmaxf(x[4 * j + k], -top), top);
-                float n = rintf(a * inv);
-                const float r = fmaf(-n, s, a);  // exact: both are multiples of a's last place, at most s apart
-                const bool odd = static_cast<int>(n) & 1;
-                if (r > half || (r == half && odd)) n += 1.0f;
-                if (r < -half || (r == -half && odd)) n -= 1.0f;
-                v |= (static_cast<uint32_t>(static_cast<int>(n)) & 0xffu) << (8 * k);
+                const float q = fminf(fmaxf(quotient(x[4 * j + k], s, inv), -127.0f), 127.0f);
+                n[k] = __float_as_uint(q + 12582912.0f);  // 1.5 * 2^23: rounds to an integer, ties to even, in the low bits
             }
+            const uint32_t v = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
             w[j] = live ? v : 0u;
         }
     }

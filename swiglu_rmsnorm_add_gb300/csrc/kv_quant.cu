@@ -10,8 +10,10 @@
 // once more to the dtype. A code can hang on the last place of its value, and with this the cache's bytes
 // follow from the definition, whoever evaluates it. (Q is rotated exactly as sra_rope_kv_store does it.)
 //
-// It is bound by a launch and a round trip to memory (2.9 us for 64 tokens), then by HBM: 4096 tokens of 12 / 2 heads of 128 (bf16, 4
-// bits, 37.6 MB) 9.9 us, 5.5 of them at the copy rate. (All three tensors' tasks in the same CTAs: 13.9.)
+// It is bound by a launch and a round trip to memory (2.5 us for 64 tokens), then by latencies between loads, tables and stores that five
+// CTAs an SM cover (4: 8.8 us, 6: 8.4 and spills) and HBM: 4096 tokens of 12 / 2 heads of 128 (bf16, 4 bits, 33 MB) 8.4 us, 4.8 at the copy rate;
+// 16384 of them 28.9. (All three tensors' tasks in the same CTAs: 4 us more; two heads of Q a thread 11.7, K's and V's CTAs among Q's
+// 10.9 for 4096 tokens.)
 //
 // Read. A CTA takes a tile of output tokens, finds each one's place in the cache once, and its threads turn groups of 16
 // codes into one 32-byte store each (two in fp32), four groups at a time. Bound by writes, four bytes in five: 16 requests of up to
@@ -84,24 +86,46 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[W]) 
     for (int j = 0; j < W; ++j) reinterpret_cast<uint32_t*>(p)[j] = w[j];  // rows are multiples of 4 bytes
 }
 
+// n / d for n < 2^31 as a product and a shift: ceil(2^(31 + l) / d) / 2^(31 + l), 2^l >= d, is off by less than 1 / (d n) (Granlund and
+// Montgomery).
+struct Divisor {
+    uint32_t d, mul, shift;
+    explicit Divisor(uint32_t by) : d(by) {
+        uint32_t l = 0;
+        while ((uint64_t(1) << l) < by) ++l;
+        mul = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + by - 1) / by);
+        shift = 31 + l;
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t n) const { return static_cast<uint32_t>(static_cast<uint64_t>(n) * mul >> shift); }
+};
+
 // Which tensor a CTA's tasks come from; each has CTAs of its own (K's first: they have the most to do), so that no warp
-// walks through two kinds' code.
+// walks through two kinds' code. Tasks are numbered over tokens, heads, groups; they, and a slot's page, are found by
+// multiplications (by divisions 4096 tokens of 12 / 2 heads took 0.5 us more).
 struct StoreGrid {
     int64_t k_ctas, v_ctas;
     bool wide;
+    bool narrow;  // every tensor's tasks are fewer than 2^31
+    Divisor q_tasks, kv_tasks, page;
 };
 
 template <typename T, int FMT, bool IL, bool NORM, int KIND>  // KIND: 0 Q, 1 K, 2 V
-__device__ __forceinline__ void store_task(const RopeArgs& a, int64_t cta, bool wide) {
+__device__ __forceinline__ void store_task(const RopeArgs& a, const StoreGrid& grid, int64_t cta) {
+    const bool wide = grid.wide;
     constexpr int CB = FMT == KV_E2M1 ? 4 : 8;  // bits per code
     constexpr bool ROW = IL || KIND == 2;       // 16 dims in a row
     const int D = a.head_dim, h = D >> 1, lg = __ffs(D) - 5;  // 2^lg tasks a head
-    const int U = (KIND == 0 ? a.n_head : a.n_kv) << lg;
-    // tasks are numbered over tokens, heads, groups
-    const int64_t first = cta * kThreads, t0 = first / U;
-    const unsigned i = static_cast<unsigned>(first - t0 * U) + threadIdx.x, lt = i / static_cast<unsigned>(U);
-    const int64_t t = t0 + lt;
-    const int u = static_cast<int>(i - lt * U), head = u >> lg, g = u & ((1 << lg) - 1);
+    const Divisor& per_token = KIND == 0 ? grid.q_tasks : grid.kv_tasks;
+    int64_t t;
+    int u;
+    if (grid.narrow) {
+        const uint32_t i = static_cast<uint32_t>(cta) * kThreads + threadIdx.x, lt = per_token.of(i);
+        t = lt, u = static_cast<int>(i - lt * per_token.d);
+    } else {
+        const int64_t i = cta * kThreads + threadIdx.x;
+        t = i / per_token.d, u = static_cast<int>(i - t * per_token.d);
+    }
+    const int head = u >> lg, g = u & ((1 << lg) - 1);
     bool live = t < a.T;
     int64_t p = 0, slot = -1;
     float x0[8], x1[8];
@@ -174,7 +198,8 @@ __device__ __forceinline__ void store_task(const RopeArgs& a, int64_t cta, bool 
         }
         if (!live) return;
         const int R = row_bytes(FMT, D), codes = code_bytes(FMT, D);
-        const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
+        const int64_t blk = slot < 0x80000000 ? grid.page.of(static_cast<uint32_t>(slot)) : slot / a.block_size,
+                      off = slot - blk * a.block_size;
         uint8_t* row = static_cast<uint8_t*>(a.cache) +
                        ((((KIND == 2 ? a.num_blocks : 0) + blk) * a.n_kv + head) * a.block_size + off) * R;
         const uint32_t c0 = scale_of<FMT>(m0), c1 = ROW ? c0 : scale_of<FMT>(m1);
@@ -193,12 +218,12 @@ __device__ __forceinline__ void store_task(const RopeArgs& a, int64_t cta, bool 
 }
 
 template <typename T, int FMT, bool IL, bool NORM>
-__global__ void __launch_bounds__(kThreads, 4) store_kernel(RopeArgs a, StoreGrid grid) {
+__global__ void __launch_bounds__(kThreads, 5) store_kernel(RopeArgs a, StoreGrid grid) {
     pdl_enter();
     const int64_t cta = blockIdx.x;
-    if (cta < grid.k_ctas) store_task<T, FMT, IL, NORM, 1>(a, cta, grid.wide);
-    else if (cta < grid.k_ctas + grid.v_ctas) store_task<T, FMT, IL, NORM, 2>(a, cta - grid.k_ctas, grid.wide);
-    else store_task<T, FMT, IL, NORM, 0>(a, cta - grid.k_ctas - grid.v_ctas, grid.wide);
+    if (cta < grid.k_ctas) store_task<T, FMT, IL, NORM, 1>(a, grid, cta);
+    else if (cta < grid.k_ctas + grid.v_ctas) store_task<T, FMT, IL, NORM, 2>(a, grid, cta - grid.k_ctas);
+    else store_task<T, FMT, IL, NORM, 0>(a, grid, cta - grid.k_ctas - grid.v_ctas);
 }
 
 template <typename T, int FMT>
@@ -207,10 +232,16 @@ cudaError_t launch_store(const RopeArgs& a, const KvQuantPlan& p, cudaStream_t s
         p.style == 0 ? (p.qk_norm ? store_kernel<T, FMT, false, true> : store_kernel<T, FMT, false, false>)
                      : (p.qk_norm ? store_kernel<T, FMT, true, true> : store_kernel<T, FMT, true, false>);
     const int64_t per_head = a.T * (a.head_dim / kGroup);
-    StoreGrid g;
-    g.k_ctas = g.v_ctas = (per_head * a.n_kv + kThreads - 1) / kThreads;
-    g.wide = p.wide;
-    const int64_t all = g.k_ctas + g.v_ctas + (per_head * a.n_head + kThreads - 1) / kThreads;
+    const int64_t kv_ctas = (per_head * a.n_kv + kThreads - 1) / kThreads, q_ctas = (per_head * a.n_head + kThreads - 1) / kThreads;
+    const int groups = a.head_dim / kGroup;
+    const int64_t all = 2 * kv_ctas + q_ctas;
+    const StoreGrid g{kv_ctas,
+                      kv_ctas,
+                      p.wide,
+                      q_ctas * kThreads <= 0x7fffffff,
+                      Divisor(static_cast<uint32_t>(a.n_head * groups)),
+                      Divisor(static_cast<uint32_t>(a.n_kv * groups)),
+                      Divisor(static_cast<uint32_t>(a.block_size))};
     return launch_kernel(kernel, dim3(static_cast<unsigned>(all)), dim3(kThreads), 0, s, p.pdl, 1, a, g);
 }
 
