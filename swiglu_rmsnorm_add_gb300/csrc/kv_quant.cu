@@ -86,8 +86,8 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[W]) 
     for (int j = 0; j < W; ++j) reinterpret_cast<uint32_t*>(p)[j] = w[j];  // rows are multiples of 4 bytes
 }
 
-// n / d for n < 2^31 as a product and a shift: ceil(2^(31 + l) / d) / 2^(31 + l), 2^l >= d, is off by less than 1 / (d n) (Granlund and
-// Montgomery).
+// n / d for n < 2^31 as a product and a shift: m = ceil(2^(31 + l) / d) with 2^l >= d, and n m / 2^(31 + l) exceeds n / d by less than
+// n / 2^(31 + l) < 1 / d (Granlund and Montgomery).
 struct Divisor {
     uint32_t d, mul, shift;
     explicit Divisor(uint32_t by) : d(by) {

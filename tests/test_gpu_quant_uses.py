@@ -246,6 +246,24 @@ def test_offsets_past_32_bits(variant):
     assert same(big[:, nb - 2], small.cache[:, 0]) and same(big[:, 3], small.cache[:, 1])
 
 
+def test_more_than_2_31_tasks():
+    """A store of so many tokens that their tasks pass 2^31: first, middle and last tokens as in a small call."""
+    n_head, hd, bs, few = 8, 64, 16, 70
+    T = 2 ** 31 // (n_head * (hd // 16)) + few
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("needs 90 GB of device memory")
+    small = Batch([1] * (3 * few), n_head=n_head, n_kv=1, hd=hd, bs=bs, dtype=HF, seed=11)
+    at = torch.cat([torch.arange(few), torch.arange(T // 2, T // 2 + few), torch.arange(T - few, T)]).to(DEV)
+    q, k, v = (torch.empty(T, n, hd, dtype=HF, device=DEV) for n in (n_head, 1, 1))
+    pos, slot = torch.full((T,), -1, device=DEV), torch.full((T,), -1, device=DEV)     # (the others' positions are bad: left alone)
+    q[at], k[at], v[at], pos[at], slot[at] = small.q, small.k, small.v, small.pos, small.slot
+    cache, err = small.cache.clone(), torch.zeros(1, dtype=torch.int32, device=DEV)
+    sra.rope_kv_store_quant(q, k, v, small.cos, small.sin, pos, slot, cache, err_count=err)
+    small.store()
+    assert int(err.item()) == T - 3 * few
+    assert same(q[at], small.q) and same(cache, small.cache)
+
+
 @pytest.mark.parametrize("B,variant", [(65536, 0), (65536, 1), (65537, 0), (100000, 0)])
 def test_batches_at_the_border(B, variant):
     """As many requests as the stream form takes, and more: most of them empty or of a token or two."""
