@@ -669,8 +669,9 @@ SRA_API int64_t sra_kv_quant_row_bytes(int head_dim, int format);
 
 /*
  * sra_rope_kv_store_quant — sra_rope_kv_store_ex (all of q_alpha .. k_gamma NULL) or sra_rope_kv_store_qk_uclip (all
- * given) into a cache held in 4 or 8 bits: q is rotated in place with their result, bit for bit; the rotated K, correctly
- * rounded to fp32 and then to `dtype`, and V are quantised into the token's slot. Token rules and err_count are theirs
+ * given) into a cache held in 4 or 8 bits: q is rotated in place with their result, bit for bit; the rotated K, each
+ * a c - b s rounded once to fp32 (from its exact value; a zero has IEEE's sign) and then to `dtype`, and V are quantised into
+ * the token's slot. Token rules and err_count are theirs
  * (two tokens with the same valid slot race for its codes and scales one by one: the slot holds a mix of both).
  * Errors: theirs; an unknown format -> SRA_ERR_ARG; a cache not 16-byte aligned -> SRA_ERR_ARG; some but not all of the four
  * parameters -> SRA_ERR_NULL; head_dim other than 64, 128 and 256 -> SRA_ERR_SHAPE; pos, slot_mapping, a table or a

@@ -6,8 +6,9 @@
 // neox pairing a K task holds half of two groups, whose other halves the neighbouring thread has (one shuffle
 // each); otherwise a task is a group.
 //
-// K's rotation is the correctly rounded fp32 number (the product difference is kept as a sum of two fp32 numbers), rounded
-// once more to the dtype. A code can hang on the last place of its value, and with this the cache's bytes
+// K's rotation is the correctly rounded fp32 number, rounded once more to the dtype: an interval that holds the difference of
+// products settles nearly all, the others are evaluated exactly (16384 tokens as below 28.4 us with neither, 28.7; in fp32, whose interval takes
+// more work, 4096 tokens of 8 / 8 heads 16.8 and 17.9). A code can hang on the last place of its value, and with this the cache's bytes
 // follow from the definition, whoever evaluates it. (Q is rotated exactly as sra_rope_kv_store does it.)
 //
 // It is bound by a launch and a round trip to memory (2.5 us for 64 tokens), then by latencies between loads, tables and stores that five
@@ -27,13 +28,75 @@ namespace kvq {
 
 constexpr int kThreads = 256;
 
-// The fp32 number nearest to a * c - b * s (of a sum that is known to about 2^-46 of the products).
+// The bits of the largest magnitude (those of infinities and NaN are above all others).
+template <int N>
+__device__ __forceinline__ uint32_t amax_bits(const float (&x)[N]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
+    return m;
+}
+// K's rotation: a * c - b * s rounded once to fp32, then to T. Each operation below is rounded by itself, whatever the compiler may
+// contract elsewhere: the error-free sums rest on it.
+
+// By 64-bit arithmetic: the products are exact there, and a difference rounded to odd (53 bits) gives the same fp32 number as the
+// exact one (Boldo and Melquiond).
+__device__ __forceinline__ float rotate_wide(float a, float c, float b, float s) {
+    const double p = __dmul_rn(a, c), q = __dmul_rn(b, s);
+    double d = __dsub_rn(p, q);
+    const double bb = __dsub_rn(d, p), e = __dsub_rn(__dsub_rn(p, __dsub_rn(d, bb)), __dadd_rn(q, bb));  // p - q = d + e
+    const long long bits = __double_as_longlong(d);
+    if ((e > 0.0 || e < 0.0) && !(bits & 1)) d = __longlong_as_double((e > 0.0) == (d > 0.0) ? bits + 1 : bits - 1);  // (then d is not 0)
+    return __double2float_rn(d);
+}
+// x + y = the result + *err, exactly (Knuth's two-sum).
+__device__ __forceinline__ float two_sum(float x, float y, float* err) {
+    const float z = __fadd_rn(x, y), yy = __fsub_rn(z, x);
+    *err = __fadd_rn(__fsub_rn(x, __fsub_rn(z, yy)), __fsub_rn(y, yy));
+    return z;
+}
+// Whether x y is 0 or so large that its rounding error is an fp32 number.
+__device__ __forceinline__ bool splits(float xy, float x, float y) { return fabsf(xy) >= 0x1p-100f || x == 0.0f || y == 0.0f; }
+// Exactly, in fp32 where two of its numbers hold the difference (the ties and zeros of 16-bit inputs).
 __device__ __forceinline__ float rotate_exact(float a, float c, float b, float s) {
-    const float p = a * c, q = b * s;
-    const float ep = fmaf(a, c, -p), eq = fmaf(b, s, -q);
-    const float d = p - q, bb = d - p;
-    const float e = (p - (d - bb)) + (-q - bb);  // p - q = d + e, exactly (Knuth's two-sum)
-    return d + (e + (ep - eq));
+    const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
+    const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
+    float e, el, tl;
+    const float d = two_sum(p, -q, &e), g = two_sum(ep, -eq, &el), t = two_sum(e, g, &tl);
+    // (without a t the sign of a zero is d's, IEEE's)
+    if (el == 0.0f && tl == 0.0f && splits(p, a, c) && splits(q, b, s)) return t == 0.0f ? d : __fadd_rn(d, t);
+    return rotate_wide(a, c, b, s);
+}
+// Nearly always: an interval that holds the difference. Where both ends of it are the same as T, so is the exact result; where not, and for
+// a difference of 0, an infinity or a NaN, `doubt` becomes other than 0 or the result is not finite.
+template <typename T>
+__device__ __forceinline__ float rotate_near(float a, float c, float b, float s, uint32_t& doubt) {
+    float ends[2];
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        // diff_of_products is off by 2^-23 of the difference at most (Jeannerod, Louvet and Muller), two places of fp32: a warp's 512
+        // values need the exact form once in 32 times (in fp16, whose numbers lie closer, it would be once in four)
+        const uint32_t bits = __float_as_uint(rope::diff_of_products(a, c, b, s));
+        ends[0] = __uint_as_float(bits - 2), ends[1] = __uint_as_float(bits + 2);
+    } else {
+        // d + t, t off by less than 2^-44 (|p| + |q|): its three roundings come to 2.5 * 2^-47, and what a product loses below 2^-149
+        // is far less than 2^-144
+        const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
+        const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
+        float e;
+        const float d = two_sum(p, -q, &e), t = __fadd_rn(e, __fsub_rn(ep, eq));
+        const float size = fmaxf(__fadd_rn(fabsf(p), fabsf(q)), 0x1p-100f);
+        ends[0] = __fadd_rn(d, __fmaf_rn(size, -0x1p-44f, t)), ends[1] = __fadd_rn(d, __fmaf_rn(size, 0x1p-44f, t));
+    }
+    if constexpr (sizeof(T) == 4) {
+        doubt |= __float_as_uint(ends[0]) ^ __float_as_uint(ends[1]);
+        return ends[0];
+    } else {
+        const uint32_t v = Elem<T>::pack_word(ends);
+        doubt |= v ^ __byte_perm(v, v, 0x1032);
+        float f[2];
+        Elem<T>::unpack_word(v, f);
+        return f[0];
+    }
 }
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, bool wide, float (&f)[8]) {
@@ -68,14 +131,6 @@ __device__ __forceinline__ void store8(T* p, bool wide, const float (&f)[8]) {
     }
 }
 
-// The bits of the largest magnitude (those of infinities and NaN are above all others).
-template <int N>
-__device__ __forceinline__ uint32_t amax_bits(const float (&x)[N]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
-    return m;
-}
 template <int FMT>
 __device__ __forceinline__ uint32_t scale_of(uint32_t bits) {
     return bits >= 0x7f800000u ? kScaleNaN : scale_code<FMT>(__uint_as_float(bits));
@@ -134,11 +189,11 @@ __device__ __forceinline__ void store_task(const RopeArgs& a, const StoreGrid& g
     // offsets of the task's two runs of eight values
     const int o0 = ROW ? 16 * g : 8 * g, o1 = ROW ? 16 * g + 8 : h + 8 * g;
     T* q = nullptr;
+    const T* src = nullptr;
     if (live) {
         const int64_t capacity = a.num_blocks * static_cast<int64_t>(a.block_size), ho = static_cast<int64_t>(head) * D;
         p = a.pos[t];
         if (KIND != 0) slot = a.slot[t];
-        const T* src;
         if (KIND == 0) src = q = static_cast<T*>(a.q) + t * a.qs + ho;
         else src = KIND == 1 ? static_cast<const T*>(a.k) + t * a.ks + ho : static_cast<const T*>(a.v) + t * a.vs + ho;
         load8(src + o0, wide, x0);
@@ -151,12 +206,12 @@ __device__ __forceinline__ void store_task(const RopeArgs& a, const StoreGrid& g
         live = pos_ok && (KIND == 0 || (slot >= 0 && !past));
     }
     if (KIND != 2 && live) {
+        const float* pa = KIND == 0 ? a.qa : a.ka;
+        const float* pg = KIND == 0 ? a.qg : a.kg;
         float c[8], s[8];
         load8(a.cos + p * h + 8 * g, wide, c);
         load8(a.sin + p * h + 8 * g, wide, s);
         if constexpr (NORM) {
-            const float* pa = KIND == 0 ? a.qa : a.ka;
-            const float* pg = KIND == 0 ? a.qg : a.kg;
             float al[8], ga[8];
             load8(pa + o0, wide, al);
             load8(pg + o0, wide, ga);
@@ -168,19 +223,39 @@ __device__ __forceinline__ void store_task(const RopeArgs& a, const StoreGrid& g
             for (int j = 0; j < 8; ++j) x1[j] = round_trip<T>(rope::uclip1(x1[j], al[j], ga[j], a.clip_lo, a.clip_hi));
         }
         // pair j: neox (x0[j], x1[j]); interleaved elements 2j and 2j + 1 of the two runs
+        auto first = [&](int j) -> float& { return IL ? (j < 4 ? x0[2 * j & 7] : x1[2 * j & 7]) : x0[j]; };
+        auto second = [&](int j) -> float& { return IL ? (j < 4 ? x0[(2 * j + 1) & 7] : x1[(2 * j + 1) & 7]) : x1[j]; };
+        uint32_t again = 0;  // K's pairs that rotate_near does not settle
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float& lo = IL ? (j < 4 ? x0[2 * j & 7] : x1[2 * j & 7]) : x0[j];
-            float& hi = IL ? (j < 4 ? x0[(2 * j + 1) & 7] : x1[(2 * j + 1) & 7]) : x1[j];
-            float y0, y1;
+            const float lo = first(j), hi = second(j);
             if constexpr (KIND == 0) {
-                y0 = rope::diff_of_products(lo, c[j], hi, s[j]);
-                y1 = rope::diff_of_products(hi, c[j], -lo, s[j]);
+                first(j) = rope::diff_of_products(lo, c[j], hi, s[j]);
+                second(j) = rope::diff_of_products(hi, c[j], -lo, s[j]);
             } else {
-                y0 = round_trip<T>(rotate_exact(lo, c[j], hi, s[j]));
-                y1 = round_trip<T>(rotate_exact(hi, c[j], -lo, s[j]));
+                uint32_t doubt = 0;
+                first(j) = rotate_near<T>(lo, c[j], hi, s[j], doubt);
+                second(j) = rotate_near<T>(hi, c[j], -lo, s[j], doubt);
+                if (doubt != 0) again |= 1u << j;
             }
-            lo = y0, hi = y1;
+        }
+        if constexpr (KIND == 1) {
+            if (max(amax_bits(x0), amax_bits(x1)) >= 0x7f800000u) again = 0xff;
+            while (again != 0) {  // (their inputs are read once more; a rolled loop, because unrolled its code comes in from far)
+                const int j = __ffs(again) - 1;
+                again &= again - 1;
+                const int i0 = IL ? o0 + 2 * j : o0 + j, i1 = IL ? i0 + 1 : o1 + j;
+                float lo = to_f32(src[i0]), hi = to_f32(src[i1]);
+                if constexpr (NORM) {
+                    lo = round_trip<T>(rope::uclip1(lo, pa[i0], pg[i0], a.clip_lo, a.clip_hi));
+                    hi = round_trip<T>(rope::uclip1(hi, pa[i1], pg[i1], a.clip_lo, a.clip_hi));
+                }
+                const float cj = a.cos[p * h + 8 * g + j], sj = a.sin[p * h + 8 * g + j];
+                const float y0 = round_trip<T>(rotate_exact(lo, cj, hi, sj)), y1 = round_trip<T>(rotate_exact(hi, cj, -lo, sj));
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k == j) first(k) = y0, second(k) = y1;
+            }
         }
     }
     if constexpr (KIND == 0) {
