@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvReadArgs a, int tile, 
                 const int64_t first = cu(lo);
                 const int64_t from = a.starts ? a.starts[lo] : 0;
                 const int64_t tok = from + (i - first);
-                const bool in_row = from >= 0 && tok < a.max_blocks * a.block_size;
+                const bool in_row = tok >= 0 && tok < a.max_blocks * a.block_size;
                 const int64_t j = in_row ? tok / a.block_size : 0, off = tok - j * a.block_size;
                 const int32_t page = in_row ? a.table[lo * a.max_blocks + j] : -1;
                 const bool ok = page >= 0 && page < a.num_blocks;
