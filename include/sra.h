@@ -694,7 +694,8 @@ SRA_API int sra_rope_kv_store_quant(void* q, const void* k, const void* v, const
  * and v likewise, each value rounded once to `dtype` (exact in fp16 and fp32, and in bf16 for 4 bits).
  * block_table: int32 [rows, max_blocks_per_seq]; cu_lens: int32 [rows + 1], not falling; starts: NULL (zeros) or int32
  * [rows]; k, v: [total, n_kv_head, head_dim], token strides k_tok_stride and v_tok_stride (views of one buffer
- * will do). What lies outside [cu_lens[0], cu_lens[rows]) is left as it was.
+ * will do). What lies outside [cu_lens[0], cu_lens[rows]) is left as it was; lengths that begin below 0 or end above total ask
+ * for what of them is in the results.
  * err_count: nullable device int32, incremented once for each entry outside [0, num_blocks) that holds a token asked
  * for and once for each row that asks for tokens outside [0, max_blocks_per_seq * block_size); those tokens are zeros.
  * Nothing is read or written out of range for any contents of the device arrays.

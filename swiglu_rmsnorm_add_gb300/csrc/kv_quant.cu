@@ -399,8 +399,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvReadArgs a, int tile, 
                 const int64_t j = in_row ? tok / a.block_size : 0, off = tok - j * a.block_size;
                 const int32_t page = in_row ? a.table[lo * a.max_blocks + j] : -1;
                 const bool ok = page >= 0 && page < a.num_blocks;
-                // one count for a bad entry (at its first token), one for each row that leaves its table (likewise)
-                if (!ok && a.err && (i == first || (in_row ? off == 0 : from >= 0 && tok == a.max_blocks * a.block_size)))
+                // one count for a bad entry (at the first of its tokens in the results), one for each row that leaves its table (likewise)
+                const int64_t seen = first < 0 ? 0 : first;
+                if (!ok && a.err && (i == seen || (in_row ? off == 0 : from + (seen - first) >= 0 && tok == a.max_blocks * a.block_size)))
                     atomicAdd(a.err, 1);
                 at = ok ? static_cast<int64_t>(page) * a.n_kv * a.block_size + off : -1;
             }

@@ -81,6 +81,14 @@ def test_starts(cu, starts, fmt, dtype, bad):
 
 
 @pytest.mark.parametrize("cu,starts", [
+    ([-3, 4, 30], None), ([-13, -2, 40], [0, 0]), ([-20, 100], [0]), ([-5, 31, 48], [-2, 29]), ([-5, 31, 48], [-9, 33]), ([-40, 10, 12], [0, 0]),
+    ([-BIG - 1, 12], [BIG]), ([-4, 12], [29])])
+@pytest.mark.parametrize("seed", range(3))
+def test_lengths_that_begin_before_the_results(cu, starts, seed):
+    check("e2m1", torch.float16, random_table(seed, len(cu) - 1, 2), cu, starts)
+
+
+@pytest.mark.parametrize("cu,starts", [
     ([5, 2, 9], None), ([0, 100, 3], None), ([9, 5, 1], [0, 1]), ([BIG, 0, -BIG - 1], [0, -BIG - 1]), ([7, -BIG - 1, BIG, 30], [BIG, -BIG - 1, 0])])
 def test_lengths_that_fall(cu, starts):
     check("int8", torch.float16, random_table(7, len(cu) - 1, 2), cu, starts, ordered=False)
