@@ -4,6 +4,7 @@ from __future__ import annotations
 import array
 import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -999,9 +1000,13 @@ def _row_bytes(fmt: str, head_dim: int) -> int:
 def quant_kv_cache(num_blocks: int, block_size: int, n_kv_head: int, head_dim: int, fmt: str = "e2m1",
                    layers: int | None = None, device="cuda") -> torch.Tensor:
     """An empty cache held in 4 ("e2m1") or 8 ("int8") bits: uint8 [2, num_blocks, n_kv_head, block_size, row_bytes],
-    with `layers` one [layers, 2, ...] tensor of them. head_dim 64, 128 or 256."""
+    with `layers` one [layers, 2, ...] tensor of them. head_dim 64, 128 or 256. Each layer is contiguous and begins on a 16-byte
+    border (where a layer's bytes are no multiple of 16, the layers lie a few bytes apart)."""
     shape = (2, num_blocks, n_kv_head, block_size, _row_bytes(fmt, head_dim))
-    return torch.zeros(shape if layers is None else (layers, *shape), dtype=torch.uint8, device=device)
+    if layers is None:
+        return torch.zeros(shape, dtype=torch.uint8, device=device)
+    n = math.prod(shape)
+    return torch.zeros((layers, -(-n // 16) * 16), dtype=torch.uint8, device=device)[:, :n].view(layers, *shape)
 
 
 def _quant_cache(kv_cache, head_dim):
