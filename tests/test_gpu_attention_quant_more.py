@@ -1,4 +1,15 @@
-"""GPU: decode attention over a cache in 4 or 8 bits: rings filled again many times.
+"""GPU: decode attention over a cache in 4 or 8 bits: rings filled again many times, tables much wider than the requests, and fp32
+queries within a bound of their own.
+
+The tolerance of fp32 queries here follows from the scores. With X = the largest sum_i |scale q_i k_i| of a head over its
+tokens and e = 2^-23:
+* a score is off by (1 + 17 + 17 * HD / 16 + HD / 16) e X at most: q in two fp16 parts (2^-23 of an element), the truncation of a
+  product of 16 terms onto a running sum (17 addends, each cut below 2^-23 of the largest; the lower part of q runs over all steps,
+  the upper starts anew at each), the additions between steps; and a few roundings of its factor and difference from the
+  maximum, 4 e of scores no larger than 1.5 X + 15;
+* a probability by that, by 2^-22 of the exponential, 2^-22 of its two parts;
+* sums over n tokens: n / 8 + 16 additions (a lane's own, then lanes, warps, CTAs), and for the values 34 truncations a tile.
+All of it relative to A = sum_t p_t |V_t|, twice (above and below the division).
 """
 import numpy as np
 import pytest
@@ -42,3 +53,44 @@ def test_rings_that_turn_often(form, fmt, hd, bs, dtype):
     torch.cuda.synchronize()
     c.check(outs[0])
     assert all(torch.equal(outs[0].view(torch.uint8), x.view(torch.uint8)) for x in outs)
+
+
+@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("auto", [False, True])
+@pytest.mark.parametrize("fmt,hd,bs,lens", [("e2m1", 128, 16, [250]), ("int8", 64, 32, [1, 0, 777, 33]), ("e2m1", 256, 8, [40] * 70),
+                                           ("int8", 128, 16, [4096] + [3] * 9)])
+def test_tables_much_wider_than_the_requests(variant, auto, fmt, hd, bs, lens):
+    """Tables for 65536 tokens: what lies behind a request's pages is not looked at."""
+    c = Case(8, 2, hd, bs, lens, fmt, BF, seed=len(lens))
+    wide = np.full((len(lens), 65536 // bs), 2 ** 31 - 1)
+    wide[::2] = -7
+    wide[:, :c.table.shape[1] - 1] = c.table[:, :-1]
+    c.table = wide
+    if not auto:
+        (got,) = attend(c, variant)
+    else:
+        d = c.dev()
+        w = sra.decode_attention_quant_workspace(len(lens), 8, 2, hd, wide.shape[1], bs, fmt, BF, DEV) if variant else None
+        got = sra.paged_decode_attention_quant(**d, scale=c.scale, workspace=w)
+    c.check(got)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("fmt", ["e2m1", "int8"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("scale", [0.0, 1e-4, 2e-3, 0.02])
+def test_fp32_queries(form, fmt, hd, scale):
+    c = Case(6, 2, hd, 16, [300, 1, 33, 77, 150], fmt, F32, seed=hd + 1, scale=scale)
+    (got,) = attend(c, FORMS[form])
+    o, A, S = c.want()
+    q, e, G = c.q.double().numpy(), 2.0 ** -23, 3
+    tol = np.zeros_like(o)
+    for b, n in enumerate(c.lens):
+        k, _ = c.tokens(b)
+        for h in range(6):
+            X = scale * (np.abs(q[b, h]) * np.abs(k[:, h // G])).sum(-1).max()
+            score = (1 + 17 + 17 * hd / 16 + hd / 16) * e * X + 4 * e * (1.5 * X + 15)
+            tol[b, h] = e / 2 * np.abs(o[b, h]) + 2 * (score + 2 * 2.0 ** -22 + (n / 8 + 16 + 34 * (n / 32 + 1)) * e / 2) * A[b, h]
+    g = got.double().cpu().numpy()
+    err = np.abs(g - o) - tol - 2.0 ** -39 * S
+    assert (err <= 0).all(), (float(err.max()), float((np.abs(g - o) / np.maximum(tol, 1e-30)).max()))
