@@ -495,6 +495,8 @@ __device__ __forceinline__ void init_barriers(unsigned char* smem) {  // each wa
     __syncwarp();
 }
 
+constexpr uint32_t kGaveUp = 1u << 31;  // a wait of this warp ran out: it asks for no more tiles
+
 // The tiles first + warp, first + warp + stride, ... below `end` of a pair whose request has `len` tokens. Leaves the CTA's
 // maxima and sums (res_ml) and unnormalised output (res_o) in shared memory; the CTA's warps meet before they are read.
 template <typename S, bool F32, int FMT, int HD, int BS>
@@ -549,6 +551,8 @@ __device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* s
 #pragma unroll
     for (int s = 0; s < ST; ++s) page[s] = entry(t0 + s * stride);
     int32_t next = entry(t0 + ST * stride);
+    uint32_t phase = *turn;  // parity of the stages' next phases, a bit each, and kGaveUp
+    if (phase & kGaveUp) end = t0;
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
         if (t0 + s * stride < end) issue(t0 + s * stride, page[s], s);
@@ -559,9 +563,15 @@ __device__ __forceinline__ void segment(const QuantAttnArgs& a, unsigned char* s
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.0f;
     int stage = 0;
-    uint32_t phase = *turn;  // parity of the stages' next phases, a bit each
     for (int t = t0; t < end; t += stride) {
-        mbar_wait(bar + stage, (phase >> stage) & 1u);
+        if (!__all_sync(FULL, mbar_wait(bar + stage, (phase >> stage) & 1u))) {  // counted; the results are void
+            for (int s = 1; s < ST; ++s) {  // the other stages' copies are out as well: none may land in another CTA's memory
+                const int other = (stage + s) % ST;
+                if (t + s * stride < end) mbar_wait(bar + other, (phase >> other) & 1u);
+            }
+            phase |= kGaveUp;
+            break;
+        }
         phase ^= 1u << stage;
         const uint32_t valid = mask[stage];
         const bool whole = valid == FULL;
