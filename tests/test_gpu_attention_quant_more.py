@@ -16,7 +16,6 @@ import pytest
 import torch
 
 import swiglu_rmsnorm_add_gb300 as sra
-from tests import quant_model as qm
 from tests.test_gpu_attention_quant import BF, DEV, F32, HF, Case
 
 pytestmark = pytest.mark.gpu

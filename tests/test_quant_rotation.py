@@ -198,3 +198,45 @@ def test_k_is_rounded_once(kind, dtype, swap, style, fmt):
     bad = (got != want).any(-1)
     t = int(bad.argmax())
     assert not bad.any(), (int(bad.sum()), int((got != want).sum()), t, got[t].tolist(), want[t].tolist())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["e2m1", "int8"])
+@pytest.mark.parametrize("style", ["neox", "interleaved"])
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("kind", ["borders", "ties", "sparse"])
+def test_behind_the_norm_and_out_of_views(kind, shift, dtype, style, fmt):
+    """The pairs that are rotated once more take the norm's values, from tensors of any alignment."""
+    T, r = 64, np.random.default_rng(7)
+    if kind == "sparse":        # two pairs of three are zeros
+        p = at_borders(T, fmt, r)
+        zero = r.integers(0, 3, (T, 32)) > 0
+        p.a[zero], p.b[zero] = -0.0, 0.0
+    else:
+        p = KINDS[kind](T, fmt, r)
+    a, b, s = p.rows(False, dtype)
+    lo, hi = (slice(0, 32), slice(32, 64)) if style == "neox" else (slice(0, None, 2), slice(1, None, 2))
+    gain = f32(2.0 ** r.integers(-2, 3, 64))
+    want, k = np.zeros((T, 1, 64)), np.zeros((T, 1, 64), dtype=np.float32)
+    want[:, 0, lo], want[:, 0, hi] = rotated32(a, p.c, b, s), rotated32(b, p.c, -a, s)
+    want = qm.encode(qm.rounded(want, dtype), fmt)[:, 0]
+    k[:, 0, lo], k[:, 0, hi] = a, b
+    k = k / gain                # (the norm's alpha puts it back: powers of two, exact away from fp16's subnormal numbers)
+    if dtype == HF:
+        k = k * (gain if kind == "ties" else 1)
+    alpha = gain if not (dtype == HF and kind == "ties") else np.ones_like(gain)
+
+    def view(x, dt):
+        x = torch.tensor(x).to(dt)
+        room = torch.zeros(x.numel() + 8, dtype=dt, device=DEV)
+        return room[shift:shift + x.numel()].view(x.shape).copy_(x)
+    one = view(np.ones(64, dtype=np.float32), F32)
+    z = torch.zeros(T, 1, 64, dtype=dtype, device=DEV)
+    cache = sra.quant_kv_cache(T // 8, 8, 1, 64, fmt, device=DEV)
+    at = torch.arange(T, device=DEV)
+    sra.rope_kv_store_quant(z.clone(), view(k, dtype), z, view(p.c, F32), view(s, F32), at, at, cache, style=style,
+                            qk_uclip=(one, one, view(alpha, F32), one), clip=(-1e30, 1e30))
+    got = cache[0].reshape(T, -1).cpu().numpy()
+    diff = np.argwhere(got != want)
+    assert not len(diff), (len(diff), diff[0].tolist())
