@@ -660,7 +660,8 @@ SRA_API int64_t sra_shared_prefix_workspace_size(int64_t B, int n_head, int n_kv
  *                scale = amax / 6 rounded to nearest (ties to an even byte), at most 10240.
  *   SRA_KV_INT8  value = n * scale, byte i = n of dim i. scale = amax / 127 rounded up, at most 512.
  * amax is the group's largest magnitude; a code is the nearest to x / scale, ties to the even code, saturating (values
- * above 61440 or 65024 are held as those). A group whose scale rounds to 0 (amax up to 6 * 2^-18, 4 bits) holds zeros.
+ * above 61440 or 65024 are held as those). In 4 bits a group's largest value is held up to 6 % short where amax is at least 6 * 2^-14,
+ * up to 6 * 2^-18 short below; a group whose scale rounds to 0 (amax up to 6 * 2^-18, 4 bits) holds zeros.
  * Every value is an fp16 number. The bytes follow from the inputs alone.
  */
 

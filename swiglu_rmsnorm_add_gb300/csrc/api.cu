@@ -2056,7 +2056,8 @@ QuantAttnForm quant_attn_form(int64_t B, int n_kv, int64_t tokens, int format, i
            tokens >= 2 * 32 * warps * static_cast<int64_t>(f.splits))
         f.splits *= 2;
     // The stream form has a second launch and a search for its parts (some 4 us), and gives every SM the same to do: for CTAs with many
-    // tokens. Both (cluster, stream), lengths alike and from 1 on: bf16, e2m1, head_dim 128, 2 heads, batch 64 x 4096 26, 30 and 21, 21 us,
+    // tokens. `tokens` is what a row of the table has room for (lengths are on the device): in tables of 32768 tokens 1 x 250 takes the
+    // stream form's 7.4 us instead of 5.0, 8 x 4096 12.8 and 9.7, 64 x 1 to 2048 19.9 and 17.0. Both (cluster, stream), lengths alike and from 1 on: bf16, e2m1, head_dim 128, 2 heads, batch 64 x 4096 26, 30 and 21, 21 us,
     // x 8192 41, 44 and 38, 31, x 16384 72, 70 and 65, 45; 256 x 4096 75, 77 and 55, 54, x 16384 254, 228 and 173, 134; int8, 16 x 4096 of
     // 8 heads 32, 37 and 30, 27, x 8192 53, 58 and 49, 38; head_dim 256, 32 x 16384 of one 41, 46 and 38, 35, x 32768 68, 70 and 64, 48.
     // fp32 does twice as much for a token: 16 x 2048 of 8 heads 16, 22 and 16, 17, x 4096 29, 32 and 25, 22.

@@ -30,8 +30,9 @@
 // for some six cycles (measured: a product with four conversions and four multiplications takes 14 cycles, not nine), the softmax, the
 // copies. A scheduler takes 0.48 us for a tile with four warps (0.64 with two; registers and rings leave room for four), where HBM's
 // copy rate would give it one in 0.41: long streams run at 5.9 TB/s. A call's start, its changes of pair and the merge come to some 20 us:
-// batch 256 x 16384 of 2 heads (from 4000 tokens on, 755 MB) 156 us, 112 at the copy rate. 8 bits have half the instructions for a
-// byte: 16 x 32768 of 8 heads 178 us, 169 at the copy rate.
+// batch 256 x 16384 of 2 heads (from 4000 tokens on, 755 MB) 157 us, 112 at the copy rate. 8 bits have half the instructions for a
+// byte: 16 x 32768 of 8 heads 188 us, 169 at the copy rate. Other forms: 32 x 32768 of one head of 256 74 us (45) in 4 bits, 110 (84) in 8,
+// where an SM has one CTA; 24 x 8192 of 4 heads of 128, fp32, 45 (17) and 52 (32); 64 x 8192 of 4 heads of 64 52 (22) and 62 (42).
 // Measured and left: the next tile's scores beside a tile's values (64 x 16384 72 -> 75 us), a third CTA an SM in 80 registers (81), tiles of 64
 // tokens (73.5), a running maximum that follows only a score of twice its weight (157.7 -> 157.3).
 #pragma once

@@ -252,7 +252,10 @@ struct QuantAttnPlan {
     int stream_ctas;  // > 0: the stream form, with that many CTAs
     bool pdl;
 };
-// Warps per CTA and CTAs per SM (alike for all dtypes and block sizes).
+// Warps per CTA and CTAs per SM (alike for all dtypes and block sizes). Eight warps, two CTAs, where the rings of as many hold two stages or
+// more of a tile's K and V (64 rows): three fit at 4608 bytes a stage. From 8704 on (8 bits of 128, 256) two do not, and four warps a CTA have
+// three stages; in 8 bits of 256 (17408) one CTA of four warps an SM. (Six warps with two stages for 8 bits of 128: within 5 % either
+// way, by lengths.)
 constexpr int quant_attn_warps(int format, int head_dim) { return 64 * kv_row_bytes(format, head_dim) <= 4608 ? 8 : 4; }
 constexpr int quant_attn_ctas(int format, int head_dim) { return format == KV_INT8 && head_dim == 256 ? 1 : 2; }
 unsigned int quant_attn_wait_timeouts();

@@ -11,9 +11,10 @@
 // multiplication makes it. An integer is chosen for the 8 bits because e4m3's smallest numbers times the
 // smallest scales are no fp16 numbers.
 //
-// The e2m1 scale is amax / 6 rounded to nearest: the largest value is clipped by 6 % at most, less than half of
-// the step (a third) that it sits in, and the other values gain. int8's is rounded up: its steps at amax
-// are 16 times finer than such a clip.
+// The e2m1 scale is amax / 6 rounded to nearest: from scales of 2^-14 on (amax 6 * 2^-14) the largest value is clipped by 6 % at most,
+// less than half of the step (a third) that it sits in, and the other values gain. Below, scales are multiples of 2^-17, and the clip is up to
+// 6 * 2^-18 (a third of amax 9 * 2^-17); a group up to 6 * 2^-18 is zeros. int8's is rounded up: its steps at amax are 16 times finer
+// than such a clip.
 //
 // A border between codes is a multiple of the scale with at most 7 (e2m1) or 12 (int8) bits, so it is an fp32 number, and the
 // correctly rounded quotient of a value and its scale lies on the same side of it: the bytes follow from the inputs exactly,

@@ -11,14 +11,18 @@
 // more work, 4096 tokens of 8 / 8 heads 16.8 and 17.9). A code can hang on the last place of its value, and with this the cache's bytes
 // follow from the definition, whoever evaluates it. (Q is rotated exactly as sra_rope_kv_store does it.)
 //
-// It is bound by a launch and a round trip to memory (2.5 us for 64 tokens), then by latencies between loads, tables and stores that five
-// CTAs an SM cover (4: 8.8 us, 6: 8.4 and spills) and HBM: 4096 tokens of 12 / 2 heads of 128 (bf16, 4 bits, 33 MB) 8.4 us, 4.8 at the copy rate;
-// 16384 of them 28.9. (All three tensors' tasks in the same CTAs: 4 us more; two heads of Q a thread 11.7, K's and V's CTAs among Q's
-// 10.9 for 4096 tokens.)
+// It is bound by a launch and a round trip to memory (2.3 us for 64 tokens), then by what a CTA does in turn, loads, tables, stores, which five
+// CTAs an SM cover in part (4: 8.8 us, 6: 8.4 and spills): 4096 tokens of 12 / 2 heads of 128 (bf16, 33 MB in 4 bits) 8.5 us, 4.8 at the copy
+// rate, 16384 28.6 and 18.7; in 8 bits 9.0 and 28.9; behind the Q/K norm, whose parameters every task reads, 12.3 and 43.2. At 16384 tokens
+// 0.61 of the issue slots are taken and L1 stands at 70 % of its peak; of 13.4 warps a scheduler 4.5 wait for loads, 2.5 for their turn, 1.2 for
+// the load and store unit. (All three tensors' tasks in the same CTAs: 4 us more; two heads of Q a thread 11.7, K's and V's CTAs among
+// Q's 10.9 for 4096 tokens.)
 //
 // Read. A CTA takes a tile of output tokens, finds each one's place in the cache once, and its threads turn groups of 16
-// codes into one 32-byte store each (two in fp32), four groups at a time. Bound by writes, four bytes in five: 16 requests of up to
-// 8192 tokens of 8 heads of 128 (4 bits to bf16, 285 MB written) 68 us, where a fill alone would take 75 (3.8 TB/s). One group at a time
+// codes into one 32-byte store each (two in fp32), four groups at a time: 16 requests of up to 8192 tokens of 8 heads of 128 (4 bits to
+// bf16, 285 MB written) 68 us, 54 at the copy rate. 16 x 4096 of 8 heads of 128: 4 bits to bf16 63 us (51 at the copy rate), 8 bits 71 (61), to
+// fp32 109 (90) and 123 (100), 5.5 to 5.8 TB/s. Neither HBM nor the issue of instructions is full (in 8 bits to bf16 0.60 of the slots, 30 warps an
+// SM by their registers): of 12.4 warps a scheduler 4.5 wait for codes and places, 1.7 at the barrier while places are found. One group at a time
 // and 16-byte stores 107; two groups at a time 72; the next tile's places found while a tile is read 70.
 #include "kv_format.cuh"
 #include "rope_math.cuh"
