@@ -338,7 +338,9 @@ __device__ __forceinline__ void softmax(float (&p)[kHalves][4], uint32_t valid, 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float now = fmaxf(m[h], mx[h]);
-        base[h] = now == -INFINITY ? 0.0f : now - kUnder;  // (no score above -inf yet: those weigh nothing)
+        // (no score above -inf yet: those weigh nothing. Rounded up: of a maximum past 2^25, whose neighbours lie 4 and more apart, the base
+        // must not lie further below than 2^14, where fp16 ends)
+        base[h] = now == -INFINITY ? 0.0f : __fsub_ru(now, kUnder);
         corr[h] = now == -INFINITY ? 1.0f : ex2(m[h] - now);
         m[h] = now;
     }

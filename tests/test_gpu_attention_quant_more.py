@@ -16,6 +16,7 @@ import pytest
 import torch
 
 import swiglu_rmsnorm_add_gb300 as sra
+from tests import quant_model as qm
 from tests.test_gpu_attention_quant import BF, DEV, F32, HF, Case
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +94,31 @@ def test_fp32_queries(form, fmt, hd, scale):
     g = got.double().cpu().numpy()
     err = np.abs(g - o) - tol - 2.0 ** -39 * S
     assert (err <= 0).all(), (float(err.max()), float((np.abs(g - o) / np.maximum(tol, 1e-30)).max()))
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("fmt", ["e2m1", "int8"])
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_whose_steps_are_large(form, fmt, dtype, sign):
+    """Scores up to 2^31, whose fp32 neighbours are up to 256 apart: the largest one takes all the weight, and the result is its V."""
+    c = Case(4, 2, 128, 16, [26, 9, 1], fmt, dtype, seed=3)
+    n = c.cache.shape[-1] - 8
+    r = np.random.default_rng(4)
+    best = []
+    for b, length in enumerate(c.lens):     # K of token t: its scale in every dim, another scale for each token
+        step = r.permutation(np.arange(100, 126))[:length]
+        for t in range(length):
+            row = c.cache[0, c.table[b, t // 16], :, t % 16]
+            row[:, :n], row[:, n:] = 0x22 if fmt == "e2m1" else 1, step[t]
+        best.append(int(step.argmax() if sign > 0 else step.argmin()))
+    c.q = torch.full_like(c.q, 64.0 * sign)
+    v = [c.tokens(b)[1] for b in range(3)]
+    for e in range(20, 32):
+        for m in (1.0, 1.3, 1.9):
+            top = max(float(np.abs(64.0 * 128 * qm.decode(c.cache[0, c.table[0, 0], 0, :16], fmt, 128)[:, 0]).max()), 1.0)
+            c.scale = m * 2.0 ** e / top / 1.4426950408889634
+            (got,) = attend(c, FORMS[form])
+            for b in range(3):
+                want = np.repeat(qm.rounded(v[b][best[b]], dtype), 2, 0)
+                assert np.array_equal(got[b].double().cpu().numpy(), want), (e, m, b)
