@@ -665,10 +665,11 @@ def _kv_caches(kv_caches):
     head_dim], a [layers, 2, ...] tensor of them, or a sequence of caches of one shape and dtype. The
     pointers are an array that has to live until the call returns. A cache in 4 or 8 bits (quant_kv_cache)
     is uint8 [2, num_blocks, n_kv_head, block_size, row_bytes]; its shape is given in the order of the others."""
-    shape, dtype, *rest = _caches_given(kv_caches)
-    if dtype is torch.uint8:
-        shape = [shape[0], shape[1], shape[3], shape[2], shape[4]]
-    return (shape, dtype, *rest)
+    given = _caches_given(kv_caches)
+    if given[1] is not torch.uint8:
+        return given
+    planes, nb, n_kv, bs, row = given[0]
+    return ([planes, nb, bs, n_kv, row], *given[1:])
 
 
 def _caches_given(kv_caches):
