@@ -8,12 +8,12 @@
 //
 // K's rotation is the correctly rounded fp32 number, rounded once more to the dtype: an interval that holds the difference of
 // products settles nearly all, the others are evaluated exactly (16384 tokens as below 28.4 us with neither, 28.7; in fp32, whose interval takes
-// more work, 4096 tokens of 8 / 8 heads 16.8 and 17.9). A code can hang on the last place of its value, and with this the cache's bytes
+// more work, 4096 tokens of 8 / 8 heads 16.8 and 18.2). A code can hang on the last place of its value, and with this the cache's bytes
 // follow from the definition, whoever evaluates it. (Q is rotated exactly as sra_rope_kv_store does it.)
 //
 // It is bound by a launch and a round trip to memory (2.3 us for 64 tokens), then by what a CTA does in turn, loads, tables, stores, which five
 // CTAs an SM cover in part (4: 8.8 us, 6: 8.4 and spills): 4096 tokens of 12 / 2 heads of 128 (bf16, 33 MB in 4 bits) 8.5 us, 4.8 at the copy
-// rate, 16384 28.6 and 18.7; in 8 bits 9.0 and 28.9; behind the Q/K norm, whose parameters every task reads, 12.3 and 43.2. At 16384 tokens
+// rate, 16384 28.6 and 18.7; in 8 bits 9.0 and 28.9; behind the Q/K norm, whose parameters every task reads, 12.8 and 43.6. At 16384 tokens
 // 0.61 of the issue slots are taken and L1 stands at 70 % of its peak; of 13.4 warps a scheduler 4.5 wait for loads, 2.5 for their turn, 1.2 for
 // the load and store unit. (All three tensors' tasks in the same CTAs: 4 us more; two heads of Q a thread 11.7, K's and V's CTAs among
 // Q's 10.9 for 4096 tokens.)
@@ -168,6 +168,14 @@ struct StoreGrid {
     Divisor q_tasks, kv_tasks, page;
 };
 
+// Whether all sixteen are zeros (of either sign).
+__device__ __forceinline__ bool zeros(const float (&x)[8], const float (&y)[8]) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) any |= __float_as_uint(x[j]) | __float_as_uint(y[j]);
+    return any << 1 == 0;
+}
+
 template <typename T, int FMT, bool IL, bool NORM, int KIND>  // KIND: 0 Q, 1 K, 2 V
 __device__ __forceinline__ void store_task(const RopeArgs& a, const StoreGrid& grid, int64_t cta) {
     const bool wide = grid.wide;
@@ -229,21 +237,30 @@ __device__ __forceinline__ void store_task(const RopeArgs& a, const StoreGrid& g
         // pair j: neox (x0[j], x1[j]); interleaved elements 2j and 2j + 1 of the two runs
         auto first = [&](int j) -> float& { return IL ? (j < 4 ? x0[2 * j & 7] : x1[2 * j & 7]) : x0[j]; };
         auto second = [&](int j) -> float& { return IL ? (j < 4 ? x0[(2 * j + 1) & 7] : x1[(2 * j + 1) & 7]) : x1[j]; };
-        uint32_t again = 0;  // K's pairs that rotate_near does not settle
+        if constexpr (KIND == 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float lo = first(j), hi = second(j);
-            if constexpr (KIND == 0) {
+            for (int j = 0; j < 8; ++j) {
+                const float lo = first(j), hi = second(j);
                 first(j) = rope::diff_of_products(lo, c[j], hi, s[j]);
                 second(j) = rope::diff_of_products(hi, c[j], -lo, s[j]);
-            } else {
+            }
+        } else if (zeros(x0, x1)) {  // (rotate_near settles none; padded dims, tokens without keys)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float lo = first(j), hi = second(j);
+                first(j) = __fsub_rn(__fmul_rn(lo, c[j]), __fmul_rn(hi, s[j]));
+                second(j) = __fsub_rn(__fmul_rn(hi, c[j]), __fmul_rn(-lo, s[j]));
+            }
+        } else {
+            uint32_t again = 0;  // pairs that rotate_near does not settle
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float lo = first(j), hi = second(j);
                 uint32_t doubt = 0;
                 first(j) = rotate_near<T>(lo, c[j], hi, s[j], doubt);
                 second(j) = rotate_near<T>(hi, c[j], -lo, s[j], doubt);
                 if (doubt != 0) again |= 1u << j;
             }
-        }
-        if constexpr (KIND == 1) {
             if (max(amax_bits(x0), amax_bits(x1)) >= 0x7f800000u) again = 0xff;
             while (again != 0) {  // (their inputs are read once more; a rolled loop, because unrolled its code comes in from far)
                 const int j = __ffs(again) - 1;
