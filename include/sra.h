@@ -619,6 +619,8 @@ SRA_API int64_t sra_kv_compact_workspace_size(int64_t num_blocks);
  * probabilities, the own tokens' too, are rounded once to the dtype before they multiply V (fp32
  * sums; in fp16 one that is subnormal is off by up to 2^-32 of its part's largest); the path without
  * a workspace keeps them to 16 bits or more.
+ * Scores (scale q . K) of 2^24 and more in fp16, of 2^30 and more in bf16, whose fp32 neighbours lie 2 and 128 apart, may
+ * leave a result with a workspace that is not finite, or zeros; the path without one holds them.
  *
  * q, kv_cache, out, scale: as in sra_paged_decode_attention. prefix_table: int32 [prefix_blocks];
  * prefix_len: device int32, one entry; block_table: int32 [B, max_blocks_per_seq]; seq_lens: int32 [B].
